@@ -15,6 +15,10 @@
  *   shuffled reduce-scatter / all-gather (SRS, SAG) -> smoe_srs, smoe_sag
  *   all of the above in one call                    -> smoe_layer_forward
  *   next-layer route predictor q = LN(d + r)        -> smoe_prefetch_predict
+ * and, around it when tokens are served,
+ *   residual add + RMS norm, with 8-bit rows        -> smoe_add_rmsnorm
+ *   the whole layer for at most 64 tokens           -> smoe_moe_forward_few
+ *   expert products / FFN in 8-bit integers         -> smoe_expert_matmul_i8, smoe_expert_ffn_i8
  *
  * Sources (page title, section):
  *   "Speculative MoE" (research-notes page): §1 top-K gating and EP
@@ -399,6 +403,95 @@ SMOE_API int smoe_moe_forward_routed(const smoe_desc* desc, const void* x,
                                      const int32_t* topk_idx, const float* topk_w,
                                      const void* w1, const void* w3, const void* w2, void* y,
                                      void* ws, size_t ws_bytes, void* stream);
+
+/* Residual add and root-mean-square norm in front of the layer (the pages have no
+ * counterpart): h = r + y, n = h gamma / sqrt(mean(h^2) + eps) over each row, in fp32.
+ *   r       [T, d] fp32 residual (as in smoe_prefetch_predict)
+ *   y       nullable [T, d] dtype: what is added to it (a layer output)
+ *   gamma   [d] fp32;  eps >= 0
+ *   r_out   nullable [T, d] fp32: h (may be the same buffer as r)
+ *   x_out   nullable [T, d] dtype: n (may be the same buffer as y)
+ *   q_out   nullable [T, d] int8: rint(n / q_scale), from n before x_out's rounding
+ *   q_scale [T] fp32, needed with q_out: max |n| / 127 of the row. A row whose scale would
+ *           be below the smallest normal fp32 number gets scale 0 and zeros; a row with an
+ *           infinity or a NaN gets scale NaN and zeros.
+ * At least one of r_out, x_out and q_out is given. d <= 16384 (a row is held in
+ * registers); else SMOE_ERR_SHAPE. No workspace.                                       */
+SMOE_API int smoe_add_rmsnorm(const smoe_desc* desc, const float* r, const void* y,
+                              const float* gamma, float eps, float* r_out, void* x_out,
+                              int8_t* q_out, float* q_scale, void* stream);
+
+/* Bytes of the workspace of smoe_moe_forward_few for this shape (of the same manner as
+ * every workspace: 256-byte aligned, its first 256 bytes zero before first use, read by
+ * smoe_get_status). Returns 0 if the descriptor is invalid or T > 64. */
+SMOE_API size_t smoe_few_workspace_size(const smoe_desc* desc);
+
+/* The whole layer for a few tokens (a decode step), in one kernel: gate, softmax, grouped
+ * top-K, the touched experts' SwiGLU FFN, shared experts included, and the weighted sum
+ * back into token order: what smoe_layer_forward computes without the shuffle. Each touched
+ * expert's weights are read once. T <= 64, else SMOE_ERR_SHAPE.
+ * Products accumulate in fp32; w_tk silu(W1 x) (W3 x) is rounded once to dtype before the
+ * down product, whose sum over the experts stays in fp32 until y. fp32 layers multiply in
+ * fp32 (not tf32). The result does not depend on timing.
+ *   x [T, d] dtype; w_gate [E, d] dtype; w1, w3 [E+n_shared, F, d], w2 [E+n_shared, d, F]
+ *   dtype; y [T, d] dtype (may be the same buffer as x)
+ *   logits nullable [T, E] fp32; topk_idx nullable [T, K] int32, topk_w nullable [T, K]
+ *   fp32: as smoe_route writes them
+ * The kernel's blocks wait on one another and are launched cooperatively, one on each SM. A
+ * wait that gives up is recorded as SMOE_ERR_DEVICE_TIMEOUT.                             */
+SMOE_API int smoe_moe_forward_few(const smoe_desc* desc, const void* x, const void* w_gate,
+                                  const void* w1, const void* w3, const void* w2, void* y,
+                                  float* logits, int32_t* topk_idx, float* topk_w, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Expert weights in 8-bit integers with a scale per output channel (device pointers):
+ * w1, w3 [E+n_shared, F, d], w2 [E+n_shared, d, F] int8; s1, s3 [E+n_shared, F],
+ * s2 [E+n_shared, d] fp32. The weight is the integer times its channel's scale. */
+typedef struct smoe_i8_weights {
+  const int8_t* w1;
+  const float* s1;
+  const int8_t* w3;
+  const float* s3;
+  const int8_t* w2;
+  const float* s2;
+} smoe_i8_weights;
+
+/* Bytes of the workspace of smoe_expert_matmul_i8 and smoe_expert_ffn_i8 for this shape
+ * (of the same manner as every workspace). Returns 0 if the descriptor is invalid. */
+SMOE_API size_t smoe_i8_workspace_size(const smoe_desc* desc);
+
+/* Grouped product in 8-bit integers with a scale per row and per output channel: for every
+ * expert e and each of its dispatched rows r,
+ *   out[r, n] = x_scale[s] w_scale[e, n] sum_k xq[s, k] wq[e, n, k],   s = row_src[r].
+ * The integer sum is exact while its partial sums stay below 2^24 in magnitude (any n_in up
+ * to 1024; in practice any), and accumulates in fp32 beyond.
+ *   xq         [T, n_in] int8 token rows when row_src is given (smoe_add_rmsnorm's q_out),
+ *              else [T K, n_in] rows already in dispatched order
+ *   x_scale    [T] or [T K] fp32, one per row of xq
+ *   row_src    nullable [T K] int32 in [0, T) (smoe_dispatch's row_token)
+ *   expert_off [E+1] int32 (from smoe_dispatch); rows outside the segments are not written
+ *   wq         [E, n_out, n_in] int8;  w_scale [E, n_out] fp32
+ *   out        [T K, n_out] dtype
+ * n_in is a multiple of 16 and at most the larger of desc->d and desc->F, n_out a multiple
+ * of 8. A row_src entry out of range gives a zero row and SMOE_ERR_DATA.               */
+SMOE_API int smoe_expert_matmul_i8(const smoe_desc* desc, int n_out, int n_in, const int8_t* xq,
+                                   const float* x_scale, const int32_t* row_src,
+                                   const int32_t* expert_off, const int8_t* wq,
+                                   const float* w_scale, void* out, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* The grouped SwiGLU expert FFN of smoe_expert_ffn in 8-bit integers: products as
+ * smoe_expert_matmul_i8; the hidden row h = silu(g) u, in fp32, is requantised with its own
+ * scale max |h| / 127 (and smoe_add_rmsnorm's rules for zero and non-finite rows).
+ *   xq, x_scale, row_src, expert_off as in smoe_expert_matmul_i8 with n_in = d; row_src is
+ *   needed when n_shared > 0 (shared expert j runs on all T rows of xq)
+ *   y_disp   [T K, d] dtype
+ *   y_shared nullable [n_shared, T, d] dtype (needed when n_shared > 0)
+ * d and F are multiples of 16. The outputs go to smoe_combine.                           */
+SMOE_API int smoe_expert_ffn_i8(const smoe_desc* desc, const int8_t* xq, const float* x_scale,
+                                const int32_t* row_src, const int32_t* expert_off,
+                                const smoe_i8_weights* weights, void* y_disp, void* y_shared,
+                                void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, returns SMOE_OK, SMOE_ERR_DATA or SMOE_ERR_DEVICE_TIMEOUT from
  * the workspace status word, and clears it. */

@@ -11,15 +11,16 @@ library (``synth``, ``build``, ``profiling``) neither imports ``binding`` nor ma
 import importlib
 
 _BINDING_NAMES = (
-    "SMOE_BF16", "SMOE_F32", "LayerIO", "LayerWeights", "SmoeDesc", "SmoeError",
-    "desc_from_config", "kernel_launches", "layer_io", "layer_weights", "lib", "make_desc",
-    "smoe_combine", "smoe_dispatch", "smoe_ep_exchange", "smoe_expert_ffn",
+    "I8Weights", "SMOE_BF16", "SMOE_F32", "LayerIO", "LayerWeights", "SmoeDesc", "SmoeError",
+    "desc_from_config", "i8_weights", "kernel_launches", "layer_io", "layer_weights", "lib", "make_desc",
+    "smoe_add_rmsnorm", "smoe_combine", "smoe_dispatch", "smoe_ep_exchange", "smoe_expert_ffn",
+    "smoe_expert_ffn_i8", "smoe_expert_matmul_i8", "smoe_moe_forward_few",
     "smoe_expert_ffn_gather", "smoe_expert_ffn_gather_fused", "smoe_get_status", "smoe_lar",
     "smoe_layer_forward", "smoe_moe_forward_routed", "smoe_layer_forward_host",
     "smoe_predict_shuffle", "smoe_predict_shuffle_inter", "smoe_predict_shuffle_noalloc",
     "smoe_prefetch_predict", "smoe_route", "smoe_sag", "smoe_selftest_device_timeout",
     "smoe_shuffle_dispatch_rows", "smoe_srs",
-    "smoe_token_cluster", "workspace", "workspace_size",
+    "smoe_token_cluster", "workspace", "workspace_few", "workspace_i8", "workspace_size",
 )
 
 __all__ = list(_BINDING_NAMES)

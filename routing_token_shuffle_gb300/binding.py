@@ -44,6 +44,10 @@ class LayerIO(ctypes.Structure):
                    ("skip_shuffle", ctypes.c_int32)]
 
 
+class I8Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "s1", "w3", "s3", "w2", "s2")]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _D = ctypes.POINTER(SmoeDesc)
@@ -74,6 +78,14 @@ SIGNATURES = {
     "smoe_prefetch_predict": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                              _P, _SZ, _P]),
     "smoe_moe_forward_routed": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_add_rmsnorm": (ctypes.c_int, [_D, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "smoe_few_workspace_size": (_SZ, [_D]),
+    "smoe_moe_forward_few": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_i8_workspace_size": (_SZ, [_D]),
+    "smoe_expert_matmul_i8": (ctypes.c_int, [_D, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, _P, _P,
+                                             _P, _P, _SZ, _P]),
+    "smoe_expert_ffn_i8": (ctypes.c_int, [_D, _P, _P, _P, _P, ctypes.POINTER(I8Weights), _P, _P, _P,
+                                          _SZ, _P]),
     "smoe_get_status": (ctypes.c_int, [_P, _P]),
     "smoe_selftest_device_timeout": (ctypes.c_int, [_P, _SZ, _P]),
     "smoe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -143,13 +155,27 @@ def workspace_size(desc: SmoeDesc) -> int:
     return lib().smoe_workspace_size(ctypes.byref(desc))
 
 
+def _zeroed(desc, fn: str, device):
+    import torch
+    n = getattr(lib(), fn)(ctypes.byref(desc))
+    if n == 0:
+        raise SmoeError(-2, fn, lib().smoe_last_error().decode())
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
 def workspace(desc: SmoeDesc, device="cuda"):
     """A zeroed workspace tensor (the status word must start at zero)."""
-    import torch
-    n = workspace_size(desc)
-    if n == 0:
-        raise SmoeError(-2, "smoe_workspace_size", "invalid descriptor")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _zeroed(desc, "smoe_workspace_size", device)
+
+
+def workspace_few(desc: SmoeDesc, device="cuda"):
+    """A zeroed workspace tensor for smoe_moe_forward_few."""
+    return _zeroed(desc, "smoe_few_workspace_size", device)
+
+
+def workspace_i8(desc: SmoeDesc, device="cuda"):
+    """A zeroed workspace tensor for smoe_expert_matmul_i8 and smoe_expert_ffn_i8."""
+    return _zeroed(desc, "smoe_i8_workspace_size", device)
 
 
 def smoe_route(desc, x, w_gate, topk_idx, topk_w, logits_in=None, logits_out=None, ws=None,
@@ -299,6 +325,45 @@ def smoe_moe_forward_routed(desc, x, topk_idx, topk_w, w1, w3, w2, y, ws, stream
                                          _ptr(topk_w), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(y),
                                          _ptr(ws), ws.numel(), _stream(stream)),
            "smoe_moe_forward_routed")
+
+
+def smoe_add_rmsnorm(desc, r, gamma, y=None, r_out=None, x_out=None, q_out=None, q_scale=None,
+                     eps=1e-6, stream=None):
+    _check(lib().smoe_add_rmsnorm(ctypes.byref(desc), _ptr(r), _ptr(y), _ptr(gamma), eps,
+                                  _ptr(r_out), _ptr(x_out), _ptr(q_out), _ptr(q_scale),
+                                  _stream(stream)), "smoe_add_rmsnorm")
+
+
+def smoe_moe_forward_few(desc, x, w_gate, w1, w3, w2, y, ws, logits=None, topk_idx=None,
+                         topk_w=None, stream=None):
+    """The whole layer for at most 64 tokens; ws from workspace_few."""
+    _check(lib().smoe_moe_forward_few(ctypes.byref(desc), _ptr(x), _ptr(w_gate), _ptr(w1),
+                                      _ptr(w3), _ptr(w2), _ptr(y), _ptr(logits), _ptr(topk_idx),
+                                      _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_moe_forward_few")
+
+
+def i8_weights(w1, s1, w3, s3, w2, s2) -> I8Weights:
+    return I8Weights(*(_ptr(t) for t in (w1, s1, w3, s3, w2, s2)))
+
+
+def smoe_expert_matmul_i8(desc, xq, x_scale, expert_off, wq, w_scale, out, ws, row_src=None,
+                          stream=None):
+    """wq [E, n_out, n_in]; n_out and n_in are taken from its shape; ws from workspace_i8."""
+    _, n_out, n_in = wq.shape
+    _check(lib().smoe_expert_matmul_i8(ctypes.byref(desc), n_out, n_in, _ptr(xq), _ptr(x_scale),
+                                       _ptr(row_src), _ptr(expert_off), _ptr(wq), _ptr(w_scale),
+                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_expert_matmul_i8")
+
+
+def smoe_expert_ffn_i8(desc, xq, x_scale, expert_off, weights: I8Weights, y_disp, ws,
+                       row_src=None, y_shared=None, stream=None):
+    """ws from workspace_i8; weights from i8_weights."""
+    _check(lib().smoe_expert_ffn_i8(ctypes.byref(desc), _ptr(xq), _ptr(x_scale), _ptr(row_src),
+                                    _ptr(expert_off), ctypes.byref(weights), _ptr(y_disp),
+                                    _ptr(y_shared), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_expert_ffn_i8")
 
 
 def kernel_launches() -> int:

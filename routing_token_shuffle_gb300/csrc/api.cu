@@ -74,15 +74,19 @@ int check_device() {
     if (e_ != cudaSuccess) return cuda_fail(e_, #call); \
   } while (0)
 
-int check_ws(const smoe_desc* d, void* ws, size_t ws_bytes) {
-  WsLayout L;
-  ws_layout(*d, &L);
+int check_ws_bytes(size_t need, void* ws, size_t ws_bytes) {
   if (ws == nullptr) return fail(SMOE_ERR_WORKSPACE, "workspace must not be NULL");
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return fail(SMOE_ERR_ALIGN, "workspace is not 256-byte aligned");
-  if (ws_bytes < L.total)
-    return fail(SMOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);
+  if (ws_bytes < need)
+    return fail(SMOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   return SMOE_OK;
+}
+
+int check_ws(const smoe_desc* d, void* ws, size_t ws_bytes) {
+  WsLayout L;
+  ws_layout(*d, &L);
+  return check_ws_bytes(L.total, ws, ws_bytes);
 }
 
 #define SMOE_CHECK(expr) \
@@ -684,6 +688,153 @@ SMOE_API int smoe_prefetch_predict(const smoe_desc* desc, const float* r, const 
   if (e != cudaSuccess) return cuda_fail(e, "prefetch route launch");
   e = launch_hits(*desc, pred_idx, true_idx, hits, s);
   if (e != cudaSuccess) return cuda_fail(e, "hits launch");
+  return SMOE_OK;
+}
+
+// Row indices of the expert matrices are 32-bit (tensor-map coordinates, work counts).
+static int check_few(const smoe_desc* d) {
+  SMOE_CHECK(check_desc(d));
+  SMOE_REQUIRE(d->T <= kFewMaxT, SMOE_ERR_SHAPE, "the few-token layer takes T <= %d (T=%d)",
+               kFewMaxT, d->T);
+  const long long G = (long long)d->E + d->n_shared;
+  SMOE_REQUIRE(G * d->F <= INT_MAX && G * d->d <= INT_MAX &&
+                   G * ((d->F + 31) / 32) * ((d->d + 31) / 32) <= INT_MAX / 2,
+               SMOE_ERR_SHAPE, "expert matrices too large");
+  return SMOE_OK;
+}
+
+static int check_i8(const smoe_desc* d) {
+  SMOE_CHECK(check_desc(d));
+  const long long G = (long long)d->E + d->n_shared;
+  SMOE_REQUIRE((long long)d->T * (d->K + d->n_shared) <= INT_MAX / 2 && G * d->F <= INT_MAX &&
+                   G * d->d <= INT_MAX,
+               SMOE_ERR_SHAPE, "expert matrices or batch too large");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_add_rmsnorm(const smoe_desc* desc, const float* r, const void* y,
+                              const float* gamma, float eps, float* r_out, void* x_out,
+                              int8_t* q_out, float* q_scale, void* stream) {
+  SMOE_CHECK(check_desc(desc));
+  SMOE_REQUIRE(desc->d <= kNormMaxDim, SMOE_ERR_SHAPE, "the RMS norm supports d <= %d", kNormMaxDim);
+  SMOE_REQUIRE(eps >= 0.0f && eps <= 1.0f, SMOE_ERR_ARG, "eps must be in [0, 1]");
+  SMOE_PTR(r);
+  SMOE_PTR(gamma);
+  SMOE_OPT_PTR(y);
+  SMOE_OPT_PTR(r_out);
+  SMOE_OPT_PTR(x_out);
+  SMOE_OPT_PTR(q_out);
+  SMOE_OPT_PTR(q_scale);
+  SMOE_REQUIRE(r_out || x_out || q_out, SMOE_ERR_ARG, "no output is given");
+  SMOE_REQUIRE(!q_out == !q_scale, SMOE_ERR_ARG, "q_out and q_scale go together");
+  if (desc->T == 0) return SMOE_OK;
+  SMOE_CHECK(check_device());
+  cudaError_t e = launch_add_rmsnorm(*desc, r, y, gamma, eps, r_out, x_out, q_out, q_scale,
+                                     static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "RMS norm launch");
+  return SMOE_OK;
+}
+
+SMOE_API size_t smoe_few_workspace_size(const smoe_desc* desc) {
+  if (check_few(desc) != SMOE_OK) return 0;
+  FewLayout L;
+  few_ws_layout(*desc, &L);
+  return L.total;
+}
+
+SMOE_API int smoe_moe_forward_few(const smoe_desc* desc, const void* x, const void* w_gate,
+                                  const void* w1, const void* w3, const void* w2, void* y,
+                                  float* logits, int32_t* topk_idx, float* topk_w, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  SMOE_CHECK(check_few(desc));
+  SMOE_PTR(x);
+  SMOE_PTR(w_gate);
+  SMOE_PTR(w1);
+  SMOE_PTR(w3);
+  SMOE_PTR(w2);
+  SMOE_PTR(y);
+  SMOE_OPT_PTR(logits);
+  SMOE_OPT_PTR(topk_idx);
+  SMOE_OPT_PTR(topk_w);
+  FewLayout L;
+  few_ws_layout(*desc, &L);
+  SMOE_CHECK(check_ws_bytes(L.total, ws, ws_bytes));
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_moe_few(*desc, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws,
+                                 static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "few-token layer launch");
+  return SMOE_OK;
+}
+
+SMOE_API size_t smoe_i8_workspace_size(const smoe_desc* desc) {
+  if (check_i8(desc) != SMOE_OK) return 0;
+  I8Layout L;
+  i8_ws_layout(*desc, &L);
+  return L.total;
+}
+
+SMOE_API int smoe_expert_matmul_i8(const smoe_desc* desc, int n_out, int n_in, const int8_t* xq,
+                                   const float* x_scale, const int32_t* row_src,
+                                   const int32_t* expert_off, const int8_t* wq,
+                                   const float* w_scale, void* out, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  SMOE_CHECK(check_i8(desc));
+  SMOE_REQUIRE(n_in > 0 && n_in % 16 == 0 && n_in <= std::max(desc->d, desc->F), SMOE_ERR_SHAPE,
+               "n_in=%d must be a multiple of 16 and at most max(d, F)=%d", n_in,
+               std::max(desc->d, desc->F));
+  SMOE_REQUIRE(n_out > 0 && n_out % 8 == 0 && (long long)desc->E * n_out <= INT_MAX,
+               SMOE_ERR_SHAPE, "n_out=%d must be a multiple of 8 with E n_out < 2^31", n_out);
+  SMOE_PTR(xq);
+  SMOE_PTR(x_scale);
+  SMOE_OPT_PTR(row_src);
+  SMOE_PTR(expert_off);
+  SMOE_PTR(wq);
+  SMOE_PTR(w_scale);
+  SMOE_PTR(out);
+  I8Layout L;
+  i8_ws_layout(*desc, &L);
+  SMOE_CHECK(check_ws_bytes(L.total, ws, ws_bytes));
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_expert_matmul_i8(*desc, n_out, n_in, xq, x_scale, row_src, expert_off, wq,
+                                          w_scale, out, ws, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit expert product launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_expert_ffn_i8(const smoe_desc* desc, const int8_t* xq, const float* x_scale,
+                                const int32_t* row_src, const int32_t* expert_off,
+                                const smoe_i8_weights* weights, void* y_disp, void* y_shared,
+                                void* ws, size_t ws_bytes, void* stream) {
+  SMOE_CHECK(check_i8(desc));
+  SMOE_REQUIRE(desc->d % 16 == 0 && desc->F % 16 == 0, SMOE_ERR_SHAPE,
+               "8-bit weights need d and F multiples of 16");
+  SMOE_REQUIRE(weights != nullptr, SMOE_ERR_ARG, "weights must not be NULL");
+  SMOE_PTR(xq);
+  SMOE_PTR(x_scale);
+  SMOE_OPT_PTR(row_src);
+  SMOE_PTR(expert_off);
+  SMOE_PTR(weights->w1);
+  SMOE_PTR(weights->s1);
+  SMOE_PTR(weights->w3);
+  SMOE_PTR(weights->s3);
+  SMOE_PTR(weights->w2);
+  SMOE_PTR(weights->s2);
+  SMOE_PTR(y_disp);
+  if (desc->n_shared > 0) {
+    SMOE_PTR(y_shared);
+    SMOE_REQUIRE(row_src != nullptr, SMOE_ERR_ARG,
+                 "shared experts need the rows of xq in token order (row_src given)");
+  }
+  I8Layout L;
+  i8_ws_layout(*desc, &L);
+  SMOE_CHECK(check_ws_bytes(L.total, ws, ws_bytes));
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_expert_ffn_i8(*desc, xq, x_scale, row_src, expert_off, *weights, y_disp,
+                                       y_shared, ws, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit expert FFN launch");
   return SMOE_OK;
 }
 

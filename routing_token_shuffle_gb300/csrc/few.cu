@@ -1,0 +1,601 @@
+// The whole MoE layer for a few tokens (T <= 64) in one kernel: gate, softmax and grouped
+// top-K, the touched experts' SwiGLU FFN (shared experts included) and the weighted sum.
+//
+// At these batches the layer is the stream of the touched experts' weights from HBM
+// (3 F d b bytes each), so the kernel is built around that stream: one persistent CTA per
+// SM, launched cooperatively, whose producer thread keeps a ring of TMA loads in flight
+// across the phases, and two grid-wide barriers where a phase needs every SM's results:
+//   gate      logits = x W_g^T, spread over the SMs          -- barrier 1 --
+//   routes    every CTA selects all T tokens' experts itself from the T x E logits
+//   up        H[slot][t] = w_{t,e} silu(W1 x_t) (W3 x_t), 0 where t is not routed to the
+//             slot's expert e (slots: the shared experts, then the touched routed ones)
+//   down      y_t = sum over slots of W2_e H[slot][t]        -- barrier 2 before it --
+// With the routing weight folded into H and zeros for the other tokens, the down product
+// over all slots is one contraction of length slots x F, whose accumulator is the layer's
+// output: no per-expert outputs, no combine.
+// The shared experts' up tiles do not wait for the routes: they stream while the gate and
+// the selection run. The W2 tiles at the head of a CTA's down range do not wait for barrier
+// 2: they are loaded into the free stages before it.
+//
+// Work is split evenly: the 128-row x 128-byte weight blocks of a phase, taken in order,
+// are cut into one contiguous range per CTA, whatever the tile borders. A tile whose blocks
+// lie in several ranges is finished by the CTA that holds its first block: the others
+// write fp32 partial sums and a flag, and the owner adds them in ascending order (the
+// result does not depend on timing). A CTA's first segment never waits, so the owner's wait
+// (for its successors' first segments) cannot be circular.
+//
+// An A tile is 128 weight rows (up: 64 rows of W1 and the same 64 of W3), the B tile is all
+// T tokens padded to NP rows; fp32 accumulation. Every wait is bounded (see tc_common.cuh).
+#include <algorithm>
+#include <climits>
+
+#include "tc_common.cuh"
+
+namespace smoe {
+namespace {
+
+constexpr int kFewThreads = 384;
+constexpr int kGateThreads = 320;          // warps 2-11 compute logits and select
+constexpr uint32_t kFewA = 128 * 128;      // A tile: 128 rows x 128 bytes
+constexpr int kFewMaxStages = 16;
+constexpr int kFewSmem = 227 * 1024;
+
+struct FewArgs {
+  const void* x;
+  const void* w_gate;
+  void* y;
+  float* logits;        // [T, E] in the workspace
+  float* logits_out;    // nullable outputs
+  int32_t* topk_idx;
+  float* topk_w;
+  void* h;              // [slots, T, F]
+  float* partial;       // [2][kFewMaxCtas][NP * 128]
+  uint32_t* flags;      // [3][kFewMaxCtas]
+  uint32_t* ctl;        // barrier 1, barrier 2 and exit counters
+  DeviceStatus* st;
+  int T, d, E, K, H, F, S, renorm, stages;
+};
+
+// The 128-byte weight blocks of a phase and this CTA's share of them.
+struct Range {
+  int kper;        // blocks of a tile
+  int total;
+  __device__ __forceinline__ int first(int cta, int n) const {
+    return (int)((long long)total * cta / n);
+  }
+};
+
+__device__ __forceinline__ bool group_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+// bounded wait for *p >= want
+__device__ __forceinline__ bool wait_ge(const uint32_t* p, uint32_t want, volatile int* abort) {
+  if (ld_acquire(p) >= want) return true;
+  const unsigned long long t0 = tc::globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (ld_acquire(p) >= want) return true;
+    if ((i & 63u) == 0 && (*abort || tc::globaltimer() - t0 > tc::kWaitTimeoutNs)) return false;
+  }
+}
+
+// 16 bytes of x and W_g: partial dot products for up to 8 tokens
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, const float* tag) {
+  float u[4], v[4];
+  unpack16(a, u, tag);
+  unpack16(b, v, tag);
+  return u[0] * v[0] + u[1] * v[1] + u[2] * v[2] + u[3] * v[3];
+}
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, const __nv_bfloat16* tag) {
+  float u[8], v[8];
+  unpack16(a, u, tag);
+  unpack16(b, v, tag);
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(u[i], v[i], s);
+  return s;
+}
+
+// Logits of this CTA's (expert, 8-token group) units by warps 2-11; red: [10][8] floats.
+template <typename TE>
+__device__ __forceinline__ void gate_logits(const FewArgs& p, float* red, int gt) {
+  constexpr int V = Elem<TE>::kPerVec16;
+  const int lane = gt & 31, gw = gt >> 5;
+  const int nv = p.d / V, groups = (p.T + 7) / 8;
+  const uint4* x = static_cast<const uint4*>(p.x);
+  const uint4* w = static_cast<const uint4*>(p.w_gate);
+  for (int u = blockIdx.x; u < p.E * groups; u += gridDim.x) {
+    const int e = u / groups, t0 = (u - e * groups) * 8, nt = min(8, p.T - t0);
+    float acc[8] = {};
+    for (int v = gt; v < nv; v += kGateThreads) {
+      const uint4 wv = __ldg(w + (size_t)e * nv + v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < nt) acc[i] += dot16(__ldg(x + (size_t)(t0 + i) * nv + v), wv, (const TE*)nullptr);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int off = 16; off; off >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    group_sync(2, kGateThreads);  // red is free
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) red[gw * 8 + i] = acc[i];
+    }
+    group_sync(2, kGateThreads);
+    if (gt < nt) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kGateThreads / 32; ++k) s += red[k * 8 + gt];
+      p.logits[(size_t)(t0 + gt) * p.E + e] = s;
+    }
+  }
+}
+
+// order-preserving image of a logit (-0 and +0 alike); 0 is kept for "taken"
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  const uint32_t k = (u >> 31) ? ~u : (u | 0x80000000u);
+  return k ? k : 1u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float((k >> 31) ? (k ^ 0x80000000u) : ~k);
+}
+
+// One warp selects token t's experts: group h's K/H largest logits, descending, the lower
+// index first on ties; weights are the softmax over all E logits at the picks.
+__device__ __forceinline__ void select_token(const FewArgs& p, int t, int lane, int32_t* s_idx,
+                                             float* s_w, unsigned long long* s_mask) {
+  uint32_t key[16];
+  uint32_t best_all = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 32 * i < p.E && e < p.E ? key_of(__ldcg(p.logits + (size_t)t * p.E + e)) : 0u;
+    best_all = max(best_all, key[i]);
+  }
+  const float mx = value_of(__reduce_max_sync(0xffffffffu, best_all));
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (key[i]) sum += expf(value_of(key[i]) - mx);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  const int per = p.E / p.H, kh = p.K / p.H;
+  int my_idx = 0;
+  float my_w = 0.0f;
+  for (int j = 0; j < p.K; ++j) {
+    const int lo = (j / kh) * per, hi = lo + per;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= lo && e < hi) m = max(m, key[i]);
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, m);
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= lo && e < hi && key[i] == top) at = min(at, (uint32_t)e);
+    }
+    const int pick = (int)__reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (lane + 32 * i == pick) key[i] = 0u;
+    if (lane == j) {
+      my_idx = pick;
+      my_w = expf(value_of(top) - mx) / sum;
+    }
+  }
+  if (p.renorm) {
+    float s = my_w;  // lanes >= K hold 0
+#pragma unroll
+    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    my_w /= s;
+  }
+  if (lane < p.K) {
+    s_idx[t * p.K + lane] = my_idx;
+    s_w[t * p.K + lane] = my_w;
+    atomicOr(s_mask + my_idx, 1ull << t);
+    if (blockIdx.x == 0) {
+      if (p.topk_idx) p.topk_idx[(size_t)t * p.K + lane] = my_idx;
+      if (p.topk_w) p.topk_w[(size_t)t * p.K + lane] = my_w;
+    }
+  }
+}
+
+template <typename TE, int NP>
+__global__ void __launch_bounds__(kFewThreads, 1)
+moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
+               const __grid_constant__ CUtensorMap tmW1,  // [(E+S) F, d], 64-row box
+               const __grid_constant__ CUtensorMap tmW3,
+               const __grid_constant__ CUtensorMap tmW2,  // [(E+S) d, F], 128-row box
+               const __grid_constant__ CUtensorMap tmH,   // [slots T, F], NP-row box
+               const FewArgs p) {
+  constexpr int BK = 128 / (int)sizeof(TE);
+  constexpr uint32_t kB = NP * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int S = p.stages;
+  uint8_t* sA = base;
+  uint8_t* sB = base + (size_t)S * kFewA;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + (size_t)S * kB);
+  uint64_t* empty = full + kFewMaxStages;
+  uint64_t* routed = empty + kFewMaxStages;
+  unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(routed + 1);
+  int* s_abort = reinterpret_cast<int*>(s_mask + p.E);
+  int* s_nact = s_abort + 1;
+  float* s_red = reinterpret_cast<float*>(s_nact + 1);     // [10][8]
+  float* s_xch = s_red + 80;                               // [64][17]
+  float* s_wcol = s_xch + 64 * 17;                         // [64]
+  int* s_use = reinterpret_cast<int*>(s_wcol + 64);        // [64]
+  int32_t* s_act = s_use + 64;                             // [E]
+  int32_t* s_idx = s_act + p.E;                            // [T K]
+  float* s_w = reinterpret_cast<float*>(s_idx + p.T * p.K);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, nc = gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 4);
+    }
+    tc::mbar_init(routed, 1);
+    *s_abort = 0;
+    *s_nact = 0;
+    tc::mbar_init_fence();
+    tc::tma_prefetch_map(&tmX);
+    tc::tma_prefetch_map(&tmW1);
+    tc::tma_prefetch_map(&tmW3);
+    tc::tma_prefetch_map(&tmW2);
+    tc::tma_prefetch_map(&tmH);
+  }
+  for (int i = threadIdx.x; i < p.E; i += kFewThreads) s_mask[i] = 0;
+  __syncthreads();
+  volatile int* abort = s_abort;
+  const int FB = (p.F + 63) / 64, nkd = (p.d + BK - 1) / BK, nkf = (p.F + BK - 1) / BK;
+  // parts: 0 up of the shared experts, 1 up of the routed ones, 2 down
+  auto part_range = [&](int part) {
+    if (part == 0) return Range{nkd, p.S * FB * nkd};
+    if (part == 1) return Range{nkd, *s_nact * FB * nkd};
+    const int kper = (p.S + *s_nact) * nkf;
+    return Range{kper, (p.d + 127) / 128 * kper};
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    uint32_t it = 0;
+    bool ok = true;
+    auto load_a = [&](uint32_t s, int part, int tile, int kb) {
+      if (part < 2) {
+        const int slot = tile / FB, fb = tile - slot * FB;
+        const int e = part == 0 ? p.E + slot : s_act[slot];
+        tc::tma_load_2d(sA + s * kFewA, &tmW1, &full[s], kb * BK, e * p.F + fb * 64);
+        tc::tma_load_2d(sA + s * kFewA + kFewA / 2, &tmW3, &full[s], kb * BK, e * p.F + fb * 64);
+      } else {
+        const int slot = kb / nkf, fb = kb - slot * nkf;
+        const int e = slot < p.S ? p.E + slot : s_act[slot - p.S];
+        tc::tma_load_2d(sA + s * kFewA, &tmW2, &full[s], fb * BK, e * p.d + tile * 128);
+      }
+    };
+    auto load_b = [&](uint32_t s, int part, int kb) {
+      if (part < 2) {
+        tc::tma_load_2d(sB + s * kB, &tmX, &full[s], kb * BK, 0);
+      } else {
+        const int slot = kb / nkf, fb = kb - slot * nkf;
+        tc::tma_load_2d(sB + s * kB, &tmH, &full[s], fb * BK, slot * p.T);
+      }
+    };
+    for (int part = 0; part < 3 && ok; ++part) {
+      if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
+      const Range r = part_range(part);
+      int i = r.first(cta, nc);
+      const int end = r.first(cta + 1, nc);
+      if (part == 2) {
+        // weights ahead of barrier 2: the A halves of the first stages
+        const uint32_t it0 = it;
+        const int ahead = min(end - i, S);
+        for (int j = 0; j < ahead; ++j, ++it) {
+          const uint32_t s = it % S, ph = (it / S) & 1u;
+          if (!tc::mbar_wait(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+          tc::mbar_expect_tx(&full[s], kFewA + kB);
+          load_a(s, part, (i + j) / r.kper, (i + j) % r.kper);
+        }
+        if (ok) ok = wait_ge(p.ctl + 1, (uint32_t)nc, abort);
+        // H was written by other SMs through the generic proxy
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        // (also after a wait that gave up: the stages' byte counts must complete)
+        for (uint32_t q = it0; q < it; ++q) load_b(q % S, part, (i + (int)(q - it0)) % r.kper);
+        i += ahead;
+        if (!ok) break;
+      }
+      for (; i < end; ++i, ++it) {
+        const uint32_t s = it % S, ph = (it / S) & 1u;
+        if (!tc::mbar_wait(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+        tc::mbar_expect_tx(&full[s], kFewA + kB);
+        load_a(s, part, i / r.kper, i % r.kper);
+        load_b(s, part, i % r.kper);
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+      // let the copies already issued land before the CTA's shared memory goes away
+      volatile int never = 0;
+      const uint32_t firstj = it > (uint32_t)S ? it - S : 0;
+      for (uint32_t j = firstj; j < it; ++j) tc::mbar_wait(&full[j % S], (j / S) & 1u, &never);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------------- gate and routes
+    const int gt = threadIdx.x - 64;
+    gate_logits<TE>(p, s_red, gt);
+    __threadfence();
+    group_sync(2, kGateThreads);
+    bool ok = true;
+    if (gt == 0) {
+      for (int q = 0; q < 3; ++q) p.flags[q * kFewMaxCtas + cta] = 0;
+      __threadfence();
+      atomicAdd(p.ctl, 1u);
+      ok = wait_ge(p.ctl, (uint32_t)nc, abort);
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+      }
+    }
+    ok = group_and(2, kGateThreads, ok);
+    if (ok) {
+      for (int t = gt >> 5; t < p.T; t += kGateThreads / 32)
+        select_token(p, t, lane, s_idx, s_w, s_mask);
+      if (p.logits_out && cta == 0)
+        for (int i = gt; i < p.T * p.E; i += kGateThreads) p.logits_out[i] = __ldcg(p.logits + i);
+      group_sync(2, kGateThreads);
+      if (gt < 32) {  // touched experts, ascending
+        int n = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+          const bool on = e0 + lane < p.E && s_mask[e0 + lane] != 0;
+          const uint32_t b = __ballot_sync(0xffffffffu, on);
+          if (on) s_act[n + __popc(b & ((1u << lane) - 1u))] = e0 + lane;
+          n += __popc(b);
+        }
+        if (lane == 0) *s_nact = n;
+      }
+      group_sync(2, kGateThreads);
+      if (gt == 0) tc::mbar_arrive(routed);
+    }
+    if (ok && warp >= 4 && warp < 8) {
+      // -------------------------------------------------------------- products, epilogue
+      const int q = warp & 3, row = q * 32 + lane;
+      uint32_t it = 0;
+      for (int part = 0; part < 3 && ok; ++part) {
+        const Range r = part_range(part);
+        const int end = r.first(cta + 1, nc);
+        float* partial = p.partial + (size_t)(part & 1) * kFewMaxCtas * NP * 128;
+        uint32_t* flags = p.flags + part * kFewMaxCtas;
+        for (int i = r.first(cta, nc); i < end && ok;) {
+          const int tile = i / r.kper, k0 = i - tile * r.kper;
+          const int k1 = min(r.kper, k0 + end - i);
+          float acc[NP] = {};
+          for (int kb = k0; kb < k1; ++kb, ++it) {
+            const uint32_t s = it % S, ph = (it / S) & 1u;
+            if (!tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
+            const uint8_t* a = sA + s * kFewA + row * 128;
+            const uint8_t* b = sB + s * kB;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float av[8];
+              unpack16(*reinterpret_cast<const uint4*>(a + ((c ^ (row & 7)) << 4)), av, (const TE*)nullptr);
+#pragma unroll
+              for (int t = 0; t < NP; ++t) {
+                float bv[8];
+                unpack16(*reinterpret_cast<const uint4*>(b + t * 128 + ((c ^ (t & 7)) << 4)), bv,
+                         (const TE*)nullptr);
+#pragma unroll
+                for (int v = 0; v < Elem<TE>::kPerVec16; ++v) acc[t] = fmaf(av[v], bv[v], acc[t]);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&empty[s]);
+          }
+          i += k1 - k0;
+          // one outcome for the four warps, which go on to barriers together
+          ok = group_and(1, 128, ok);
+          if (!ok) break;
+          if (k0 != 0) {  // the tile belongs to an earlier CTA
+            float* out = partial + (size_t)cta * NP * 128 + row;
+#pragma unroll
+            for (int t = 0; t < NP; ++t)
+              if (t < p.T) __stcg(out + t * 128, acc[t]);
+            __threadfence();
+            group_sync(1, 128);
+            if (row == 0) st_release(flags + cta, 1u);
+            continue;
+          }
+          if (k1 != r.kper) {  // add the following CTAs' sums, in order
+            const int tile_end = (tile + 1) * r.kper;
+            int c1 = cta + 1;
+            while (r.first(c1, nc) < tile_end) ++c1;  // CTAs cta + 1 .. c1 - 1 hold the rest
+            for (int c = cta + 1 + row; c < c1; c += 128)
+              if (r.first(c, nc) < r.first(c + 1, nc)) ok &= wait_ge(flags + c, 1u, abort);
+            ok = group_and(1, 128, ok);
+            if (!ok) break;
+            for (int c = cta + 1; c < c1; ++c) {
+              if (r.first(c, nc) == r.first(c + 1, nc)) continue;
+              const float* in = partial + (size_t)c * NP * 128 + row;
+#pragma unroll
+              for (int t = 0; t < NP; ++t)
+                if (t < p.T) acc[t] += __ldcg(in + t * 128);
+            }
+          }
+          if (part < 2) {
+            const int li = tile / FB, fb = tile - li * FB, slot = part == 0 ? li : p.S + li;
+            if (row < 64) {  // the tokens of this expert and their weights
+              float w = 1.0f;
+              int use = row < p.T;
+              if (part == 1) {
+                const int e = s_act[li];
+                use = 0;
+                for (int k = 0; k < p.K && row < p.T; ++k)
+                  if (s_idx[row * p.K + k] == e) {
+                    use = 1;
+                    w = s_w[row * p.K + k];
+                  }
+              }
+              s_wcol[row] = w;
+              s_use[row] = use;
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < NP; c0 += 16) {
+              if (c0 >= p.T) break;
+              if (q >= 2) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t) s_xch[(row - 64) * 17 + t] = acc[c0 + t];
+              }
+              group_sync(1, 128);
+              if (q < 2) {
+                const int f = fb * 64 + row;
+                TE* out = static_cast<TE*>(p.h) + ((size_t)slot * p.T + c0) * p.F + f;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                  const float g = acc[c0 + t];
+                  const float hv = g / (1.0f + expf(-g)) * s_xch[row * 17 + t] * s_wcol[c0 + t];
+                  if (c0 + t < p.T && f < p.F)
+                    out[(size_t)t * p.F] = Elem<TE>::from_f32(s_use[c0 + t] ? hv : 0.0f);
+                }
+              }
+              group_sync(1, 128);
+            }
+          } else {
+            const int n = tile * 128 + row;
+#pragma unroll
+            for (int t = 0; t < NP; ++t)
+              if (t < p.T && n < p.d)
+                static_cast<TE*>(p.y)[(size_t)t * p.d + n] = Elem<TE>::from_f32(acc[t]);
+          }
+        }
+        if (part == 1 && ok) {  // this CTA's part of H is written: barrier 2
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+          __threadfence();
+          group_sync(1, 128);
+          if (row == 0) atomicAdd(p.ctl + 1, 1u);
+        }
+      }
+      if (!ok && lane == 0) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // the last CTA leaves the counters at zero for the next call on this workspace
+    __threadfence();
+    if (atomicAdd(p.ctl + 2, 1u) == (uint32_t)nc - 1u) {
+      p.ctl[0] = 0;
+      p.ctl[1] = 0;
+      p.ctl[2] = 0;
+    }
+  }
+}
+
+template <typename TE, int NP>
+cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const void* w1,
+                    const void* w3, const void* w2, void* y, float* logits, int32_t* topk_idx,
+                    float* topk_w, void* ws, cudaStream_t s) {
+  constexpr bool kF32 = sizeof(TE) == 4;
+  constexpr uint32_t BK = 128 / sizeof(TE);
+  FewLayout L;
+  few_ws_layout(d, &L);
+  const uint64_t G = (uint64_t)d.E + d.n_shared;
+  alignas(64) CUtensorMap tX, tW1, tW3, tW2, tH;
+  void* h = ws_ptr<char>(ws, L.h);
+  if (!encode_tmap_2d(&tX, x, kF32, d.T, d.d, NP, BK) ||
+      !encode_tmap_2d(&tW1, w1, kF32, G * d.F, d.d, 64, BK) ||
+      !encode_tmap_2d(&tW3, w3, kF32, G * d.F, d.d, 64, BK) ||
+      !encode_tmap_2d(&tW2, w2, kF32, G * d.d, d.F, 128, BK) ||
+      !encode_tmap_2d(&tH, h, kF32, L.slots * d.T, d.F, NP, BK))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  FewArgs p{x, w_gate, y, ws_ptr<float>(ws, L.logits), logits, topk_idx, topk_w, h,
+            ws_ptr<float>(ws, L.partial), ws_ptr<uint32_t>(ws, L.flags),
+            ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
+            d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
+  const size_t misc = 1024 + (2 * kFewMaxStages + 1) * 8 + 8 * (size_t)d.E + 8 + 4 * (80 + 64 * 17 + 128) +
+                      4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
+  p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + NP * 128));
+  auto kern = moe_few_kernel<TE, NP>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident: they wait on one another
+  attr[0].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(sms, kFewMaxCtas));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  SMOE_COUNT_LAUNCH(1);
+  return cudaLaunchKernelEx(&cfg, kern, tX, tW1, tW3, tW2, tH, p);
+}
+
+template <typename TE>
+cudaError_t run_few_t(const smoe_desc& d, const void* x, const void* w_gate, const void* w1,
+                      const void* w3, const void* w2, void* y, float* logits, int32_t* topk_idx,
+                      float* topk_w, void* ws, cudaStream_t s) {
+  if (d.T <= 16) return run_few<TE, 16>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  if (d.T <= 32) return run_few<TE, 32>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  return run_few<TE, 64>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+}
+
+}  // namespace
+
+void few_ws_layout(const smoe_desc& d, FewLayout* L) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  L->slots = std::min<size_t>(d.E, (size_t)d.T * d.K) + d.n_shared;
+  const size_t np = d.T <= 16 ? 16 : d.T <= 32 ? 32 : 64;
+  L->status = take(256);
+  L->flags = take(4 * 3 * kFewMaxCtas);
+  L->logits = take(4 * (size_t)d.T * d.E);
+  L->partial = take(4 * 2 * kFewMaxCtas * np * 128);
+  L->h = take(L->slots * d.T * d.F * elem_size(d));
+  L->total = off;
+}
+
+cudaError_t launch_moe_few(const smoe_desc& d, const void* x, const void* w_gate, const void* w1,
+                           const void* w3, const void* w2, void* y, float* logits,
+                           int32_t* topk_idx, float* topk_w, void* ws, cudaStream_t s) {
+  if (d.dtype == SMOE_F32)
+    return run_few_t<float>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  return run_few_t<__nv_bfloat16>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+}
+
+}  // namespace smoe

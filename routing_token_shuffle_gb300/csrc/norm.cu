@@ -1,0 +1,173 @@
+// Root-mean-square norm of the residual stream with the layer output's addition, in front
+// of the router and the expert products:
+//   h = r + y,   n = (h gamma) rsqrt(mean(h^2) + eps),
+//   q = rint(n / s), s = max |n| / 127 (one scale per row).
+// Each element is read once and every output written once: 4 + b bytes in and up to
+// 4 + b + 1 out per element (b = bytes of the layer's dtype), so HBM is the bound. A row
+// lives in registers between its loads and its stores; the sum of squares and the largest
+// |h gamma| come from one pass over them and one block reduction, because rounding is
+// monotonic: max over fl(fl(h gamma) rs) is fl(max |fl(h gamma)| rs).
+#include <algorithm>
+#include <cfloat>
+
+#include "smoe_internal.cuh"
+
+namespace smoe {
+namespace {
+
+// Rows of at most 1024 elements take one warp each (8 rows per block), longer ones a block.
+constexpr int kWarpRowMax = 1024;
+
+struct NormArgs {
+  const float* r;
+  const void* y;       // nullable
+  const float* gamma;
+  float* r_out;        // nullable
+  void* x_out;         // nullable
+  int8_t* q_out;       // nullable, with q_scale
+  float* q_scale;
+  int T, d;
+  float eps;
+};
+
+// 8 consecutive elements as fp32
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  unpack16(*reinterpret_cast<const uint4*>(p), v, (const __nv_bfloat16*)nullptr);
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = pack16(v, (const __nv_bfloat16*)nullptr);
+}
+
+// One row per group of kThreads threads (a warp or the block); thread i holds the 8-element
+// chunks i, i + kThreads, ... of it.
+template <typename TE, int kChunks, bool kWarp>
+__global__ void __launch_bounds__(1024)
+add_rmsnorm_kernel(const NormArgs p) {
+  pdl_wait_and_trigger();
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nthr = kWarp ? 32 : (int)blockDim.x, me = kWarp ? lane : (int)threadIdx.x;
+  const int rows_per_block = kWarp ? (int)blockDim.x >> 5 : 1;
+  const int nchunk = p.d >> 3;
+  for (long long row = (long long)blockIdx.x * rows_per_block + (kWarp ? warp : 0); row < p.T;
+       row += (long long)gridDim.x * rows_per_block) {
+    const size_t base = (size_t)row * p.d;
+    float h[kChunks][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int ch = me + c * nthr;
+      if (ch >= nchunk) continue;
+      load8(p.r + base + ch * 8, h[c]);
+      if (p.y) {
+        float v[8];
+        load8(static_cast<const TE*>(p.y) + base + ch * 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[c][i] += v[i];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int ch = me + c * nthr;
+      if (ch >= nchunk) continue;
+      if (p.r_out) store8(p.r_out + base + ch * 8, h[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
+    }
+    // |h gamma| is compared as an unsigned integer: the order of the magnitudes, and a NaN
+    // is above every number, so a row that holds one does not pass for a finite row
+    uint32_t big = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int ch = me + c * nthr;
+      if (ch >= nchunk) continue;
+      float g[8];
+      load8(p.gamma + ch * 8, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[c][i] *= g[i];
+        big = max(big, __float_as_uint(h[c][i]) & 0x7fffffffu);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    big = __reduce_max_sync(0xffffffffu, big);
+    if (!kWarp) {
+      __syncthreads();  // the previous row's sums have been read
+      if (lane == 0) {
+        s_sum[warp] = sum;
+        s_max[warp] = big;
+      }
+      __syncthreads();
+      sum = 0.0f;
+      for (int w = 0; w < (int)blockDim.x >> 5; ++w) {
+        sum += s_sum[w];
+        big = max(big, s_max[w]);
+      }
+    }
+    const float rs = 1.0f / sqrtf(sum / (float)p.d + p.eps);
+    const float amax = __uint_as_float(big) * rs;
+    // a row whose scale would be subnormal counts as zero; a row with an infinity or a NaN
+    // gets the scale NaN and zeros, so that what is computed from it shows it
+    const bool finite = amax <= FLT_MAX && sum <= FLT_MAX;
+    float scale = amax / 127.0f;
+    const bool zero = !finite || scale < FLT_MIN;
+    if (zero) scale = finite ? 0.0f : __int_as_float(0x7fc00000);
+    if (p.q_out && me == 0) p.q_scale[row] = scale;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int ch = me + c * nthr;
+      if (ch >= nchunk) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] *= rs;
+      if (p.x_out) store8(static_cast<TE*>(p.x_out) + base + ch * 8, h[c]);
+      if (p.q_out) {
+        uint32_t w[2] = {0u, 0u};
+        if (!zero) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            w[i >> 2] |= ((uint32_t)__float2int_rn(h[c][i] / scale) & 0xffu) << (8 * (i & 3));
+        }
+        *reinterpret_cast<uint2*>(p.q_out + base + ch * 8) = make_uint2(w[0], w[1]);
+      }
+    }
+  }
+}
+
+template <typename TE>
+cudaError_t run_norm(const NormArgs& p, cudaStream_t s) {
+  const int nchunk = p.d >> 3;
+  if (p.d <= kWarpRowMax) {
+    const int grid = ceil_div(p.T, 8);
+    if (nchunk <= 32) SMOE_LAUNCH((add_rmsnorm_kernel<TE, 1, true>), grid, 256, 0, s, p);
+    else SMOE_LAUNCH((add_rmsnorm_kernel<TE, 4, true>), grid, 256, 0, s, p);
+    return cudaGetLastError();
+  }
+  // up to 8192 elements: one chunk a thread while the batch is small (latency), else two
+  const int per = p.d > 8192 ? 4 : 2;
+  const int threads = (ceil_div(nchunk, per) + 31) / 32 * 32;
+  if (per == 2) SMOE_LAUNCH((add_rmsnorm_kernel<TE, 2, false>), p.T, threads, 0, s, p);
+  else SMOE_LAUNCH((add_rmsnorm_kernel<TE, 4, false>), p.T, threads, 0, s, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const smoe_desc& d, const float* r, const void* y,
+                               const float* gamma, float eps, float* r_out, void* x_out,
+                               int8_t* q_out, float* q_scale, cudaStream_t s) {
+  const NormArgs p{r, y, gamma, r_out, x_out, q_out, q_scale, d.T, d.d, eps};
+  return d.dtype == SMOE_F32 ? run_norm<float>(p, s) : run_norm<__nv_bfloat16>(p, s);
+}
+
+}  // namespace smoe

@@ -23,7 +23,7 @@ struct DeviceStatus {
 
 enum : int32_t {
   kBadTokenId = 1, kBadExpertPart = 2, kBadTopkIdx = 3, kBadPerm = 4, kBadPairRow = 5,
-  kBadSrcPart = 6, kTimeoutGemm = 16, kTimeoutProbe = 17
+  kBadSrcPart = 6, kTimeoutGemm = 16, kTimeoutProbe = 17, kTimeoutFew = 18
 };
 
 __device__ __forceinline__ void record_error(DeviceStatus* st, uint32_t flag, int32_t kind,
@@ -257,5 +257,39 @@ cudaError_t launch_prefetch_ln(const smoe_desc& d, const float* r, const float* 
 
 cudaError_t launch_hits(const smoe_desc& d, const int32_t* pred_idx, const int32_t* true_idx,
                         unsigned long long* hits, cudaStream_t s);
+
+// Residual add + RMS norm, with 8-bit rows (norm.cu); y, r_out, x_out, q_out nullable.
+constexpr int kNormMaxDim = 16384;  // a row is held in registers
+cudaError_t launch_add_rmsnorm(const smoe_desc& d, const float* r, const void* y,
+                               const float* gamma, float eps, float* r_out, void* x_out,
+                               int8_t* q_out, float* q_scale, cudaStream_t s);
+
+// The few-token layer's own workspace (few.cu). Its grid-barrier counters live in the first
+// 256 bytes, behind the status word: they start at zero and the kernel leaves them at zero.
+constexpr int kFewMaxT = 64;
+constexpr int kFewMaxCtas = 160;   // one per SM
+constexpr size_t kFewCtl = 128;
+struct FewLayout {
+  size_t status, flags, logits, partial, h, total;
+  size_t slots;   // most shared + touched experts
+};
+void few_ws_layout(const smoe_desc& d, FewLayout* out);
+cudaError_t launch_moe_few(const smoe_desc& d, const void* x, const void* w_gate, const void* w1,
+                           const void* w3, const void* w2, void* y, float* logits,
+                           int32_t* topk_idx, float* topk_w, void* ws, cudaStream_t s);
+
+// The 8-bit expert products' own workspace (expert_i8.cu).
+struct I8Layout {
+  size_t status, tiles, h, hq, hs, total;
+};
+void i8_ws_layout(const smoe_desc& d, I8Layout* out);
+cudaError_t launch_expert_matmul_i8(const smoe_desc& d, int n_out, int n_in, const int8_t* xq,
+                                    const float* xs, const int32_t* row_src,
+                                    const int32_t* expert_off, const int8_t* wq, const float* ws_n,
+                                    void* out, void* ws, cudaStream_t s);
+cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const float* xs,
+                                 const int32_t* row_src, const int32_t* expert_off,
+                                 const smoe_i8_weights& W, void* y_disp, void* y_sh, void* ws,
+                                 cudaStream_t s);
 
 }  // namespace smoe
