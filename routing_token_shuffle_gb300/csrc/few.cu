@@ -233,6 +233,8 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
                const FewArgs p) {
   constexpr int BK = 128 / (int)sizeof(TE);
   constexpr uint32_t kB = NP * 128;
+  constexpr bool kTC = sizeof(TE) == 2;            // bf16: tcgen05; fp32: FMAs on the CUDA cores
+  constexpr uint32_t kCols = 2 * NP;               // TMEM: two accumulators of NP columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -241,11 +243,15 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   uint8_t* sB = base + (size_t)S * kFewA;
   uint64_t* full = reinterpret_cast<uint64_t*>(sB + (size_t)S * kB);
   uint64_t* empty = full + kFewMaxStages;
-  uint64_t* routed = empty + kFewMaxStages;
+  uint64_t* tfull = empty + kFewMaxStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint64_t* routed = drain + 1;
   unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(routed + 1);
   int* s_abort = reinterpret_cast<int*>(s_mask + p.E);
   int* s_nact = s_abort + 1;
-  float* s_red = reinterpret_cast<float*>(s_nact + 1);     // [10][8]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_nact + 1);
+  float* s_red = reinterpret_cast<float*>(s_tmem + 2);     // [10][8]
   float* s_xch = s_red + 80;                               // [64][17]
   float* s_wcol = s_xch + 64 * 17;                         // [64]
   int* s_use = reinterpret_cast<int*>(s_wcol + 64);        // [64]
@@ -258,8 +264,13 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], 4);
+      tc::mbar_init(&empty[s], kTC ? 1 : 4);
     }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(&tfull[a], 1);
+      tc::mbar_init(&tempty[a], 128);
+    }
+    tc::mbar_init(drain, 1);
     tc::mbar_init(routed, 1);
     *s_abort = 0;
     *s_nact = 0;
@@ -271,7 +282,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     tc::tma_prefetch_map(&tmH);
   }
   for (int i = threadIdx.x; i < p.E; i += kFewThreads) s_mask[i] = 0;
+  if (kTC && warp == 2) {
+    tc::tmem_alloc(s_tmem, kCols);
+    tc::tmem_relinquish();
+  }
+  if (kTC) tc::fence_before_sync();
   __syncthreads();
+  if (kTC) tc::fence_after_sync();
+  const uint32_t tmem = kTC ? *s_tmem : 0u;
   volatile int* abort = s_abort;
   const int FB = (p.F + 63) / 64, nkd = (p.d + BK - 1) / BK, nkf = (p.F + BK - 1) / BK;
   // parts: 0 up of the shared experts, 1 up of the routed ones, 2 down
@@ -345,6 +363,43 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       const uint32_t firstj = it > (uint32_t)S ? it - S : 0;
       for (uint32_t j = firstj; j < it; ++j) tc::mbar_wait(&full[j % S], (j / S) & 1u, &never);
     }
+  } else if (kTC && warp == 1 && lane == 0) {
+    // ---------------------------------------------------------------- MMA issuer
+    uint32_t it = 0, tcount = 0;
+    bool ok = true;
+    constexpr uint32_t kIdesc = tc::instr_desc(false, 128, NP);
+    for (int part = 0; part < 3 && ok; ++part) {
+      if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
+      const Range r = part_range(part);
+      const int end = r.first(cta + 1, nc);
+      for (int i = r.first(cta, nc); i < end && ok; ++tcount) {
+        const int n = min(r.kper - i % r.kper, end - i);
+        const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
+        if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
+        tc::fence_after_sync();
+        for (int j = 0; j < n; ++j, ++it) {
+          const uint32_t s = it % S, ph = (it / S) & 1u;
+          if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kFewA));
+          const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kB));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16(tmem + a * NP, adesc + 2 * k, bdesc + 2 * k, kIdesc, (j > 0 || k > 0) ? 1u : 0u);
+          tc::commit(&empty[s]);
+        }
+        i += n;
+        if (ok) tc::commit(&tfull[a]);
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+    }
+    // wait for every MMA this thread issued before TMEM is released
+    volatile int never = 0;
+    tc::commit(drain);
+    tc::mbar_wait(drain, 0, &never);
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- gate and routes
     const int gt = threadIdx.x - 64;
@@ -385,7 +440,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     if (ok && warp >= 4 && warp < 8) {
       // -------------------------------------------------------------- products, epilogue
       const int q = warp & 3, row = q * 32 + lane;
-      uint32_t it = 0;
+      uint32_t it = 0, tcount = 0;
       for (int part = 0; part < 3 && ok; ++part) {
         const Range r = part_range(part);
         const int end = r.first(cta + 1, nc);
@@ -395,31 +450,40 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           const int tile = i / r.kper, k0 = i - tile * r.kper;
           const int k1 = min(r.kper, k0 + end - i);
           float acc[NP] = {};
-          for (int kb = k0; kb < k1; ++kb, ++it) {
-            const uint32_t s = it % S, ph = (it / S) & 1u;
-            if (!tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
-            const uint8_t* a = sA + s * kFewA + row * 128;
-            const uint8_t* b = sB + s * kB;
+          if (kTC) {
+            const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
+            ++tcount;
+            // one outcome for the four warps, which go on to barriers together
+            ok = group_and(1, 128, tc::mbar_wait_warp(&tfull[a], aph, abort));
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c0 = 0; c0 < NP; c0 += 16)
+              tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + a * NP + c0, acc + c0);
+            tc::fence_before_sync();
+            tc::mbar_arrive(&tempty[a]);
+          } else {
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+              const uint32_t s = it % S, ph = (it / S) & 1u;
+              if (!tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
+              const uint8_t* a = sA + s * kFewA + row * 128;
+              const uint8_t* b = sB + s * kB;
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              float av[8];
-              unpack16(*reinterpret_cast<const uint4*>(a + ((c ^ (row & 7)) << 4)), av, (const TE*)nullptr);
+              for (int c = 0; c < 8; ++c) {
+                const float4 av = *reinterpret_cast<const float4*>(a + ((c ^ (row & 7)) << 4));
 #pragma unroll
-              for (int t = 0; t < NP; ++t) {
-                float bv[8];
-                unpack16(*reinterpret_cast<const uint4*>(b + t * 128 + ((c ^ (t & 7)) << 4)), bv,
-                         (const TE*)nullptr);
-#pragma unroll
-                for (int v = 0; v < Elem<TE>::kPerVec16; ++v) acc[t] = fmaf(av[v], bv[v], acc[t]);
+                for (int t = 0; t < NP; ++t) {
+                  const float4 bv = *reinterpret_cast<const float4*>(b + t * 128 + ((c ^ (t & 7)) << 4));
+                  acc[t] = fmaf(av.x, bv.x, fmaf(av.y, bv.y, fmaf(av.z, bv.z, fmaf(av.w, bv.w, acc[t]))));
+                }
               }
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&empty[s]);
             }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&empty[s]);
+            ok = group_and(1, 128, ok);
+            if (!ok) break;
           }
           i += k1 - k0;
-          // one outcome for the four warps, which go on to barriers together
-          ok = group_and(1, 128, ok);
-          if (!ok) break;
           if (k0 != 0) {  // the tile belongs to an earlier CTA
             float* out = partial + (size_t)cta * NP * 128 + row;
 #pragma unroll
@@ -505,7 +569,12 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       }
     }
   }
+  if (kTC) tc::fence_before_sync();
   __syncthreads();
+  if (kTC) {
+    tc::fence_after_sync();
+    if (warp == 2) tc::tmem_dealloc(tmem, kCols);
+  }
   if (threadIdx.x == 0) {
     // the last CTA leaves the counters at zero for the next call on this workspace
     __threadfence();
@@ -542,7 +611,7 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
             ws_ptr<float>(ws, L.partial), ws_ptr<uint32_t>(ws, L.flags),
             ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
             d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
-  const size_t misc = 1024 + (2 * kFewMaxStages + 1) * 8 + 8 * (size_t)d.E + 8 + 4 * (80 + 64 * 17 + 128) +
+  const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 + 4 * (80 + 64 * 17 + 128) +
                       4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
   p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + NP * 128));
   auto kern = moe_few_kernel<TE, NP>;
