@@ -51,18 +51,21 @@ struct FewArgs {
   void* h;              // [slots, T, F]
   float* partial;       // [2][kFewMaxCtas][NP * 128]
   uint32_t* flags;      // [3][kFewMaxCtas]
-  uint32_t* ctl;        // barrier 1, barrier 2 and exit counters
+  int32_t* ridx;        // [T, K] routes in the workspace (T > kSelectAll)
+  float* rw;
+  uint32_t* ctl;        // barrier 1, barrier 2, selected tokens, exits
   DeviceStatus* st;
   int T, d, E, K, H, F, S, renorm, stages;
 };
 
-// The 128-byte weight blocks of a phase and this CTA's share of them.
+// The 128-byte weight blocks of a phase, kper to a tile, cut into one range per CTA (the
+// first `rem` of them one block longer).
 struct Range {
-  int kper;        // blocks of a tile
-  int total;
-  __device__ __forceinline__ int first(int cta, int n) const {
-    return (int)((long long)total * cta / n);
-  }
+  int kper, quot, rem;
+  __device__ __forceinline__ Range(int kper_, int total, int n)
+      : kper(kper_), quot(total / n), rem(total - total / n * n) {}
+  __device__ __forceinline__ int first(int cta) const { return cta * quot + min(cta, rem); }
+  __device__ __forceinline__ bool any(int cta) const { return quot > 0 || cta < rem; }
 };
 
 __device__ __forceinline__ bool group_and(int id, int threads, bool v) {
@@ -87,6 +90,9 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
 __device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+__device__ __forceinline__ void add_release(uint32_t* p) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
+}
 // bounded wait for *p >= want
 __device__ __forceinline__ bool wait_ge(const uint32_t* p, uint32_t want, volatile int* abort) {
   if (ld_acquire(p) >= want) return true;
@@ -97,24 +103,28 @@ __device__ __forceinline__ bool wait_ge(const uint32_t* p, uint32_t want, volati
   }
 }
 
-// 16 bytes of x and W_g: partial dot products for up to 8 tokens
-__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, const float* tag) {
+// 16 bytes of x and W_g: their contribution to a logit
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s, const float* tag) {
   float u[4], v[4];
   unpack16(a, u, tag);
   unpack16(b, v, tag);
-  return u[0] * v[0] + u[1] * v[1] + u[2] * v[2] + u[3] * v[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = fmaf(u[i], v[i], s);
+  return s;
 }
-__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, const __nv_bfloat16* tag) {
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s,
+                                       const __nv_bfloat16* tag) {
   float u[8], v[8];
   unpack16(a, u, tag);
   unpack16(b, v, tag);
-  float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = fmaf(u[i], v[i], s);
   return s;
 }
 
-// Logits of this CTA's (expert, 8-token group) units by warps 2-11; red: [10][8] floats.
+// Logits of this CTA's units, 4 experts x 8 tokens each, by warps 2-11, which split the
+// contraction; red: [10][32] floats. The 32 sums of a warp's lanes are added by halving:
+// after 31 shuffles lane l holds sum l.
 template <typename TE>
 __device__ __forceinline__ void gate_logits(const FewArgs& p, float* red, int gt) {
   constexpr int V = Elem<TE>::kPerVec16;
@@ -122,31 +132,45 @@ __device__ __forceinline__ void gate_logits(const FewArgs& p, float* red, int gt
   const int nv = p.d / V, groups = (p.T + 7) / 8;
   const uint4* x = static_cast<const uint4*>(p.x);
   const uint4* w = static_cast<const uint4*>(p.w_gate);
-  for (int u = blockIdx.x; u < p.E * groups; u += gridDim.x) {
-    const int e = u / groups, t0 = (u - e * groups) * 8, nt = min(8, p.T - t0);
-    float acc[8] = {};
+  const int units = (p.E + 3) / 4 * groups;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int e0 = u / groups * 4, t0 = (u % groups) * 8, nt = min(8, p.T - t0);
+    float acc[32] = {};  // [token][expert]
+#pragma unroll 1
     for (int v = gt; v < nv; v += kGateThreads) {
-      const uint4 wv = __ldg(w + (size_t)e * nv + v);
+      uint4 wv[4], xv[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wv[j] = __ldg(w + (size_t)min(e0 + j, p.E - 1) * nv + v);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < nt) acc[i] += dot16(__ldg(x + (size_t)(t0 + i) * nv + v), wv, (const TE*)nullptr);
+        if (i < nt) xv[i] = __ldg(x + (size_t)(t0 + i) * nv + v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < nt) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[4 * i + j] = dot16(xv[i], wv[j], acc[4 * i + j], (const TE*)nullptr);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int half = 16; half; half >>= 1) {
+      const bool up = lane & half;
 #pragma unroll
-      for (int off = 16; off; off >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+      for (int i = 0; i < half; ++i) {
+        const float give = up ? acc[i] : acc[i + half];
+        acc[i] = (up ? acc[i + half] : acc[i]) + __shfl_xor_sync(0xffffffffu, give, half);
+      }
+    }
     group_sync(2, kGateThreads);  // red is free
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) red[gw * 8 + i] = acc[i];
-    }
+    red[gt] = acc[0];
     group_sync(2, kGateThreads);
-    if (gt < nt) {
-      float s = 0.0f;
+    if (gt < 32 && (lane >> 2) < nt && e0 + (lane & 3) < p.E) {
+      float sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kGateThreads / 32; ++k) s += red[k * 8 + gt];
-      p.logits[(size_t)(t0 + gt) * p.E + e] = s;
+      for (int k = 0; k < kGateThreads / 32; ++k) sum += red[k * 32 + lane];
+      p.logits[(size_t)(t0 + (lane >> 2)) * p.E + e0 + (lane & 3)] = sum;
     }
+    (void)gw;
   }
 }
 
@@ -161,67 +185,66 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 }
 
 // One warp selects token t's experts: group h's K/H largest logits, descending, the lower
-// index first on ties; weights are the softmax over all E logits at the picks.
-__device__ __forceinline__ void select_token(const FewArgs& p, int t, int lane, int32_t* s_idx,
-                                             float* s_w, unsigned long long* s_mask) {
-  uint32_t key[16];
-  uint32_t best_all = 0;
+// index first on ties; weights are the softmax over all E logits at the picks. Lane j < K
+// returns pick j and its weight; lane l holds the logits of experts l, l + 32, ...
+// (kPer of them: the fewer, the shorter each pick and the code to fetch, which runs once or
+// a few times per launch).
+template <int kPer>
+__device__ __forceinline__ void select_token(const FewArgs& p, int t, int lane, int* idx, float* w) {
+  uint32_t key[kPer], best = 0;
+  float v[kPer];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = 32 * i < p.E && e < p.E ? key_of(__ldcg(p.logits + (size_t)t * p.E + e)) : 0u;
-    best_all = max(best_all, key[i]);
+  for (int i = 0; i < kPer; ++i)
+    v[i] = lane + 32 * i < p.E ? __ldcg(p.logits + (size_t)t * p.E + lane + 32 * i) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    key[i] = lane + 32 * i < p.E ? key_of(v[i]) : 0u;
+    best = max(best, key[i]);
   }
-  const float mx = value_of(__reduce_max_sync(0xffffffffu, best_all));
+  const float mx = value_of(__reduce_max_sync(0xffffffffu, best));
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (key[i]) sum += expf(value_of(key[i]) - mx);
+  for (int i = 0; i < kPer; ++i)
+    if (key[i]) sum += expf(v[i] - mx);
 #pragma unroll
   for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   const int per = p.E / p.H, kh = p.K / p.H;
   int my_idx = 0;
-  float my_w = 0.0f;
-  for (int j = 0; j < p.K; ++j) {
-    const int lo = (j / kh) * per, hi = lo + per;
-    uint32_t m = 0;
+  uint32_t my_key = 0;
+#pragma unroll 1
+  for (int h = 0, j = 0; h < p.H; ++h) {
+    const int lo = h * per - lane, hi = lo + per;  // expert lane + 32 i is in [lo, hi) + lane
+#pragma unroll 1
+    for (int q = 0; q < kh; ++q, ++j) {
+      uint32_t m = 0;
+      int at = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= lo && e < hi) m = max(m, key[i]);
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, m);
-    uint32_t at = 0xffffffffu;
+      for (int i = 0; i < kPer; ++i)
+        if (32 * i >= lo && 32 * i < hi && key[i] > m) { m = key[i]; at = 32 * i; }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, m);
+      const int pick = (int)__reduce_min_sync(0xffffffffu, m == top ? (uint32_t)(lane + at) : ~0u);
+      if (lane == j) { my_idx = pick; my_key = top; }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= lo && e < hi && key[i] == top) at = min(at, (uint32_t)e);
-    }
-    const int pick = (int)__reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (lane + 32 * i == pick) key[i] = 0u;
-    if (lane == j) {
-      my_idx = pick;
-      my_w = expf(value_of(top) - mx) / sum;
+      for (int i = 0; i < kPer; ++i)
+        if (lane + 32 * i == pick) key[i] = 0u;
     }
   }
+  float my_w = lane < p.K ? expf(value_of(my_key) - mx) / sum : 0.0f;
   if (p.renorm) {
-    float s = my_w;  // lanes >= K hold 0
+    float s = my_w;
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     my_w /= s;
   }
-  if (lane < p.K) {
-    s_idx[t * p.K + lane] = my_idx;
-    s_w[t * p.K + lane] = my_w;
-    atomicOr(s_mask + my_idx, 1ull << t);
-    if (blockIdx.x == 0) {
-      if (p.topk_idx) p.topk_idx[(size_t)t * p.K + lane] = my_idx;
-      if (p.topk_w) p.topk_w[(size_t)t * p.K + lane] = my_w;
-    }
-  }
+  *idx = my_idx;
+  *w = my_w;
 }
+
+// Up to this many tokens every CTA selects all of them, one per warp: shared memory holds
+// the routes without another pass through L2. Above it CTA t selects token t alone and the
+// CTAs exchange the routes, one more grid-wide wait: 64 tokens of 160 experts took 22 us
+// in rounds of ten tokens per CTA.
+constexpr int kSelectAll = kGateThreads / 32;
 
 template <typename TE, int NP>
 __global__ void __launch_bounds__(kFewThreads, 1)
@@ -235,6 +258,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   constexpr uint32_t kB = NP * 128;
   constexpr bool kTC = sizeof(TE) == 2;            // bf16: tcgen05; fp32: FMAs on the CUDA cores
   constexpr uint32_t kCols = 2 * NP;               // TMEM: two accumulators of NP columns
+  // consumer threads: 4 warps read the accumulators (bf16); 8 warps multiply (fp32), the
+  // second four for every other group of four tokens
+  constexpr int kCons = kTC ? 128 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -251,9 +277,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   int* s_abort = reinterpret_cast<int*>(s_mask + p.E);
   int* s_nact = s_abort + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_nact + 1);
-  float* s_red = reinterpret_cast<float*>(s_tmem + 2);     // [10][8]
-  float* s_xch = s_red + 80;                               // [64][17]
-  float* s_wcol = s_xch + 64 * 17;                         // [64]
+  float* s_red = reinterpret_cast<float*>(s_tmem + 2);     // [10][32]
+  float* s_xch = s_red + kGateThreads;                     // [128][17]
+  float* s_wcol = s_xch + 128 * 17;                        // [64]
   int* s_use = reinterpret_cast<int*>(s_wcol + 64);        // [64]
   int32_t* s_act = s_use + 64;                             // [E]
   int32_t* s_idx = s_act + p.E;                            // [T K]
@@ -264,7 +290,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], kTC ? 1 : 4);
+      tc::mbar_init(&empty[s], kTC ? 1 : kCons / 32);
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&tfull[a], 1);
@@ -294,10 +320,10 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   const int FB = (p.F + 63) / 64, nkd = (p.d + BK - 1) / BK, nkf = (p.F + BK - 1) / BK;
   // parts: 0 up of the shared experts, 1 up of the routed ones, 2 down
   auto part_range = [&](int part) {
-    if (part == 0) return Range{nkd, p.S * FB * nkd};
-    if (part == 1) return Range{nkd, *s_nact * FB * nkd};
+    if (part == 0) return Range(nkd, p.S * FB * nkd, nc);
+    if (part == 1) return Range(nkd, *s_nact * FB * nkd, nc);
     const int kper = (p.S + *s_nact) * nkf;
-    return Range{kper, (p.d + 127) / 128 * kper};
+    return Range(kper, (p.d + 127) / 128 * kper, nc);
   };
 
   if (warp == 0 && lane == 0) {
@@ -327,8 +353,8 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     for (int part = 0; part < 3 && ok; ++part) {
       if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
-      int i = r.first(cta, nc);
-      const int end = r.first(cta + 1, nc);
+      int i = r.first(cta);
+      const int end = r.first(cta + 1);
       if (part == 2) {
         // weights ahead of barrier 2: the A halves of the first stages
         const uint32_t it0 = it;
@@ -371,8 +397,8 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     for (int part = 0; part < 3 && ok; ++part) {
       if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
-      const int end = r.first(cta + 1, nc);
-      for (int i = r.first(cta, nc); i < end && ok; ++tcount) {
+      const int end = r.first(cta + 1);
+      for (int i = r.first(cta); i < end && ok; ++tcount) {
         const int n = min(r.kper - i % r.kper, end - i);
         const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
         if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
@@ -404,23 +430,53 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     // ---------------------------------------------------------------- gate and routes
     const int gt = threadIdx.x - 64;
     gate_logits<TE>(p, s_red, gt);
-    __threadfence();
     group_sync(2, kGateThreads);
     bool ok = true;
     if (gt == 0) {
       for (int q = 0; q < 3; ++q) p.flags[q * kFewMaxCtas + cta] = 0;
-      __threadfence();
-      atomicAdd(p.ctl, 1u);
+      add_release(p.ctl);  // after every write of this CTA that the barrier ordered before it
       ok = wait_ge(p.ctl, (uint32_t)nc, abort);
-      if (!ok) {
-        *abort = 1;
-        record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
-      }
     }
     ok = group_and(2, kGateThreads, ok);
     if (ok) {
-      for (int t = gt >> 5; t < p.T; t += kGateThreads / 32)
-        select_token(p, t, lane, s_idx, s_w, s_mask);
+      const int step = p.T <= kSelectAll ? p.T : nc;
+      for (int t = p.T <= kSelectAll ? gt >> 5 : gt < 32 ? cta : p.T; t < p.T; t += step) {
+        int idx;
+        float w;
+        if (p.E <= 128) select_token<4>(p, t, lane, &idx, &w);
+        else if (p.E <= 256) select_token<8>(p, t, lane, &idx, &w);
+        else select_token<16>(p, t, lane, &idx, &w);
+        if (lane < p.K) {
+          const int at = t * p.K + lane;
+          if (p.T > kSelectAll) {
+            p.ridx[at] = idx;
+            p.rw[at] = w;
+          } else {
+            s_idx[at] = idx;
+            s_w[at] = w;
+            atomicOr(s_mask + idx, 1ull << t);
+          }
+          if (p.topk_idx && (cta == 0 || p.T > kSelectAll)) p.topk_idx[at] = idx;
+          if (p.topk_w && (cta == 0 || p.T > kSelectAll)) p.topk_w[at] = w;
+        }
+        __syncwarp();
+        if (p.T > kSelectAll && lane == 0) add_release(p.ctl + 2);
+      }
+      if (p.T > kSelectAll) {
+        if (gt == 0) ok = wait_ge(p.ctl + 2, (uint32_t)p.T, abort);
+        ok = group_and(2, kGateThreads, ok);
+        for (int i = gt; ok && i < p.T * p.K; i += kGateThreads) {
+          s_idx[i] = __ldcg(p.ridx + i);
+          s_w[i] = __ldcg(p.rw + i);
+          atomicOr(s_mask + s_idx[i], 1ull << (i / p.K));
+        }
+      }
+    }
+    if (!ok && gt == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+    }
+    if (ok) {
       if (p.logits_out && cta == 0)
         for (int i = gt; i < p.T * p.E; i += kGateThreads) p.logits_out[i] = __ldcg(p.logits + i);
       group_sync(2, kGateThreads);
@@ -437,130 +493,165 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       group_sync(2, kGateThreads);
       if (gt == 0) tc::mbar_arrive(routed);
     }
-    if (ok && warp >= 4 && warp < 8) {
+    if (ok && warp >= 4 && warp < 4 + kCons / 32) {
       // -------------------------------------------------------------- products, epilogue
-      const int q = warp & 3, row = q * 32 + lane;
+      const int q = warp & 3, row = q * 32 + lane, half = (warp - 4) >> 2, ct = row + 128 * half;
       uint32_t it = 0, tcount = 0;
       for (int part = 0; part < 3 && ok; ++part) {
         const Range r = part_range(part);
-        const int end = r.first(cta + 1, nc);
+        const int end = r.first(cta + 1);
         float* partial = p.partial + (size_t)(part & 1) * kFewMaxCtas * NP * 128;
         uint32_t* flags = p.flags + part * kFewMaxCtas;
-        for (int i = r.first(cta, nc); i < end && ok;) {
+        for (int i = r.first(cta); i < end && ok;) {
           const int tile = i / r.kper, k0 = i - tile * r.kper;
           const int k1 = min(r.kper, k0 + end - i);
-          float acc[NP] = {};
+          float acc[kTC ? 1 : NP / 2] = {};  // groups half, half + 2, ... of four tokens
+          const uint32_t ta = tcount & 1u, taph = (tcount >> 1) & 1u;
+          ++tcount;
           if (kTC) {
-            const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
-            ++tcount;
-            // one outcome for the four warps, which go on to barriers together
-            ok = group_and(1, 128, tc::mbar_wait_warp(&tfull[a], aph, abort));
-            if (!ok) break;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int c0 = 0; c0 < NP; c0 += 16)
-              tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + a * NP + c0, acc + c0);
-            tc::fence_before_sync();
-            tc::mbar_arrive(&tempty[a]);
+            ok = tc::mbar_wait_warp(&tfull[ta], taph, abort);
           } else {
-            for (int kb = k0; kb < k1; ++kb, ++it) {
+            for (int kb = k0; kb < k1 && ok; ++kb, ++it) {
               const uint32_t s = it % S, ph = (it / S) & 1u;
-              if (!tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
+              ok = tc::mbar_wait_warp(&full[s], ph, abort);
+              if (!ok) break;
+              // only the tokens of the block's expert: the others are not kept (up) or zero
+              const int e = part == 0 ? -1 : part == 1 ? s_act[tile / FB]
+                            : kb / nkf < p.S ? -1 : s_act[kb / nkf - p.S];
+              const unsigned long long on = e < 0 ? ~0ull >> (64 - p.T) : s_mask[e];
               const uint8_t* a = sA + s * kFewA + row * 128;
               const uint8_t* b = sB + s * kB;
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                const float4 av = *reinterpret_cast<const float4*>(a + ((c ^ (row & 7)) << 4));
+              float4 av[8];
 #pragma unroll
-                for (int t = 0; t < NP; ++t) {
-                  const float4 bv = *reinterpret_cast<const float4*>(b + t * 128 + ((c ^ (t & 7)) << 4));
-                  acc[t] = fmaf(av.x, bv.x, fmaf(av.y, bv.y, fmaf(av.z, bv.z, fmaf(av.w, bv.w, acc[t]))));
-                }
+              for (int c = 0; c < 8; ++c) av[c] = *reinterpret_cast<const float4*>(a + ((c ^ (row & 7)) << 4));
+#pragma unroll
+              for (int g = 0; g < (kTC ? 0 : NP / 8); ++g) {
+                const int t = 8 * g + 4 * half;
+                if (((on >> t) & 15) == 0) continue;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) {
+                    const float4 bv = *reinterpret_cast<const float4*>(
+                        b + (t + u) * 128 + ((c ^ (4 * half + u)) << 4));
+                    float& s4 = acc[kTC ? 0 : 4 * g + u];
+                    s4 = fmaf(av[c].x, bv.x, s4);
+                    s4 = fmaf(av[c].y, bv.y, s4);
+                    s4 = fmaf(av[c].z, bv.z, s4);
+                    s4 = fmaf(av[c].w, bv.w, s4);
+                  }
               }
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&empty[s]);
             }
-            ok = group_and(1, 128, ok);
-            if (!ok) break;
           }
+          // whether other CTAs hold later blocks of a tile that starts here
+          int c1 = cta + 1;
+          if (k0 == 0 && k1 != r.kper) {
+            while (r.first(c1) < (tile + 1) * r.kper) ++c1;  // cta + 1 .. c1 - 1 hold the rest
+            for (int c = cta + 1 + ct; c < c1; c += kCons)
+              if (r.any(c)) ok = ok && wait_ge(flags + c, 1u, abort);
+          }
+          // one outcome for the consumer warps, which go on to barriers together
+          ok = group_and(1, kCons, ok);
+          if (!ok) break;
           i += k1 - k0;
-          if (k0 != 0) {  // the tile belongs to an earlier CTA
-            float* out = partial + (size_t)cta * NP * 128 + row;
-#pragma unroll
-            for (int t = 0; t < NP; ++t)
-              if (t < p.T) __stcg(out + t * 128, acc[t]);
-            __threadfence();
-            group_sync(1, 128);
-            if (row == 0) st_release(flags + cta, 1u);
-            continue;
+          if (kTC) tc::fence_after_sync();
+          const int li = tile / FB, fb = tile - li * FB, slot = part == 0 ? li : p.S + li;
+          if (part < 2 && k0 == 0 && ct < 64) {  // the tokens of this expert and their weights
+            float w = 1.0f;
+            int use = row < p.T;
+            if (part == 1) {
+              const int e = s_act[li];
+              use = (int)((s_mask[e] >> row) & 1);
+#pragma unroll 1
+              for (int k = 0; k < p.K && use; ++k)
+                if (s_idx[row * p.K + k] == e) w = s_w[row * p.K + k];
+            }
+            s_wcol[row] = w;
+            s_use[row] = use;
           }
-          if (k1 != r.kper) {  // add the following CTAs' sums, in order
-            const int tile_end = (tile + 1) * r.kper;
-            int c1 = cta + 1;
-            while (r.first(c1, nc) < tile_end) ++c1;  // CTAs cta + 1 .. c1 - 1 hold the rest
-            for (int c = cta + 1 + row; c < c1; c += 128)
-              if (r.first(c, nc) < r.first(c + 1, nc)) ok &= wait_ge(flags + c, 1u, abort);
-            ok = group_and(1, 128, ok);
-            if (!ok) break;
-            for (int c = cta + 1; c < c1; ++c) {
-              if (r.first(c, nc) == r.first(c + 1, nc)) continue;
-              const float* in = partial + (size_t)c * NP * 128 + row;
+          float* mine = s_xch + row * 17;
 #pragma unroll
-              for (int t = 0; t < NP; ++t)
-                if (t < p.T) acc[t] += __ldcg(in + t * 128);
+          for (int c0 = 0; c0 < NP; c0 += 16) {
+            if (c0 >= p.T) break;
+            const int nt = min(16, p.T - c0);
+            if (kTC) {
+              float v[16];
+              tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + ta * NP + c0, v);
+#pragma unroll
+              for (int t = 0; t < 16; ++t) mine[t] = v[t];
+            } else {
+              if (c0) group_sync(1, kCons);  // the last 16 tokens' sums have been used
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+                mine[8 * (t >> 2) + 4 * half + (t & 3)] = acc[kTC ? 0 : c0 / 2 + t];
+              group_sync(1, kCons);
+            }
+            if (k0 != 0) {  // the tile belongs to an earlier CTA
+              float* out = partial + ((size_t)cta * NP + c0) * 128 + row;
+#pragma unroll 1
+              for (int t = half; t < nt; t += kCons / 128) __stcg(out + t * 128, mine[t]);
+              continue;
+            }
+            // add the following CTAs' sums in order, 16 loads in flight
+            if (nt == 1) {
+#pragma unroll 1
+              for (int cb = cta + 1; cb < c1 && half == 0; cb += 16) {
+                float in[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  in[c] = cb + c < c1 && r.any(cb + c)
+                              ? __ldcg(partial + ((size_t)(cb + c) * NP + c0) * 128 + row) : 0.0f;
+                float v = mine[0];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v += in[c];
+                mine[0] = v;
+              }
+            } else if (half == 0) {
+#pragma unroll 1
+              for (int c = cta + 1; c < c1; ++c) {
+                if (!r.any(c)) continue;
+                const float* src = partial + ((size_t)c * NP + c0) * 128 + row;
+                float in[16];
+#pragma unroll
+                for (int t = 0; t < 16; ++t) in[t] = t < nt ? __ldcg(src + t * 128) : 0.0f;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) mine[t] += in[t];
+              }
+            }
+            if (!kTC) group_sync(1, kCons);
+            if (part < 2) {
+              if (kTC) group_sync(1, kCons);
+#pragma unroll 1
+              for (int j = ct; j < 64 * nt; j += kCons) {
+                const int fr = j & 63, t = j >> 6, f = fb * 64 + fr;
+                const float g = s_xch[fr * 17 + t];
+                const float hv = g / (1.0f + expf(-g)) * s_xch[(64 + fr) * 17 + t] * s_wcol[c0 + t];
+                if (f < p.F)
+                  static_cast<TE*>(p.h)[((size_t)slot * p.T + c0 + t) * p.F + f] =
+                      Elem<TE>::from_f32(s_use[c0 + t] ? hv : 0.0f);
+              }
+              if (kTC) group_sync(1, kCons);
+            } else {
+              const int n = tile * 128 + row;
+              if (n < p.d) {
+#pragma unroll 1
+                for (int t = half; t < nt; t += kCons / 128)
+                  static_cast<TE*>(p.y)[(size_t)(c0 + t) * p.d + n] = Elem<TE>::from_f32(mine[t]);
+              }
             }
           }
-          if (part < 2) {
-            const int li = tile / FB, fb = tile - li * FB, slot = part == 0 ? li : p.S + li;
-            if (row < 64) {  // the tokens of this expert and their weights
-              float w = 1.0f;
-              int use = row < p.T;
-              if (part == 1) {
-                const int e = s_act[li];
-                use = 0;
-                for (int k = 0; k < p.K && row < p.T; ++k)
-                  if (s_idx[row * p.K + k] == e) {
-                    use = 1;
-                    w = s_w[row * p.K + k];
-                  }
-              }
-              s_wcol[row] = w;
-              s_use[row] = use;
-            }
-#pragma unroll
-            for (int c0 = 0; c0 < NP; c0 += 16) {
-              if (c0 >= p.T) break;
-              if (q >= 2) {
-#pragma unroll
-                for (int t = 0; t < 16; ++t) s_xch[(row - 64) * 17 + t] = acc[c0 + t];
-              }
-              group_sync(1, 128);
-              if (q < 2) {
-                const int f = fb * 64 + row;
-                TE* out = static_cast<TE*>(p.h) + ((size_t)slot * p.T + c0) * p.F + f;
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                  const float g = acc[c0 + t];
-                  const float hv = g / (1.0f + expf(-g)) * s_xch[row * 17 + t] * s_wcol[c0 + t];
-                  if (c0 + t < p.T && f < p.F)
-                    out[(size_t)t * p.F] = Elem<TE>::from_f32(s_use[c0 + t] ? hv : 0.0f);
-                }
-              }
-              group_sync(1, 128);
-            }
-          } else {
-            const int n = tile * 128 + row;
-#pragma unroll
-            for (int t = 0; t < NP; ++t)
-              if (t < p.T && n < p.d)
-                static_cast<TE*>(p.y)[(size_t)t * p.d + n] = Elem<TE>::from_f32(acc[t]);
+          if (kTC) {  // the accumulator is read out: the MMAs of another tile may start
+            tc::fence_before_sync();
+            tc::mbar_arrive(&tempty[ta]);
           }
+          if (k0 != 0 || !kTC) group_sync(1, kCons);
+          if (k0 != 0 && ct == 0) st_release(flags + cta, 1u);
         }
         if (part == 1 && ok) {  // this CTA's part of H is written: barrier 2
-          asm volatile("fence.proxy.async.global;" ::: "memory");
-          __threadfence();
-          group_sync(1, 128);
-          if (row == 0) atomicAdd(p.ctl + 1, 1u);
+          group_sync(1, kCons);
+          if (ct == 0) add_release(p.ctl + 1);
         }
       }
       if (!ok && lane == 0) {
@@ -578,10 +669,11 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   if (threadIdx.x == 0) {
     // the last CTA leaves the counters at zero for the next call on this workspace
     __threadfence();
-    if (atomicAdd(p.ctl + 2, 1u) == (uint32_t)nc - 1u) {
+    if (atomicAdd(p.ctl + 3, 1u) == (uint32_t)nc - 1u) {
       p.ctl[0] = 0;
       p.ctl[1] = 0;
       p.ctl[2] = 0;
+      p.ctl[3] = 0;
     }
   }
 }
@@ -609,10 +701,11 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
   if (e != cudaSuccess) return e;
   FewArgs p{x, w_gate, y, ws_ptr<float>(ws, L.logits), logits, topk_idx, topk_w, h,
             ws_ptr<float>(ws, L.partial), ws_ptr<uint32_t>(ws, L.flags),
+            ws_ptr<int32_t>(ws, L.ridx), ws_ptr<float>(ws, L.rw),
             ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
             d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
-  const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 + 4 * (80 + 64 * 17 + 128) +
-                      4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
+  const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 +
+                      4 * (kGateThreads + 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
   p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + NP * 128));
   auto kern = moe_few_kernel<TE, NP>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
@@ -654,6 +747,8 @@ void few_ws_layout(const smoe_desc& d, FewLayout* L) {
   L->status = take(256);
   L->flags = take(4 * 3 * kFewMaxCtas);
   L->logits = take(4 * (size_t)d.T * d.E);
+  L->ridx = take(4 * (size_t)d.T * d.K);
+  L->rw = take(4 * (size_t)d.T * d.K);
   L->partial = take(4 * 2 * kFewMaxCtas * np * 128);
   L->h = take(L->slots * d.T * d.F * elem_size(d));
   L->total = off;

@@ -270,7 +270,7 @@ constexpr int kFewMaxT = 64;
 constexpr int kFewMaxCtas = 160;   // one per SM
 constexpr size_t kFewCtl = 128;
 struct FewLayout {
-  size_t status, flags, logits, partial, h, total;
+  size_t status, flags, logits, ridx, rw, partial, h, total;
   size_t slots;   // most shared + touched experts
 };
 void few_ws_layout(const smoe_desc& d, FewLayout* out);
