@@ -258,8 +258,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   constexpr uint32_t kB = NP * 128;
   constexpr bool kTC = sizeof(TE) == 2;            // bf16: tcgen05; fp32: FMAs on the CUDA cores
   constexpr uint32_t kCols = 2 * NP;               // TMEM: two accumulators of NP columns
-  // consumer threads: 4 warps read the accumulators (bf16); 8 warps multiply (fp32), the
-  // second four for every other group of four tokens
+  // consumer threads: 4 warps read the accumulators (bf16); 8 warps multiply (fp32), four on
+  // each half of a block's contraction (splitting the tokens instead leaves one half idle
+  // on most experts and reads the weights twice from shared memory)
   constexpr int kCons = kTC ? 128 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -330,55 +331,93 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     // ---------------------------------------------------------------- TMA producer
     uint32_t it = 0;
     bool ok = true;
-    auto load_a = [&](uint32_t s, int part, int tile, int kb) {
-      if (part < 2) {
-        const int slot = tile / FB, fb = tile - slot * FB;
-        const int e = part == 0 ? p.E + slot : s_act[slot];
-        tc::tma_load_2d(sA + s * kFewA, &tmW1, &full[s], kb * BK, e * p.F + fb * 64);
-        tc::tma_load_2d(sA + s * kFewA + kFewA / 2, &tmW3, &full[s], kb * BK, e * p.F + fb * 64);
+    // The place of the next block, stepped without divisions: this thread's instructions
+    // between two stages are the stream's rate (decoding every block from its index with
+    // divisions held the stream at 5.3 TB/s).
+    struct Place {
+      int tile, kb, fb, slot, row;  // fb, slot: down only; row: of the A tile
+    };
+    auto row_of = [&](int part, int tile, int slot) {
+      if (part == 2) return (slot < p.S ? p.E + slot : s_act[slot - p.S]) * p.d + tile * 128;
+      const int li = tile / FB;
+      return (part == 0 ? p.E + li : s_act[li]) * p.F + (tile - li * FB) * 64;
+    };
+    auto place = [&](int part, const Range& r, int i) {
+      Place at;
+      at.tile = i / r.kper;
+      at.kb = i - at.tile * r.kper;
+      at.slot = part == 2 ? at.kb / nkf : 0;
+      at.fb = at.kb - at.slot * nkf;
+      at.row = row_of(part, at.tile, at.slot);
+      return at;
+    };
+    auto step = [&](int part, const Range& r, Place& at) {
+      ++at.fb;
+      if (++at.kb == r.kper) {
+        ++at.tile;
+        at.kb = at.slot = at.fb = 0;
+      } else if (part == 2 && at.fb == nkf) {
+        ++at.slot;
+        at.fb = 0;
       } else {
-        const int slot = kb / nkf, fb = kb - slot * nkf;
-        const int e = slot < p.S ? p.E + slot : s_act[slot - p.S];
-        tc::tma_load_2d(sA + s * kFewA, &tmW2, &full[s], fb * BK, e * p.d + tile * 128);
+        return;
+      }
+      at.row = row_of(part, at.tile, at.slot);
+    };
+    auto load_a = [&](uint32_t s, int part, const Place& at) {
+      tc::mbar_expect_tx(&full[s], kFewA + kB);
+      if (part < 2) {
+        tc::tma_load_2d(sA + s * kFewA, &tmW1, &full[s], at.kb * BK, at.row);
+        tc::tma_load_2d(sA + s * kFewA + kFewA / 2, &tmW3, &full[s], at.kb * BK, at.row);
+      } else {
+        tc::tma_load_2d(sA + s * kFewA, &tmW2, &full[s], at.fb * BK, at.row);
       }
     };
-    auto load_b = [&](uint32_t s, int part, int kb) {
-      if (part < 2) {
-        tc::tma_load_2d(sB + s * kB, &tmX, &full[s], kb * BK, 0);
-      } else {
-        const int slot = kb / nkf, fb = kb - slot * nkf;
-        tc::tma_load_2d(sB + s * kB, &tmH, &full[s], fb * BK, slot * p.T);
-      }
+    auto load_b = [&](uint32_t s, int part, const Place& at) {
+      if (part < 2) tc::tma_load_2d(sB + s * kB, &tmX, &full[s], at.kb * BK, 0);
+      else tc::tma_load_2d(sB + s * kB, &tmH, &full[s], at.fb * BK, at.slot * p.T);
+    };
+    uint32_t s = 0, ph = 1;  // stage and the parity its release is awaited with
+    auto next_stage = [&] {
+      ++it;
+      if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
     };
     for (int part = 0; part < 3 && ok; ++part) {
       if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
       int i = r.first(cta);
       const int end = r.first(cta + 1);
+      if (i == end) continue;
+      Place at = place(part, r, i);
       if (part == 2) {
         // weights ahead of barrier 2: the A halves of the first stages
-        const uint32_t it0 = it;
-        const int ahead = min(end - i, S);
-        for (int j = 0; j < ahead; ++j, ++it) {
-          const uint32_t s = it % S, ph = (it / S) & 1u;
-          if (!tc::mbar_wait(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
-          tc::mbar_expect_tx(&full[s], kFewA + kB);
-          load_a(s, part, (i + j) / r.kper, (i + j) % r.kper);
+        const uint32_t s0 = s, it0 = it;
+        Place ahead = at;
+        for (int j = min(end - i, S); j > 0; --j) {
+          if (!tc::mbar_wait(&empty[s], ph, abort)) { ok = false; break; }
+          load_a(s, part, ahead);
+          step(part, r, ahead);
+          next_stage();
         }
         if (ok) ok = wait_ge(p.ctl + 1, (uint32_t)nc, abort);
         // H was written by other SMs through the generic proxy
         asm volatile("fence.proxy.async.global;" ::: "memory");
         // (also after a wait that gave up: the stages' byte counts must complete)
-        for (uint32_t q = it0; q < it; ++q) load_b(q % S, part, (i + (int)(q - it0)) % r.kper);
-        i += ahead;
+        uint32_t sb = s0;
+        for (uint32_t q = it0; q < it; ++q) {
+          load_b(sb, part, at);
+          step(part, r, at);
+          if (++sb == (uint32_t)S) sb = 0;
+        }
+        i += (int)(it - it0);
         if (!ok) break;
       }
-      for (; i < end; ++i, ++it) {
-        const uint32_t s = it % S, ph = (it / S) & 1u;
-        if (!tc::mbar_wait(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
-        tc::mbar_expect_tx(&full[s], kFewA + kB);
-        load_a(s, part, i / r.kper, i % r.kper);
-        load_b(s, part, i % r.kper);
+      for (; i < end; ++i) {
+        if (!tc::mbar_wait(&empty[s], ph, abort)) { ok = false; break; }
+        load_a(s, part, at);
+        load_b(s, part, at);
+        step(part, r, at);
+        next_stage();
       }
     }
     if (!ok) {
@@ -391,7 +430,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     }
   } else if (kTC && warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
-    uint32_t it = 0, tcount = 0;
+    uint32_t s = 0, ph = 0, tcount = 0;
     bool ok = true;
     constexpr uint32_t kIdesc = tc::instr_desc(false, 128, NP);
     for (int part = 0; part < 3 && ok; ++part) {
@@ -403,8 +442,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
         if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
         tc::fence_after_sync();
-        for (int j = 0; j < n; ++j, ++it) {
-          const uint32_t s = it % S, ph = (it / S) & 1u;
+        for (int j = 0; j < n; ++j) {
           if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
           tc::fence_after_sync();
           const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kFewA));
@@ -413,6 +451,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           for (int k = 0; k < 4; ++k)
             tc::mma_bf16(tmem + a * NP, adesc + 2 * k, bdesc + 2 * k, kIdesc, (j > 0 || k > 0) ? 1u : 0u);
           tc::commit(&empty[s]);
+          if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
         }
         i += n;
         if (ok) tc::commit(&tfull[a]);
@@ -496,7 +535,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     if (ok && warp >= 4 && warp < 4 + kCons / 32) {
       // -------------------------------------------------------------- products, epilogue
       const int q = warp & 3, row = q * 32 + lane, half = (warp - 4) >> 2, ct = row + 128 * half;
-      uint32_t it = 0, tcount = 0;
+      uint32_t s = 0, ph = 0, tcount = 0;
       for (int part = 0; part < 3 && ok; ++part) {
         const Range r = part_range(part);
         const int end = r.first(cta + 1);
@@ -505,36 +544,42 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         for (int i = r.first(cta); i < end && ok;) {
           const int tile = i / r.kper, k0 = i - tile * r.kper;
           const int k1 = min(r.kper, k0 + end - i);
-          float acc[kTC ? 1 : NP / 2] = {};  // groups half, half + 2, ... of four tokens
+          float acc[kTC ? 1 : NP] = {};
           const uint32_t ta = tcount & 1u, taph = (tcount >> 1) & 1u;
           ++tcount;
           if (kTC) {
             ok = tc::mbar_wait_warp(&tfull[ta], taph, abort);
           } else {
-            for (int kb = k0; kb < k1 && ok; ++kb, ++it) {
-              const uint32_t s = it % S, ph = (it / S) & 1u;
+            // only the tokens of a block's expert: the others are not kept (up) or zero (down)
+            const unsigned long long every = ~0ull >> (64 - p.T);
+            int slot = part == 2 ? k0 / nkf : part == 1 ? p.S + tile / FB : 0;
+            int left = part == 2 ? (slot + 1) * nkf - k0 : r.kper;
+            unsigned long long on = slot < p.S ? every : s_mask[s_act[slot - p.S]];
+            for (int kb = k0; kb < k1 && ok; ++kb) {
+              if (left-- == 0) {
+                ++slot;
+                left = nkf - 1;
+                on = slot < p.S ? every : s_mask[s_act[slot - p.S]];
+              }
               ok = tc::mbar_wait_warp(&full[s], ph, abort);
               if (!ok) break;
-              // only the tokens of the block's expert: the others are not kept (up) or zero
-              const int e = part == 0 ? -1 : part == 1 ? s_act[tile / FB]
-                            : kb / nkf < p.S ? -1 : s_act[kb / nkf - p.S];
-              const unsigned long long on = e < 0 ? ~0ull >> (64 - p.T) : s_mask[e];
               const uint8_t* a = sA + s * kFewA + row * 128;
               const uint8_t* b = sB + s * kB;
-              float4 av[8];
+              float4 av[4];
 #pragma unroll
-              for (int c = 0; c < 8; ++c) av[c] = *reinterpret_cast<const float4*>(a + ((c ^ (row & 7)) << 4));
+              for (int c = 0; c < 4; ++c)
+                av[c] = *reinterpret_cast<const float4*>(a + (((4 * half + c) ^ (row & 7)) << 4));
+              // groups of four tokens: four independent chains of FMAs
 #pragma unroll
-              for (int g = 0; g < (kTC ? 0 : NP / 8); ++g) {
-                const int t = 8 * g + 4 * half;
+              for (int t = 0; t < (kTC ? 0 : NP); t += 4) {
                 if (((on >> t) & 15) == 0) continue;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                   for (int u = 0; u < 4; ++u) {
                     const float4 bv = *reinterpret_cast<const float4*>(
-                        b + (t + u) * 128 + ((c ^ (4 * half + u)) << 4));
-                    float& s4 = acc[kTC ? 0 : 4 * g + u];
+                        b + (t + u) * 128 + (((4 * half + c) ^ ((t + u) & 7)) << 4));
+                    float& s4 = acc[kTC ? 0 : t + u];
                     s4 = fmaf(av[c].x, bv.x, s4);
                     s4 = fmaf(av[c].y, bv.y, s4);
                     s4 = fmaf(av[c].z, bv.z, s4);
@@ -543,6 +588,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
               }
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&empty[s]);
+              if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
             }
           }
           // whether other CTAs hold later blocks of a tile that starts here
@@ -583,9 +629,15 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
               for (int t = 0; t < 16; ++t) mine[t] = v[t];
             } else {
               if (c0) group_sync(1, kCons);  // the last 16 tokens' sums have been used
+              if (half == 0) {
 #pragma unroll
-              for (int t = 0; t < 8; ++t)
-                mine[8 * (t >> 2) + 4 * half + (t & 3)] = acc[kTC ? 0 : c0 / 2 + t];
+                for (int t = 0; t < 16; ++t) mine[t] = acc[kTC ? 0 : c0 + t];
+              }
+              group_sync(1, kCons);
+              if (half == 1) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t) mine[t] += acc[kTC ? 0 : c0 + t];
+              }
               group_sync(1, kCons);
             }
             if (k0 != 0) {  // the tile belongs to an earlier CTA
