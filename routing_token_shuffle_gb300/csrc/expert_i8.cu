@@ -1,178 +1,513 @@
 // Expert products in 8-bit integers with a scale per row (token) and per output channel:
 //   out[r, n] = xs[r] ws[e(r), n] sum_k xq[r, k] wq[e(r), n, k],
 // and the SwiGLU FFN made of three of them, its hidden rows requantised in between.
+//
+// GB300's tensor cores have no fast 8-bit integer rate, but every int8 value is exact in
+// fp16, every product of two is below 2^14, and the accumulator is fp32: the fp16 products
+// give the integer sum exactly while it stays below 2^24. So the rows are widened to fp16
+// once (they are small), the weights travel and are staged as bytes (what bounds a decode
+// batch is their stream from HBM) and are widened on the way into the tensor core: warps
+// read the staged bytes, turn them into fp16 pairs (1.25 instructions a value: the byte with
+// its sign bit flipped, under the exponent of 1024, is 1152 + value) and write them to
+// TMEM, from where tcgen05.mma takes its A operand. Shared memory holds no widened copy.
+//
+// One persistent CTA per SM walks the tiles (group, 128-channel tile, row tile), row tiles
+// fastest so that neighbours share the weights through L2:
+//   warp 0      TMA: weight bytes (128 channels x 128) and fp16 rows (NT rows x 64)
+//   warps 8-15  widen a weight stage into one of four TMEM operand stages
+//   warp 1      tcgen05.mma, M = 128 channels, N = the tile's rows rounded up to 16
+//   warps 4-7   epilogue: scales, SwiGLU, stores (up: fp32 hidden rows and their largest
+//               magnitude, by an integer atomicMax, whose result has no order)
+// The up product's A tile is 64 channels of W1 and the same 64 of W3.
 #include <algorithm>
 #include <cfloat>
-#include <type_traits>
+#include <cuda_fp16.h>
 
-#include "smoe_internal.cuh"
+#include "tc_common.cuh"
 
 namespace smoe {
 namespace {
 
-constexpr int kRows = 64, kCols = 64;  // output tile of a block
-constexpr int kStep = 64;              // contraction bytes per step
+constexpr int kI8Threads = 512;
+constexpr int kStageW = 128 * 128;   // weight stage: 128 channels x 128 bytes
+constexpr int kOpStages = 4;         // widened operand stages in TMEM, 64 columns each
+constexpr int kOpCol = 256;          // their first column
+constexpr int kXchPitch = 17;
+constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 
-// Group g < E: rows expert_off[g] .. expert_off[g+1]; group E + j: shared expert j, T rows.
-// tile_start[g] = first row tile of group g. A bad expert_off schedules nothing.
-__global__ void i8_tiles_kernel(const int32_t* __restrict__ expert_off, int E, int n_shared, int T,
-                                int TK, int bm, int32_t* __restrict__ tile_start, DeviceStatus* st) {
-  pdl_wait_and_trigger();
-  const int lane = threadIdx.x, G = E + n_shared;
+// NT: most rows of a tile. 64: weight streaming, a deep weight ring and two accumulators.
+// 256: batches whose experts fill it, one accumulator.
+template <int NT> struct I8Cfg;
+template <> struct I8Cfg<64> { static constexpr int kW = 8, kB = 8, kAcc = 2; };
+template <> struct I8Cfg<256> { static constexpr int kW = 3, kB = 5, kAcc = 1; };
+
+template <int NT>
+constexpr size_t i8_smem() {
+  return 1024 + (size_t)I8Cfg<NT>::kW * kStageW + (size_t)I8Cfg<NT>::kB * NT * 128 +
+         4 * 128 * kXchPitch + 8 * (2 * (I8Cfg<NT>::kW + I8Cfg<NT>::kB + kOpStages) + 5) + 16 +
+         4 * kMaxGroupTab;
+}
+
+struct I8Args {
+  const int32_t* expert_off;
+  const float* xs;          // scale of each row of the operand (routed rows, then shared)
+  const float *sa, *sb;     // [G, N] channel scales (sb: W3)
+  void* out;                // [TK, N]; up: [TK + S T, N] fp32
+  void* out_sh;             // shared rows of the down product [S T, N]
+  uint32_t* row_max;        // up: largest |h| of each row, as bits
+  DeviceStatus* st;
+  int E, G, T, TK, N, KD;
+  int shared_rows;          // first operand row of shared expert j: TK + (down ? j T : 0)
+};
+
+struct I8Tile {
+  int g, n0, r0, rows;      // group, first channel, first row of the tile in its group, rows left
+  int brow;                 // first operand row
+  long long orow;           // first output row
+  bool shared;
+};
+
+// Row tiles per group from expert_off (s_ts, prefix; s_off a copy), by one warp. A bad
+// expert_off (or none) schedules nothing.
+template <int NT>
+__device__ __forceinline__ void group_table(const I8Args& p, int32_t* s_ts, int32_t* s_off, int lane) {
   bool bad = false;
-  for (int g = lane; g < E; g += 32) {
-    const int lo = expert_off[g], hi = expert_off[g + 1];
-    bad |= lo < 0 || hi < lo || hi > TK;
+  for (int g = lane; g <= p.E; g += 32) {
+    const int lo = p.expert_off[g], hi = g < p.E ? p.expert_off[g + 1] : lo;
+    bad |= lo < 0 || hi < lo || hi > p.TK;
+    s_off[g] = lo;
   }
   bad = __any_sync(0xffffffffu, bad);
-  if (bad && lane == 0) record_error(st, kStatusData, kBadPairRow, -1);
+  if (bad && lane == 0) record_error(p.st, kStatusData, kBadPairRow, -1);
+  __syncwarp();
   int carry = 0;
-  for (int g0 = 0; g0 < G; g0 += 32) {
+  for (int g0 = 0; g0 < p.G; g0 += 32) {
     const int g = g0 + lane;
     int rows = 0;
-    if (!bad && g < E) rows = expert_off[g + 1] - expert_off[g];
-    else if (!bad && g < G) rows = T;
-    const int n = (rows + bm - 1) / bm;
+    if (!bad && g < p.E) rows = s_off[g + 1] - s_off[g];
+    else if (!bad && g < p.G) rows = p.T;
+    const int n = (rows + NT - 1) / NT;
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += y;
     }
-    if (g < G) tile_start[g] = carry + incl - n;
+    if (g < p.G) s_ts[g] = carry + incl - n;
     carry += __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (lane == 0) tile_start[G] = carry;
+  if (lane == 0) s_ts[p.G] = carry;
 }
 
-struct I8Args {
-  const int8_t* x;            // rows: [n_src, KD] (read through map), or [TK (+ S T), KD]
-  const float* xs;            // [n_src] or [TK (+ S T)]
-  const int32_t* map;         // nullable: source row of each dispatched row
-  const int32_t* expert_off;
-  const int32_t* tile_start;
-  const int8_t *wa, *wb;      // [G, N, KD]; wb: the W3 of the up product
-  const float *sa, *sb;       // [G, N]
-  void* out;                  // routed rows [TK, N]; up: all rows [TK + S T, N] fp32
-  void* out_sh;               // down: shared rows [S T, N]
-  DeviceStatus* st;
-  int E, G, T, TK, N, KD, n_src;
-};
+template <bool UP, int NT>
+__device__ __forceinline__ I8Tile decode(const I8Args& p, const int32_t* ts, const int32_t* off,
+                                         int ntile, int t) {
+  int lo = 0, hi = p.G - 1;
+  while (lo < hi) {  // largest g whose first tile is <= t (empty groups are skipped)
+    const int mid = (lo + hi + 1) >> 1;
+    if (ts[mid] * ntile <= t) lo = mid; else hi = mid - 1;
+  }
+  const int g = lo, mt = ts[g + 1] - ts[g], local = t - ts[g] * ntile;
+  const int n_tile = local / mt, m_tile = local - n_tile * mt;
+  I8Tile r;
+  r.g = g;
+  r.n0 = n_tile * (UP ? 64 : 128);
+  r.r0 = m_tile * NT;
+  r.shared = g >= p.E;
+  const int j = g - p.E;
+  r.rows = (r.shared ? p.T : off[g + 1] - off[g]) - r.r0;
+  // the up product reads the tokens' own rows for every shared expert
+  r.brow = (r.shared ? p.shared_rows + (UP ? 0 : j * p.T) : off[g]) + r.r0;
+  r.orow = (r.shared ? (UP ? (long long)p.TK : 0LL) + (long long)j * p.T : (long long)off[g]) + r.r0;
+  return r;
+}
+
+__device__ __forceinline__ int tile_n(int rows, int nt) { return min(nt, (rows + 15) & ~15); }
+
+// 4 signed bytes to 4 fp16
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
-template <bool UP, typename TO>
-__global__ void __launch_bounds__(256)
-i8_product_kernel(const I8Args p) {
+template <bool UP, int NT, typename TO>
+__global__ void __launch_bounds__(kI8Threads, 1)
+i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit pairs; up: 64-row box
+               const __grid_constant__ CUtensorMap tmWb,   // (W3), else 128-row box
+               const __grid_constant__ CUtensorMap tmX16,  // fp16 rows, boxes of 16, 64 and NT rows
+               const __grid_constant__ CUtensorMap tmX64,
+               const __grid_constant__ CUtensorMap tmX, const I8Args p) {
   pdl_wait_and_trigger();
-  __shared__ int sx[kRows][kStep / 4 + 1], sw[UP ? 2 : 1][kCols][kStep / 4 + 1];
-  __shared__ int s_src[kRows];
-  const int total = p.tile_start[p.G];
-  for (int t = blockIdx.y; t < total; t += gridDim.y) {
-    int lo = 0, hi = p.G - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+  using C = I8Cfg<NT>;
+  constexpr uint32_t kBStage = NT * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sW = base;
+  uint8_t* sB = sW + C::kW * kStageW;
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(sB + C::kB * kBStage);
+  uint64_t* wempty = wfull + C::kW;
+  uint64_t* bfull = wempty + C::kW;
+  uint64_t* bempty = bfull + C::kB;
+  uint64_t* afull = bempty + C::kB;
+  uint64_t* aempty = afull + kOpStages;
+  uint64_t* dfull = aempty + kOpStages;
+  uint64_t* dempty = dfull + 2;
+  uint64_t* drain = dempty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  float* s_xch = reinterpret_cast<float*>(s_abort + 1);  // [128][17]
+  int32_t* s_ts = reinterpret_cast<int32_t*>(s_xch + 128 * kXchPitch);
+  int32_t* s_off = s_ts + kMaxGroups + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kW; ++s) {
+      tc::mbar_init(&wfull[s], 1);
+      tc::mbar_init(&wempty[s], 8);
     }
-    const int g = lo, r0 = (t - p.tile_start[g]) * kRows, n0 = blockIdx.x * kCols;
-    const bool shared = g >= p.E;
-    const int first = shared ? 0 : p.expert_off[g];
-    const int rows = shared ? p.T : p.expert_off[g + 1] - first;
-    // rows of the operand and of the output: shared expert j's follow the T K routed ones
-    const long long orow = (shared ? (long long)p.TK + (long long)(g - p.E) * p.T : first) + r0;
-    __syncthreads();
-    if (threadIdx.x < kRows) {
-      int src = -1;
-      if (r0 + (int)threadIdx.x < rows) {
-        if (p.map || (shared && UP)) {  // the tokens' rows
-          src = shared ? r0 + threadIdx.x : p.map[orow + threadIdx.x];
-          if ((unsigned)src >= (unsigned)p.n_src) {
-            record_error(p.st, kStatusData, kBadPerm, orow + threadIdx.x);
-            src = -1;
+    for (int s = 0; s < C::kB; ++s) {
+      tc::mbar_init(&bfull[s], 1);
+      tc::mbar_init(&bempty[s], 1);
+    }
+    for (int s = 0; s < kOpStages; ++s) {
+      tc::mbar_init(&afull[s], 8);
+      tc::mbar_init(&aempty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(&dfull[a], 1);
+      tc::mbar_init(&dempty[a], 128);
+    }
+    tc::mbar_init(drain, 1);
+    *s_abort = 0;
+    tc::mbar_init_fence();
+    tc::tma_prefetch_map(&tmWa);
+    tc::tma_prefetch_map(&tmWb);
+    tc::tma_prefetch_map(&tmX16);
+    tc::tma_prefetch_map(&tmX64);
+    tc::tma_prefetch_map(&tmX);
+  }
+  if (warp == 2) {
+    tc::tmem_alloc(s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 3) group_table<NT>(p, s_ts, s_off, lane);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  const int ntile = (p.N + (UP ? 63 : 127)) / (UP ? 64 : 128);
+  const int total = s_ts[p.G] * ntile;
+  const int nk = (p.KD + 127) / 128, nb = (p.KD + 63) / 64;
+  volatile int* abort = s_abort;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    uint32_t ws = 0, wph = 1, bs = 0, bph = 1;
+    uint32_t wit = 0, bit = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
+      const int wrow = tl.g * p.N + tl.n0;
+      const int box = tl.rows <= 16 ? 16 : tl.rows <= 64 || NT == 64 ? 64 : NT;
+      const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 64 ? &tmX64 : &tmX;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!tc::mbar_wait(&wempty[ws], wph, abort)) { ok = false; break; }
+        tc::mbar_expect_tx(&wfull[ws], kStageW);
+        tc::tma_load_2d(sW + ws * kStageW, &tmWa, &wfull[ws], kb * 64, wrow);
+        if (UP) tc::tma_load_2d(sW + ws * kStageW + kStageW / 2, &tmWb, &wfull[ws], kb * 64, wrow);
+        ++wit;
+        if (++ws == C::kW) { ws = 0; wph ^= 1u; }
+        for (int j = 0; j < 2 && 2 * kb + j < nb; ++j) {
+          if (!tc::mbar_wait(&bempty[bs], bph, abort)) { ok = false; break; }
+          tc::mbar_expect_tx(&bfull[bs], box * 128);
+          tc::tma_load_2d(sB + bs * kBStage, xmap, &bfull[bs], (2 * kb + j) * 64, tl.brow);
+          ++bit;
+          if (++bs == C::kB) { bs = 0; bph ^= 1u; }
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      // let the copies already issued land before the CTA's shared memory goes away
+      volatile int never = 0;
+      for (uint32_t j = wit > C::kW ? wit - C::kW : 0; j < wit; ++j)
+        tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
+      for (uint32_t j = bit > C::kB ? bit - C::kB : 0; j < bit; ++j)
+        tc::mbar_wait(&bfull[j % C::kB], (j / C::kB) & 1u, &never);
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ---------------------------------------------------------------- MMA issuer
+    uint32_t bs = 0, bph = 0, as = 0, aph = 0, d = 0, dph = 1;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
+      const uint32_t idesc = tc::instr_desc_f16(128, tile_n(tl.rows, NT));
+      if (!tc::mbar_wait(&dempty[d], dph, abort)) { ok = false; break; }
+      tc::fence_after_sync();
+      const uint32_t acc = tmem + d * NT;
+      for (int kb = 0; kb < nk && ok; ++kb) {
+        if (!tc::mbar_wait(&afull[as], aph, abort)) { ok = false; break; }
+        for (int j = 0; j < 2 && 2 * kb + j < nb; ++j) {
+          if (!tc::mbar_wait(&bfull[bs], bph, abort)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + bs * kBStage));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f16_tmem_a(acc, tmem + kOpCol + as * 64 + j * 32 + k * 8, bdesc + 2 * k, idesc,
+                               (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
+          tc::commit(&bempty[bs]);
+          if (++bs == C::kB) { bs = 0; bph ^= 1u; }
+        }
+        if (!ok) break;
+        tc::commit(&aempty[as]);
+        if (++as == kOpStages) { as = 0; aph ^= 1u; }
+      }
+      if (!ok) break;
+      tc::commit(&dfull[d]);
+      if (++d == C::kAcc) { d = 0; dph ^= 1u; }
+    }
+    if (!ok) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+    // wait for every MMA this thread issued before TMEM is released
+    volatile int never = 0;
+    tc::commit(drain);
+    tc::mbar_wait(drain, 0, &never);
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- widen the weights
+    const int q = warp & 3, half = (warp - 8) >> 2, row = q * 32 + lane;
+    uint32_t ws = 0, wph = 0, as = 0, aph = 1;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x)
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = tc::mbar_wait_warp(&wfull[ws], wph, abort);
+        if (!ok) break;
+        const uint8_t* src = sW + ws * kStageW + row * 128;
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
+          widen4(v.x, r[8 * c], r[8 * c + 1]);
+          widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+          widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+          widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&wempty[ws]);
+        if (++ws == C::kW) { ws = 0; wph ^= 1u; }
+        ok = tc::mbar_wait_warp(&aempty[as], aph, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        tc::tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + kOpCol + as * 64 + half * 32, r);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&afull[as]);
+        if (++as == kOpStages) { as = 0; aph ^= 1u; }
+      }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3, row = q * 32 + lane;
+    uint32_t d = 0, dph = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
+      bool ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
+      if (UP) {  // one outcome for the four warps, which go on to barriers together
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+            "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+            : "=r"(r) : "r"((uint32_t)ok) : "memory");
+        ok = r != 0;
+      }
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+        break;
+      }
+      tc::fence_after_sync();
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + d * NT;
+      const int nt = min(NT, tl.rows), n16 = (nt + 15) >> 4;
+      const size_t scale0 = (size_t)tl.g * p.N;
+      const float* xs = p.xs + tl.brow;
+      TO* out = static_cast<TO*>(!UP && tl.shared ? p.out_sh : p.out);
+      float sc = 0.0f, sc3 = 0.0f;
+      const int fr = row & 63, tq = row >> 6;  // up: this thread's feature and token parity
+      if (UP) {
+        if (tl.n0 + fr < p.N) {
+          sc = p.sa[scale0 + tl.n0 + fr];
+          sc3 = p.sb[scale0 + tl.n0 + fr];
+        }
+      } else if (tl.n0 + row < p.N) {
+        sc = p.sa[scale0 + tl.n0 + row];
+      }
+#pragma unroll 1
+      for (int c = 0; c < n16; ++c) {
+        float v[16];
+        tc::tmem_ld16(taddr + 16 * c, v);
+        if (c == n16 - 1) {  // read out: the next tile's MMAs may start
+          tc::fence_before_sync();
+          tc::mbar_arrive(&dempty[d]);
+        }
+        if (UP) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s_xch[row * kXchPitch + i] = v[i];
+          asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int tk = 16 * c + 2 * i + tq;
+            float h = 0.0f;
+            if (tk < nt && tl.n0 + fr < p.N) {
+              const float x = xs[tk];
+              h = silu(s_xch[fr * kXchPitch + 2 * i + tq] * x * sc) *
+                  (s_xch[(64 + fr) * kXchPitch + 2 * i + tq] * x * sc3);
+              out[(size_t)(tl.orow + tk) * p.N + tl.n0 + fr] = Elem<TO>::from_f32(h);
+            }
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+            if (lane == 0 && tk < nt) atomicMax(p.row_max + tl.orow + tk, m);
           }
-        } else {
-          src = (int)(orow + threadIdx.x);
+          asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+        } else if (tl.n0 + row < p.N) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int tk = 16 * c + i;
+            if (tk < nt)
+              out[(size_t)(tl.orow + tk) * p.N + tl.n0 + row] = Elem<TO>::from_f32(v[i] * xs[tk] * sc);
+          }
         }
       }
-      s_src[threadIdx.x] = src;
+      if (++d == C::kAcc) { d = 0; dph ^= 1u; }
     }
-    int acc[UP ? 2 : 1][4][4] = {};
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int k0 = 0; k0 < p.KD; k0 += kStep) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kRows * (kStep / 4); i += 256) {
-        const int rr = i / (kStep / 4), kk = i % (kStep / 4);
-        const bool in = k0 + 4 * kk < p.KD;
-        sx[rr][kk] = in && s_src[rr] >= 0
-                         ? *reinterpret_cast<const int*>(p.x + (size_t)s_src[rr] * p.KD + k0 + 4 * kk)
-                         : 0;
-        const bool inw = in && n0 + rr < p.N;
-        const size_t wo = ((size_t)g * p.N + n0 + rr) * p.KD + k0 + 4 * kk;
-        sw[0][rr][kk] = inw ? *reinterpret_cast<const int*>(p.wa + wo) : 0;
-        if (UP) sw[1][rr][kk] = inw ? *reinterpret_cast<const int*>(p.wb + wo) : 0;
-      }
-      __syncthreads();
-#pragma unroll 4
-      for (int kk = 0; kk < kStep / 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[0][i][j] = __dp4a(sx[ty + 16 * i][kk], sw[0][tx + 16 * j][kk], acc[0][i][j]);
-            if (UP) acc[UP][i][j] = __dp4a(sx[ty + 16 * i][kk], sw[UP][tx + 16 * j][kk], acc[UP][i][j]);
-          }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+}
+
+// The product's rows in fp16, in dispatched order, with their scales: row r < TK is xq[map[r]]
+// (or xq[r]), row TK + t the token t (shared experts). Also clears the hidden rows' maxima.
+__global__ void __launch_bounds__(256)
+i8_rows_kernel(const uint4* __restrict__ xq, const float* __restrict__ xs,
+               const int32_t* __restrict__ map, const int32_t* __restrict__ expert_off, int E,
+               int TK, int rows, int n_src, int vecs,
+               uint4* __restrict__ out, float* __restrict__ out_s, uint32_t* __restrict__ row_max,
+               int max_rows, DeviceStatus* st) {
+  pdl_wait_and_trigger();
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < max_rows; i += gridDim.x * 256) row_max[i] = 0u;
+  const int end = expert_off[E];  // rows behind the last segment belong to nobody
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
+    if (r >= end && r < TK) continue;
+    const int src = r >= TK ? r - TK : map ? map[r] : r;
+    const bool in = (unsigned)src < (unsigned)n_src;
+    if (lane == 0) {
+      if (!in) record_error(st, kStatusData, kBadPerm, r);
+      out_s[r] = in ? xs[src] : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rr = ty + 16 * i;
-      if (r0 + rr >= rows) continue;
-      const float xs = s_src[rr] >= 0 ? p.xs[s_src[rr]] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx + 16 * j;
-        if (n >= p.N) continue;
-        float v = (float)acc[0][i][j] * xs * p.sa[(size_t)g * p.N + n];
-        if (UP) v = silu(v) * ((float)acc[UP][i][j] * xs * p.sb[(size_t)g * p.N + n]);
-        TO* out = static_cast<TO*>(!UP && shared ? p.out_sh : p.out);
-        const long long ro = !UP && shared ? orow - p.TK : orow;
-        out[(size_t)(ro + rr) * p.N + n] = Elem<TO>::from_f32(v);
-      }
+    for (int v = lane; v < vecs; v += 32) {
+      const uint4 b = in ? __ldg(xq + (size_t)src * vecs + v) : make_uint4(0, 0, 0, 0);
+      uint4 lo, hi;
+      widen4(b.x, lo.x, lo.y);
+      widen4(b.y, lo.z, lo.w);
+      widen4(b.z, hi.x, hi.y);
+      widen4(b.w, hi.z, hi.w);
+      out[((size_t)r * vecs + v) * 2] = lo;
+      out[((size_t)r * vecs + v) * 2 + 1] = hi;
     }
   }
 }
 
-// hq = rint(h / s), s = max |h| / 127 of the row (0 for a row that is zero or whose scale
-// would be subnormal, NaN for a row that is not finite).
+// Hidden rows requantised: s = max |h| / 127, rint(h / s) as fp16 (an integer, exact). s is 0
+// for a row that is zero or whose scale would be subnormal, NaN for a row that is not finite.
 __global__ void __launch_bounds__(256)
-i8_quantise_rows_kernel(const float* __restrict__ h, int8_t* __restrict__ q, float* __restrict__ s,
-                        int rows, int F) {
+i8_quantise_rows_kernel(const float* __restrict__ h, const uint32_t* __restrict__ row_max,
+                        uint4* __restrict__ q, float* __restrict__ s, int rows, int vecs) {
   pdl_wait_and_trigger();
-  __shared__ uint32_t red[8];
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const float* row = h + (size_t)r * F;
-    uint32_t big = 0;
-    for (int i = threadIdx.x; i < F; i += 256) big = max(big, __float_as_uint(row[i]) & 0x7fffffffu);
-    big = __reduce_max_sync(0xffffffffu, big);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = big;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) big = max(big, red[w]);
-    const float amax = __uint_as_float(big);
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
+    const float amax = __uint_as_float(row_max[r]);
     const bool finite = amax <= FLT_MAX;
     float scale = amax / 127.0f;
     const bool zero = !finite || scale < FLT_MIN;
     if (zero) scale = finite ? 0.0f : __int_as_float(0x7fc00000);
-    if (threadIdx.x == 0) s[r] = scale;
-    for (int i = threadIdx.x; i < F; i += 256)
-      q[(size_t)r * F + i] = zero ? (int8_t)0 : (int8_t)__float2int_rn(row[i] / scale);
+    if (lane == 0) s[r] = scale;
+    for (int v = lane; v < vecs; v += 32) {  // 8 values
+      const float4* in = reinterpret_cast<const float4*>(h) + ((size_t)r * vecs + v) * 2;
+      const float4 a = __ldcs(in), b = __ldcs(in + 1);
+      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 o = zero ? __float2half2_rn(0.0f)
+                               : __floats2half2_rn(rintf(f[2 * i] / scale), rintf(f[2 * i + 1] / scale));
+        w[i] = *reinterpret_cast<const uint32_t*>(&o);
+      }
+      q[(size_t)r * vecs + v] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
+// A tile of NT = 256 rows reads a weight byte once per 256 rows and needs experts that fill
+// it; below, the weights' stream is the work, and 64-row tiles keep more of it in flight.
+constexpr int kWideRows = 96;
+
+int i8_sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 148;
+}
+
+template <bool UP, int NT, typename TO>
+cudaError_t run_gemm(const I8Args& p, const int8_t* wa, const int8_t* wb, const void* x16,
+                     long long xrows, cudaStream_t s) {
+  alignas(64) CUtensorMap ta, tb, x1, x6, xn;
+  const uint64_t wrows = (uint64_t)p.G * p.N;
+  if (!encode_tmap_2d(&ta, wa, false, wrows, p.KD / 2, UP ? 64 : 128, 64) ||
+      !encode_tmap_2d(&tb, UP ? wb : wa, false, wrows, p.KD / 2, UP ? 64 : 128, 64) ||
+      !encode_tmap_2d(&x1, x16, false, xrows, p.KD, 16, 64) ||
+      !encode_tmap_2d(&x6, x16, false, xrows, p.KD, 64, 64) ||
+      !encode_tmap_2d(&xn, x16, false, xrows, p.KD, NT, 64))
+    return cudaErrorInvalidValue;
+  auto kern = i8_gemm_kernel<UP, NT, TO>;
+  const int smem = (int)i8_smem<NT>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  SMOE_LAUNCH(kern, i8_sm_count(), kI8Threads, smem, s, ta, tb, x1, x6, xn, p);
+  return cudaGetLastError();
+}
+
 template <bool UP, typename TO>
-cudaError_t run_product(const I8Args& p, int n_shared, cudaStream_t s) {
-  const long long bound = (long long)ceil_div(p.TK, kRows) + p.E + (long long)n_shared * ceil_div(p.T, kRows);
-  SMOE_LAUNCH((i8_product_kernel<UP, TO>), dim3(ceil_div(p.N, kCols), (int)std::min(bound, 32768LL)), 256, 0, s, p);
+cudaError_t run_product(const smoe_desc& d, const I8Args& p, const int8_t* wa, const int8_t* wb,
+                        const void* x16, long long xrows, cudaStream_t s) {
+  if ((long long)d.T * d.K >= (long long)kWideRows * d.E)
+    return run_gemm<UP, 256, TO>(p, wa, wb, x16, xrows, s);
+  return run_gemm<UP, 64, TO>(p, wa, wb, x16, xrows, s);
+}
+
+cudaError_t run_rows(const int8_t* xq, const float* xs, const int32_t* map, const int32_t* expert_off,
+                     int E, int TK, int rows, int n_src, int n_in, void* x16, float* x16_s, uint32_t* row_max, int max_rows,
+                     DeviceStatus* st, cudaStream_t s) {
+  const int grid = std::max(1, std::min(std::max(ceil_div(rows, 8), ceil_div(max_rows, 256)), 152 * 8));
+  SMOE_LAUNCH(i8_rows_kernel, grid, 256, 0, s, reinterpret_cast<const uint4*>(xq), xs, map,
+              expert_off, E, TK, rows,
+              n_src, n_in / 16, static_cast<uint4*>(x16), x16_s, row_max, max_rows, st);
   return cudaGetLastError();
 }
 
@@ -185,12 +520,15 @@ void i8_ws_layout(const smoe_desc& d, I8Layout* L) {
     off += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t rows = (size_t)d.T * d.K + (size_t)d.n_shared * d.T;
+  const size_t TK = (size_t)d.T * d.K, rows = TK + (size_t)d.n_shared * d.T;
+  const size_t xrows = TK + (d.n_shared ? d.T : 0);
   L->status = take(256);
-  L->tiles = take(4 * ((size_t)d.E + d.n_shared + 1));
+  L->x16 = take(xrows * std::max(d.d, d.F) * 2);
+  L->x16_s = take(xrows * 4);
   L->h = take(rows * d.F * 4);
-  L->hq = take(rows * d.F);
-  L->hs = take(rows * 4);
+  L->row_max = take(rows * 4);
+  L->h16 = take(rows * d.F * 2);
+  L->h16_s = take(rows * 4);
   L->total = off;
 }
 
@@ -200,14 +538,17 @@ cudaError_t launch_expert_matmul_i8(const smoe_desc& d, int n_out, int n_in, con
                                     void* out, void* ws, cudaStream_t s) {
   I8Layout L;
   i8_ws_layout(d, &L);
-  int32_t* tiles = ws_ptr<int32_t>(ws, L.tiles);
   DeviceStatus* st = ws_ptr<DeviceStatus>(ws, L.status);
   const int TK = d.T * d.K;
-  SMOE_LAUNCH(i8_tiles_kernel, 1, 32, 0, s, expert_off, d.E, 0, d.T, TK, kRows, tiles, st);
-  const I8Args p{xq, xs, row_src, expert_off, tiles, wq, nullptr, ws_n, nullptr, out, nullptr, st,
-                 d.E, d.E, d.T, TK, n_out, n_in, row_src ? d.T : TK};
-  return d.dtype == SMOE_F32 ? run_product<false, float>(p, 0, s)
-                             : run_product<false, __nv_bfloat16>(p, 0, s);
+  void* x16 = ws_ptr<char>(ws, L.x16);
+  float* x16_s = ws_ptr<float>(ws, L.x16_s);
+  cudaError_t e = run_rows(xq, xs, row_src, expert_off, d.E, TK, TK, row_src ? d.T : TK, n_in, x16, x16_s, nullptr, 0,
+                           st, s);
+  if (e != cudaSuccess) return e;
+  const I8Args p{expert_off, x16_s, ws_n, nullptr, out, nullptr, nullptr, st,
+                 d.E, d.E, d.T, TK, n_out, n_in, TK};
+  return d.dtype == SMOE_F32 ? run_product<false, float>(d, p, wq, nullptr, x16, TK, s)
+                             : run_product<false, __nv_bfloat16>(d, p, wq, nullptr, x16, TK, s);
 }
 
 cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const float* xs,
@@ -216,22 +557,26 @@ cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const flo
                                  cudaStream_t s) {
   I8Layout L;
   i8_ws_layout(d, &L);
-  int32_t* tiles = ws_ptr<int32_t>(ws, L.tiles);
   DeviceStatus* st = ws_ptr<DeviceStatus>(ws, L.status);
   const int TK = d.T * d.K, G = d.E + d.n_shared, rows = TK + d.n_shared * d.T;
-  float* h = ws_ptr<float>(ws, L.h);
-  int8_t* hq = ws_ptr<int8_t>(ws, L.hq);
-  float* hs = ws_ptr<float>(ws, L.hs);
-  SMOE_LAUNCH(i8_tiles_kernel, 1, 32, 0, s, expert_off, d.E, d.n_shared, d.T, TK, kRows, tiles, st);
-  const I8Args up{xq, xs, row_src, expert_off, tiles, W.w1, W.w3, W.s1, W.s3, h, nullptr, st,
-                  d.E, G, d.T, TK, d.F, d.d, row_src ? d.T : TK};
-  cudaError_t e = run_product<true, float>(up, d.n_shared, s);
+  const int xrows = TK + (d.n_shared ? d.T : 0);
+  void *x16 = ws_ptr<char>(ws, L.x16), *h16 = ws_ptr<char>(ws, L.h16);
+  float *x16_s = ws_ptr<float>(ws, L.x16_s), *h = ws_ptr<float>(ws, L.h);
+  float* h16_s = ws_ptr<float>(ws, L.h16_s);
+  uint32_t* row_max = ws_ptr<uint32_t>(ws, L.row_max);
+  cudaError_t e = run_rows(xq, xs, row_src, expert_off, d.E, TK, xrows, row_src ? d.T : TK, d.d, x16, x16_s, row_max,
+                           rows, st, s);
   if (e != cudaSuccess) return e;
-  SMOE_LAUNCH(i8_quantise_rows_kernel, std::min(rows, 4096), 256, 0, s, h, hq, hs, rows, d.F);
-  const I8Args dn{hq, hs, nullptr, expert_off, tiles, W.w2, nullptr, W.s2, nullptr, y_disp, y_sh,
-                  st, d.E, G, d.T, TK, d.d, d.F, rows};
-  return d.dtype == SMOE_F32 ? run_product<false, float>(dn, d.n_shared, s)
-                             : run_product<false, __nv_bfloat16>(dn, d.n_shared, s);
+  const I8Args up{expert_off, x16_s, W.s1, W.s3, h, nullptr, row_max, st,
+                  d.E, G, d.T, TK, d.F, d.d, TK};
+  e = run_product<true, float>(d, up, W.w1, W.w3, x16, xrows, s);
+  if (e != cudaSuccess) return e;
+  SMOE_LAUNCH(i8_quantise_rows_kernel, std::min(ceil_div(rows, 8), 152 * 8), 256, 0, s, h, row_max,
+              static_cast<uint4*>(h16), h16_s, rows, d.F / 8);
+  const I8Args dn{expert_off, h16_s, W.s2, nullptr, y_disp, y_sh, nullptr, st,
+                  d.E, G, d.T, TK, d.d, d.F, TK};
+  return d.dtype == SMOE_F32 ? run_product<false, float>(d, dn, W.w2, nullptr, h16, rows, s)
+                             : run_product<false, __nv_bfloat16>(d, dn, W.w2, nullptr, h16, rows, s);
 }
 
 }  // namespace smoe
