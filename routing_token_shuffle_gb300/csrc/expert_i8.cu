@@ -208,8 +208,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   const int nk = (p.KD + 127) / 128, nb = (p.KD + 63) / 64;
   volatile int* abort = s_abort;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
+    const bool lead = tc::elect_one();
     uint32_t ws = 0, wph = 1, bs = 0, bph = 1;
     uint32_t wit = 0, bit = 0;
     bool ok = true;
@@ -219,23 +220,29 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       const int box = tl.rows <= 16 ? 16 : tl.rows <= 64 || NT == 64 ? 64 : NT;
       const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 64 ? &tmX64 : &tmX;
       for (int kb = 0; kb < nk; ++kb) {
-        if (!tc::mbar_wait(&wempty[ws], wph, abort)) { ok = false; break; }
-        tc::mbar_expect_tx(&wfull[ws], kStageW);
-        tc::tma_load_2d(sW + ws * kStageW, &tmWa, &wfull[ws], kb * 64, wrow);
-        if (UP) tc::tma_load_2d(sW + ws * kStageW + kStageW / 2, &tmWb, &wfull[ws], kb * 64, wrow);
+        if (!tc::mbar_wait_warp(&wempty[ws], wph, abort)) { ok = false; break; }
+        if (lead) {
+          tc::mbar_expect_tx(&wfull[ws], kStageW);
+          tc::tma_load_2d(sW + ws * kStageW, &tmWa, &wfull[ws], kb * 64, wrow);
+          if (UP) tc::tma_load_2d(sW + ws * kStageW + kStageW / 2, &tmWb, &wfull[ws], kb * 64, wrow);
+        }
+        __syncwarp();
         ++wit;
         if (++ws == C::kW) { ws = 0; wph ^= 1u; }
         for (int j = 0; j < 2 && 2 * kb + j < nb; ++j) {
-          if (!tc::mbar_wait(&bempty[bs], bph, abort)) { ok = false; break; }
-          tc::mbar_expect_tx(&bfull[bs], box * 128);
-          tc::tma_load_2d(sB + bs * kBStage, xmap, &bfull[bs], (2 * kb + j) * 64, tl.brow);
+          if (!tc::mbar_wait_warp(&bempty[bs], bph, abort)) { ok = false; break; }
+          if (lead) {
+            tc::mbar_expect_tx(&bfull[bs], box * 128);
+            tc::tma_load_2d(sB + bs * kBStage, xmap, &bfull[bs], (2 * kb + j) * 64, tl.brow);
+          }
+          __syncwarp();
           ++bit;
           if (++bs == C::kB) { bs = 0; bph ^= 1u; }
         }
         if (!ok) break;
       }
     }
-    if (!ok) {
+    if (!ok && lead) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
       // let the copies already issued land before the CTA's shared memory goes away
@@ -245,45 +252,54 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       for (uint32_t j = bit > C::kB ? bit - C::kB : 0; j < bit; ++j)
         tc::mbar_wait(&bfull[j % C::kB], (j / C::kB) & 1u, &never);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
+    const bool lead = tc::elect_one();
     uint32_t bs = 0, bph = 0, as = 0, aph = 0, d = 0, dph = 1;
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
       const uint32_t idesc = tc::instr_desc_f16(128, tile_n(tl.rows, NT));
-      if (!tc::mbar_wait(&dempty[d], dph, abort)) { ok = false; break; }
+      if (!tc::mbar_wait_warp(&dempty[d], dph, abort)) { ok = false; break; }
       tc::fence_after_sync();
       const uint32_t acc = tmem + d * NT;
       for (int kb = 0; kb < nk && ok; ++kb) {
-        if (!tc::mbar_wait(&afull[as], aph, abort)) { ok = false; break; }
+        if (!tc::mbar_wait_warp(&afull[as], aph, abort)) { ok = false; break; }
         for (int j = 0; j < 2 && 2 * kb + j < nb; ++j) {
-          if (!tc::mbar_wait(&bfull[bs], bph, abort)) { ok = false; break; }
+          if (!tc::mbar_wait_warp(&bfull[bs], bph, abort)) { ok = false; break; }
           tc::fence_after_sync();
           const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + bs * kBStage));
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_f16_tmem_a(acc, tmem + kOpCol + as * 64 + j * 32 + k * 8, bdesc + 2 * k, idesc,
-                               (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
-          tc::commit(&bempty[bs]);
+            for (int k = 0; k < 4; ++k)
+              tc::mma_f16_tmem_a(acc, tmem + kOpCol + as * 64 + j * 32 + k * 8, bdesc + 2 * k, idesc,
+                                 (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
+            tc::commit(&bempty[bs]);
+          }
+          __syncwarp();
           if (++bs == C::kB) { bs = 0; bph ^= 1u; }
         }
         if (!ok) break;
-        tc::commit(&aempty[as]);
+        if (lead) tc::commit(&aempty[as]);
+        __syncwarp();
         if (++as == kOpStages) { as = 0; aph ^= 1u; }
       }
       if (!ok) break;
-      tc::commit(&dfull[d]);
+      if (lead) tc::commit(&dfull[d]);
+      __syncwarp();
       if (++d == C::kAcc) { d = 0; dph ^= 1u; }
     }
-    if (!ok) {
-      *abort = 1;
-      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // wait for every MMA this thread issued before TMEM is released
+      volatile int never = 0;
+      tc::commit(drain);
+      tc::mbar_wait(drain, 0, &never);
     }
-    // wait for every MMA this thread issued before TMEM is released
-    volatile int never = 0;
-    tc::commit(drain);
-    tc::mbar_wait(drain, 0, &never);
+    __syncwarp();
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- widen the weights
     const int q = warp & 3, half = (warp - 8) >> 2, row = q * 32 + lane;

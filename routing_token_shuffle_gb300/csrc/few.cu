@@ -327,8 +327,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     return Range(kper, (p.d + 127) / 128 * kper, nc);
   };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
+    const bool lead = tc::elect_one();
     uint32_t it = 0;
     bool ok = true;
     // The place of the next block, stepped without divisions: this thread's instructions
@@ -365,6 +366,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       at.row = row_of(part, at.tile, at.slot);
     };
     auto load_a = [&](uint32_t s, int part, const Place& at) {
+      if (!lead) return;
       tc::mbar_expect_tx(&full[s], kFewA + kB);
       if (part < 2) {
         tc::tma_load_2d(sA + s * kFewA, &tmW1, &full[s], at.kb * BK, at.row);
@@ -374,6 +376,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       }
     };
     auto load_b = [&](uint32_t s, int part, const Place& at) {
+      if (!lead) return;
       if (part < 2) tc::tma_load_2d(sB + s * kB, &tmX, &full[s], at.kb * BK, 0);
       else tc::tma_load_2d(sB + s * kB, &tmH, &full[s], at.fb * BK, at.slot * p.T);
     };
@@ -383,7 +386,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
     };
     for (int part = 0; part < 3 && ok; ++part) {
-      if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
+      if (part == 1 && !tc::mbar_wait_warp(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
       int i = r.first(cta);
       const int end = r.first(cta + 1);
@@ -394,12 +397,12 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         const uint32_t s0 = s, it0 = it;
         Place ahead = at;
         for (int j = min(end - i, S); j > 0; --j) {
-          if (!tc::mbar_wait(&empty[s], ph, abort)) { ok = false; break; }
+          if (!tc::mbar_wait_warp(&empty[s], ph, abort)) { ok = false; break; }
           load_a(s, part, ahead);
           step(part, r, ahead);
           next_stage();
         }
-        if (ok) ok = wait_ge(p.ctl + 1, (uint32_t)nc, abort);
+        if (ok) ok = __all_sync(0xffffffffu, !lead || wait_ge(p.ctl + 1, (uint32_t)nc, abort));
         // H was written by other SMs through the generic proxy
         asm volatile("fence.proxy.async.global;" ::: "memory");
         // (also after a wait that gave up: the stages' byte counts must complete)
@@ -413,14 +416,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         if (!ok) break;
       }
       for (; i < end; ++i) {
-        if (!tc::mbar_wait(&empty[s], ph, abort)) { ok = false; break; }
+        if (!tc::mbar_wait_warp(&empty[s], ph, abort)) { ok = false; break; }
         load_a(s, part, at);
         load_b(s, part, at);
         step(part, r, at);
         next_stage();
       }
     }
-    if (!ok) {
+    if (!ok && lead) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
       // let the copies already issued land before the CTA's shared memory goes away
@@ -428,43 +431,51 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       const uint32_t firstj = it > (uint32_t)S ? it - S : 0;
       for (uint32_t j = firstj; j < it; ++j) tc::mbar_wait(&full[j % S], (j / S) & 1u, &never);
     }
-  } else if (kTC && warp == 1 && lane == 0) {
+  } else if (kTC && warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
+    const bool lead = tc::elect_one();
     uint32_t s = 0, ph = 0, tcount = 0;
     bool ok = true;
     constexpr uint32_t kIdesc = tc::instr_desc(false, 128, NP);
     for (int part = 0; part < 3 && ok; ++part) {
-      if (part == 1 && !tc::mbar_wait(routed, 0, abort)) { ok = false; break; }
+      if (part == 1 && !tc::mbar_wait_warp(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
       const int end = r.first(cta + 1);
       for (int i = r.first(cta); i < end && ok; ++tcount) {
         const int n = min(r.kper - i % r.kper, end - i);
         const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
-        if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
+        if (!tc::mbar_wait_warp(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
         tc::fence_after_sync();
         for (int j = 0; j < n; ++j) {
-          if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
+          if (!tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
           tc::fence_after_sync();
           const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kFewA));
           const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kB));
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16(tmem + a * NP, adesc + 2 * k, bdesc + 2 * k, kIdesc, (j > 0 || k > 0) ? 1u : 0u);
-          tc::commit(&empty[s]);
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16(tmem + a * NP, adesc + 2 * k, bdesc + 2 * k, kIdesc, (j > 0 || k > 0) ? 1u : 0u);
+            tc::commit(&empty[s]);
+          }
+          __syncwarp();
           if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
         }
         i += n;
-        if (ok) tc::commit(&tfull[a]);
+        if (ok && lead) tc::commit(&tfull[a]);
+        __syncwarp();
       }
     }
-    if (!ok) {
-      *abort = 1;
-      record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+      }
+      // wait for every MMA this thread issued before TMEM is released
+      volatile int never = 0;
+      tc::commit(drain);
+      tc::mbar_wait(drain, 0, &never);
     }
-    // wait for every MMA this thread issued before TMEM is released
-    volatile int never = 0;
-    tc::commit(drain);
-    tc::mbar_wait(drain, 0, &never);
+    __syncwarp();
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- gate and routes
     const int gt = threadIdx.x - 64;

@@ -71,6 +71,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// True in one lane of a converged warp. A role that issues TMA or tcgen05.mma runs as a
+// whole warp and issues under this predicate: their operands are warp-uniform registers,
+// and inside a branch on the lane number moving them there cost 119 clocks per
+// tcgen05.mma, against 50-75 under elect (M = 128, N <= 128, A in TMEM).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+               : "=r"(r));
+  return r != 0;
+}
+
 // mbar_wait by every lane of a warp, with one outcome for all of them: a warp that goes
 // on to warp-collective instructions (tcgen05.ld, shuffles) must not split on a wait
 // that gave up for some lanes only.
