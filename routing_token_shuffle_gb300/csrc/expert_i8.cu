@@ -30,22 +30,25 @@ namespace {
 
 constexpr int kI8Threads = 512;
 constexpr int kStageW = 128 * 128;   // weight stage: 128 channels x 128 bytes
-constexpr int kOpStages = 4;         // widened operand stages in TMEM, 64 columns each
-constexpr int kOpCol = 256;          // their first column
 constexpr int kXchPitch = 17;
 constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 
-// NT: most rows of a tile. 64: weight streaming, a deep weight ring and two accumulators.
-// 256: batches whose experts fill it, one accumulator.
+// NT: most rows of a tile. TMEM holds two accumulators of NT columns, then the widened
+// operand stages (64 columns: 128 contraction values), kOp of them.
+// 64: weight streaming. A deep weight ring; the rows of an operand stage (two 64-value
+//     halves) sit beside it under the same barrier, so that the MMA warp waits once and
+//     commits once per 128 values: with separate barriers for the halves it was the
+//     bottleneck (1190 clocks a stage, against 780 at the HBM rate).
+// 192: batches whose experts fill it. The rows have a ring of their own, in 64-value halves.
 template <int NT> struct I8Cfg;
-template <> struct I8Cfg<64> { static constexpr int kW = 8, kB = 8, kAcc = 2; };
-template <> struct I8Cfg<256> { static constexpr int kW = 3, kB = 5, kAcc = 1; };
+template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0; };
+template <> struct I8Cfg<192> { static constexpr int kW = 4, kOp = 2, kB = 6; };
 
 template <int NT>
 constexpr size_t i8_smem() {
-  return 1024 + (size_t)I8Cfg<NT>::kW * kStageW + (size_t)I8Cfg<NT>::kB * NT * 128 +
-         4 * 128 * kXchPitch + 8 * (2 * (I8Cfg<NT>::kW + I8Cfg<NT>::kB + kOpStages) + 5) + 16 +
-         4 * kMaxGroupTab;
+  using C = I8Cfg<NT>;
+  return 1024 + (size_t)C::kW * kStageW + (size_t)(C::kB ? C::kB : 2 * C::kOp) * NT * 128 +
+         4 * 128 * kXchPitch + 8 * (2 * (C::kW + C::kB + C::kOp) + 5) + 16 + 4 * kMaxGroupTab;
 }
 
 struct I8Args {
@@ -146,19 +149,21 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
                const __grid_constant__ CUtensorMap tmX, const I8Args p) {
   pdl_wait_and_trigger();
   using C = I8Cfg<NT>;
-  constexpr uint32_t kBStage = NT * 128;
+  constexpr uint32_t kHalf = NT * 128;   // rows x 64 values
+  constexpr bool kOwnB = C::kB > 0;      // a ring of their own for the rows
+  constexpr int kOpCol = 2 * NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sW = base;
   uint8_t* sB = sW + C::kW * kStageW;
-  uint64_t* wfull = reinterpret_cast<uint64_t*>(sB + C::kB * kBStage);
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(sB + (kOwnB ? C::kB : 2 * C::kOp) * kHalf);
   uint64_t* wempty = wfull + C::kW;
   uint64_t* bfull = wempty + C::kW;
   uint64_t* bempty = bfull + C::kB;
   uint64_t* afull = bempty + C::kB;
-  uint64_t* aempty = afull + kOpStages;
-  uint64_t* dfull = aempty + kOpStages;
+  uint64_t* aempty = afull + C::kOp;
+  uint64_t* dfull = aempty + C::kOp;
   uint64_t* dempty = dfull + 2;
   uint64_t* drain = dempty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -177,8 +182,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       tc::mbar_init(&bfull[s], 1);
       tc::mbar_init(&bempty[s], 1);
     }
-    for (int s = 0; s < kOpStages; ++s) {
-      tc::mbar_init(&afull[s], 8);
+    for (int s = 0; s < C::kOp; ++s) {
+      tc::mbar_init(&afull[s], kOwnB ? 8 : 9);  // the widening warps, and the rows' copy
       tc::mbar_init(&aempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -211,6 +216,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     const bool lead = tc::elect_one();
+    constexpr uint32_t kRing = kOwnB ? C::kB : C::kOp;  // of row copies
+    uint64_t* bar = kOwnB ? bfull : afull;
+    uint64_t* free = kOwnB ? bempty : aempty;
     uint32_t ws = 0, wph = 1, bs = 0, bph = 1;
     uint32_t wit = 0, bit = 0;
     bool ok = true;
@@ -219,8 +227,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       const int wrow = tl.g * p.N + tl.n0;
       const int box = tl.rows <= 16 ? 16 : tl.rows <= 64 || NT == 64 ? 64 : NT;
       const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 64 ? &tmX64 : &tmX;
-      for (int kb = 0; kb < nk; ++kb) {
-        if (!tc::mbar_wait_warp(&wempty[ws], wph, abort)) { ok = false; break; }
+      for (int kb = 0; kb < nk && ok; ++kb) {
+        ok = tc::mbar_wait_warp(&wempty[ws], wph, abort);
+        if (!ok) break;
         if (lead) {
           tc::mbar_expect_tx(&wfull[ws], kStageW);
           tc::tma_load_2d(sW + ws * kStageW, &tmWa, &wfull[ws], kb * 64, wrow);
@@ -229,28 +238,33 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         __syncwarp();
         ++wit;
         if (++ws == C::kW) { ws = 0; wph ^= 1u; }
-        for (int j = 0; j < 2 && 2 * kb + j < nb; ++j) {
-          if (!tc::mbar_wait_warp(&bempty[bs], bph, abort)) { ok = false; break; }
+        const int halves = min(2, nb - 2 * kb);
+        for (int j = 0; j < (kOwnB ? halves : 1); ++j) {
+          ok = tc::mbar_wait_warp(&free[bs], bph, abort);
+          if (!ok) break;
           if (lead) {
-            tc::mbar_expect_tx(&bfull[bs], box * 128);
-            tc::tma_load_2d(sB + bs * kBStage, xmap, &bfull[bs], (2 * kb + j) * 64, tl.brow);
+            uint8_t* dst = sB + bs * (kOwnB ? 1 : 2) * kHalf;
+            tc::mbar_expect_tx(&bar[bs], box * 128 * (kOwnB ? 1 : halves));
+            tc::tma_load_2d(dst, xmap, &bar[bs], (2 * kb + j) * 64, tl.brow);
+            if (!kOwnB && halves == 2)
+              tc::tma_load_2d(dst + kHalf, xmap, &bar[bs], (2 * kb + 1) * 64, tl.brow);
           }
           __syncwarp();
           ++bit;
-          if (++bs == C::kB) { bs = 0; bph ^= 1u; }
+          if (++bs == kRing) { bs = 0; bph ^= 1u; }
         }
-        if (!ok) break;
       }
     }
     if (!ok && lead) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      // let the copies already issued land before the CTA's shared memory goes away
+      // let the copies already issued land before the CTA's shared memory goes away; what
+      // shares a barrier with the widening warps may never complete it: wait out the limit
       volatile int never = 0;
       for (uint32_t j = wit > C::kW ? wit - C::kW : 0; j < wit; ++j)
         tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
-      for (uint32_t j = bit > C::kB ? bit - C::kB : 0; j < bit; ++j)
-        tc::mbar_wait(&bfull[j % C::kB], (j / C::kB) & 1u, &never);
+      for (uint32_t j = bit > kRing ? bit - kRing : 0; j < bit; ++j)
+        if (!tc::mbar_wait(&bar[j % kRing], (j / kRing) & 1u, &never)) break;
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -265,29 +279,31 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       const uint32_t acc = tmem + d * NT;
       for (int kb = 0; kb < nk && ok; ++kb) {
         if (!tc::mbar_wait_warp(&afull[as], aph, abort)) { ok = false; break; }
-        for (int j = 0; j < 2 && 2 * kb + j < nb; ++j) {
-          if (!tc::mbar_wait_warp(&bfull[bs], bph, abort)) { ok = false; break; }
+        const int halves = min(2, nb - 2 * kb);
+        for (int j = 0; j < halves; ++j) {
+          if (kOwnB && !tc::mbar_wait_warp(&bfull[bs], bph, abort)) { ok = false; break; }
           tc::fence_after_sync();
-          const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + bs * kBStage));
+          const uint8_t* rows = sB + (kOwnB ? bs : 2 * as + j) * kHalf;
+          const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(rows));
           if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc::mma_f16_tmem_a(acc, tmem + kOpCol + as * 64 + j * 32 + k * 8, bdesc + 2 * k, idesc,
                                  (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
-            tc::commit(&bempty[bs]);
+            if (kOwnB) tc::commit(&bempty[bs]);
           }
           __syncwarp();
-          if (++bs == C::kB) { bs = 0; bph ^= 1u; }
+          if (kOwnB && ++bs == C::kB) { bs = 0; bph ^= 1u; }
         }
         if (!ok) break;
         if (lead) tc::commit(&aempty[as]);
         __syncwarp();
-        if (++as == kOpStages) { as = 0; aph ^= 1u; }
+        if (++as == C::kOp) { as = 0; aph ^= 1u; }
       }
       if (!ok) break;
       if (lead) tc::commit(&dfull[d]);
       __syncwarp();
-      if (++d == C::kAcc) { d = 0; dph ^= 1u; }
+      if (++d == 2) { d = 0; dph ^= 1u; }
     }
     if (lead) {
       if (!ok) {
@@ -330,7 +346,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&afull[as]);
-        if (++as == kOpStages) { as = 0; aph ^= 1u; }
+        if (++as == C::kOp) { as = 0; aph ^= 1u; }
       }
     if (!ok && lane == 0) {
       *abort = 1;
@@ -381,6 +397,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
           tc::mbar_arrive(&dempty[d]);
         }
         if (UP) {
+          float xr[8];  // loaded together, ahead of the stores they may not pass
+#pragma unroll
+          for (int i = 0; i < 8; ++i) xr[i] = 16 * c + 2 * i + tq < nt ? __ldg(xs + 16 * c + 2 * i + tq) : 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) s_xch[row * kXchPitch + i] = v[i];
           asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
@@ -389,7 +408,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
             const int tk = 16 * c + 2 * i + tq;
             float h = 0.0f;
             if (tk < nt && tl.n0 + fr < p.N) {
-              const float x = xs[tk];
+              const float x = xr[i];
               h = silu(s_xch[fr * kXchPitch + 2 * i + tq] * x * sc) *
                   (s_xch[(64 + fr) * kXchPitch + 2 * i + tq] * x * sc3);
               out[(size_t)(tl.orow + tk) * p.N + tl.n0 + fr] = Elem<TO>::from_f32(h);
@@ -399,15 +418,16 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
           }
           asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
         } else if (tl.n0 + row < p.N) {
+          float xr[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int tk = 16 * c + i;
-            if (tk < nt)
-              out[(size_t)(tl.orow + tk) * p.N + tl.n0 + row] = Elem<TO>::from_f32(v[i] * xs[tk] * sc);
-          }
+          for (int i = 0; i < 16; ++i) xr[i] = 16 * c + i < nt ? __ldg(xs + 16 * c + i) : 0.0f;
+          TO* o = out + (size_t)(tl.orow + 16 * c) * p.N + tl.n0 + row;
+#pragma unroll
+          for (int i = 0; i < 16; ++i, o += p.N)
+            if (16 * c + i < nt) *o = Elem<TO>::from_f32(v[i] * xr[i] * sc);
         }
       }
-      if (++d == C::kAcc) { d = 0; dph ^= 1u; }
+      if (++d == 2) { d = 0; dph ^= 1u; }
     }
   }
   tc::fence_before_sync();
@@ -479,7 +499,7 @@ i8_quantise_rows_kernel(const float* __restrict__ h, const uint32_t* __restrict_
   }
 }
 
-// A tile of NT = 256 rows reads a weight byte once per 256 rows and needs experts that fill
+// A tile of NT = 192 rows reads a weight byte once per 192 rows and needs experts that fill
 // it; below, the weights' stream is the work, and 64-row tiles keep more of it in flight.
 constexpr int kWideRows = 96;
 
@@ -513,7 +533,7 @@ template <bool UP, typename TO>
 cudaError_t run_product(const smoe_desc& d, const I8Args& p, const int8_t* wa, const int8_t* wb,
                         const void* x16, long long xrows, cudaStream_t s) {
   if ((long long)d.T * d.K >= (long long)kWideRows * d.E)
-    return run_gemm<UP, 256, TO>(p, wa, wb, x16, xrows, s);
+    return run_gemm<UP, 192, TO>(p, wa, wb, x16, xrows, s);
   return run_gemm<UP, 64, TO>(p, wa, wb, x16, xrows, s);
 }
 
