@@ -39,15 +39,19 @@ constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 //     halves) sit beside it under the same barrier, so that the MMA warp waits once and
 //     commits once per 128 values: with separate barriers for the halves it was the
 //     bottleneck (1190 clocks a stage, against 780 at the HBM rate).
-// 192: batches whose experts fill it. The rows have a ring of their own, in 64-value halves.
+// 192: batches whose experts fill it, on pairs of CTAs (a cluster on the two SMs of a TPC):
+//     256 channels, each CTA widening its own 128, and half of the rows in each CTA's
+//     shared memory, in a ring of their own. One CTA alone moves 155
+//     bytes a clock through shared memory at the MMAs' rate (rows written and read, weight
+//     bytes written and read), the pair 97; the limit is 128.
 template <int NT> struct I8Cfg;
-template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0; };
-template <> struct I8Cfg<192> { static constexpr int kW = 4, kOp = 2, kB = 6; };
+template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0, kRows = 64; };
+template <> struct I8Cfg<192> { static constexpr int kW = 6, kOp = 2, kB = 4, kRows = 96; };
 
 template <int NT>
 constexpr size_t i8_smem() {
   using C = I8Cfg<NT>;
-  return 1024 + (size_t)C::kW * kStageW + (size_t)(C::kB ? C::kB : 2 * C::kOp) * NT * 128 +
+  return 1024 + (size_t)C::kW * kStageW + (size_t)2 * (C::kB ? C::kB : C::kOp) * C::kRows * 128 +
          4 * 128 * kXchPitch + 8 * (2 * (C::kW + C::kB + C::kOp) + 5) + 16 + 4 * kMaxGroupTab;
 }
 
@@ -104,7 +108,7 @@ __device__ __forceinline__ void group_table(const I8Args& p, int32_t* s_ts, int3
 
 template <bool UP, int NT>
 __device__ __forceinline__ I8Tile decode(const I8Args& p, const int32_t* ts, const int32_t* off,
-                                         int ntile, int t) {
+                                         int ntile, int t, uint32_t rank) {
   int lo = 0, hi = p.G - 1;
   while (lo < hi) {  // largest g whose first tile is <= t (empty groups are skipped)
     const int mid = (lo + hi + 1) >> 1;
@@ -114,7 +118,7 @@ __device__ __forceinline__ I8Tile decode(const I8Args& p, const int32_t* ts, con
   const int n_tile = local / mt, m_tile = local - n_tile * mt;
   I8Tile r;
   r.g = g;
-  r.n0 = n_tile * (UP ? 64 : 128);
+  r.n0 = (n_tile * (I8Cfg<NT>::kB ? 2 : 1) + (int)rank) * (UP ? 64 : 128);
   r.r0 = m_tile * NT;
   r.shared = g >= p.E;
   const int j = g - p.E;
@@ -125,7 +129,11 @@ __device__ __forceinline__ I8Tile decode(const I8Args& p, const int32_t* ts, con
   return r;
 }
 
-__device__ __forceinline__ int tile_n(int rows, int nt) { return min(nt, (rows + 15) & ~15); }
+// MMA columns of a tile: its rows rounded up to 16 (to 32 on a pair, half for each CTA)
+template <int NT>
+__device__ __forceinline__ int tile_n(int rows) {
+  return I8Cfg<NT>::kB ? min(NT, (rows + 31) & ~31) : min(NT, (rows + 15) & ~15);
+}
 
 // 4 signed bytes to 4 fp16
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -144,20 +152,21 @@ template <bool UP, int NT, typename TO>
 __global__ void __launch_bounds__(kI8Threads, 1)
 i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit pairs; up: 64-row box
                const __grid_constant__ CUtensorMap tmWb,   // (W3), else 128-row box
-               const __grid_constant__ CUtensorMap tmX16,  // fp16 rows, boxes of 16, 64 and NT rows
-               const __grid_constant__ CUtensorMap tmX64,
+               const __grid_constant__ CUtensorMap tmX16,  // fp16 rows, boxes of 16, 48 and kRows
+               const __grid_constant__ CUtensorMap tmX48,
                const __grid_constant__ CUtensorMap tmX, const I8Args p) {
   pdl_wait_and_trigger();
   using C = I8Cfg<NT>;
-  constexpr uint32_t kHalf = NT * 128;   // rows x 64 values
-  constexpr bool kOwnB = C::kB > 0;      // a ring of their own for the rows
+  constexpr uint32_t kHalf = C::kRows * 128;  // rows x 64 values
+  constexpr bool kOwnB = C::kB > 0;           // a ring of their own for the rows, on CTA pairs
+  constexpr bool kPair = kOwnB;
   constexpr int kOpCol = 2 * NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sW = base;
   uint8_t* sB = sW + C::kW * kStageW;
-  uint64_t* wfull = reinterpret_cast<uint64_t*>(sB + (kOwnB ? C::kB : 2 * C::kOp) * kHalf);
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(sB + 2 * (kOwnB ? C::kB : C::kOp) * kHalf);
   uint64_t* wempty = wfull + C::kW;
   uint64_t* bfull = wempty + C::kW;
   uint64_t* bempty = bfull + C::kB;
@@ -173,6 +182,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   int32_t* s_off = s_ts + kMaxGroups + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? tc::cluster_rank() : 0u;
+  const int first = kPair ? blockIdx.x >> 1 : blockIdx.x, stride = kPair ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kW; ++s) {
       tc::mbar_init(&wfull[s], 1);
@@ -183,12 +194,12 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       tc::mbar_init(&bempty[s], 1);
     }
     for (int s = 0; s < C::kOp; ++s) {
-      tc::mbar_init(&afull[s], kOwnB ? 8 : 9);  // the widening warps, and the rows' copy
+      tc::mbar_init(&afull[s], kPair ? 16 : 9);  // both CTAs' widening warps; or with the rows' copy
       tc::mbar_init(&aempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&dfull[a], 1);
-      tc::mbar_init(&dempty[a], 128);
+      tc::mbar_init(&dempty[a], kPair ? 256 : 128);
     }
     tc::mbar_init(drain, 1);
     *s_abort = 0;
@@ -196,19 +207,26 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     tc::tma_prefetch_map(&tmWa);
     tc::tma_prefetch_map(&tmWb);
     tc::tma_prefetch_map(&tmX16);
-    tc::tma_prefetch_map(&tmX64);
+    tc::tma_prefetch_map(&tmX48);
     tc::tma_prefetch_map(&tmX);
   }
   if (warp == 2) {
-    tc::tmem_alloc(s_tmem, 512);
-    tc::tmem_relinquish();
+    if (kPair) {
+      tc::tmem_alloc_pair(s_tmem, 512);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(s_tmem, 512);
+      tc::tmem_relinquish();
+    }
   }
   if (warp == 3) group_table<NT>(p, s_ts, s_off, lane);
   tc::fence_before_sync();
   __syncthreads();
+  if (kPair) tc::cluster_sync();  // both CTAs' barriers are initialised before a remote signal
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
-  const int ntile = (p.N + (UP ? 63 : 127)) / (UP ? 64 : 128);
+  constexpr int kChan = (UP ? 64 : 128) * (kPair ? 2 : 1);
+  const int ntile = (p.N + kChan - 1) / kChan;
   const int total = s_ts[p.G] * ntile;
   const int nk = (p.KD + 127) / 128, nb = (p.KD + 63) / 64;
   volatile int* abort = s_abort;
@@ -222,11 +240,14 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     uint32_t ws = 0, wph = 1, bs = 0, bph = 1;
     uint32_t wit = 0, bit = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
+    for (int t = first; t < total && ok; t += stride) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
       const int wrow = tl.g * p.N + tl.n0;
-      const int box = tl.rows <= 16 ? 16 : tl.rows <= 64 || NT == 64 ? 64 : NT;
-      const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 64 ? &tmX64 : &tmX;
+      // this CTA's rows: all of the tile's, or its half of the MMA's columns
+      const int mine = kPair ? tile_n<NT>(tl.rows) / 2 : tl.rows;
+      const int box = mine <= 16 ? 16 : mine <= 48 ? 48 : C::kRows;
+      const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 48 ? &tmX48 : &tmX;
+      const int brow = tl.brow + (kPair ? (int)rank * mine : 0);
       for (int kb = 0; kb < nk && ok; ++kb) {
         ok = tc::mbar_wait_warp(&wempty[ws], wph, abort);
         if (!ok) break;
@@ -239,69 +260,86 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         ++wit;
         if (++ws == C::kW) { ws = 0; wph ^= 1u; }
         const int halves = min(2, nb - 2 * kb);
-        for (int j = 0; j < (kOwnB ? halves : 1); ++j) {
-          ok = tc::mbar_wait_warp(&free[bs], bph, abort);
-          if (!ok) break;
-          if (lead) {
-            uint8_t* dst = sB + bs * (kOwnB ? 1 : 2) * kHalf;
-            tc::mbar_expect_tx(&bar[bs], box * 128 * (kOwnB ? 1 : halves));
-            tc::tma_load_2d(dst, xmap, &bar[bs], (2 * kb + j) * 64, tl.brow);
-            if (!kOwnB && halves == 2)
-              tc::tma_load_2d(dst + kHalf, xmap, &bar[bs], (2 * kb + 1) * 64, tl.brow);
+        ok = tc::mbar_wait_warp(&free[bs], bph, abort);
+        if (!ok) break;
+        if (lead) {
+          uint8_t* dst = sB + 2 * bs * kHalf;
+          if (kPair) {  // both CTAs' bytes complete on the leader's barrier
+            const uint32_t on = tc::cluster_addr(&bar[bs], 0);
+            if (rank == 0) tc::mbar_expect_tx(&bar[bs], 2 * box * 128 * halves);
+            tc::tma_load_2d_pair(dst, xmap, on, 2 * kb * 64, brow);
+            if (halves == 2) tc::tma_load_2d_pair(dst + kHalf, xmap, on, (2 * kb + 1) * 64, brow);
+          } else {
+            tc::mbar_expect_tx(&bar[bs], box * 128 * halves);
+            tc::tma_load_2d(dst, xmap, &bar[bs], 2 * kb * 64, brow);
+            if (halves == 2) tc::tma_load_2d(dst + kHalf, xmap, &bar[bs], (2 * kb + 1) * 64, brow);
           }
-          __syncwarp();
-          ++bit;
-          if (++bs == kRing) { bs = 0; bph ^= 1u; }
         }
+        __syncwarp();
+        ++bit;
+        if (++bs == kRing) { bs = 0; bph ^= 1u; }
       }
     }
     if (!ok && lead) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      // let the copies already issued land before the CTA's shared memory goes away; what
-      // shares a barrier with the widening warps may never complete it: wait out the limit
+      // let the copies already issued land before the CTA's shared memory goes away; a
+      // barrier that others share may never complete: wait out the limit
       volatile int never = 0;
       for (uint32_t j = wit > C::kW ? wit - C::kW : 0; j < wit; ++j)
         tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
-      for (uint32_t j = bit > kRing ? bit - kRing : 0; j < bit; ++j)
+      for (uint32_t j = bit > kRing ? bit - kRing : 0; j < bit && rank == 0; ++j)
         if (!tc::mbar_wait(&bar[j % kRing], (j / kRing) & 1u, &never)) break;
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- MMA issuer (of the pair)
     const bool lead = tc::elect_one();
     uint32_t bs = 0, bph = 0, as = 0, aph = 0, d = 0, dph = 1;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
-      const uint32_t idesc = tc::instr_desc_f16(128, tile_n(tl.rows, NT));
+    bool ok = true, a_in = false, b_in = false;
+    for (int t = first; t < total && ok; t += stride) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      const uint32_t idesc = tc::instr_desc_f16(kPair ? 256 : 128, tile_n<NT>(tl.rows));
       if (!tc::mbar_wait_warp(&dempty[d], dph, abort)) { ok = false; break; }
       tc::fence_after_sync();
       const uint32_t acc = tmem + d * NT;
-      for (int kb = 0; kb < nk && ok; ++kb) {
-        if (!tc::mbar_wait_warp(&afull[as], aph, abort)) { ok = false; break; }
-        const int halves = min(2, nb - 2 * kb);
-        for (int j = 0; j < halves; ++j) {
-          if (kOwnB && !tc::mbar_wait_warp(&bfull[bs], bph, abort)) { ok = false; break; }
-          tc::fence_after_sync();
-          const uint8_t* rows = sB + (kOwnB ? bs : 2 * as + j) * kHalf;
-          const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(rows));
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_f16_tmem_a(acc, tmem + kOpCol + as * 64 + j * 32 + k * 8, bdesc + 2 * k, idesc,
-                                 (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
-            if (kOwnB) tc::commit(&bempty[bs]);
-          }
-          __syncwarp();
-          if (kOwnB && ++bs == C::kB) { bs = 0; bph ^= 1u; }
-        }
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!a_in) ok = tc::mbar_wait_warp(&afull[as], aph, abort);
+        if (kOwnB && !b_in && ok) ok = tc::mbar_wait_warp(&bfull[bs], bph, abort);
         if (!ok) break;
-        if (lead) tc::commit(&aempty[as]);
-        __syncwarp();
+        tc::fence_after_sync();
+        const uint32_t a0 = tmem + kOpCol + as * 64;
+        const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + 2 * (kOwnB ? bs : as) * kHalf));
+        uint64_t *a_free = &aempty[as], *b_free = &bempty[bs];
         if (++as == C::kOp) { as = 0; aph ^= 1u; }
+        if (kOwnB && ++bs == C::kB) { bs = 0; bph ^= 1u; }
+        // look at the next stage's barriers while this stage's MMAs are issued: asking costs
+        // over 100 clocks even when they have completed
+        const bool a_next = tc::mbar_test(&afull[as], aph);
+        const bool b_next = kOwnB && tc::mbar_test(&bfull[bs], bph);
+        if (lead) {
+          const int n = 4 * min(2, nb - 2 * kb);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (k >= n) break;
+            const uint64_t b = bdesc + (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
+            if (kPair) tc::mma_f16_tmem_a_pair(acc, a0 + k * 8, b, idesc, kb > 0 || k > 0);
+            else tc::mma_f16_tmem_a(acc, a0 + k * 8, b, idesc, kb > 0 || k > 0);
+          }
+          if (kPair) {
+            tc::commit_pair(b_free, 0x3);
+            tc::commit_pair(a_free, 0x3);
+          } else {
+            tc::commit(a_free);
+          }
+        }
+        a_in = __all_sync(0xffffffffu, a_next);
+        b_in = __all_sync(0xffffffffu, b_next);
       }
       if (!ok) break;
-      if (lead) tc::commit(&dfull[d]);
+      if (lead) {
+        if (kPair) tc::commit_pair(&dfull[d], 0x3);
+        else tc::commit(&dfull[d]);
+      }
       __syncwarp();
       if (++d == 2) { d = 0; dph ^= 1u; }
     }
@@ -312,7 +350,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       }
       // wait for every MMA this thread issued before TMEM is released
       volatile int never = 0;
-      tc::commit(drain);
+      if (kPair) tc::commit_pair(drain, 0x1);
+      else tc::commit(drain);
       tc::mbar_wait(drain, 0, &never);
     }
     __syncwarp();
@@ -321,7 +360,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     const int q = warp & 3, half = (warp - 8) >> 2, row = q * 32 + lane;
     uint32_t ws = 0, wph = 0, as = 0, aph = 1;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x)
+    for (int t = first; t < total && ok; t += stride)
       for (int kb = 0; kb < nk; ++kb) {
         ok = tc::mbar_wait_warp(&wfull[ws], wph, abort);
         if (!ok) break;
@@ -345,7 +384,10 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&afull[as]);
+        if (lane == 0) {
+          if (kPair) tc::mbar_arrive_remote(tc::cluster_addr(&afull[as], 0));
+          else tc::mbar_arrive(&afull[as]);
+        }
         if (++as == C::kOp) { as = 0; aph ^= 1u; }
       }
     if (!ok && lane == 0) {
@@ -356,8 +398,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, row = q * 32 + lane;
     uint32_t d = 0, dph = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t);
+    for (int t = first; t < total; t += stride) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
       bool ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
       if (UP) {  // one outcome for the four warps, which go on to barriers together
         uint32_t r;
@@ -394,7 +436,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         tc::tmem_ld16(taddr + 16 * c, v);
         if (c == n16 - 1) {  // read out: the next tile's MMAs may start
           tc::fence_before_sync();
-          tc::mbar_arrive(&dempty[d]);
+          if (kPair) tc::mbar_arrive_remote(tc::cluster_addr(&dempty[d], 0));
+          else tc::mbar_arrive(&dempty[d]);
         }
         if (UP) {
           float xr[8];  // loaded together, ahead of the stores they may not pass
@@ -432,8 +475,12 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (kPair) tc::cluster_sync();  // no signal or copy of the other CTA is on its way here
   tc::fence_after_sync();
-  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+  if (warp == 2) {
+    if (kPair) tc::tmem_dealloc_pair(tmem, 512);
+    else tc::tmem_dealloc(tmem, 512);
+  }
 }
 
 // The product's rows in fp16, in dispatched order, with their scales: row r < TK is xq[map[r]]
@@ -513,20 +560,34 @@ int i8_sm_count() {
 template <bool UP, int NT, typename TO>
 cudaError_t run_gemm(const I8Args& p, const int8_t* wa, const int8_t* wb, const void* x16,
                      long long xrows, cudaStream_t s) {
-  alignas(64) CUtensorMap ta, tb, x1, x6, xn;
+  alignas(64) CUtensorMap ta, tb, x1, x4, xn;
   const uint64_t wrows = (uint64_t)p.G * p.N;
   if (!encode_tmap_2d(&ta, wa, false, wrows, p.KD / 2, UP ? 64 : 128, 64) ||
       !encode_tmap_2d(&tb, UP ? wb : wa, false, wrows, p.KD / 2, UP ? 64 : 128, 64) ||
       !encode_tmap_2d(&x1, x16, false, xrows, p.KD, 16, 64) ||
-      !encode_tmap_2d(&x6, x16, false, xrows, p.KD, 64, 64) ||
-      !encode_tmap_2d(&xn, x16, false, xrows, p.KD, NT, 64))
+      !encode_tmap_2d(&x4, x16, false, xrows, p.KD, 48, 64) ||
+      !encode_tmap_2d(&xn, x16, false, xrows, p.KD, I8Cfg<NT>::kRows, 64))
     return cudaErrorInvalidValue;
   auto kern = i8_gemm_kernel<UP, NT, TO>;
   const int smem = (int)i8_smem<NT>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  SMOE_LAUNCH(kern, i8_sm_count(), kI8Threads, smem, s, ta, tb, x1, x6, xn, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(I8Cfg<NT>::kB ? i8_sm_count() / 2 * 2 : i8_sm_count());
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = I8Cfg<NT>::kB ? 2 : 1;
+  SMOE_COUNT_LAUNCH(1);
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, x1, x4, xn, p);
 }
 
 template <bool UP, typename TO>
