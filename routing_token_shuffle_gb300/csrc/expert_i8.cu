@@ -13,7 +13,8 @@
 //
 // One persistent CTA per SM walks the tiles (group, 128-channel tile, row tile), row tiles
 // fastest so that neighbours share the weights through L2:
-//   warp 0      TMA: weight bytes (128 channels x 128) and fp16 rows (NT rows x 64)
+//   warp 0      TMA: weight bytes (128 channels x 128)
+//   warp 3      TMA: fp16 rows (NT rows x 128)
 //   warps 8-15  widen a weight stage into one of four TMEM operand stages
 //   warp 1      tcgen05.mma, M = 128 channels, N = the tile's rows rounded up to 16
 //   warps 4-7   epilogue: scales, SwiGLU, stores (up: fp32 hidden rows and their largest
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kI8Threads = 512;
 constexpr int kStageW = 128 * 128;   // weight stage: 128 channels x 128 bytes
-constexpr int kXchPitch = 17;
+constexpr int kXchPitch = 33;
 constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 
 // NT: most rows of a tile. TMEM holds two accumulators of NT columns, then the widened
@@ -52,7 +53,7 @@ template <int NT>
 constexpr size_t i8_smem() {
   using C = I8Cfg<NT>;
   return 1024 + (size_t)C::kW * kStageW + (size_t)2 * (C::kB ? C::kB : C::kOp) * C::kRows * 128 +
-         4 * 128 * kXchPitch + 8 * (2 * (C::kW + C::kB + C::kOp) + 5) + 16 + 4 * kMaxGroupTab;
+         4 * (128 * kXchPitch + NT) + 8 * (2 * (C::kW + C::kB + C::kOp) + 5) + 16 + 4 * kMaxGroupTab;
 }
 
 struct I8Args {
@@ -146,8 +147,6 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
-
 template <bool UP, int NT, typename TO>
 __global__ void __launch_bounds__(kI8Threads, 1)
 i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit pairs; up: 64-row box
@@ -155,7 +154,10 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
                const __grid_constant__ CUtensorMap tmX16,  // fp16 rows, boxes of 16, 48 and kRows
                const __grid_constant__ CUtensorMap tmX48,
                const __grid_constant__ CUtensorMap tmX, const I8Args p) {
-  pdl_wait_and_trigger();
+  // The kernel before this one in the stream writes the rows and has itself waited for what
+  // is before it, so the weights and expert_off are read without waiting for it: the weight
+  // ring fills while it runs. The rows' producer and the epilogue wait.
+  pdl_trigger();
   using C = I8Cfg<NT>;
   constexpr uint32_t kHalf = C::kRows * 128;  // rows x 64 values
   constexpr bool kOwnB = C::kB > 0;           // a ring of their own for the rows, on CTA pairs
@@ -177,8 +179,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   uint64_t* drain = dempty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  float* s_xch = reinterpret_cast<float*>(s_abort + 1);  // [128][17]
-  int32_t* s_ts = reinterpret_cast<int32_t*>(s_xch + 128 * kXchPitch);
+  float* s_xch = reinterpret_cast<float*>(s_abort + 1);  // [128][33]
+  float* s_xs = s_xch + 128 * kXchPitch;                 // [NT] row scales of the tile
+  int32_t* s_ts = reinterpret_cast<int32_t*>(s_xs + NT);
   int32_t* s_off = s_ts + kMaxGroups + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -232,23 +235,14 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   volatile int* abort = s_abort;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
+    // ---------------------------------------------------------------- weight producer
     const bool lead = tc::elect_one();
-    constexpr uint32_t kRing = kOwnB ? C::kB : C::kOp;  // of row copies
-    uint64_t* bar = kOwnB ? bfull : afull;
-    uint64_t* free = kOwnB ? bempty : aempty;
-    uint32_t ws = 0, wph = 1, bs = 0, bph = 1;
-    uint32_t wit = 0, bit = 0;
+    uint32_t ws = 0, wph = 1, wit = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += stride) {
       const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
       const int wrow = tl.g * p.N + tl.n0;
-      // this CTA's rows: all of the tile's, or its half of the MMA's columns
-      const int mine = kPair ? tile_n<NT>(tl.rows) / 2 : tl.rows;
-      const int box = mine <= 16 ? 16 : mine <= 48 ? 48 : C::kRows;
-      const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 48 ? &tmX48 : &tmX;
-      const int brow = tl.brow + (kPair ? (int)rank * mine : 0);
-      for (int kb = 0; kb < nk && ok; ++kb) {
+      for (int kb = 0; kb < nk; ++kb) {
         ok = tc::mbar_wait_warp(&wempty[ws], wph, abort);
         if (!ok) break;
         if (lead) {
@@ -259,10 +253,38 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         __syncwarp();
         ++wit;
         if (++ws == C::kW) { ws = 0; wph ^= 1u; }
-        const int halves = min(2, nb - 2 * kb);
+      }
+    }
+    if (!ok && lead) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      // let the copies already issued land before the CTA's shared memory goes away
+      volatile int never = 0;
+      for (uint32_t j = wit > C::kW ? wit - C::kW : 0; j < wit; ++j)
+        tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- row producer
+    pdl_wait();
+    const bool lead = tc::elect_one();
+    constexpr uint32_t kRing = kOwnB ? C::kB : C::kOp;
+    uint64_t* bar = kOwnB ? bfull : afull;
+    uint64_t* free = kOwnB ? bempty : aempty;
+    uint32_t bs = 0, bph = 1, bit = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += stride) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      // this CTA's rows: all of the tile's, or its half of the MMA's columns
+      const int mine = kPair ? tile_n<NT>(tl.rows) / 2 : tl.rows;
+      const int box = mine <= 16 ? 16 : mine <= 48 ? 48 : C::kRows;
+      const CUtensorMap* xmap = box == 16 ? &tmX16 : box == 48 ? &tmX48 : &tmX;
+      const int brow = tl.brow + (kPair ? (int)rank * mine : 0);
+      for (int kb = 0; kb < nk; ++kb) {
         ok = tc::mbar_wait_warp(&free[bs], bph, abort);
         if (!ok) break;
         if (lead) {
+          const int halves = min(2, nb - 2 * kb);
           uint8_t* dst = sB + 2 * bs * kHalf;
           if (kPair) {  // both CTAs' bytes complete on the leader's barrier
             const uint32_t on = tc::cluster_addr(&bar[bs], 0);
@@ -283,14 +305,12 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     if (!ok && lead) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      // let the copies already issued land before the CTA's shared memory goes away; a
-      // barrier that others share may never complete: wait out the limit
+      // as above; a barrier that others share may never complete: wait out the limit once
       volatile int never = 0;
-      for (uint32_t j = wit > C::kW ? wit - C::kW : 0; j < wit; ++j)
-        tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
       for (uint32_t j = bit > kRing ? bit - kRing : 0; j < bit && rank == 0; ++j)
         if (!tc::mbar_wait(&bar[j % kRing], (j / kRing) & 1u, &never)) break;
     }
+    __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- MMA issuer (of the pair)
     const bool lead = tc::elect_one();
@@ -396,80 +416,71 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
+    pdl_wait();
     const int q = warp & 3, row = q * 32 + lane;
+    const int fr = row & 63, tq = row >> 6;  // up: this thread's feature and token parity
     uint32_t d = 0, dph = 0;
     for (int t = first; t < total; t += stride) {
       const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      const int nt = min(NT, tl.rows), n32 = (nt + 31) >> 5;
+      const int chan = tl.n0 + (UP ? fr : row);  // this thread's channel
+      const bool has = chan < p.N;
+      // the tile's scales, ahead of its accumulator
+      for (int i = row; i < NT; i += 128) s_xs[i] = i < nt ? __ldg(p.xs + tl.brow + i) : 0.0f;
+      const float sc = has ? __ldg(p.sa + (size_t)tl.g * p.N + chan) : 0.0f;
+      const float sc3 = UP && has ? __ldg(p.sb + (size_t)tl.g * p.N + chan) : 0.0f;
       bool ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
-      if (UP) {  // one outcome for the four warps, which go on to barriers together
-        uint32_t r;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-            "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-            : "=r"(r) : "r"((uint32_t)ok) : "memory");
-        ok = r != 0;
-      }
-      if (!ok) {
+      // one outcome for the four warps, which meet at barriers
+      uint32_t all;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+          : "=r"(all) : "r"((uint32_t)ok) : "memory");
+      if (!all) {
         *abort = 1;
         record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
         break;
       }
       tc::fence_after_sync();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + d * NT;
-      const int nt = min(NT, tl.rows), n16 = (nt + 15) >> 4;
-      const size_t scale0 = (size_t)tl.g * p.N;
-      const float* xs = p.xs + tl.brow;
-      TO* out = static_cast<TO*>(!UP && tl.shared ? p.out_sh : p.out);
-      float sc = 0.0f, sc3 = 0.0f;
-      const int fr = row & 63, tq = row >> 6;  // up: this thread's feature and token parity
-      if (UP) {
-        if (tl.n0 + fr < p.N) {
-          sc = p.sa[scale0 + tl.n0 + fr];
-          sc3 = p.sb[scale0 + tl.n0 + fr];
-        }
-      } else if (tl.n0 + row < p.N) {
-        sc = p.sa[scale0 + tl.n0 + row];
-      }
+      TO* out = static_cast<TO*>(!UP && tl.shared ? p.out_sh : p.out) + (size_t)tl.orow * p.N + chan;
 #pragma unroll 1
-      for (int c = 0; c < n16; ++c) {
-        float v[16];
-        tc::tmem_ld16(taddr + 16 * c, v);
-        if (c == n16 - 1) {  // read out: the next tile's MMAs may start
+      for (int c = 0; c < n32; ++c) {
+        uint32_t v[32];
+        tc::tmem_ld32(taddr + 32 * c, v);
+        tc::tmem_ld_wait();
+        if (c == n32 - 1) {  // read out: another tile's MMAs may start
           tc::fence_before_sync();
           if (kPair) tc::mbar_arrive_remote(tc::cluster_addr(&dempty[d], 0));
           else tc::mbar_arrive(&dempty[d]);
         }
+        const int left = nt - 32 * c;
         if (UP) {
-          float xr[8];  // loaded together, ahead of the stores they may not pass
 #pragma unroll
-          for (int i = 0; i < 8; ++i) xr[i] = 16 * c + 2 * i + tq < nt ? __ldg(xs + 16 * c + 2 * i + tq) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s_xch[row * kXchPitch + i] = v[i];
+          for (int i = 0; i < 32; ++i) s_xch[row * kXchPitch + i] = __uint_as_float(v[i]);
           asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int tk = 16 * c + 2 * i + tq;
-            float h = 0.0f;
-            if (tk < nt && tl.n0 + fr < p.N) {
-              const float x = xr[i];
-              h = silu(s_xch[fr * kXchPitch + 2 * i + tq] * x * sc) *
-                  (s_xch[(64 + fr) * kXchPitch + 2 * i + tq] * x * sc3);
-              out[(size_t)(tl.orow + tk) * p.N + tl.n0 + fr] = Elem<TO>::from_f32(h);
-            }
+          TO* o = out + (size_t)(32 * c + tq) * p.N;
+          uint32_t* mx = p.row_max + tl.orow + 32 * c + tq;
+#pragma unroll 4
+          for (int i = tq; i < 32; i += 2, o += 2 * (size_t)p.N, mx += 2) {
+            if (i >= left) break;
+            const float x = s_xs[32 * c + i];
+            const float g = s_xch[fr * kXchPitch + i] * x * sc;
+            const float u = s_xch[(64 + fr) * kXchPitch + i] * x * sc3;
+            const float h = has ? __fdividef(g, 1.0f + expf(-g)) * u : 0.0f;
+            if (has) *o = Elem<TO>::from_f32(h);
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-            if (lane == 0 && tk < nt) atomicMax(p.row_max + tl.orow + tk, m);
+            if (lane == 0) atomicMax(mx, m);
           }
           asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-        } else if (tl.n0 + row < p.N) {
-          float xr[16];
+        } else if (has) {
+          TO* o = out + (size_t)(32 * c) * p.N;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) xr[i] = 16 * c + i < nt ? __ldg(xs + 16 * c + i) : 0.0f;
-          TO* o = out + (size_t)(tl.orow + 16 * c) * p.N + tl.n0 + row;
-#pragma unroll
-          for (int i = 0; i < 16; ++i, o += p.N)
-            if (16 * c + i < nt) *o = Elem<TO>::from_f32(v[i] * xr[i] * sc);
+          for (int i = 0; i < 32; ++i, o += p.N)
+            if (i < left) *o = Elem<TO>::from_f32(__uint_as_float(v[i]) * s_xs[32 * c + i] * sc);
         }
       }
+      if (!UP) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");  // s_xs has been read
       if (++d == 2) { d = 0; dph ^= 1u; }
     }
   }
