@@ -497,7 +497,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
 // The product's rows in fp16, in dispatched order, with their scales: row r < TK is xq[map[r]]
 // (or xq[r]), row TK + t the token t (shared experts). Also clears the hidden rows' maxima.
 __global__ void __launch_bounds__(256)
-i8_rows_kernel(const uint4* __restrict__ xq, const float* __restrict__ xs,
+i8_rows_kernel(const uint2* __restrict__ xq, const float* __restrict__ xs,
                const int32_t* __restrict__ map, const int32_t* __restrict__ expert_off, int E,
                int TK, int rows, int n_src, int vecs,
                uint4* __restrict__ out, float* __restrict__ out_s, uint32_t* __restrict__ row_max,
@@ -514,15 +514,15 @@ i8_rows_kernel(const uint4* __restrict__ xq, const float* __restrict__ xs,
       if (!in) record_error(st, kStatusData, kBadPerm, r);
       out_s[r] = in ? xs[src] : 0.0f;
     }
-    for (int v = lane; v < vecs; v += 32) {
-      const uint4 b = in ? __ldg(xq + (size_t)src * vecs + v) : make_uint4(0, 0, 0, 0);
-      uint4 lo, hi;
-      widen4(b.x, lo.x, lo.y);
-      widen4(b.y, lo.z, lo.w);
-      widen4(b.z, hi.x, hi.y);
-      widen4(b.w, hi.z, hi.w);
-      out[((size_t)r * vecs + v) * 2] = lo;
-      out[((size_t)r * vecs + v) * 2 + 1] = hi;
+    const uint2* from = xq + (size_t)src * vecs;
+    uint4* to = out + (size_t)r * vecs;
+#pragma unroll 4
+    for (int v = lane; v < vecs; v += 32) {  // 8 values: a warp's stores are 512 bytes in a row
+      const uint2 b = in ? __ldg(from + v) : make_uint2(0u, 0u);
+      uint4 o;
+      widen4(b.x, o.x, o.y);
+      widen4(b.y, o.z, o.w);
+      to[v] = o;
     }
   }
 }
@@ -531,7 +531,7 @@ i8_rows_kernel(const uint4* __restrict__ xq, const float* __restrict__ xs,
 // for a row that is zero or whose scale would be subnormal, NaN for a row that is not finite.
 __global__ void __launch_bounds__(256)
 i8_quantise_rows_kernel(const float* __restrict__ h, const uint32_t* __restrict__ row_max,
-                        uint4* __restrict__ q, float* __restrict__ s, int rows, int vecs) {
+                        uint2* __restrict__ q, float* __restrict__ s, int rows, int vecs) {
   pdl_wait_and_trigger();
   const int lane = threadIdx.x & 31;
   for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
@@ -541,18 +541,16 @@ i8_quantise_rows_kernel(const float* __restrict__ h, const uint32_t* __restrict_
     const bool zero = !finite || scale < FLT_MIN;
     if (zero) scale = finite ? 0.0f : __int_as_float(0x7fc00000);
     if (lane == 0) s[r] = scale;
-    for (int v = lane; v < vecs; v += 32) {  // 8 values
-      const float4* in = reinterpret_cast<const float4*>(h) + ((size_t)r * vecs + v) * 2;
-      const float4 a = __ldcs(in), b = __ldcs(in + 1);
-      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 o = zero ? __float2half2_rn(0.0f)
-                               : __floats2half2_rn(rintf(f[2 * i] / scale), rintf(f[2 * i + 1] / scale));
-        w[i] = *reinterpret_cast<const uint32_t*>(&o);
-      }
-      q[(size_t)r * vecs + v] = make_uint4(w[0], w[1], w[2], w[3]);
+    const float inv = zero ? 0.0f : 1.0f / scale;
+    const float4* in = reinterpret_cast<const float4*>(h) + (size_t)r * vecs;
+    uint2* out = q + (size_t)r * vecs;
+#pragma unroll 4
+    for (int v = lane; v < vecs; v += 32) {  // 4 values
+      const float4 a = __ldcs(in + v);
+      const __half2 lo = __floats2half2_rn(rintf(a.x * inv), rintf(a.y * inv));
+      const __half2 hi = __floats2half2_rn(rintf(a.z * inv), rintf(a.w * inv));
+      out[v] = zero ? make_uint2(0u, 0u)
+                    : make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
 }
@@ -613,9 +611,9 @@ cudaError_t run_rows(const int8_t* xq, const float* xs, const int32_t* map, cons
                      int E, int TK, int rows, int n_src, int n_in, void* x16, float* x16_s, uint32_t* row_max, int max_rows,
                      DeviceStatus* st, cudaStream_t s) {
   const int grid = std::max(1, std::min(std::max(ceil_div(rows, 8), ceil_div(max_rows, 256)), 152 * 8));
-  SMOE_LAUNCH(i8_rows_kernel, grid, 256, 0, s, reinterpret_cast<const uint4*>(xq), xs, map,
+  SMOE_LAUNCH(i8_rows_kernel, grid, 256, 0, s, reinterpret_cast<const uint2*>(xq), xs, map,
               expert_off, E, TK, rows,
-              n_src, n_in / 16, static_cast<uint4*>(x16), x16_s, row_max, max_rows, st);
+              n_src, n_in / 8, static_cast<uint4*>(x16), x16_s, row_max, max_rows, st);
   return cudaGetLastError();
 }
 
@@ -680,7 +678,7 @@ cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const flo
   e = run_product<true, float>(d, up, W.w1, W.w3, x16, xrows, s);
   if (e != cudaSuccess) return e;
   SMOE_LAUNCH(i8_quantise_rows_kernel, std::min(ceil_div(rows, 8), 152 * 8), 256, 0, s, h, row_max,
-              static_cast<uint4*>(h16), h16_s, rows, d.F / 8);
+              static_cast<uint2*>(h16), h16_s, rows, d.F / 4);
   const I8Args dn{expert_off, h16_s, W.s2, nullptr, y_disp, y_sh, nullptr, st,
                   d.E, G, d.T, TK, d.d, d.F, TK};
   return d.dtype == SMOE_F32 ? run_product<false, float>(d, dn, W.w2, nullptr, h16, rows, s)
