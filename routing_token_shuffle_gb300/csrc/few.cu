@@ -258,10 +258,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   constexpr uint32_t kB = NP * 128;
   constexpr bool kTC = sizeof(TE) == 2;            // bf16: tcgen05; fp32: FMAs on the CUDA cores
   constexpr uint32_t kCols = 2 * NP;               // TMEM: two accumulators of NP columns
-  // consumer threads: 4 warps read the accumulators (bf16); 8 warps multiply (fp32), four on
-  // each half of a block's contraction (splitting the tokens instead leaves one half idle
-  // on most experts and reads the weights twice from shared memory)
+  // Consumer threads: 4 warps read the accumulators (bf16), 8 warps multiply (fp32). Each of
+  // those takes all 128 rows of a block, four to a lane, 16 tokens and a share of the
+  // contraction: shared memory returns 128 bytes a clock, broadcast or not, so a token's
+  // values have to serve four rows (one row a lane and all tokens: 512 clocks of shared
+  // memory for every four tokens of a block, against 712 that its load from HBM takes; now
+  // 128).
   constexpr int kCons = kTC ? 128 : 256;
+  constexpr int kTokSplit = NP / 16, kKSplit = 8 / kTokSplit;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -279,8 +283,8 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   int* s_nact = s_abort + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_nact + 1);
   float* s_red = reinterpret_cast<float*>(s_tmem + 2);     // [10][32]
-  float* s_xch = s_red + kGateThreads;                     // [128][17]
-  float* s_wcol = s_xch + 128 * 17;                        // [64]
+  float* s_xch = s_red + kGateThreads;                     // [128][17], four of them for fp32
+  float* s_wcol = s_xch + (kTC ? 1 : 4) * 128 * 17;         // [64]
   int* s_use = reinterpret_cast<int*>(s_wcol + 64);        // [64]
   int32_t* s_act = s_use + 64;                             // [E]
   int32_t* s_idx = s_act + p.E;                            // [T K]
@@ -546,6 +550,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     if (ok && warp >= 4 && warp < 4 + kCons / 32) {
       // -------------------------------------------------------------- products, epilogue
       const int q = warp & 3, row = q * 32 + lane, half = (warp - 4) >> 2, ct = row + 128 * half;
+      const int ks = (warp - 4) % kKSplit, tq = (warp - 4) / kKSplit;  // fp32: this warp's share
+      (void)ks;
+      (void)tq;
       uint32_t s = 0, ph = 0, tcount = 0;
       for (int part = 0; part < 3 && ok; ++part) {
         const Range r = part_range(part);
@@ -555,7 +562,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         for (int i = r.first(cta); i < end && ok;) {
           const int tile = i / r.kper, k0 = i - tile * r.kper;
           const int k1 = min(r.kper, k0 + end - i);
-          float acc[kTC ? 1 : NP] = {};
+          float acc[kTC ? 1 : 4][kTC ? 1 : 16] = {};  // [rows lane + 32 r][tokens 16 tq + t]
           const uint32_t ta = tcount & 1u, taph = (tcount >> 1) & 1u;
           ++tcount;
           if (kTC) {
@@ -574,28 +581,33 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
               }
               ok = tc::mbar_wait_warp(&full[s], ph, abort);
               if (!ok) break;
-              const uint8_t* a = sA + s * kFewA + row * 128;
-              const uint8_t* b = sB + s * kB;
-              float4 av[4];
+              const uint8_t* a = sA + s * kFewA + lane * 128;
+              const uint8_t* b = sB + s * kB + tq * 16 * 128;
+              const uint32_t on16 = (uint32_t)(on >> (16 * tq)) & 0xffffu;
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                av[c] = *reinterpret_cast<const float4*>(a + (((4 * half + c) ^ (row & 7)) << 4));
-              // groups of four tokens: four independent chains of FMAs
+              for (int cc = 0; cc < (kTC ? 0 : 8 / kKSplit); ++cc) {
+                if (on16 == 0) break;
+                const int c = ks * (8 / kKSplit) + cc;
+                float4 av[4];
 #pragma unroll
-              for (int t = 0; t < (kTC ? 0 : NP); t += 4) {
-                if (((on >> t) & 15) == 0) continue;
+                for (int r4 = 0; r4 < 4; ++r4)
+                  av[r4] = *reinterpret_cast<const float4*>(a + r4 * 4096 + ((c ^ (lane & 7)) << 4));
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int t = 0; t < 16; t += 4) {
+                  if (((on16 >> t) & 15) == 0) continue;
 #pragma unroll
                   for (int u = 0; u < 4; ++u) {
-                    const float4 bv = *reinterpret_cast<const float4*>(
-                        b + (t + u) * 128 + (((4 * half + c) ^ ((t + u) & 7)) << 4));
-                    float& s4 = acc[kTC ? 0 : t + u];
-                    s4 = fmaf(av[c].x, bv.x, s4);
-                    s4 = fmaf(av[c].y, bv.y, s4);
-                    s4 = fmaf(av[c].z, bv.z, s4);
-                    s4 = fmaf(av[c].w, bv.w, s4);
+                    const float4 bv = *reinterpret_cast<const float4*>(b + (t + u) * 128 + ((c ^ ((t + u) & 7)) << 4));
+#pragma unroll
+                    for (int r4 = 0; r4 < 4; ++r4) {
+                      float& s4 = acc[kTC ? 0 : r4][kTC ? 0 : t + u];
+                      s4 = fmaf(av[r4].x, bv.x, s4);
+                      s4 = fmaf(av[r4].y, bv.y, s4);
+                      s4 = fmaf(av[r4].z, bv.z, s4);
+                      s4 = fmaf(av[r4].w, bv.w, s4);
+                    }
                   }
+                }
               }
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&empty[s]);
@@ -640,20 +652,41 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
               for (int t = 0; t < 16; ++t) mine[t] = v[t];
             } else {
               if (c0) group_sync(1, kCons);  // the last 16 tokens' sums have been used
-              if (half == 0) {
+              // the contraction's shares: into min(kKSplit, 4) buffers, four more added to
+              // them, and the buffers' sum into the first
+              constexpr int kBuf = kKSplit < 4 ? kKSplit : 4;
+              float* buf = s_xch + (ks & 3) * 128 * 17 + lane * 17;
+#pragma unroll 1
+              for (int k = 0; k < kKSplit; k += 4) {
+                if (tq == c0 / 16 && (ks & ~3) == k) {
 #pragma unroll
-                for (int t = 0; t < 16; ++t) mine[t] = acc[kTC ? 0 : c0 + t];
+                  for (int r4 = 0; r4 < (kTC ? 0 : 4); ++r4) {
+                    float* x = buf + 32 * r4 * 17;
+                    float old[16];
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) old[t] = k == 0 ? 0.0f : x[t];
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) x[t] = old[t] + acc[kTC ? 0 : r4][kTC ? 0 : t];
+                  }
+                }
+                group_sync(1, kCons);
               }
-              group_sync(1, kCons);
-              if (half == 1) {
+              {
+                float sum[8];
 #pragma unroll
-                for (int t = 0; t < 16; ++t) mine[t] += acc[kTC ? 0 : c0 + t];
+                for (int t = 0; t < 8; ++t) sum[t] = mine[8 * half + t];
+#pragma unroll
+                for (int k = 1; k < kBuf; ++k)
+#pragma unroll
+                  for (int t = 0; t < 8; ++t) sum[t] += mine[k * 128 * 17 + 8 * half + t];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) mine[8 * half + t] = sum[t];
               }
               group_sync(1, kCons);
             }
             if (k0 != 0) {  // the tile belongs to an earlier CTA
               float* out = partial + ((size_t)cta * NP + c0) * 128 + row;
-#pragma unroll 1
+#pragma unroll 4
               for (int t = half; t < nt; t += kCons / 128) __stcg(out + t * 128, mine[t]);
               continue;
             }
@@ -768,7 +801,7 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
             ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
             d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
   const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 +
-                      4 * (kGateThreads + 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
+                      4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
   p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + NP * 128));
   auto kern = moe_few_kernel<TE, NP>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
