@@ -58,15 +58,49 @@ struct FewArgs {
   int T, d, E, K, H, F, S, renorm, stages;
 };
 
-// The 128-byte weight blocks of a phase, kper to a tile, cut into one range per CTA (the
-// first `rem` of them one block longer).
+// The 128-byte weight blocks of a phase, kper to a tile, cut into one range per CTA.
+// bf16: equal ranges (the first `rem` of them one block longer); the stream from HBM is the
+// time of a block whatever its tokens.
+// fp32: ranges of equal weight; a block takes longer the more tokens its expert has, and
+// equal ranges left the slowest CTA at 1.4 times the mean. Weight 2 + (groups of four
+// tokens), measured 900 clocks with one group and 1700 with four.
 struct Range {
   int kper, quot, rem;
+  const int* table;  // fp32: first block of each CTA, in shared memory
   __device__ __forceinline__ Range(int kper_, int total, int n)
-      : kper(kper_), quot(total / n), rem(total - total / n * n) {}
-  __device__ __forceinline__ int first(int cta) const { return cta * quot + min(cta, rem); }
-  __device__ __forceinline__ bool any(int cta) const { return quot > 0 || cta < rem; }
+      : kper(kper_), quot(total / n), rem(total - total / n * n), table(nullptr) {}
+  __device__ __forceinline__ Range(int kper_, const int* table_)
+      : kper(kper_), quot(0), rem(0), table(table_) {}
+  __device__ __forceinline__ int first(int cta) const {
+    return table ? table[cta] : cta * quot + min(cta, rem);
+  }
+  __device__ __forceinline__ bool any(int cta) const {
+    return table ? table[cta] < table[cta + 1] : quot > 0 || cta < rem;
+  }
 };
+
+// First block of CTA `cta` of nc when the blocks of `tiles` tiles, each of nshared slots of
+// weight wshared and nact slots of the weights in pre (a prefix), per_slot blocks a slot,
+// are cut by weight.
+__device__ __forceinline__ int weighted_first(int cta, int nc, int tiles, int per_slot, int nshared,
+                                              int wshared, const int* pre, int nact) {
+  const long long tile_w = (long long)(nshared * wshared + pre[nact]) * per_slot;
+  const long long at = tile_w * tiles * cta / nc;
+  const int tile = (int)(at / tile_w);
+  const int base = tile * (nshared + nact) * per_slot;
+  if (tile == tiles) return base;
+  long long left = at - tile_w * tile;
+  const long long shared_w = (long long)nshared * wshared * per_slot;
+  if (left < shared_w) return base + (int)(left / wshared);
+  left -= shared_w;
+  int lo = 0, hi = nact - 1;
+  while (lo < hi) {  // largest slot whose weight prefix is at most what is left
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)pre[mid] * per_slot <= left) lo = mid; else hi = mid - 1;
+  }
+  const int in = (int)((left - (long long)pre[lo] * per_slot) / (pre[lo + 1] - pre[lo]));
+  return base + (nshared + lo) * per_slot + in;
+}
 
 __device__ __forceinline__ bool group_and(int id, int threads, bool v) {
   uint32_t r;
@@ -289,6 +323,8 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   int32_t* s_act = s_use + 64;                             // [E]
   int32_t* s_idx = s_act + p.E;                            // [T K]
   float* s_w = reinterpret_cast<float*>(s_idx + p.T * p.K);
+  int32_t* s_first = reinterpret_cast<int32_t*>(s_w + p.T * p.K);  // fp32: [2][kFewMaxCtas + 1]
+  int32_t* s_pre = s_first + 2 * (kFewMaxCtas + 1);                // fp32: [E + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, nc = gridDim.x;
@@ -326,9 +362,12 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   // parts: 0 up of the shared experts, 1 up of the routed ones, 2 down
   auto part_range = [&](int part) {
     if (part == 0) return Range(nkd, p.S * FB * nkd, nc);
+    const int down = (p.d + 127) / 128;
+    if (!kTC && part == 1) return Range(nkd, s_first);
+    if (!kTC) return Range((p.S + *s_nact) * nkf, s_first + kFewMaxCtas + 1);
     if (part == 1) return Range(nkd, *s_nact * FB * nkd, nc);
     const int kper = (p.S + *s_nact) * nkf;
-    return Range(kper, (p.d + 127) / 128 * kper, nc);
+    return Range(kper, down * kper, nc);
   };
 
   if (warp == 0) {
@@ -543,8 +582,45 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           n += __popc(b);
         }
         if (lane == 0) *s_nact = n;
+        if (!kTC) {  // the slots' weights (see Range), as a prefix
+          __syncwarp();
+          int carry = 0;
+          for (int i0 = 0; i0 < n; i0 += 32) {
+            int w = 0;
+            if (i0 + lane < n) {
+              const unsigned long long m = s_mask[s_act[i0 + lane]];
+              int most = 0;
+#pragma unroll 1
+              for (int q16 = 0; q16 < kTokSplit; ++q16) {
+                uint32_t g = (uint32_t)(m >> (16 * q16)) & 0xffffu;
+                g |= g >> 2;
+                g |= g >> 1;
+                most = max(most, __popc(g & 0x1111u));
+              }
+              w = 2 + kTokSplit * most;
+            }
+            int incl = w;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, incl, off);
+              if (lane >= off) incl += y;
+            }
+            if (i0 + lane < n) s_pre[i0 + lane] = carry + incl - w;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+          }
+          if (lane == 0) s_pre[n] = carry;
+        }
       }
       group_sync(2, kGateThreads);
+      if (!kTC) {
+        const int every = 2 + kTokSplit * ((min(p.T, 16) + 3) / 4);
+        for (int i = gt; i < 2 * (nc + 1); i += kGateThreads) {
+          if (i <= nc) s_first[i] = weighted_first(i, nc, 1, FB * nkd, 0, every, s_pre, *s_nact);
+          else s_first[kFewMaxCtas + i - nc] =
+                   weighted_first(i - nc - 1, nc, (p.d + 127) / 128, nkf, p.S, every, s_pre, *s_nact);
+        }
+        group_sync(2, kGateThreads);
+      }
       if (gt == 0) tc::mbar_arrive(routed);
     }
     if (ok && warp >= 4 && warp < 4 + kCons / 32) {
@@ -706,14 +782,18 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
               }
             } else if (half == 0) {
 #pragma unroll 1
-              for (int c = cta + 1; c < c1; ++c) {
-                if (!r.any(c)) continue;
+              for (int c = cta + 1; c < c1; c += 2) {
                 const float* src = partial + ((size_t)c * NP + c0) * 128 + row;
-                float in[16];
+                const bool one = r.any(c), two = c + 1 < c1 && r.any(c + 1);
+                float in[2][16], v[16];
 #pragma unroll
-                for (int t = 0; t < 16; ++t) in[t] = t < nt ? __ldcg(src + t * 128) : 0.0f;
+                for (int t = 0; t < 16; ++t) {
+                  in[0][t] = one && t < nt ? __ldcg(src + t * 128) : 0.0f;
+                  in[1][t] = two && t < nt ? __ldcg(src + (size_t)NP * 128 + t * 128) : 0.0f;
+                  v[t] = mine[t];
+                }
 #pragma unroll
-                for (int t = 0; t < 16; ++t) mine[t] += in[t];
+                for (int t = 0; t < 16; ++t) mine[t] = v[t] + in[0][t] + in[1][t];
               }
             }
             if (!kTC) group_sync(1, kCons);
@@ -801,7 +881,8 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
             ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
             d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
   const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 +
-                      4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K;
+                      4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K +
+                      (kF32 ? 4 * ((size_t)d.E + 1 + 2 * (kFewMaxCtas + 1)) : 0);
   p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + NP * 128));
   auto kern = moe_few_kernel<TE, NP>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
