@@ -359,9 +359,13 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   const uint32_t tmem = kTC ? *s_tmem : 0u;
   volatile int* abort = s_abort;
   const int FB = (p.F + 63) / 64, nkd = (p.d + BK - 1) / BK, nkf = (p.F + BK - 1) / BK;
-  // parts: 0 up of the shared experts, 1 up of the routed ones, 2 down
+  // parts: 0 up of the shared experts (fp32: none, all of them are in part 1, where the
+  // tiles cut at its borders would cost more than the early start gains), 1 up of the routed
+  // ones, 2 down. Slots: the shared experts, then the touched ones.
+  const int slot1 = kTC ? p.S : 0;  // first slot of part 1
+  auto expert_of = [&](int slot) { return slot < p.S ? p.E + slot : s_act[slot - p.S]; };
   auto part_range = [&](int part) {
-    if (part == 0) return Range(nkd, p.S * FB * nkd, nc);
+    if (part == 0) return Range(nkd, kTC ? p.S * FB * nkd : 0, nc);
     const int down = (p.d + 127) / 128;
     if (!kTC && part == 1) return Range(nkd, s_first);
     if (!kTC) return Range((p.S + *s_nact) * nkf, s_first + kFewMaxCtas + 1);
@@ -382,9 +386,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       int tile, kb, fb, slot, row;  // fb, slot: down only; row: of the A tile
     };
     auto row_of = [&](int part, int tile, int slot) {
-      if (part == 2) return (slot < p.S ? p.E + slot : s_act[slot - p.S]) * p.d + tile * 128;
+      if (part == 2) return expert_of(slot) * p.d + tile * 128;
       const int li = tile / FB;
-      return (part == 0 ? p.E + li : s_act[li]) * p.F + (tile - li * FB) * 64;
+      return expert_of((part == 0 ? 0 : slot1) + li) * p.F + (tile - li * FB) * 64;
     };
     auto place = [&](int part, const Range& r, int i) {
       Place at;
@@ -615,7 +619,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       if (!kTC) {
         const int every = 2 + kTokSplit * ((min(p.T, 16) + 3) / 4);
         for (int i = gt; i < 2 * (nc + 1); i += kGateThreads) {
-          if (i <= nc) s_first[i] = weighted_first(i, nc, 1, FB * nkd, 0, every, s_pre, *s_nact);
+          if (i <= nc) s_first[i] = weighted_first(i, nc, 1, FB * nkd, p.S, every, s_pre, *s_nact);
           else s_first[kFewMaxCtas + i - nc] =
                    weighted_first(i - nc - 1, nc, (p.d + 127) / 128, nkf, p.S, every, s_pre, *s_nact);
         }
@@ -646,7 +650,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           } else {
             // only the tokens of a block's expert: the others are not kept (up) or zero (down)
             const unsigned long long every = ~0ull >> (64 - p.T);
-            int slot = part == 2 ? k0 / nkf : part == 1 ? p.S + tile / FB : 0;
+            int slot = part == 2 ? k0 / nkf : slot1 + tile / FB;
             int left = part == 2 ? (slot + 1) * nkf - k0 : r.kper;
             unsigned long long on = slot < p.S ? every : s_mask[s_act[slot - p.S]];
             for (int kb = k0; kb < k1 && ok; ++kb) {
@@ -702,12 +706,12 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           if (!ok) break;
           i += k1 - k0;
           if (kTC) tc::fence_after_sync();
-          const int li = tile / FB, fb = tile - li * FB, slot = part == 0 ? li : p.S + li;
+          const int li = tile / FB, fb = tile - li * FB, slot = (part == 0 ? 0 : slot1) + li;
           if (part < 2 && k0 == 0 && ct < 64) {  // the tokens of this expert and their weights
             float w = 1.0f;
             int use = row < p.T;
-            if (part == 1) {
-              const int e = s_act[li];
+            if (slot >= p.S) {
+              const int e = s_act[slot - p.S];
               use = (int)((s_mask[e] >> row) & 1);
 #pragma unroll 1
               for (int k = 0; k < p.K && use; ++k)
