@@ -56,6 +56,21 @@ constexpr size_t i8_smem() {
          4 * (128 * kXchPitch + NT) + 8 * (2 * (C::kW + C::kB + C::kOp) + 5) + 16 + 4 * kMaxGroupTab;
 }
 
+// What the product's fp16 rows [rows, KD] and their scales are made from: token rows (xq,
+// read through map) or fp32 hidden rows with their largest magnitudes (h, row_max).
+struct RowSource {
+  const int8_t* xq;
+  const float* xs;
+  const int32_t* map;       // nullable
+  const float* h;           // nullable
+  const uint32_t* row_max;
+  uint4* out;
+  float* out_s;
+  int rows, TK, n_src;
+};
+
+// Kept small: with another 110 bytes of parameters beside the five tensor maps consecutive
+// calls no longer overlapped (a decode batch's product 188 -> 202 us).
 struct I8Args {
   const int32_t* expert_off;
   const float* xs;          // scale of each row of the operand (routed rows, then shared)
@@ -69,7 +84,7 @@ struct I8Args {
 };
 
 struct I8Tile {
-  int g, n0, r0, rows;      // group, first channel, first row of the tile in its group, rows left
+  int g, n0, r0, rows;      // group, first channel, first row of the tile in its group, rows
   int brow;                 // first operand row
   long long orow;           // first output row
   bool shared;
@@ -107,23 +122,24 @@ __device__ __forceinline__ void group_table(const I8Args& p, int32_t* s_ts, int3
   if (lane == 0) s_ts[p.G] = carry;
 }
 
+// Tile t of this CTA's walk, whose tiles ascend; g: the last one's group. A group's row tiles
+// are equally long, not NT rows and a rest.
 template <bool UP, int NT>
 __device__ __forceinline__ I8Tile decode(const I8Args& p, const int32_t* ts, const int32_t* off,
-                                         int ntile, int t, uint32_t rank) {
-  int lo = 0, hi = p.G - 1;
-  while (lo < hi) {  // largest g whose first tile is <= t (empty groups are skipped)
-    const int mid = (lo + hi + 1) >> 1;
-    if (ts[mid] * ntile <= t) lo = mid; else hi = mid - 1;
-  }
-  const int g = lo, mt = ts[g + 1] - ts[g], local = t - ts[g] * ntile;
+                                         int ntile, int t, uint32_t rank, int& g) {
+  constexpr int kRound = I8Cfg<NT>::kB ? 32 : 16;
+  while (ts[g + 1] * ntile <= t) ++g;
+  const int mt = ts[g + 1] - ts[g], local = t - ts[g] * ntile;
   const int n_tile = local / mt, m_tile = local - n_tile * mt;
   I8Tile r;
   r.g = g;
   r.n0 = (n_tile * (I8Cfg<NT>::kB ? 2 : 1) + (int)rank) * (UP ? 64 : 128);
-  r.r0 = m_tile * NT;
   r.shared = g >= p.E;
   const int j = g - p.E;
-  r.rows = (r.shared ? p.T : off[g + 1] - off[g]) - r.r0;
+  const int rows = r.shared ? p.T : off[g + 1] - off[g];
+  const int step = ((rows + mt - 1) / mt + kRound - 1) & ~(kRound - 1);
+  r.r0 = m_tile * step;
+  r.rows = min(step, rows - r.r0);
   // the up product reads the tokens' own rows for every shared expert
   r.brow = (r.shared ? p.shared_rows + (UP ? 0 : j * p.T) : off[g]) + r.r0;
   r.orow = (r.shared ? (UP ? (long long)p.TK : 0LL) + (long long)j * p.T : (long long)off[g]) + r.r0;
@@ -145,6 +161,79 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
   lo = *reinterpret_cast<const uint32_t*>(&x);
   hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// One row of the product's operand, by a warp. Token rows: row r < TK is xq[map[r]] (or
+// xq[r]), row TK + t the token t (shared experts); rows behind the last segment (`end`)
+// belong to nobody. Hidden rows: s = max |h| / 127, rint(h / s), an integer that fp16 holds;
+// s is 0 for a row that is zero or whose scale would be subnormal, NaN for a row that is not
+// finite.
+__device__ __forceinline__ void make_row(const RowSource& p, int r, int end, int KD, DeviceStatus* st,
+                                         int lane) {
+  if (p.h == nullptr) {
+    if (r >= end && r < p.TK) return;
+    const int src = r >= p.TK ? r - p.TK : p.map ? p.map[r] : r;
+    const bool in = (unsigned)src < (unsigned)p.n_src;
+    if (lane == 0) {
+      if (!in) record_error(st, kStatusData, kBadPerm, r);
+      p.out_s[r] = in ? p.xs[src] : 0.0f;
+    }
+    const int vecs = KD >> 3;  // 8 values: a warp's stores are 512 bytes in a row
+    const uint2* from = reinterpret_cast<const uint2*>(p.xq) + (size_t)src * vecs;
+    uint4* to = p.out + (size_t)r * vecs;
+    for (int v = lane; v < vecs; v += 32 * 8) {  // eight loads ahead of the stores
+      uint2 b[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        b[u] = in && v + 32 * u < vecs ? __ldg(from + v + 32 * u) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        uint4 o;
+        widen4(b[u].x, o.x, o.y);
+        widen4(b[u].y, o.z, o.w);
+        if (v + 32 * u < vecs) to[v + 32 * u] = o;
+      }
+    }
+    return;
+  }
+  const float amax = __uint_as_float(p.row_max[r]);
+  const bool finite = amax <= FLT_MAX;
+  float scale = amax / 127.0f;
+  const bool zero = !finite || scale < FLT_MIN;
+  if (zero) scale = finite ? 0.0f : __int_as_float(0x7fc00000);
+  if (lane == 0) p.out_s[r] = scale;
+  const float inv = zero ? 0.0f : 1.0f / scale;
+  const int vecs = KD >> 2;
+  const float4* in = reinterpret_cast<const float4*>(p.h) + (size_t)r * vecs;
+  uint2* out = reinterpret_cast<uint2*>(p.out) + (size_t)r * vecs;
+  for (int v = lane; v < vecs; v += 32 * 4) {  // 4 values a lane, four loads ahead
+    float4 a[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      a[u] = v + 32 * u < vecs ? __ldcs(in + v + 32 * u) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const __half2 lo = __floats2half2_rn(rintf(a[u].x * inv), rintf(a[u].y * inv));
+      const __half2 hi = __floats2half2_rn(rintf(a[u].z * inv), rintf(a[u].w * inv));
+      if (v + 32 * u < vecs)
+        out[v + 32 * u] = zero ? make_uint2(0u, 0u)
+                               : make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                            *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  }
+}
+
+// The rows, by a kernel of their own. (Made inside the product by spare warps, behind
+// completion counters, 131072 rows of 2048 took 401 us with their product, against 376.) Also
+// clears the maxima of the hidden rows that the product will write.
+__global__ void __launch_bounds__(256)
+i8_rows_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E, int KD,
+               uint32_t* __restrict__ clear, int nclear, DeviceStatus* st) {
+  pdl_wait_and_trigger();
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < nclear; i += gridDim.x * 256) clear[i] = 0u;
+  const int end = p.h ? p.rows : expert_off[E];
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < p.rows; r += gridDim.x * 8)
+    make_row(p, r, end, KD, st, threadIdx.x & 31);
 }
 
 template <bool UP, int NT, typename TO>
@@ -239,8 +328,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     const bool lead = tc::elect_one();
     uint32_t ws = 0, wph = 1, wit = 0;
     bool ok = true;
+    int g = 0;
     for (int t = first; t < total && ok; t += stride) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank, g);
       const int wrow = tl.g * p.N + tl.n0;
       for (int kb = 0; kb < nk; ++kb) {
         ok = tc::mbar_wait_warp(&wempty[ws], wph, abort);
@@ -273,8 +363,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     uint64_t* free = kOwnB ? bempty : aempty;
     uint32_t bs = 0, bph = 1, bit = 0;
     bool ok = true;
+    int g = 0;
     for (int t = first; t < total && ok; t += stride) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank, g);
       // this CTA's rows: all of the tile's, or its half of the MMA's columns
       const int mine = kPair ? tile_n<NT>(tl.rows) / 2 : tl.rows;
       const int box = mine <= 16 ? 16 : mine <= 48 ? 48 : C::kRows;
@@ -316,8 +407,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     const bool lead = tc::elect_one();
     uint32_t bs = 0, bph = 0, as = 0, aph = 0, d = 0, dph = 1;
     bool ok = true, a_in = false, b_in = false;
+    int g = 0;
     for (int t = first; t < total && ok; t += stride) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank, g);
       const uint32_t idesc = tc::instr_desc_f16(kPair ? 256 : 128, tile_n<NT>(tl.rows));
       if (!tc::mbar_wait_warp(&dempty[d], dph, abort)) { ok = false; break; }
       tc::fence_after_sync();
@@ -420,8 +512,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     const int q = warp & 3, row = q * 32 + lane;
     const int fr = row & 63, tq = row >> 6;  // up: this thread's feature and token parity
     uint32_t d = 0, dph = 0;
+    int g = 0;
     for (int t = first; t < total; t += stride) {
-      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank);
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank, g);
       const int nt = min(NT, tl.rows), n32 = (nt + 31) >> 5;
       const int chan = tl.n0 + (UP ? fr : row);  // this thread's channel
       const bool has = chan < p.N;
@@ -429,7 +522,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       for (int i = row; i < NT; i += 128) s_xs[i] = i < nt ? __ldg(p.xs + tl.brow + i) : 0.0f;
       const float sc = has ? __ldg(p.sa + (size_t)tl.g * p.N + chan) : 0.0f;
       const float sc3 = UP && has ? __ldg(p.sb + (size_t)tl.g * p.N + chan) : 0.0f;
-      bool ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
+      const bool ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
       // one outcome for the four warps, which meet at barriers
       uint32_t all;
       asm volatile(
@@ -494,67 +587,6 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   }
 }
 
-// The product's rows in fp16, in dispatched order, with their scales: row r < TK is xq[map[r]]
-// (or xq[r]), row TK + t the token t (shared experts). Also clears the hidden rows' maxima.
-__global__ void __launch_bounds__(256)
-i8_rows_kernel(const uint2* __restrict__ xq, const float* __restrict__ xs,
-               const int32_t* __restrict__ map, const int32_t* __restrict__ expert_off, int E,
-               int TK, int rows, int n_src, int vecs,
-               uint4* __restrict__ out, float* __restrict__ out_s, uint32_t* __restrict__ row_max,
-               int max_rows, DeviceStatus* st) {
-  pdl_wait_and_trigger();
-  const int lane = threadIdx.x & 31;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < max_rows; i += gridDim.x * 256) row_max[i] = 0u;
-  const int end = expert_off[E];  // rows behind the last segment belong to nobody
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
-    if (r >= end && r < TK) continue;
-    const int src = r >= TK ? r - TK : map ? map[r] : r;
-    const bool in = (unsigned)src < (unsigned)n_src;
-    if (lane == 0) {
-      if (!in) record_error(st, kStatusData, kBadPerm, r);
-      out_s[r] = in ? xs[src] : 0.0f;
-    }
-    const uint2* from = xq + (size_t)src * vecs;
-    uint4* to = out + (size_t)r * vecs;
-#pragma unroll 4
-    for (int v = lane; v < vecs; v += 32) {  // 8 values: a warp's stores are 512 bytes in a row
-      const uint2 b = in ? __ldg(from + v) : make_uint2(0u, 0u);
-      uint4 o;
-      widen4(b.x, o.x, o.y);
-      widen4(b.y, o.z, o.w);
-      to[v] = o;
-    }
-  }
-}
-
-// Hidden rows requantised: s = max |h| / 127, rint(h / s) as fp16 (an integer, exact). s is 0
-// for a row that is zero or whose scale would be subnormal, NaN for a row that is not finite.
-__global__ void __launch_bounds__(256)
-i8_quantise_rows_kernel(const float* __restrict__ h, const uint32_t* __restrict__ row_max,
-                        uint2* __restrict__ q, float* __restrict__ s, int rows, int vecs) {
-  pdl_wait_and_trigger();
-  const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
-    const float amax = __uint_as_float(row_max[r]);
-    const bool finite = amax <= FLT_MAX;
-    float scale = amax / 127.0f;
-    const bool zero = !finite || scale < FLT_MIN;
-    if (zero) scale = finite ? 0.0f : __int_as_float(0x7fc00000);
-    if (lane == 0) s[r] = scale;
-    const float inv = zero ? 0.0f : 1.0f / scale;
-    const float4* in = reinterpret_cast<const float4*>(h) + (size_t)r * vecs;
-    uint2* out = q + (size_t)r * vecs;
-#pragma unroll 4
-    for (int v = lane; v < vecs; v += 32) {  // 4 values
-      const float4 a = __ldcs(in + v);
-      const __half2 lo = __floats2half2_rn(rintf(a.x * inv), rintf(a.y * inv));
-      const __half2 hi = __floats2half2_rn(rintf(a.z * inv), rintf(a.w * inv));
-      out[v] = zero ? make_uint2(0u, 0u)
-                    : make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    }
-  }
-}
-
 // A tile of NT = 192 rows reads a weight byte once per 192 rows and needs experts that fill
 // it; below, the weights' stream is the work, and 64-row tiles keep more of it in flight.
 constexpr int kWideRows = 96;
@@ -607,13 +639,10 @@ cudaError_t run_product(const smoe_desc& d, const I8Args& p, const int8_t* wa, c
   return run_gemm<UP, 64, TO>(p, wa, wb, x16, xrows, s);
 }
 
-cudaError_t run_rows(const int8_t* xq, const float* xs, const int32_t* map, const int32_t* expert_off,
-                     int E, int TK, int rows, int n_src, int n_in, void* x16, float* x16_s, uint32_t* row_max, int max_rows,
-                     DeviceStatus* st, cudaStream_t s) {
-  const int grid = std::max(1, std::min(std::max(ceil_div(rows, 8), ceil_div(max_rows, 256)), 152 * 8));
-  SMOE_LAUNCH(i8_rows_kernel, grid, 256, 0, s, reinterpret_cast<const uint2*>(xq), xs, map,
-              expert_off, E, TK, rows,
-              n_src, n_in / 8, static_cast<uint4*>(x16), x16_s, row_max, max_rows, st);
+cudaError_t run_rows(const RowSource& r, const int32_t* expert_off, int E, int KD, uint32_t* clear,
+                     int nclear, DeviceStatus* st, cudaStream_t s) {
+  const int grid = std::max(1, std::min(std::max(ceil_div(r.rows, 8), ceil_div(nclear, 256)), 152 * 8));
+  SMOE_LAUNCH(i8_rows_kernel, grid, 256, 0, s, r, expert_off, E, KD, clear, nclear, st);
   return cudaGetLastError();
 }
 
@@ -632,9 +661,9 @@ void i8_ws_layout(const smoe_desc& d, I8Layout* L) {
   L->x16 = take(xrows * std::max(d.d, d.F) * 2);
   L->x16_s = take(xrows * 4);
   L->h = take(rows * d.F * 4);
-  L->row_max = take(rows * 4);
   L->h16 = take(rows * d.F * 2);
   L->h16_s = take(rows * 4);
+  L->row_max = take(rows * 4);
   L->total = off;
 }
 
@@ -646,10 +675,10 @@ cudaError_t launch_expert_matmul_i8(const smoe_desc& d, int n_out, int n_in, con
   i8_ws_layout(d, &L);
   DeviceStatus* st = ws_ptr<DeviceStatus>(ws, L.status);
   const int TK = d.T * d.K;
-  void* x16 = ws_ptr<char>(ws, L.x16);
+  uint4* x16 = ws_ptr<uint4>(ws, L.x16);
   float* x16_s = ws_ptr<float>(ws, L.x16_s);
-  cudaError_t e = run_rows(xq, xs, row_src, expert_off, d.E, TK, TK, row_src ? d.T : TK, n_in, x16, x16_s, nullptr, 0,
-                           st, s);
+  const RowSource r{xq, xs, row_src, nullptr, nullptr, x16, x16_s, TK, TK, row_src ? d.T : TK};
+  cudaError_t e = run_rows(r, expert_off, d.E, n_in, nullptr, 0, st, s);
   if (e != cudaSuccess) return e;
   const I8Args p{expert_off, x16_s, ws_n, nullptr, out, nullptr, nullptr, st,
                  d.E, d.E, d.T, TK, n_out, n_in, TK};
@@ -666,19 +695,20 @@ cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const flo
   DeviceStatus* st = ws_ptr<DeviceStatus>(ws, L.status);
   const int TK = d.T * d.K, G = d.E + d.n_shared, rows = TK + d.n_shared * d.T;
   const int xrows = TK + (d.n_shared ? d.T : 0);
-  void *x16 = ws_ptr<char>(ws, L.x16), *h16 = ws_ptr<char>(ws, L.h16);
+  uint4 *x16 = ws_ptr<uint4>(ws, L.x16), *h16 = ws_ptr<uint4>(ws, L.h16);
   float *x16_s = ws_ptr<float>(ws, L.x16_s), *h = ws_ptr<float>(ws, L.h);
   float* h16_s = ws_ptr<float>(ws, L.h16_s);
   uint32_t* row_max = ws_ptr<uint32_t>(ws, L.row_max);
-  cudaError_t e = run_rows(xq, xs, row_src, expert_off, d.E, TK, xrows, row_src ? d.T : TK, d.d, x16, x16_s, row_max,
-                           rows, st, s);
+  const RowSource rx{xq, xs, row_src, nullptr, nullptr, x16, x16_s, xrows, TK, row_src ? d.T : TK};
+  const RowSource rh{nullptr, nullptr, nullptr, h, row_max, h16, h16_s, rows, TK, 0};
+  cudaError_t e = run_rows(rx, expert_off, d.E, d.d, row_max, rows, st, s);
   if (e != cudaSuccess) return e;
   const I8Args up{expert_off, x16_s, W.s1, W.s3, h, nullptr, row_max, st,
                   d.E, G, d.T, TK, d.F, d.d, TK};
   e = run_product<true, float>(d, up, W.w1, W.w3, x16, xrows, s);
   if (e != cudaSuccess) return e;
-  SMOE_LAUNCH(i8_quantise_rows_kernel, std::min(ceil_div(rows, 8), 152 * 8), 256, 0, s, h, row_max,
-              static_cast<uint2*>(h16), h16_s, rows, d.F / 4);
+  e = run_rows(rh, expert_off, d.E, d.F, nullptr, 0, st, s);
+  if (e != cudaSuccess) return e;
   const I8Args dn{expert_off, h16_s, W.s2, nullptr, y_disp, y_sh, nullptr, st,
                   d.E, G, d.T, TK, d.d, d.F, TK};
   return d.dtype == SMOE_F32 ? run_product<false, float>(d, dn, W.w2, nullptr, h16, rows, s)
