@@ -432,7 +432,9 @@ SMOE_API size_t smoe_few_workspace_size(const smoe_desc* desc);
  * expert's weights are read once. T <= 64, else SMOE_ERR_SHAPE.
  * Products accumulate in fp32; w_tk silu(W1 x) (W3 x) is rounded once to dtype before the
  * down product, whose sum over the experts stays in fp32 until y. fp32 layers multiply in
- * fp32 (not tf32). The result does not depend on timing.
+ * fp32 (not tf32). The result does not depend on timing. A token's products stay apart from
+ * the other tokens', but the weights of W2 have to be finite: one that is not reaches every
+ * token of the call.
  *   x [T, d] dtype; w_gate [E, d] dtype; w1, w3 [E+n_shared, F, d], w2 [E+n_shared, d, F]
  *   dtype; y [T, d] dtype (may be the same buffer as x)
  *   logits nullable [T, E] fp32; topk_idx nullable [T, K] int32, topk_w nullable [T, K]

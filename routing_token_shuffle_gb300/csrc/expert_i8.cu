@@ -15,11 +15,16 @@
 // fastest so that neighbours share the weights through L2:
 //   warp 0      TMA: weight bytes (128 channels x 128)
 //   warp 3      TMA: fp16 rows (NT rows x 128)
-//   warps 8-15  widen a weight stage into one of four TMEM operand stages
-//   warp 1      tcgen05.mma, M = 128 channels, N = the tile's rows rounded up to 16
+//   warps 8-15  widen a weight stage into a TMEM operand stage
+//   warp 1      tcgen05.mma, M = 128 channels (256 on a pair of CTAs), N = the tile's rows
 //   warps 4-7   epilogue: scales, SwiGLU, stores (up: fp32 hidden rows and their largest
 //               magnitude, by an integer atomicMax, whose result has no order)
 // The up product's A tile is 64 channels of W1 and the same 64 of W3.
+//
+// Measured: 384 rows over 160 experts of 5120 x 1536 188 us (6.1 TB/s of weights); 131072 rows
+// of 2048 over 128 experts of 768 channels 376 us with their widening (110 us of it), the
+// product itself at 1.5 PFLOP/s of fp16; the FFN of 8192 tokens (6 of 160 experts and two
+// shared ones, 5120 x 1536) 2.54 ms, 1.22 PFLOP/s.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -42,9 +47,9 @@ constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 //     bottleneck (1190 clocks a stage, against 780 at the HBM rate).
 // 192: batches whose experts fill it, on pairs of CTAs (a cluster on the two SMs of a TPC):
 //     256 channels, each CTA widening its own 128, and half of the rows in each CTA's
-//     shared memory, in a ring of their own. One CTA alone moves 155
-//     bytes a clock through shared memory at the MMAs' rate (rows written and read, weight
-//     bytes written and read), the pair 97; the limit is 128.
+//     shared memory, in a ring of their own. One CTA alone moves 155 bytes a clock through
+//     shared memory at the MMAs' rate (rows written and read, weight bytes written and
+//     read), the pair 97; the limit is 128.
 template <int NT> struct I8Cfg;
 template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0, kRows = 64; };
 template <> struct I8Cfg<192> { static constexpr int kW = 6, kOp = 2, kB = 4, kRows = 96; };
@@ -587,9 +592,12 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   }
 }
 
-// A tile of NT = 192 rows reads a weight byte once per 192 rows and needs experts that fill
-// it; below, the weights' stream is the work, and 64-row tiles keep more of it in flight.
-constexpr int kWideRows = 96;
+// From this many rows per expert on average the wide tiles win: they read a weight byte once
+// per 192 rows and issue fewer MMAs for them; below, the weights' stream is the work, and the
+// narrow tiles keep more of it in flight. Measured (FFN, 160 experts of 5120 x 1536): 32 rows
+// 651 us narrow and 686 wide, 64 rows 845 and 736; 8 experts of 4096 x 14336: 279 and 292,
+// 368 and 325; 128 experts of 2048 x 768: 143 and 143, 189 and 182.
+constexpr int kWideRows = 40;
 
 int i8_sm_count() {
   int dev = 0, n = 0;

@@ -3,10 +3,10 @@
 //
 // At these batches the layer is the stream of the touched experts' weights from HBM
 // (3 F d b bytes each), so the kernel is built around that stream: one persistent CTA per
-// SM, launched cooperatively, whose producer thread keeps a ring of TMA loads in flight
+// SM, launched cooperatively, whose producer warp keeps a ring of TMA loads in flight
 // across the phases, and two grid-wide barriers where a phase needs every SM's results:
 //   gate      logits = x W_g^T, spread over the SMs          -- barrier 1 --
-//   routes    every CTA selects all T tokens' experts itself from the T x E logits
+//   routes    every CTA selects the T tokens' experts from the T x E logits (see kSelectAll)
 //   up        H[slot][t] = w_{t,e} silu(W1 x_t) (W3 x_t), 0 where t is not routed to the
 //             slot's expert e (slots: the shared experts, then the touched routed ones)
 //   down      y_t = sum over slots of W2_e H[slot][t]        -- barrier 2 before it --
@@ -17,6 +17,9 @@
 // the selection run. The W2 tiles at the head of a CTA's down range do not wait for barrier
 // 2: they are loaded into the free stages before it.
 //
+// (Zeros for the tokens of other experts also mean that a weight of W2 that is not finite
+// reaches every token of the call.)
+//
 // Work is split evenly: the 128-row x 128-byte weight blocks of a phase, taken in order,
 // are cut into one contiguous range per CTA, whatever the tile borders. A tile whose blocks
 // lie in several ranges is finished by the CTA that holds its first block: the others
@@ -26,6 +29,12 @@
 //
 // An A tile is 128 weight rows (up: 64 rows of W1 and the same 64 of W3), the B tile is all
 // T tokens padded to NP rows; fp32 accumulation. Every wait is bounded (see tc_common.cuh).
+//
+// Measured: bf16, 64 tokens of a 160-expert layer of 5120 x 1536 with two shared experts 1.03
+// ms (6.4 TB/s of the touched weights, 0.96 of the measured copy rate), 3 tokens of 8 experts
+// of 4096 x 14336 242 us (6 TB/s), one token of 128 experts of 2048 x 768 30 us (75 MB: 11 us
+// of stream, 7 us until the routes are known, two barriers and the joining of sums). fp32, 13
+// tokens of 24 experts of 1000 x 1416 108 us: FMAs and shared memory, not HBM (53 us).
 #include <algorithm>
 #include <climits>
 
@@ -169,7 +178,7 @@ __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s,
 template <typename TE>
 __device__ __forceinline__ void gate_logits(const FewArgs& p, float* red, int gt) {
   constexpr int V = Elem<TE>::kPerVec16;
-  const int lane = gt & 31, gw = gt >> 5;
+  const int lane = gt & 31;
   const int nv = p.d / V, groups = (p.T + 7) / 8;
   const uint4* x = static_cast<const uint4*>(p.x);
   const uint4* w = static_cast<const uint4*>(p.w_gate);
@@ -211,7 +220,6 @@ __device__ __forceinline__ void gate_logits(const FewArgs& p, float* red, int gt
       for (int k = 0; k < kGateThreads / 32; ++k) sum += red[k * 32 + lane];
       p.logits[(size_t)(t0 + (lane >> 2)) * p.E + e0 + (lane & 3)] = sum;
     }
-    (void)gw;
   }
 }
 

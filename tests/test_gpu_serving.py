@@ -310,6 +310,20 @@ def test_moe_few_graphs_share_a_workspace_and_streams():
         a.check()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_moe_few_reads_nothing_of_an_old_workspace(dt):
+    """Only a workspace's first 256 bytes have to be zero; one buffer serves several shapes."""
+    big = Few(40, 640, 48, 4, 1, 320, 1, dt)
+    ws = torch.full((2 * big.ws.numel(),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    small = Few(2, 320, 8, 2, 2, 96, 0, dt)
+    for c in (big, small, big):
+        c.ws = ws
+        c.run()
+        c.check()
+        assert (ws[:256] == 0).all()  # as it was, for the next call
+
+
 def test_moe_few_two_streams_at_once():
     """Two calls with their own workspaces on two streams."""
     cs = [Few(3 + i, 768, 16, 2, 1, 384, i, "bf16", seed=i) for i in range(2)]
@@ -359,6 +373,7 @@ MM = [
     (1, 1, 1, 16, 8), (1, 6, 40, 5120, 1536), (2, 2, 8, 64, 8), (3, 1, 2, 48, 72),
     (64, 6, 160, 1024, 264), (100, 8, 16, 2048, 768), (257, 2, 5, 272, 136), (7, 2, 3, 4096, 1032),
     (1000, 4, 8, 512, 640), (2000, 2, 4, 128, 256), (130, 1, 1, 1040, 3000), (513, 3, 31, 96, 200),
+    (39, 1, 1, 80, 24), (40, 1, 1, 80, 24), (193, 1, 1, 208, 520), (385, 1, 1, 64, 8),
 ]
 
 
@@ -420,6 +435,65 @@ def test_expert_matmul_i8_leaves_other_rows():
     assert (out[90:] == 7.0).all()
     ref, _ = matmul_ref(xq, xs, src, off, wq, sw)
     assert ((out[:90].double() - ref[:90]).abs() <= 2.1 * HALF["f32"] * ref[:90].abs()).all()
+
+
+def test_expert_matmul_i8_padded_batch():
+    """Rows behind the last segment may name no token: they are neither read nor written."""
+    g = gen(9)
+    T, K, E, n_in, n_out = 64, 2, 3, 192, 264
+    xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
+    src, off = rows_of(T // 2, K, E, 4)
+    src = torch.cat([src, torch.full((T * K - len(src),), -1, dtype=torch.int32, device="cuda")])
+    xs, sw = torch.rand(T, generator=g, device="cuda"), torch.rand(E, n_out, generator=g, device="cuda")
+    desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, "f32")
+    ws = smoe.workspace_i8(desc)
+    ws[256:] = 0xFF
+    out = torch.full((T * K, n_out), 7.0, device="cuda")
+    smoe.smoe_expert_matmul_i8(desc, xq, xs, off, wq, sw, out, ws, row_src=src)
+    smoe.smoe_get_status(ws)
+    n = int(off[-1])
+    ref, _ = matmul_ref(xq, xs, src[:n], off, wq, sw)
+    assert ((out[:n].double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
+    assert (out[n:] == 7.0).all()
+
+
+def test_expert_matmul_i8_scales_that_are_not_finite():
+    """A NaN channel scale gives NaN in that channel of that expert, a NaN row scale in that
+    token's rows, nowhere else."""
+    g = gen(10)
+    T, K, E, n_in, n_out = 50, 2, 2, 128, 136
+    xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
+    src, off = rows_of(T, K, E, 5)
+    xs, sw = torch.rand(T, generator=g, device="cuda"), torch.rand(E, n_out, generator=g, device="cuda")
+    xs[11], sw[1, 77] = math.nan, math.nan
+    desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, "bf16")
+    ws, out = smoe.workspace_i8(desc), torch.empty(T * K, n_out, dtype=torch.bfloat16, device="cuda")
+    smoe.smoe_expert_matmul_i8(desc, xq, xs, off, wq, sw, out, ws, row_src=src)
+    want = torch.zeros(T * K, n_out, dtype=torch.bool, device="cuda")
+    want[src == 11] = True
+    want[int(off[1]):, 77] = True
+    assert torch.equal(out.isnan(), want)
+
+
+def test_expert_matmul_i8_two_streams_at_once():
+    g = gen(11)
+    cs = []
+    for i in range(2):
+        T, K, E, n_in, n_out = 300 + 7 * i, 2, 4, 512, 264
+        xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
+        src, off = rows_of(T, K, E, i)
+        xs, sw = torch.rand(T, generator=g, device="cuda"), torch.rand(E, n_out, generator=g, device="cuda")
+        desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, "f32")
+        cs.append((desc, xq, xs, src, off, wq, sw, smoe.workspace_i8(desc), torch.empty(T * K, n_out, device="cuda"),
+                   torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for desc, xq, xs, src, off, wq, sw, ws, out, stream in cs:
+            smoe.smoe_expert_matmul_i8(desc, xq, xs, off, wq, sw, out, ws, row_src=src, stream=stream)
+    torch.cuda.synchronize()
+    for desc, xq, xs, src, off, wq, sw, ws, out, _ in cs:
+        ref, _ = matmul_ref(xq, xs, src, off, wq, sw)
+        assert ((out.double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
 
 
 def test_expert_matmul_i8_reports_bad_rows():
@@ -502,7 +576,7 @@ FFN = [
     # T, d, E, K, F, S
     (1, 16, 1, 1, 16, 0), (1, 512, 8, 2, 768, 0), (5, 1024, 40, 6, 512, 2), (64, 640, 160, 6, 96, 2),
     (33, 272, 4, 3, 144, 1), (500, 256, 8, 2, 1040, 0), (300, 2048, 16, 8, 768, 0),
-    (1000, 512, 4, 2, 256, 1),
+    (1000, 512, 4, 2, 256, 1), (193, 64, 1, 1, 48, 1), (65, 32, 2, 1, 16, 8),
 ]
 
 
