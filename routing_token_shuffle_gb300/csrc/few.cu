@@ -307,9 +307,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   constexpr uint32_t kB = NP * 128;
   constexpr bool kTC = sizeof(TE) == 2;            // bf16: tcgen05; fp32: FMAs on the CUDA cores
   constexpr uint32_t kCols = 2 * NP;               // TMEM: two accumulators of NP columns
-  // Consumer threads: 4 warps read the accumulators (bf16), 8 warps multiply (fp32). Each of
-  // those takes all 128 rows of a block, four to a lane, 16 tokens and a share of the
-  // contraction: shared memory returns 128 bytes a clock, broadcast or not, so a token's
+  // Consumer threads: 4 warps read the accumulators (bf16), 8 warps multiply (fp32): two
+  // groups of four, which take every other block. A warp takes all 128 rows of its block, four
+  // to a lane, 16 tokens and a share of the contraction: shared memory returns 128 bytes a clock, broadcast or not, so a token's
   // values have to serve four rows (one row a lane and all tokens: 512 clocks of shared
   // memory for every four tokens of a block, against 712 that its load from HBM takes; now
   // 128).
@@ -346,7 +346,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], kTC ? 1 : kCons / 32);
+      tc::mbar_init(&empty[s], kTC ? 1 : kCons / 64);
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&tfull[a], 1);
@@ -674,15 +674,19 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
                 left = nkf - 1;
                 on = slot < p.S ? every : s_mask[s_act[slot - p.S]];
               }
+              if (((kb - k0) & 1) != ks / (kKSplit / 2)) {  // the other group's block
+                if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
+                continue;
+              }
               ok = tc::mbar_wait_warp(&full[s], ph, abort);
               if (!ok) break;
               const uint8_t* a = sA + s * kFewA + lane * 128;
               const uint8_t* b = sB + s * kB + tq * 16 * 128;
               const uint32_t on16 = (uint32_t)(on >> (16 * tq)) & 0xffffu;
 #pragma unroll
-              for (int cc = 0; cc < (kTC ? 0 : 8 / kKSplit); ++cc) {
+              for (int cc = 0; cc < (kTC ? 0 : 16 / kKSplit); ++cc) {
                 if (on16 == 0) break;
-                const int c = ks * (8 / kKSplit) + cc;
+                const int c = ks % (kKSplit / 2) * (16 / kKSplit) + cc;
                 float4 av[4];
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4)
