@@ -14,7 +14,8 @@
 // One persistent CTA per SM walks the tiles (group, 128-channel tile, row tile), row tiles
 // fastest so that neighbours share the weights through L2:
 //   warp 0      TMA: weight bytes (128 channels x 128)
-//   warp 3      TMA: fp16 rows (NT rows x 128)
+//   warp 3      TMA: fp16 rows (NT rows x 128); or three warps gather them with 16-byte
+//               asynchronous copies (see kGatherChannels) and warp 2 hands them over
 //   warps 8-15  widen a weight stage into a TMEM operand stage
 //   warp 1      tcgen05.mma, M = 128 channels (256 on a pair of CTAs), N = the tile's rows
 //   warps 4-7   epilogue: scales, SwiGLU, stores (up: fp32 hidden rows and their largest
@@ -22,8 +23,7 @@
 // The up product's A tile is 64 channels of W1 and the same 64 of W3.
 //
 // Measured: 384 rows over 160 experts of 5120 x 1536 188 us (6.1 TB/s of weights); 131072 rows
-// of 2048 over 128 experts of 768 channels 376 us with their widening (110 us of it), the
-// product itself at 1.5 PFLOP/s of fp16; the FFN of 8192 tokens (6 of 160 experts and two
+// of 2048 over 128 experts of 768 channels 328 us, 1.26 PFLOP/s of fp16; the FFN of 8192 tokens (6 of 160 experts and two
 // shared ones, 5120 x 1536) 2.54 ms, 1.22 PFLOP/s.
 #include <algorithm>
 #include <cfloat>
@@ -35,6 +35,7 @@ namespace smoe {
 namespace {
 
 constexpr int kI8Threads = 512;
+constexpr int kCopyWarps = 3;        // that gather rows: warp 3 and two more
 constexpr int kStageW = 128 * 128;   // weight stage: 128 channels x 128 bytes
 constexpr int kXchPitch = 33;
 constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
@@ -58,7 +59,7 @@ template <int NT>
 constexpr size_t i8_smem() {
   using C = I8Cfg<NT>;
   return 1024 + (size_t)C::kW * kStageW + (size_t)2 * (C::kB ? C::kB : C::kOp) * C::kRows * 128 +
-         4 * (128 * kXchPitch + NT) + 8 * (2 * (C::kW + C::kB + C::kOp) + 5) + 16 + 4 * kMaxGroupTab;
+         4 * (128 * kXchPitch + NT) + 8 * (2 * (C::kW + C::kB + C::kOp) + C::kB + 5) + 16 + 4 * (kMaxGroupTab + C::kRows);
 }
 
 // What the product's fp16 rows [rows, KD] and their scales are made from: token rows (xq,
@@ -86,6 +87,10 @@ struct I8Args {
   DeviceStatus* st;
   int E, G, T, TK, N, KD;
   int shared_rows;          // first operand row of shared expert j: TK + (down ? j T : 0)
+  // pairs, token rows: the fp16 tokens [T + 1, KD], the last one zero, and the token of each
+  // dispatched row (NULL: the operand's rows are in place)
+  const char* tok;
+  const int32_t* row_tok;
 };
 
 struct I8Tile {
@@ -228,9 +233,40 @@ __device__ __forceinline__ void make_row(const RowSource& p, int r, int end, int
   }
 }
 
-// The rows, by a kernel of their own. (Made inside the product by spare warps, behind
-// completion counters, 131072 rows of 2048 took 401 us with their product, against 376.) Also
-// clears the maxima of the hidden rows that the product will write.
+// For gathered rows: the tokens in fp16 and a zero row behind them, with their scales, and the
+// token of each dispatched row, the zero row where it is out of range. Also clears the maxima
+// of the hidden rows that the product will write.
+__global__ void __launch_bounds__(256)
+i8_tokens_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E, int KD,
+                 int32_t* __restrict__ row_tok, uint32_t* __restrict__ clear, int nclear,
+                 DeviceStatus* st) {
+  pdl_wait_and_trigger();
+  const int end = expert_off[E], T = p.n_src;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < max(nclear, p.TK); i += gridDim.x * 256) {
+    if (i < nclear) clear[i] = 0u;
+    if (i < p.TK) {
+      const int t = i < end ? p.map[i] : T;
+      const bool in = (unsigned)t < (unsigned)T;
+      if (!in && i < end) record_error(st, kStatusData, kBadPerm, i);
+      row_tok[i] = in ? t : T;
+    }
+  }
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r <= T; r += gridDim.x * 8) {
+    if (r < T) {
+      RowSource one = p;
+      one.map = nullptr;
+      make_row(one, r, T, KD, st, lane);
+    } else {
+      for (int v = lane; v < KD / 8; v += 32) p.out[(size_t)T * (KD / 8) + v] = make_uint4(0, 0, 0, 0);
+      if (lane == 0) p.out_s[T] = 0.0f;
+    }
+  }
+}
+
+// The rows put in place, by a kernel of their own. (Made inside the product by spare warps,
+// behind completion counters, 131072 rows of 2048 took 401 us with their product, against
+// 376.) Also clears the maxima of the hidden rows that the product will write.
 __global__ void __launch_bounds__(256)
 i8_rows_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E, int KD,
                uint32_t* __restrict__ clear, int nclear, DeviceStatus* st) {
@@ -241,8 +277,9 @@ i8_rows_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E,
     make_row(p, r, end, KD, st, threadIdx.x & 31);
 }
 
-template <bool UP, int NT, typename TO>
-__global__ void __launch_bounds__(kI8Threads, 1)
+// GATHER (pairs): the token rows are gathered by the product itself.
+template <bool UP, int NT, typename TO, bool GATHER>
+__global__ void __launch_bounds__(GATHER ? kI8Threads + 32 * (kCopyWarps - 1) : kI8Threads, 1)
 i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit pairs; up: 64-row box
                const __grid_constant__ CUtensorMap tmWb,   // (W3), else 128-row box
                const __grid_constant__ CUtensorMap tmX16,  // fp16 rows, boxes of 16, 48 and kRows
@@ -271,12 +308,14 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   uint64_t* dfull = aempty + C::kOp;
   uint64_t* dempty = dfull + 2;
   uint64_t* drain = dempty + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* rfull = drain + 1;  // pairs: this CTA's gathered rows of a stage
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(rfull + C::kB);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
   float* s_xch = reinterpret_cast<float*>(s_abort + 1);  // [128][33]
   float* s_xs = s_xch + 128 * kXchPitch;                 // [NT] row scales of the tile
   int32_t* s_ts = reinterpret_cast<int32_t*>(s_xs + NT);
   int32_t* s_off = s_ts + kMaxGroups + 2;
+  int32_t* s_row = s_off + kMaxGroups + 2;               // pairs: the tokens of this CTA's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? tc::cluster_rank() : 0u;
@@ -287,8 +326,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       tc::mbar_init(&wempty[s], 8);
     }
     for (int s = 0; s < C::kB; ++s) {
-      tc::mbar_init(&bfull[s], 1);
+      tc::mbar_init(&bfull[s], GATHER ? 2 : 1);  // both CTAs' gathered rows, or the copies' bytes
       tc::mbar_init(&bempty[s], 1);
+      tc::mbar_init(&rfull[s], 32 * kCopyWarps);
     }
     for (int s = 0; s < C::kOp; ++s) {
       tc::mbar_init(&afull[s], kPair ? 16 : 9);  // both CTAs' widening warps; or with the rows' copy
@@ -359,8 +399,73 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
     }
     __syncwarp();
+  } else if (GATHER && (warp >= 16 || warp == 3)) {
+    // ---------------------------------------------------------------- row producer: gather
+    // Two rows of 256 bytes (128 values) an instruction, into the two 128-byte-swizzled
+    // halves of the stage.
+    // The copying warps take groups of 16 rows in turn (six of them for 192 MMA columns).
+    pdl_wait();
+    const int cw = warp == 3 ? 0 : warp - 15;
+    uint32_t bs = 0, bph = 1;
+    bool ok = true;
+    int g = 0;
+    const int c = lane & 15;
+    const uint32_t half = (uint32_t)(c >> 3) * kHalf;
+    for (int t = first; t < total && ok; t += stride) {
+      const I8Tile tl = decode<UP, NT>(p, s_ts, s_off, ntile, t, rank, g);
+      const int mine = tile_n<NT>(tl.rows) / 2;  // a multiple of 16
+      __syncwarp();
+      for (int i = 16 * cw + lane; i < mine && lane < 16; i += 16 * kCopyWarps) {
+        const int r = (int)rank * mine + i;  // row of the tile
+        s_row[i] = r >= tl.rows ? p.T : tl.shared ? tl.r0 + r : __ldg(p.row_tok + tl.brow + r);
+      }
+      __syncwarp();
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = tc::mbar_wait_warp(&bempty[bs], bph, abort);
+        if (!ok) break;
+        const uint32_t dst = tc::smem_u32(sB + 2 * bs * kHalf) + half;
+        const int left = p.KD * 2 - kb * 256 - c * 16;
+        const uint32_t valid = left > 0 ? 16u : 0u;
+        const char* src = p.tok + (left > 0 ? kb * 256 + c * 16 : 0);
+        for (int i0 = 16 * cw + (lane >> 4); i0 < mine; i0 += 16 * kCopyWarps) {
+          const char* from[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) from[u] = src + (size_t)s_row[i0 + 2 * u] * (2 * p.KD);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            tc::cp_async16(dst + (i0 + 2 * u) * 128 + (((c & 7) ^ ((i0 + 2 * u) & 7)) << 4), from[u], valid);
+        }
+        tc::cp_async_arrive(&rfull[bs]);
+        if (++bs == C::kB) { bs = 0; bph ^= 1u; }
+      }
+    }
+    tc::cp_async_wait_all();
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+    __syncwarp();
+  } else if (GATHER && warp == 2) {
+    // ---------------------------------------------------------------- gathered rows' signal
+    // The copies wrote through the generic proxy, the MMA reads through the async proxy.
+    const int stages = total > first ? (total - first + stride - 1) / stride * nk : 0;
+    uint32_t bs = 0, ph = 0;
+    bool ok = true;
+    for (int i = 0; i < stages; ++i) {
+      ok = tc::mbar_wait_warp(&rfull[bs], ph, abort);
+      if (!ok) break;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_remote(tc::cluster_addr(&bfull[bs], 0));
+      if (++bs == C::kB) { bs = 0; ph ^= 1u; }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+    __syncwarp();
   } else if (warp == 3) {
-    // ---------------------------------------------------------------- row producer
+    // ---------------------------------------------------------------- row producer: in place
     pdl_wait();
     const bool lead = tc::elect_one();
     constexpr uint32_t kRing = kOwnB ? C::kB : C::kOp;
@@ -524,7 +629,11 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       const int chan = tl.n0 + (UP ? fr : row);  // this thread's channel
       const bool has = chan < p.N;
       // the tile's scales, ahead of its accumulator
-      for (int i = row; i < NT; i += 128) s_xs[i] = i < nt ? __ldg(p.xs + tl.brow + i) : 0.0f;
+      for (int i = row; i < NT; i += 128) {
+        int r = tl.brow + i;
+        if (GATHER && i < nt) r = tl.shared ? tl.r0 + i : __ldg(p.row_tok + r);
+        s_xs[i] = i < nt ? __ldg(p.xs + r) : 0.0f;
+      }
       const float sc = has ? __ldg(p.sa + (size_t)tl.g * p.N + chan) : 0.0f;
       const float sc3 = UP && has ? __ldg(p.sb + (size_t)tl.g * p.N + chan) : 0.0f;
       const bool ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
@@ -598,6 +707,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
 // 651 us narrow and 686 wide, 64 rows 845 and 736; 8 experts of 4096 x 14336: 279 and 292,
 // 368 and 325; 128 experts of 2048 x 768: 143 and 143, 189 and 182.
 constexpr int kWideRows = 40;
+bool wide(const smoe_desc& d) { return (long long)d.T * d.K >= (long long)kWideRows * d.E; }
 
 int i8_sm_count() {
   int dev = 0, n = 0;
@@ -606,7 +716,7 @@ int i8_sm_count() {
   return n > 0 ? n : 148;
 }
 
-template <bool UP, int NT, typename TO>
+template <bool UP, int NT, typename TO, bool GATHER = false>
 cudaError_t run_gemm(const I8Args& p, const int8_t* wa, const int8_t* wb, const void* x16,
                      long long xrows, cudaStream_t s) {
   alignas(64) CUtensorMap ta, tb, x1, x4, xn;
@@ -617,7 +727,7 @@ cudaError_t run_gemm(const I8Args& p, const int8_t* wa, const int8_t* wb, const 
       !encode_tmap_2d(&x4, x16, false, xrows, p.KD, 48, 64) ||
       !encode_tmap_2d(&xn, x16, false, xrows, p.KD, I8Cfg<NT>::kRows, 64))
     return cudaErrorInvalidValue;
-  auto kern = i8_gemm_kernel<UP, NT, TO>;
+  auto kern = i8_gemm_kernel<UP, NT, TO, GATHER>;
   const int smem = (int)i8_smem<NT>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -630,7 +740,7 @@ cudaError_t run_gemm(const I8Args& p, const int8_t* wa, const int8_t* wb, const 
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(I8Cfg<NT>::kB ? i8_sm_count() / 2 * 2 : i8_sm_count());
-  cfg.blockDim = dim3(kI8Threads);
+  cfg.blockDim = dim3(GATHER ? kI8Threads + 32 * (kCopyWarps - 1) : kI8Threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -642,8 +752,8 @@ cudaError_t run_gemm(const I8Args& p, const int8_t* wa, const int8_t* wb, const 
 template <bool UP, typename TO>
 cudaError_t run_product(const smoe_desc& d, const I8Args& p, const int8_t* wa, const int8_t* wb,
                         const void* x16, long long xrows, cudaStream_t s) {
-  if ((long long)d.T * d.K >= (long long)kWideRows * d.E)
-    return run_gemm<UP, 192, TO>(p, wa, wb, x16, xrows, s);
+  if (p.row_tok) return run_gemm<UP, 192, TO, true>(p, wa, wb, x16, xrows, s);
+  if (wide(d)) return run_gemm<UP, 192, TO>(p, wa, wb, x16, xrows, s);
   return run_gemm<UP, 64, TO>(p, wa, wb, x16, xrows, s);
 }
 
@@ -651,6 +761,27 @@ cudaError_t run_rows(const RowSource& r, const int32_t* expert_off, int E, int K
                      int nclear, DeviceStatus* st, cudaStream_t s) {
   const int grid = std::max(1, std::min(std::max(ceil_div(r.rows, 8), ceil_div(nclear, 256)), 152 * 8));
   SMOE_LAUNCH(i8_rows_kernel, grid, 256, 0, s, r, expert_off, E, KD, clear, nclear, st);
+  return cudaGetLastError();
+}
+
+// Up to this many output channels a product of wide tiles gathers its rows from the widened
+// tokens; above, a kernel puts them in place and TMA loads them. Gathering spares writing
+// every row (K times the tokens) and slows the product by about a tenth, which more channels
+// make dearer. Measured (in place, gathered): 131072 rows of 2048: 256 channels 226, 127 us;
+// 768: 366, 318; 1536: 595, 601. 49152 rows of 5120: 1024 channels 465, 417; 1536: 627, 593.
+// 16384 rows of 4096: 1024 channels 112, 109; 2048: 185, 194; 4096: 318, 347.
+constexpr int kGatherChannels = 1536;
+
+// Token rows for the product `p`: gathered by it (wide tiles), or put in place for it.
+cudaError_t run_token_rows(const smoe_desc& d, I8Args* p, const RowSource& r, uint32_t* clear,
+                           int nclear, int32_t* row_tok, int channels, cudaStream_t s) {
+  if (!wide(d) || r.map == nullptr || channels > kGatherChannels)
+    return run_rows(r, p->expert_off, d.E, p->KD, clear, nclear, p->st, s);
+  const int grid = std::min(std::max(ceil_div(d.T + 1, 8), ceil_div(std::max(nclear, r.TK), 256)), 152 * 8);
+  SMOE_LAUNCH(i8_tokens_kernel, grid, 256, 0, s, r, p->expert_off, d.E, p->KD, row_tok, clear, nclear,
+              p->st);
+  p->tok = reinterpret_cast<const char*>(r.out);
+  p->row_tok = row_tok;
   return cudaGetLastError();
 }
 
@@ -664,7 +795,8 @@ void i8_ws_layout(const smoe_desc& d, I8Layout* L) {
     return o;
   };
   const size_t TK = (size_t)d.T * d.K, rows = TK + (size_t)d.n_shared * d.T;
-  const size_t xrows = TK + (d.n_shared ? d.T : 0);
+  // rows in place, or the tokens and a zero row
+  const size_t xrows = std::max(TK + (d.n_shared ? d.T : 0), (size_t)d.T + 1);
   L->status = take(256);
   L->x16 = take(xrows * std::max(d.d, d.F) * 2);
   L->x16_s = take(xrows * 4);
@@ -672,6 +804,7 @@ void i8_ws_layout(const smoe_desc& d, I8Layout* L) {
   L->h16 = take(rows * d.F * 2);
   L->h16_s = take(rows * 4);
   L->row_max = take(rows * 4);
+  L->row_tok = take(TK * 4);
   L->total = off;
 }
 
@@ -686,10 +819,10 @@ cudaError_t launch_expert_matmul_i8(const smoe_desc& d, int n_out, int n_in, con
   uint4* x16 = ws_ptr<uint4>(ws, L.x16);
   float* x16_s = ws_ptr<float>(ws, L.x16_s);
   const RowSource r{xq, xs, row_src, nullptr, nullptr, x16, x16_s, TK, TK, row_src ? d.T : TK};
-  cudaError_t e = run_rows(r, expert_off, d.E, n_in, nullptr, 0, st, s);
+  I8Args p{expert_off, x16_s, ws_n, nullptr, out, nullptr, nullptr, st,
+           d.E, d.E, d.T, TK, n_out, n_in, TK, nullptr, nullptr};
+  const cudaError_t e = run_token_rows(d, &p, r, nullptr, 0, ws_ptr<int32_t>(ws, L.row_tok), n_out, s);
   if (e != cudaSuccess) return e;
-  const I8Args p{expert_off, x16_s, ws_n, nullptr, out, nullptr, nullptr, st,
-                 d.E, d.E, d.T, TK, n_out, n_in, TK};
   return d.dtype == SMOE_F32 ? run_product<false, float>(d, p, wq, nullptr, x16, TK, s)
                              : run_product<false, __nv_bfloat16>(d, p, wq, nullptr, x16, TK, s);
 }
@@ -709,16 +842,16 @@ cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const flo
   uint32_t* row_max = ws_ptr<uint32_t>(ws, L.row_max);
   const RowSource rx{xq, xs, row_src, nullptr, nullptr, x16, x16_s, xrows, TK, row_src ? d.T : TK};
   const RowSource rh{nullptr, nullptr, nullptr, h, row_max, h16, h16_s, rows, TK, 0};
-  cudaError_t e = run_rows(rx, expert_off, d.E, d.d, row_max, rows, st, s);
+  I8Args up{expert_off, x16_s, W.s1, W.s3, h, nullptr, row_max, st,
+            d.E, G, d.T, TK, d.F, d.d, TK, nullptr, nullptr};
+  cudaError_t e = run_token_rows(d, &up, rx, row_max, rows, ws_ptr<int32_t>(ws, L.row_tok), 2 * d.F, s);
   if (e != cudaSuccess) return e;
-  const I8Args up{expert_off, x16_s, W.s1, W.s3, h, nullptr, row_max, st,
-                  d.E, G, d.T, TK, d.F, d.d, TK};
   e = run_product<true, float>(d, up, W.w1, W.w3, x16, xrows, s);
   if (e != cudaSuccess) return e;
   e = run_rows(rh, expert_off, d.E, d.F, nullptr, 0, st, s);
   if (e != cudaSuccess) return e;
   const I8Args dn{expert_off, h16_s, W.s2, nullptr, y_disp, y_sh, nullptr, st,
-                  d.E, G, d.T, TK, d.d, d.F, TK};
+                  d.E, G, d.T, TK, d.d, d.F, TK, nullptr, nullptr};
   return d.dtype == SMOE_F32 ? run_product<false, float>(d, dn, W.w2, nullptr, h16, rows, s)
                              : run_product<false, __nv_bfloat16>(d, dn, W.w2, nullptr, h16, rows, s);
 }

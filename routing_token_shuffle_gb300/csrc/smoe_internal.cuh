@@ -280,7 +280,7 @@ cudaError_t launch_moe_few(const smoe_desc& d, const void* x, const void* w_gate
 
 // The 8-bit expert products' own workspace (expert_i8.cu).
 struct I8Layout {
-  size_t status, x16, x16_s, h, h16, h16_s, row_max, total;
+  size_t status, x16, x16_s, h, h16, h16_s, row_max, row_tok, total;
 };
 void i8_ws_layout(const smoe_desc& d, I8Layout* out);
 cudaError_t launch_expert_matmul_i8(const smoe_desc& d, int n_out, int n_in, const int8_t* xq,

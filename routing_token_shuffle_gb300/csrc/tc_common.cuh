@@ -118,6 +118,17 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// 16 bytes to shared memory without a register between; bytes past `valid` are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, uint32_t valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(valid)
+               : "memory");
+}
+// One of `bar`'s arrivals, made when this thread's cp_async16 so far have completed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ------------------------------------------------------------------ CTA pairs
 // Helpers for two-SM MMA (a cluster of two CTAs; rank 0 is the leader).
 __device__ __forceinline__ uint32_t cluster_rank() {
