@@ -399,10 +399,11 @@ def test_expert_matmul_i8(T, K, E, n_in, n_out, dt):
         assert ((out.double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("T,n_out", [(20, 40), (90, 40), (90, 1552)])
 @pytest.mark.parametrize("n_in", [1024, 5120])
-def test_expert_matmul_i8_largest_values(n_in):
+def test_expert_matmul_i8_largest_values(n_in, T, n_out):
     """Every product 127 x 127 (exact to n_in = 1024; beyond 2^24 fp32 roundings of the sum)."""
-    T, E, n_out = 20, 2, 40
+    E = 2
     xq = torch.full((T, n_in), 127, dtype=torch.int8, device="cuda")
     xq[1::2] = -127
     wq = torch.full((E, n_out, n_in), 127, dtype=torch.int8, device="cuda")
@@ -437,10 +438,11 @@ def test_expert_matmul_i8_leaves_other_rows():
     assert ((out[:90].double() - ref[:90]).abs() <= 2.1 * HALF["f32"] * ref[:90].abs()).all()
 
 
-def test_expert_matmul_i8_padded_batch():
+@pytest.mark.parametrize("T,n_out", [(16, 264), (64, 264), (64, 1600)])
+def test_expert_matmul_i8_padded_batch(T, n_out):
     """Rows behind the last segment may name no token: they are neither read nor written."""
     g = gen(9)
-    T, K, E, n_in, n_out = 64, 2, 3, 192, 264
+    K, E, n_in = 2, 3, 192
     xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
     src, off = rows_of(T // 2, K, E, 4)
     src = torch.cat([src, torch.full((T * K - len(src),), -1, dtype=torch.int32, device="cuda")])
@@ -457,11 +459,12 @@ def test_expert_matmul_i8_padded_batch():
     assert (out[n:] == 7.0).all()
 
 
-def test_expert_matmul_i8_scales_that_are_not_finite():
+@pytest.mark.parametrize("T,n_out", [(12, 136), (50, 136), (50, 1608)])
+def test_expert_matmul_i8_scales_that_are_not_finite(T, n_out):
     """A NaN channel scale gives NaN in that channel of that expert, a NaN row scale in that
     token's rows, nowhere else."""
     g = gen(10)
-    T, K, E, n_in, n_out = 50, 2, 2, 128, 136
+    K, E, n_in = 2, 2, 128
     xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
     src, off = rows_of(T, K, E, 5)
     xs, sw = torch.rand(T, generator=g, device="cuda"), torch.rand(E, n_out, generator=g, device="cuda")
@@ -496,10 +499,16 @@ def test_expert_matmul_i8_two_streams_at_once():
         assert ((out.double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
 
 
-def test_expert_matmul_i8_reports_bad_rows():
+# rows per expert and channels that take the narrow tiles, the wide ones that gather their
+# rows, and the wide ones whose rows are put in place
+TILES = [(30, 32), (200, 32), (200, 1544)]
+
+
+@pytest.mark.parametrize("T,n_out", TILES)
+def test_expert_matmul_i8_reports_bad_rows(T, n_out):
     """A row_src entry out of range: a zero row and SMOE_ERR_DATA; a bad expert_off: nothing."""
     g = gen(2)
-    T, E, n_in, n_out = 30, 2, 64, 32
+    E, n_in = 2, 64
     xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
     src, off = rows_of(T, 1, E, 1)
     src[4], src[9] = T, -1
@@ -576,7 +585,7 @@ FFN = [
     # T, d, E, K, F, S
     (1, 16, 1, 1, 16, 0), (1, 512, 8, 2, 768, 0), (5, 1024, 40, 6, 512, 2), (64, 640, 160, 6, 96, 2),
     (33, 272, 4, 3, 144, 1), (500, 256, 8, 2, 1040, 0), (300, 2048, 16, 8, 768, 0),
-    (1000, 512, 4, 2, 256, 1), (193, 64, 1, 1, 48, 1), (65, 32, 2, 1, 16, 8),
+    (1000, 512, 4, 2, 256, 1), (193, 64, 1, 1, 48, 1), (65, 32, 2, 1, 16, 8), (150, 96, 3, 2, 784, 2),
 ]
 
 
