@@ -23,8 +23,9 @@
 // The up product's A tile is 64 channels of W1 and the same 64 of W3.
 //
 // Measured: 384 rows over 160 experts of 5120 x 1536 188 us (6.1 TB/s of weights); 131072 rows
-// of 2048 over 128 experts of 768 channels 328 us, 1.26 PFLOP/s of fp16; the FFN of 8192 tokens (6 of 160 experts and two
-// shared ones, 5120 x 1536) 2.54 ms, 1.22 PFLOP/s.
+// of 2048 over 128 experts of 768 channels 331 us, 1.25 PFLOP/s of fp16; the FFN of 8192
+// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.5 to 2.7 ms with the clock that
+// the power cap allows, 1.15 to 1.22 PFLOP/s.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -46,13 +47,17 @@ constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 //     halves) sit beside it under the same barrier, so that the MMA warp waits once and
 //     commits once per 128 values: with separate barriers for the halves it was the
 //     bottleneck (1190 clocks a stage, against 780 at the HBM rate).
-// 192: batches whose experts fill it, on pairs of CTAs (a cluster on the two SMs of a TPC):
-//     256 channels, each CTA widening its own 128, and half of the rows in each CTA's
+// 160, 192: batches whose experts fill them, on pairs of CTAs (a cluster on the two SMs of a
+//     TPC): 256 channels, each CTA widening its own 128, and half of the rows in each CTA's
 //     shared memory, in a ring of their own. One CTA alone moves 155 bytes a clock through
 //     shared memory at the MMAs' rate (rows written and read, weight bytes written and
-//     read), the pair 97; the limit is 128.
+//     read), the pair 97; the limit is 128. 160 leaves TMEM for three operand stages, so
+//     that widening does not wait for the MMAs of the stage before last (1001 tokens over 8
+//     experts of 4096 x 14336: 665 -> 638 us); 192 serves the gathering products, whose
+//     copies take as long for fewer rows (331 us, against 337 to 347 with 160).
 template <int NT> struct I8Cfg;
 template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0, kRows = 64; };
+template <> struct I8Cfg<160> { static constexpr int kW = 6, kOp = 3, kB = 5, kRows = 80; };
 template <> struct I8Cfg<192> { static constexpr int kW = 6, kOp = 2, kB = 4, kRows = 96; };
 
 template <int NT>
@@ -581,28 +586,37 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     // ---------------------------------------------------------------- widen the weights
     const int q = warp & 3, half = (warp - 8) >> 2, row = q * 32 + lane;
     uint32_t ws = 0, wph = 0, as = 0, aph = 1;
-    bool ok = true;
+    bool ok = true, w_in = false;
     for (int t = first; t < total && ok; t += stride)
       for (int kb = 0; kb < nk; ++kb) {
-        ok = tc::mbar_wait_warp(&wfull[ws], wph, abort);
+        if (!w_in) ok = tc::mbar_wait_warp(&wfull[ws], wph, abort);
         if (!ok) break;
+        // the operand stage is asked for while the bytes are read, the next bytes while they
+        // are widened: each asking costs over 100 of the stage's 600 to 850 clocks
+        const bool a_free = tc::mbar_test(&aempty[as], aph);
         const uint8_t* src = sW + ws * kStageW + row * 128;
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[c] = *reinterpret_cast<const uint4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
+        uint64_t* w_done = &wempty[ws];
+        if (++ws == C::kW) { ws = 0; wph ^= 1u; }
+        const bool w_next = tc::mbar_test(&wfull[ws], wph);
         uint32_t r[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
-          widen4(v.x, r[8 * c], r[8 * c + 1]);
-          widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-          widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-          widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+          widen4(v[c].x, r[8 * c], r[8 * c + 1]);
+          widen4(v[c].y, r[8 * c + 2], r[8 * c + 3]);
+          widen4(v[c].z, r[8 * c + 4], r[8 * c + 5]);
+          widen4(v[c].w, r[8 * c + 6], r[8 * c + 7]);
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&wempty[ws]);
-        if (++ws == C::kW) { ws = 0; wph ^= 1u; }
-        ok = tc::mbar_wait_warp(&aempty[as], aph, abort);
+        if (lane == 0) tc::mbar_arrive(w_done);
+        if (!__all_sync(0xffffffffu, a_free)) ok = tc::mbar_wait_warp(&aempty[as], aph, abort);
         if (!ok) break;
         tc::fence_after_sync();
         tc::tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + kOpCol + as * 64 + half * 32, r);
+        w_in = __all_sync(0xffffffffu, w_next);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
@@ -702,7 +716,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
 }
 
 // From this many rows per expert on average the wide tiles win: they read a weight byte once
-// per 192 rows and issue fewer MMAs for them; below, the weights' stream is the work, and the
+// per 160 rows and issue fewer MMAs for them; below, the weights' stream is the work, and the
 // narrow tiles keep more of it in flight. Measured (FFN, 160 experts of 5120 x 1536): 32 rows
 // 651 us narrow and 686 wide, 64 rows 845 and 736; 8 experts of 4096 x 14336: 279 and 292,
 // 368 and 325; 128 experts of 2048 x 768: 143 and 143, 189 and 182.
@@ -753,7 +767,7 @@ template <bool UP, typename TO>
 cudaError_t run_product(const smoe_desc& d, const I8Args& p, const int8_t* wa, const int8_t* wb,
                         const void* x16, long long xrows, cudaStream_t s) {
   if (p.row_tok) return run_gemm<UP, 192, TO, true>(p, wa, wb, x16, xrows, s);
-  if (wide(d)) return run_gemm<UP, 192, TO>(p, wa, wb, x16, xrows, s);
+  if (wide(d)) return run_gemm<UP, 160, TO>(p, wa, wb, x16, xrows, s);
   return run_gemm<UP, 64, TO>(p, wa, wb, x16, xrows, s);
 }
 
