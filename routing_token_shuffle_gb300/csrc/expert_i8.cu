@@ -52,9 +52,9 @@ constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 //     shared memory, in a ring of their own. One CTA alone moves 155 bytes a clock through
 //     shared memory at the MMAs' rate (rows written and read, weight bytes written and
 //     read), the pair 97; the limit is 128. 160 leaves TMEM for three operand stages, so
-//     that widening does not wait for the MMAs of the stage before last (1001 tokens over 8
-//     experts of 4096 x 14336: 665 -> 638 us); 192 serves the gathering products, whose
-//     copies take as long for fewer rows (331 us, against 337 to 347 with 160).
+//     that widening does not wait for the MMAs of the stage before last; 192 issues fewer
+//     MMAs a row (see kTallRows), and serves the gathering products, whose copies take as
+//     long for fewer rows (331 us, against 337 to 347 with 160).
 template <int NT> struct I8Cfg;
 template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0, kRows = 64; };
 template <> struct I8Cfg<160> { static constexpr int kW = 6, kOp = 3, kB = 5, kRows = 80; };
@@ -721,6 +721,11 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
 // 651 us narrow and 686 wide, 64 rows 845 and 736; 8 experts of 4096 x 14336: 279 and 292,
 // 368 and 325; 128 experts of 2048 x 768: 143 and 143, 189 and 182.
 constexpr int kWideRows = 40;
+// From this many on, 192-row tiles instead of 160 where the rows are in place: fewer MMAs a
+// row, against a third operand stage (FFN, 160 and 192 rows: 100 rows an expert 342 and 360
+// us, 175: 467 and 488, 250: 617 and 641; 307: 2440 and 2423, 512: 269 and 258, 1024: 2018 and
+// 1953).
+constexpr int kTallRows = 288;
 bool wide(const smoe_desc& d) { return (long long)d.T * d.K >= (long long)kWideRows * d.E; }
 
 int i8_sm_count() {
@@ -767,6 +772,8 @@ template <bool UP, typename TO>
 cudaError_t run_product(const smoe_desc& d, const I8Args& p, const int8_t* wa, const int8_t* wb,
                         const void* x16, long long xrows, cudaStream_t s) {
   if (p.row_tok) return run_gemm<UP, 192, TO, true>(p, wa, wb, x16, xrows, s);
+  if ((long long)d.T * d.K >= (long long)kTallRows * d.E)
+    return run_gemm<UP, 192, TO>(p, wa, wb, x16, xrows, s);
   if (wide(d)) return run_gemm<UP, 160, TO>(p, wa, wb, x16, xrows, s);
   return run_gemm<UP, 64, TO>(p, wa, wb, x16, xrows, s);
 }

@@ -499,9 +499,9 @@ def test_expert_matmul_i8_two_streams_at_once():
         assert ((out.double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
 
 
-# rows per expert and channels that take the narrow tiles, the wide ones that gather their
-# rows, and the wide ones whose rows are put in place
-TILES = [(30, 32), (200, 32), (200, 1544)]
+# tokens and channels that take the narrow tiles, the wide ones that gather their rows, and
+# the wide ones whose rows are put in place (160 and 192 rows high)
+TILES = [(30, 32), (200, 32), (200, 1544), (600, 1544)]
 
 
 @pytest.mark.parametrize("T,n_out", TILES)
@@ -586,6 +586,7 @@ FFN = [
     (1, 16, 1, 1, 16, 0), (1, 512, 8, 2, 768, 0), (5, 1024, 40, 6, 512, 2), (64, 640, 160, 6, 96, 2),
     (33, 272, 4, 3, 144, 1), (500, 256, 8, 2, 1040, 0), (300, 2048, 16, 8, 768, 0),
     (1000, 512, 4, 2, 256, 1), (193, 64, 1, 1, 48, 1), (65, 32, 2, 1, 16, 8), (150, 96, 3, 2, 784, 2),
+    (700, 128, 2, 1, 800, 0),
 ]
 
 
