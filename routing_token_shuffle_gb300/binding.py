@@ -351,7 +351,9 @@ def i8_weights(w1, s1, w3, s3, w2, s2) -> I8Weights:
 def smoe_expert_matmul_i8(desc, xq, x_scale, expert_off, wq, w_scale, out, ws, row_src=None,
                           stream=None):
     """wq [E, n_out, n_in]; n_out and n_in are taken from its shape; ws from workspace_i8."""
-    _, n_out, n_in = wq.shape
+    E, n_out, n_in = wq.shape
+    if E != desc.E:
+        raise ValueError(f"wq holds {E} experts, the descriptor {desc.E}")
     _check(lib().smoe_expert_matmul_i8(ctypes.byref(desc), n_out, n_in, _ptr(xq), _ptr(x_scale),
                                        _ptr(row_src), _ptr(expert_off), _ptr(wq), _ptr(w_scale),
                                        _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),

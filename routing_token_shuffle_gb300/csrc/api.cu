@@ -691,13 +691,16 @@ SMOE_API int smoe_prefetch_predict(const smoe_desc* desc, const float* r, const 
   return SMOE_OK;
 }
 
-// Row indices of the expert matrices are 32-bit (tensor-map coordinates, work counts).
+// Row indices of the expert matrices are 32-bit (tensor-map coordinates, work counts), with
+// room for a tile that starts behind the last row.
+constexpr long long kMaxMatrixRows = INT_MAX - 1024;
+
 static int check_few(const smoe_desc* d) {
   SMOE_CHECK(check_desc(d));
   SMOE_REQUIRE(d->T <= kFewMaxT, SMOE_ERR_SHAPE, "the few-token layer takes T <= %d (T=%d)",
                kFewMaxT, d->T);
   const long long G = (long long)d->E + d->n_shared;
-  SMOE_REQUIRE(G * d->F <= INT_MAX && G * d->d <= INT_MAX &&
+  SMOE_REQUIRE(G * d->F <= kMaxMatrixRows && G * d->d <= kMaxMatrixRows &&
                    G * ((d->F + 31) / 32) * ((d->d + 31) / 32) <= INT_MAX / 2,
                SMOE_ERR_SHAPE, "expert matrices too large");
   return SMOE_OK;
@@ -706,8 +709,8 @@ static int check_few(const smoe_desc* d) {
 static int check_i8(const smoe_desc* d) {
   SMOE_CHECK(check_desc(d));
   const long long G = (long long)d->E + d->n_shared;
-  SMOE_REQUIRE((long long)d->T * (d->K + d->n_shared) <= INT_MAX / 2 && G * d->F <= INT_MAX &&
-                   G * d->d <= INT_MAX,
+  SMOE_REQUIRE((long long)d->T * (d->K + d->n_shared) <= INT_MAX / 2 && G * d->F <= kMaxMatrixRows &&
+                   G * d->d <= kMaxMatrixRows,
                SMOE_ERR_SHAPE, "expert matrices or batch too large");
   return SMOE_OK;
 }
@@ -783,8 +786,8 @@ SMOE_API int smoe_expert_matmul_i8(const smoe_desc* desc, int n_out, int n_in, c
   SMOE_REQUIRE(n_in > 0 && n_in % 16 == 0 && n_in <= std::max(desc->d, desc->F), SMOE_ERR_SHAPE,
                "n_in=%d must be a multiple of 16 and at most max(d, F)=%d", n_in,
                std::max(desc->d, desc->F));
-  SMOE_REQUIRE(n_out > 0 && n_out % 8 == 0 && (long long)desc->E * n_out <= INT_MAX,
-               SMOE_ERR_SHAPE, "n_out=%d must be a multiple of 8 with E n_out < 2^31", n_out);
+  SMOE_REQUIRE(n_out > 0 && n_out % 8 == 0 && (long long)desc->E * n_out <= kMaxMatrixRows,
+               SMOE_ERR_SHAPE, "n_out=%d must be a multiple of 8 with E n_out < 2^31 - 1024", n_out);
   SMOE_PTR(xq);
   SMOE_PTR(x_scale);
   SMOE_OPT_PTR(row_src);

@@ -179,14 +179,14 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 // One row of the product's operand, by a warp. Token rows: row r < TK is xq[map[r]] (or
-// xq[r]), row TK + t the token t (shared experts); rows behind the last segment (`end`)
+// xq[r]), row TK + t the token t (shared experts); rows outside the segments [begin, end)
 // belong to nobody. Hidden rows: s = max |h| / 127, rint(h / s), an integer that fp16 holds;
 // s is 0 for a row that is zero or whose scale would be subnormal, NaN for a row that is not
 // finite.
-__device__ __forceinline__ void make_row(const RowSource& p, int r, int end, int KD, DeviceStatus* st,
-                                         int lane) {
+__device__ __forceinline__ void make_row(const RowSource& p, int r, int begin, int end, int KD,
+                                         DeviceStatus* st, int lane) {
   if (p.h == nullptr) {
-    if (r >= end && r < p.TK) return;
+    if ((r < begin || r >= end) && r < p.TK) return;
     const int src = r >= p.TK ? r - p.TK : p.map ? p.map[r] : r;
     const bool in = (unsigned)src < (unsigned)p.n_src;
     if (lane == 0) {
@@ -246,13 +246,14 @@ i8_tokens_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int 
                  int32_t* __restrict__ row_tok, uint32_t* __restrict__ clear, int nclear,
                  DeviceStatus* st) {
   pdl_wait_and_trigger();
-  const int end = expert_off[E], T = p.n_src;
+  const int begin = expert_off[0], end = expert_off[E], T = p.n_src;
   for (int i = blockIdx.x * 256 + threadIdx.x; i < max(nclear, p.TK); i += gridDim.x * 256) {
     if (i < nclear) clear[i] = 0u;
     if (i < p.TK) {
-      const int t = i < end ? p.map[i] : T;
+      const bool used = i >= begin && i < end;
+      const int t = used ? p.map[i] : T;
       const bool in = (unsigned)t < (unsigned)T;
-      if (!in && i < end) record_error(st, kStatusData, kBadPerm, i);
+      if (!in && used) record_error(st, kStatusData, kBadPerm, i);
       row_tok[i] = in ? t : T;
     }
   }
@@ -261,7 +262,7 @@ i8_tokens_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int 
     if (r < T) {
       RowSource one = p;
       one.map = nullptr;
-      make_row(one, r, T, KD, st, lane);
+      make_row(one, r, 0, T, KD, st, lane);
     } else {
       for (int v = lane; v < KD / 8; v += 32) p.out[(size_t)T * (KD / 8) + v] = make_uint4(0, 0, 0, 0);
       if (lane == 0) p.out_s[T] = 0.0f;
@@ -277,9 +278,9 @@ i8_rows_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E,
                uint32_t* __restrict__ clear, int nclear, DeviceStatus* st) {
   pdl_wait_and_trigger();
   for (int i = blockIdx.x * 256 + threadIdx.x; i < nclear; i += gridDim.x * 256) clear[i] = 0u;
-  const int end = p.h ? p.rows : expert_off[E];
+  const int begin = p.h ? 0 : expert_off[0], end = p.h ? p.rows : expert_off[E];
   for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < p.rows; r += gridDim.x * 8)
-    make_row(p, r, end, KD, st, threadIdx.x & 31);
+    make_row(p, r, begin, end, KD, st, threadIdx.x & 31);
 }
 
 // GATHER (pairs): the token rows are gathered by the product itself.

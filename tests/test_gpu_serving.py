@@ -440,12 +440,15 @@ def test_expert_matmul_i8_leaves_other_rows():
 
 @pytest.mark.parametrize("T,n_out", [(16, 264), (64, 264), (64, 1600)])
 def test_expert_matmul_i8_padded_batch(T, n_out):
-    """Rows behind the last segment may name no token: they are neither read nor written."""
+    """Rows outside the segments may name no token: they are neither read nor written."""
     g = gen(9)
     K, E, n_in = 2, 3, 192
     xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
     src, off = rows_of(T // 2, K, E, 4)
-    src = torch.cat([src, torch.full((T * K - len(src),), -1, dtype=torch.int32, device="cuda")])
+    lead = 5  # rows in front of the first segment
+    src = torch.cat([torch.full((lead,), T, dtype=torch.int32, device="cuda"), src,
+                     torch.full((T * K - len(src) - lead,), -1, dtype=torch.int32, device="cuda")])
+    off = off + lead
     xs, sw = torch.rand(T, generator=g, device="cuda"), torch.rand(E, n_out, generator=g, device="cuda")
     desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, "f32")
     ws = smoe.workspace_i8(desc)
@@ -454,9 +457,9 @@ def test_expert_matmul_i8_padded_batch(T, n_out):
     smoe.smoe_expert_matmul_i8(desc, xq, xs, off, wq, sw, out, ws, row_src=src)
     smoe.smoe_get_status(ws)
     n = int(off[-1])
-    ref, _ = matmul_ref(xq, xs, src[:n], off, wq, sw)
-    assert ((out[:n].double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
-    assert (out[n:] == 7.0).all()
+    ref, _ = matmul_ref(xq, xs, src, off, wq, sw)
+    assert ((out[lead:n].double() - ref[lead:n]).abs() <= 2.1 * HALF["f32"] * ref[lead:n].abs()).all()
+    assert (out[n:] == 7.0).all() and (out[:lead] == 7.0).all()
 
 
 @pytest.mark.parametrize("T,n_out", [(12, 136), (50, 136), (50, 1608)])

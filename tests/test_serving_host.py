@@ -124,4 +124,13 @@ def test_binding_refuses_strided_rows(lib):
         B.smoe_add_rmsnorm(d, torch.zeros(16, 256)[:, ::2], torch.ones(128), r_out=torch.zeros(16, 128),
                            stream=0)
     with pytest.raises(ValueError, match="not contiguous"):
+        B.smoe_moe_forward_few(d, torch.zeros(128, 16).t(), *[torch.zeros(1)] * 6, stream=0)
+    with pytest.raises(ValueError, match="not contiguous"):
         B.i8_weights(torch.zeros(8, 128, 256).transpose(1, 2), *[torch.zeros(8, 256)] * 5)
+
+
+def test_binding_refuses_weights_of_another_expert_count(lib):
+    import torch
+    z = torch.zeros(16)
+    with pytest.raises(ValueError, match="7 experts"):
+        B.smoe_expert_matmul_i8(desc(), z, z, z, torch.zeros(7, 16, 16, dtype=torch.int8), z, z, z, stream=0)
