@@ -430,8 +430,9 @@ SMOE_API size_t smoe_few_workspace_size(const smoe_desc* desc);
  * top-K, the touched experts' SwiGLU FFN, shared experts included, and the weighted sum
  * back into token order: what smoe_layer_forward computes without the shuffle. Each touched
  * expert's weights are read once. T <= 64, else SMOE_ERR_SHAPE.
- * Products accumulate in fp32; w_tk silu(W1 x) (W3 x) is rounded once to dtype before the
- * down product, whose sum over the experts stays in fp32 until y. fp32 layers multiply in
+ * Products accumulate in fp32; the down product reads w_tk silu(W1 x) (W3 x) in fp32 layers as
+ * it is and in bf16 layers as the sum of two bf16 values (16 bits of it), and its sum over the
+ * experts stays in fp32 until y: y's rounding is the layer's error. fp32 layers multiply in
  * fp32 (not tf32). The result does not depend on timing. A token's products stay apart from
  * the other tokens', but the weights of W2 have to be finite: one that is not reaches every
  * token of the call.

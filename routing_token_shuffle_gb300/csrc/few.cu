@@ -30,12 +30,13 @@
 // An A tile is 128 weight rows (up: 64 rows of W1 and the same 64 of W3), the B tile is all
 // T tokens padded to NP rows; fp32 accumulation. Every wait is bounded (see tc_common.cuh).
 //
-// Measured: bf16, 64 tokens of a 160-expert layer of 5120 x 1536 with two shared experts 1.03
-// ms (6.4 TB/s of the touched weights, 0.96 of the measured copy rate), 3 tokens of 8 experts
+// Measured: bf16, 64 tokens of a 160-expert layer of 5120 x 1536 with two shared experts 1.06
+// ms (6.2 TB/s of the touched weights, 0.93 of the measured copy rate), 3 tokens of 8 experts
 // of 4096 x 14336 242 us (6 TB/s), one token of 128 experts of 2048 x 768 30 us (75 MB: 11 us
 // of stream, 7 us until the routes are known, two barriers and the joining of sums). fp32, 13
-// tokens of 24 experts of 1000 x 1416 108 us: FMAs and shared memory, not HBM (53 us).
+// tokens of 24 experts of 1000 x 1416 106 us: FMAs and shared memory, not HBM (53 us).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "tc_common.cuh"
@@ -57,7 +58,7 @@ struct FewArgs {
   float* logits_out;    // nullable outputs
   int32_t* topk_idx;
   float* topk_w;
-  void* h;              // [slots, T, F]
+  void* h;              // [slots, T, F] fp32, or [slots, 2, T, F] bf16
   float* partial;       // [2][kFewMaxCtas][NP * 128]
   uint32_t* flags;      // [3][kFewMaxCtas]
   int32_t* ridx;        // [T, K] routes in the workspace (T > kSelectAll)
@@ -295,18 +296,25 @@ __device__ __forceinline__ void select_token(const FewArgs& p, int t, int lane, 
 // in rounds of ten tokens per CTA.
 constexpr int kSelectAll = kGateThreads / 32;
 
-template <typename TE, int NP>
+// NP, ND: rows of the B tile of the up and of the down product. fp32: ND = NP, one row of H a
+// token. bf16: two rows a token, H's bf16 rounding and the bf16 rounding of what it left, so
+// that the down product sees 16 bits of H: T tokens' rows, then T rows of rests, whose
+// accumulator columns the epilogue adds to the first ones. Rounding H to bf16 alone made the
+// layer's error 1.4 to 1.6 times that of rounding its output; the second row is free up to 32
+// tokens (the stream from HBM is the time) and takes 64 tokens from 1.03 to 1.06 ms.
+template <typename TE, int NP, int ND>
 __global__ void __launch_bounds__(kFewThreads, 1)
 moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
                const __grid_constant__ CUtensorMap tmW1,  // [(E+S) F, d], 64-row box
                const __grid_constant__ CUtensorMap tmW3,
                const __grid_constant__ CUtensorMap tmW2,  // [(E+S) d, F], 128-row box
-               const __grid_constant__ CUtensorMap tmH,   // [slots T, F], NP-row box
+               const __grid_constant__ CUtensorMap tmH,   // [slots T (bf16: 2 T), F], ND-row box
                const FewArgs p) {
   constexpr int BK = 128 / (int)sizeof(TE);
-  constexpr uint32_t kB = NP * 128;
+  constexpr uint32_t kB = ND * 128;                // B stage (the up product's tile may be smaller)
   constexpr bool kTC = sizeof(TE) == 2;            // bf16: tcgen05; fp32: FMAs on the CUDA cores
-  constexpr uint32_t kCols = 2 * NP;               // TMEM: two accumulators of NP columns
+  // TMEM: two accumulators of ND columns (reads of 16 columns may start at column T)
+  constexpr uint32_t kCols = ND == 16 ? 64 : 2 * ND;
   // Consumer threads: 4 warps read the accumulators (bf16), 8 warps multiply (fp32): two
   // groups of four, which take every other block. A warp takes all 128 rows of its block, four
   // to a lane, 16 tokens and a share of the contraction: shared memory returns 128 bytes a clock, broadcast or not, so a token's
@@ -429,7 +437,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     };
     auto load_a = [&](uint32_t s, int part, const Place& at) {
       if (!lead) return;
-      tc::mbar_expect_tx(&full[s], kFewA + kB);
+      tc::mbar_expect_tx(&full[s], kFewA + (part < 2 ? NP : ND) * 128);
       if (part < 2) {
         tc::tma_load_2d(sA + s * kFewA, &tmW1, &full[s], at.kb * BK, at.row);
         tc::tma_load_2d(sA + s * kFewA + kFewA / 2, &tmW3, &full[s], at.kb * BK, at.row);
@@ -440,7 +448,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     auto load_b = [&](uint32_t s, int part, const Place& at) {
       if (!lead) return;
       if (part < 2) tc::tma_load_2d(sB + s * kB, &tmX, &full[s], at.kb * BK, 0);
-      else tc::tma_load_2d(sB + s * kB, &tmH, &full[s], at.fb * BK, at.slot * p.T);
+      else tc::tma_load_2d(sB + s * kB, &tmH, &full[s], at.fb * BK, at.slot * p.T * (kTC ? 2 : 1));
     };
     uint32_t s = 0, ph = 1;  // stage and the parity its release is awaited with
     auto next_stage = [&] {
@@ -498,11 +506,11 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     const bool lead = tc::elect_one();
     uint32_t s = 0, ph = 0, tcount = 0;
     bool ok = true;
-    constexpr uint32_t kIdesc = tc::instr_desc(false, 128, NP);
     for (int part = 0; part < 3 && ok; ++part) {
       if (part == 1 && !tc::mbar_wait_warp(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
       const int end = r.first(cta + 1);
+      const uint32_t idesc = tc::instr_desc(false, 128, part < 2 ? NP : ND);
       for (int i = r.first(cta); i < end && ok; ++tcount) {
         const int n = min(r.kper - i % r.kper, end - i);
         const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
@@ -516,7 +524,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc::mma_bf16(tmem + a * NP, adesc + 2 * k, bdesc + 2 * k, kIdesc, (j > 0 || k > 0) ? 1u : 0u);
+              tc::mma_bf16(tmem + a * ND, adesc + 2 * k, bdesc + 2 * k, idesc, (j > 0 || k > 0) ? 1u : 0u);
             tc::commit(&empty[s]);
           }
           __syncwarp();
@@ -745,8 +753,15 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
             if (c0 >= p.T) break;
             const int nt = min(16, p.T - c0);
             if (kTC) {
+              const uint32_t col = tmem + ((uint32_t)(q * 32) << 16) + ta * ND + c0;
               float v[16];
-              tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + ta * NP + c0, v);
+              tc::tmem_ld16(col, v);
+              if (part == 2) {  // and the rests' products
+                float w[16];
+                tc::tmem_ld16(col + p.T, w);
+#pragma unroll
+                for (int t = 0; t < 16; ++t) v[t] += w[t];
+              }
 #pragma unroll
               for (int t = 0; t < 16; ++t) mine[t] = v[t];
             } else {
@@ -827,9 +842,16 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
                 const int fr = j & 63, t = j >> 6, f = fb * 64 + fr;
                 const float g = s_xch[fr * 17 + t];
                 const float hv = g / (1.0f + expf(-g)) * s_xch[(64 + fr) * 17 + t] * s_wcol[c0 + t];
-                if (f < p.F)
-                  static_cast<TE*>(p.h)[((size_t)slot * p.T + c0 + t) * p.F + f] =
-                      Elem<TE>::from_f32(s_use[c0 + t] ? hv : 0.0f);
+                if (f < p.F) {
+                  const float use = s_use[c0 + t] ? hv : 0.0f;
+                  const TE hi = Elem<TE>::from_f32(use);
+                  TE* out = static_cast<TE*>(p.h) + ((size_t)slot * (kTC ? 2 : 1) * p.T + c0 + t) * p.F + f;
+                  *out = hi;
+                  if (kTC) {
+                    const float back = Elem<TE>::to_f32(hi);
+                    out[(size_t)p.T * p.F] = Elem<TE>::from_f32(fabsf(back) <= FLT_MAX ? use - back : 0.0f);
+                  }
+                }
               }
               if (kTC) group_sync(1, kCons);
             } else {
@@ -877,7 +899,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   }
 }
 
-template <typename TE, int NP>
+template <typename TE, int NP, int ND>
 cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const void* w1,
                     const void* w3, const void* w2, void* y, float* logits, int32_t* topk_idx,
                     float* topk_w, void* ws, cudaStream_t s) {
@@ -892,7 +914,7 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
       !encode_tmap_2d(&tW1, w1, kF32, G * d.F, d.d, 64, BK) ||
       !encode_tmap_2d(&tW3, w3, kF32, G * d.F, d.d, 64, BK) ||
       !encode_tmap_2d(&tW2, w2, kF32, G * d.d, d.F, 128, BK) ||
-      !encode_tmap_2d(&tH, h, kF32, L.slots * d.T, d.F, NP, BK))
+      !encode_tmap_2d(&tH, h, kF32, L.slots * d.T * (kF32 ? 1 : 2), d.F, ND, BK))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -906,8 +928,8 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
   const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 +
                       4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K +
                       (kF32 ? 4 * ((size_t)d.E + 1 + 2 * (kFewMaxCtas + 1)) : 0);
-  p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + NP * 128));
-  auto kern = moe_few_kernel<TE, NP>;
+  p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + ND * 128));
+  auto kern = moe_few_kernel<TE, NP, ND>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -928,9 +950,14 @@ template <typename TE>
 cudaError_t run_few_t(const smoe_desc& d, const void* x, const void* w_gate, const void* w1,
                       const void* w3, const void* w2, void* y, float* logits, int32_t* topk_idx,
                       float* topk_w, void* ws, cudaStream_t s) {
-  if (d.T <= 16) return run_few<TE, 16>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
-  if (d.T <= 32) return run_few<TE, 32>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
-  return run_few<TE, 64>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  constexpr int W = sizeof(TE) == 2 ? 2 : 1;  // B rows of a token in the down product
+  if (W == 2 && d.T <= 8)
+    return run_few<TE, 16, 16>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  if (d.T <= 16)
+    return run_few<TE, 16, 16 * W>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  if (d.T <= 32)
+    return run_few<TE, 32, 32 * W>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
+  return run_few<TE, 64, 64 * W>(d, x, w_gate, w1, w3, w2, y, logits, topk_idx, topk_w, ws, s);
 }
 
 }  // namespace
@@ -950,7 +977,7 @@ void few_ws_layout(const smoe_desc& d, FewLayout* L) {
   L->ridx = take(4 * (size_t)d.T * d.K);
   L->rw = take(4 * (size_t)d.T * d.K);
   L->partial = take(4 * 2 * kFewMaxCtas * np * 128);
-  L->h = take(L->slots * d.T * d.F * elem_size(d));
+  L->h = take(L->slots * d.T * d.F * 4);  // fp32, or two bf16 a value
   L->total = off;
 }
 

@@ -196,8 +196,8 @@ class Few:
         err = (self.y.double() - y).abs()
         rms = sq.sqrt()
         if self.dt == "bf16":
-            # h rounded once, y rounded once; the fp32 sums are below both
-            tol = HALF["bf16"] * y.abs() + (6 / math.sqrt(3) * HALF["bf16"] + 1e-4) * rms
+            # y rounded once; h as two bf16 values (2^-8 of 2^-8); the fp32 sums are below both
+            tol = HALF["bf16"] * y.abs() + (6 / math.sqrt(3) * HALF["bf16"] ** 2 + 1e-4) * rms
         else:
             # three chained fp32 contractions of d, d and F (K F) terms: each
             # sqrt(n) 2^-24 / sqrt(3) of the typical sum, six standard deviations
