@@ -213,7 +213,8 @@ FEW = [
     (32, 768, 8, 8, 1, 200, 0, 0), (33, 1000, 24, 3, 3, 1416, 1, 0), (64, 1024, 160, 6, 1, 384, 2, 1),
     (64, 136, 4, 1, 1, 72, 0, 0), (3, 4096, 8, 2, 1, 1792, 0, 0), (1, 8, 1, 1, 1, 8, 0, 0),
     (7, 8, 512, 32, 1, 8, 8, 1), (64, 64, 512, 32, 32, 64, 0, 0), (1, 128, 4, 1, 1, 128, 0, 0),
-    (64, 72, 2, 1, 1, 4096, 0, 0), (13, 4096, 33, 3, 1, 24, 0, 0),
+    (64, 72, 2, 1, 1, 4096, 0, 0), (13, 4096, 33, 3, 1, 24, 0, 0), (8, 768, 20, 2, 1, 448, 1, 0),
+    (9, 768, 20, 2, 1, 448, 1, 0), (10, 264, 300, 5, 1, 64, 0, 1), (11, 264, 130, 13, 13, 72, 0, 0),
 ]
 
 
@@ -677,6 +678,86 @@ def test_norm_route_dispatch_ffn_combine():
     ref = c.ysh[0].double() + (w.double()[..., None] * c.y[pair_row.long()].double()).sum(1)
     mag = c.ysh[0].double().abs() + (w.double()[..., None] * c.y[pair_row.long()].double().abs()).sum(1)
     assert ((out.double() - ref).abs() <= HALF["bf16"] * ref.abs() + 8 * HALF["f32"] * mag).all()
+
+
+def test_the_8bit_layer_captured():
+    """The same run captured into a graph and replayed on new inputs, equal to the eager run."""
+    T, d, E, K, F, S = 120, 256, 8, 2, 192, 1
+    c = Ffn8(T, d, E, K, F, S, "bf16")
+    g = gen(8)
+    r0 = randn(g, T, d)
+    r, y = r0.clone(), randn(g, T, d).bfloat16()
+    gamma, w_gate = 1 + 0.1 * randn(g, d), (randn(g, E, d) / math.sqrt(d)).bfloat16()
+    ws = smoe.workspace(c.desc)
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    c.xq, c.xs = torch.empty(T, d, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    idx, w = i32(T, K), torch.empty(T, K, device="cuda")
+    pair_row, c.src, c.off = i32(T, K), i32(T * K), i32(E + 1)
+    out = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+
+    def layer():
+        smoe.smoe_add_rmsnorm(c.desc, r, gamma, y=y, r_out=r, x_out=x, q_out=c.xq, q_scale=c.xs)
+        smoe.smoe_route(c.desc, x, w_gate, idx, w, ws=ws)
+        smoe.smoe_dispatch(c.desc, idx, c.off, pair_row, c.src, ws)
+        c.run()
+        smoe.smoe_combine(c.desc, c.y, pair_row, w, out, ws, y_shared=c.ysh)
+
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    for i in range(3):
+        y.copy_(randn(g, T, d).bfloat16())
+        r.copy_(r0 * (i + 1))
+        layer()
+        want = out.clone()
+        r.copy_(r0 * (i + 1))
+        out.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        c.check()
+    smoe.smoe_get_status(ws)
+
+
+def test_few_beside_the_8bit_products():
+    """The cooperative few-token kernel and the 8-bit FFN's pairs on two streams at once."""
+    a, b = Few(6, 1024, 16, 2, 1, 512, 1, "bf16"), Ffn8(400, 512, 8, 2, 320, 1, "bf16")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a.run(stream=streams[0])
+        b.run(stream=streams[1])
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
+def test_decode_steps_captured():
+    """Norm, few-token layer and norm in one graph, step after step on the residual it updates."""
+    c = Few(3, 512, 16, 2, 1, 256, 1, "bf16")
+    g = gen(12)
+    r, gamma = randn(g, 3, 512), 1 + 0.1 * randn(g, 512)
+    eager = r.clone()
+
+    def step(res):
+        smoe.smoe_add_rmsnorm(c.desc, res, gamma, x_out=c.x)
+        c.run()
+        smoe.smoe_add_rmsnorm(c.desc, res, gamma, y=c.y, r_out=res)
+
+    for _ in range(4):
+        step(eager)
+    torch.cuda.synchronize()
+    graph, res = torch.cuda.CUDAGraph(), r.clone()
+    with torch.cuda.graph(graph):
+        step(res)
+    res.copy_(r)
+    for _ in range(4):
+        graph.replay()
+    torch.cuda.synchronize()
+    smoe.smoe_get_status(c.ws)
+    assert torch.equal(res, eager)
 
 
 def test_norm_then_few():
