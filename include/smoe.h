@@ -33,7 +33,8 @@
  * Conventions shared by every entry point
  *   - Memory: every pointer is a caller-owned DEVICE pointer unless the argument
  *     says host. The library allocates nothing; scratch space is the caller's
- *     workspace (size from smoe_workspace_size). Pointers must be 16-byte aligned
+ *     workspace (size from smoe_workspace_size; smoe_moe_forward_few and the 8-bit entry
+ *     points have size functions of their own). Pointers must be 16-byte aligned
  *     (SMOE_ERR_ALIGN otherwise). Matrices are row-major and dense.
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream). Every call is asynchronous on that stream; the return value covers
@@ -94,7 +95,8 @@ typedef struct smoe_desc {
 } smoe_desc;
 
 /* Bytes of workspace that every entry point below accepts for this shape (one
- * buffer serves all of them). Returns 0 if the descriptor is invalid. */
+ * buffer serves all of them, but for smoe_moe_forward_few and the 8-bit entry points).
+ * Returns 0 if the descriptor is invalid. */
 SMOE_API size_t smoe_workspace_size(const smoe_desc* desc);
 
 /* a1/a2 -- gate GEMM, softmax and grouped top-K ("Speculative MoE" §1: each token
