@@ -32,7 +32,7 @@
 //
 // Measured: bf16, 64 tokens of a 160-expert layer of 5120 x 1536 with two shared experts 1.06
 // ms (6.2 TB/s of the touched weights, 0.93 of the measured copy rate), 3 tokens of 8 experts
-// of 4096 x 14336 242 us (6 TB/s), one token of 128 experts of 2048 x 768 30 us (75 MB: 11 us
+// of 4096 x 14336 242 us (6 TB/s), one token of 128 experts of 2048 x 768 29 us (75 MB: 11 us
 // of stream, 7 us until the routes are known, two barriers and the joining of sums). fp32, 13
 // tokens of 24 experts of 1000 x 1416 106 us: FMAs and shared memory, not HBM (53 us).
 #include <algorithm>
@@ -505,7 +505,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     // ---------------------------------------------------------------- MMA issuer
     const bool lead = tc::elect_one();
     uint32_t s = 0, ph = 0, tcount = 0;
-    bool ok = true;
+    bool ok = true, in = false;
     for (int part = 0; part < 3 && ok; ++part) {
       if (part == 1 && !tc::mbar_wait_warp(routed, 0, abort)) { ok = false; break; }
       const Range r = part_range(part);
@@ -517,18 +517,22 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         if (!tc::mbar_wait_warp(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
         tc::fence_after_sync();
         for (int j = 0; j < n; ++j) {
-          if (!tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
+          if (!in && !tc::mbar_wait_warp(&full[s], ph, abort)) { ok = false; break; }
           tc::fence_after_sync();
           const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kFewA));
           const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kB));
+          uint64_t* used = &empty[s];
+          if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
+          // asking for the next stage takes ~100 clocks: while this one's MMAs are issued
+          // (one token of the 128-expert layer 29.8 -> 29.0 us, 64 tokens level)
+          const bool next = tc::mbar_test(&full[s], ph);
           if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc::mma_bf16(tmem + a * ND, adesc + 2 * k, bdesc + 2 * k, idesc, (j > 0 || k > 0) ? 1u : 0u);
-            tc::commit(&empty[s]);
+            tc::commit(used);
           }
-          __syncwarp();
-          if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
+          in = __all_sync(0xffffffffu, next);
         }
         i += n;
         if (ok && lead) tc::commit(&tfull[a]);
