@@ -24,8 +24,9 @@
 //
 // Measured: 384 rows over 160 experts of 5120 x 1536 188 us (6.1 TB/s of weights); 131072 rows
 // of 2048 over 128 experts of 768 channels 331 us, 1.25 PFLOP/s of fp16; the FFN of 8192
-// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.5 to 2.7 ms with the clock that
-// the power cap allows, 1.15 to 1.22 PFLOP/s.
+// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.4 to 2.5 ms with the clock that
+// the power cap allows, 1.23 to 1.27 PFLOP/s; of 1001 tokens (2 of 8 experts of 4096 x 14336)
+// 578 us, 1.22 PFLOP/s.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -38,7 +39,7 @@ namespace {
 constexpr int kI8Threads = 512;
 constexpr int kCopyWarps = 3;        // that gather rows: warp 3 and two more
 constexpr int kStageW = 128 * 128;   // weight stage: 128 channels x 128 bytes
-constexpr int kXchPitch = 33;
+constexpr int kXchPitch = 20;        // floats: 16 of a thread; 16-byte accesses without bank conflicts
 constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 
 // NT: most rows of a tile. TMEM holds two accumulators of NT columns, then the widened
@@ -64,7 +65,7 @@ template <int NT>
 constexpr size_t i8_smem() {
   using C = I8Cfg<NT>;
   return 1024 + (size_t)C::kW * kStageW + (size_t)2 * (C::kB ? C::kB : C::kOp) * C::kRows * 128 +
-         4 * (128 * kXchPitch + NT) + 8 * (2 * (C::kW + C::kB + C::kOp) + C::kB + 5) + 16 + 4 * (kMaxGroupTab + C::kRows);
+         4 * (2 * 128 * kXchPitch + NT) + 8 * (2 * (C::kW + C::kB + C::kOp) + C::kB + 5) + 16 + 4 * (kMaxGroupTab + C::kRows);
 }
 
 // What the product's fp16 rows [rows, KD] and their scales are made from: token rows (xq,
@@ -305,7 +306,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sW = base;
   uint8_t* sB = sW + C::kW * kStageW;
-  uint64_t* wfull = reinterpret_cast<uint64_t*>(sB + 2 * (kOwnB ? C::kB : C::kOp) * kHalf);
+  float* s_xch = reinterpret_cast<float*>(sB + 2 * (kOwnB ? C::kB : C::kOp) * kHalf);  // [2][128][20]
+  float* s_xs = s_xch + 2 * 128 * kXchPitch;             // [NT] row scales of the tile
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(s_xs + NT);
   uint64_t* wempty = wfull + C::kW;
   uint64_t* bfull = wempty + C::kW;
   uint64_t* bempty = bfull + C::kB;
@@ -317,9 +320,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
   uint64_t* rfull = drain + 1;  // pairs: this CTA's gathered rows of a stage
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(rfull + C::kB);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  float* s_xch = reinterpret_cast<float*>(s_abort + 1);  // [128][33]
-  float* s_xs = s_xch + 128 * kXchPitch;                 // [NT] row scales of the tile
-  int32_t* s_ts = reinterpret_cast<int32_t*>(s_xs + NT);
+  int32_t* s_ts = reinterpret_cast<int32_t*>(s_abort + 1);
   int32_t* s_off = s_ts + kMaxGroups + 2;
   int32_t* s_row = s_off + kMaxGroups + 2;               // pairs: the tokens of this CTA's rows
 
@@ -635,7 +636,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     // ---------------------------------------------------------------- epilogue
     pdl_wait();
     const int q = warp & 3, row = q * 32 + lane;
-    const int fr = row & 63, tq = row >> 6;  // up: this thread's feature and token parity
+    const int fr = row & 63, tq = row >> 6;  // up: this thread's feature and half of 32 tokens
     uint32_t d = 0, dph = 0;
     int g = 0;
     for (int t = first; t < total; t += stride) {
@@ -668,41 +669,68 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       TO* out = static_cast<TO*>(!UP && tl.shared ? p.out_sh : p.out) + (size_t)tl.orow * p.N + chan;
 #pragma unroll 1
       for (int c = 0; c < n32; ++c) {
-        uint32_t v[32];
-        tc::tmem_ld32(taddr + 32 * c, v);
-        tc::tmem_ld_wait();
-        if (c == n32 - 1) {  // read out: another tile's MMAs may start
+        auto read_out = [&] {  // after the last chunk another tile's MMAs may start
+          if (c != n32 - 1) return;
           tc::fence_before_sync();
           if (kPair) tc::mbar_arrive_remote(tc::cluster_addr(&dempty[d], 0));
           else tc::mbar_arrive(&dempty[d]);
-        }
-        const int left = nt - 32 * c;
+        };
         if (UP) {
+          // Lanes 0-63 hold gates, 64-127 the same features' up values. A thread keeps 16 of
+          // its 32 tokens and gives the other 16 to its counterpart; the largest magnitudes of
+          // 16 rows leave in one atomic instruction. This work overlaps the next tile's MMAs
+          // and still takes shared memory, issue slots and power from them: with both values
+          // through shared memory and an atomic for each row, 1001 tokens of 8 wide experts
+          // took 635 us, now 578; 8192 tokens of 160 experts 2.57 ms, now 2.48.
+          float keep[16], give[16], other[16];
+          tc::tmem_ld16(taddr + 32 * c + 16 * tq, keep);
+          tc::tmem_ld16(taddr + 32 * c + 16 * (tq ^ 1), give);
+          read_out();
+          float* xch = s_xch + (c & 1) * 128 * kXchPitch;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s_xch[row * kXchPitch + i] = __uint_as_float(v[i]);
-          asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-          TO* o = out + (size_t)(32 * c + tq) * p.N;
-          uint32_t* mx = p.row_max + tl.orow + 32 * c + tq;
-#pragma unroll 4
-          for (int i = tq; i < 32; i += 2, o += 2 * (size_t)p.N, mx += 2) {
-            if (i >= left) break;
-            const float x = s_xs[32 * c + i];
-            const float g = s_xch[fr * kXchPitch + i] * x * sc;
-            const float u = s_xch[(64 + fr) * kXchPitch + i] * x * sc3;
-            const float h = has ? __fdividef(g, 1.0f + expf(-g)) * u : 0.0f;
-            if (has) *o = Elem<TO>::from_f32(h);
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-            if (lane == 0) atomicMax(mx, m);
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(xch + row * kXchPitch + i) =
+                make_float4(give[i], give[i + 1], give[i + 2], give[i + 3]);
+          asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + (q & 1)) : "memory");
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(xch + (row ^ 64) * kXchPitch + i);
+            other[i] = f.x; other[i + 1] = f.y; other[i + 2] = f.z; other[i + 3] = f.w;
           }
-          asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-        } else if (has) {
+          const int at = 32 * c + 16 * tq, left = nt - at;
+          auto hidden = [&](const float (&gate)[16], const float (&up)[16]) {
+            TO* o = out + (size_t)at * p.N;
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, o += p.N) {
+              const float x = s_xs[at + i];
+              const float g = gate[i] * x * sc;
+              const float u = up[i] * x * sc3;
+              const float h = has ? __fdividef(g, 1.0f + expf(-g)) * u : 0.0f;
+              if (has && i < left) *o = Elem<TO>::from_f32(h);
+              const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+              if (lane == i) most = m;
+            }
+            if (lane < 16 && lane < left) atomicMax(p.row_max + tl.orow + at + lane, most);
+          };
+          if (left > 0) {
+            if (tq == 0) hidden(keep, other);
+            else hidden(other, keep);
+          }
+        } else {
+          uint32_t v[32];
+          tc::tmem_ld32(taddr + 32 * c, v);
+          tc::tmem_ld_wait();
+          read_out();
+          const int left = nt - 32 * c;
+          if (!has) continue;
           TO* o = out + (size_t)(32 * c) * p.N;
 #pragma unroll
           for (int i = 0; i < 32; ++i, o += p.N)
             if (i < left) *o = Elem<TO>::from_f32(__uint_as_float(v[i]) * s_xs[32 * c + i] * sc);
         }
       }
-      if (!UP) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");  // s_xs has been read
+      asm volatile("barrier.cta.sync 1, 128;" ::: "memory");  // s_xs has been read
       if (++d == 2) { d = 0; dph ^= 1u; }
     }
   }
