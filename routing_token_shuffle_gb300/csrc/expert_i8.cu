@@ -699,17 +699,22 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
           }
           const int at = 32 * c + 16 * tq, left = nt - at;
           auto hidden = [&](const float (&gate)[16], const float (&up)[16]) {
+            const int stop = has ? left : 0;
             TO* o = out + (size_t)at * p.N;
             uint32_t most = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i, o += p.N) {
-              const float x = s_xs[at + i];
-              const float g = gate[i] * x * sc;
-              const float u = up[i] * x * sc3;
-              const float h = has ? __fdividef(g, 1.0f + expf(-g)) * u : 0.0f;
-              if (has && i < left) *o = Elem<TO>::from_f32(h);
-              const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-              if (lane == i) most = m;
+            for (int i = 0; i < 16; i += 4) {
+              const float4 x4 = *reinterpret_cast<const float4*>(s_xs + at + i);
+              const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j, o += p.N) {
+                const float g = gate[i + j] * x[j] * sc;
+                const float u = up[i + j] * x[j] * sc3;
+                const float h = has ? __fdividef(g, 1.0f + expf(-g)) * u : 0.0f;
+                if (i + j < stop) *o = Elem<TO>::from_f32(h);
+                const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+                if (lane == i + j) most = m;
+              }
             }
             if (lane < 16 && lane < left) atomicMax(p.row_max + tl.orow + at + lane, most);
           };
@@ -722,12 +727,17 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
           tc::tmem_ld32(taddr + 32 * c, v);
           tc::tmem_ld_wait();
           read_out();
-          const int left = nt - 32 * c;
-          if (!has) continue;
+          const int stop = has ? nt - 32 * c : 0;
           TO* o = out + (size_t)(32 * c) * p.N;
 #pragma unroll
-          for (int i = 0; i < 32; ++i, o += p.N)
-            if (i < left) *o = Elem<TO>::from_f32(__uint_as_float(v[i]) * s_xs[32 * c + i] * sc);
+          for (int i = 0; i < 32; i += 4) {  // (scales read one by one: FFN prefill 2.50 ms, by four 2.38)
+            const float4 x = *reinterpret_cast<const float4*>(s_xs + 32 * c + i);
+            const float y[4] = {__uint_as_float(v[i]) * x.x * sc, __uint_as_float(v[i + 1]) * x.y * sc,
+                                __uint_as_float(v[i + 2]) * x.z * sc, __uint_as_float(v[i + 3]) * x.w * sc};
+#pragma unroll
+            for (int j = 0; j < 4; ++j, o += p.N)
+              if (i + j < stop) *o = Elem<TO>::from_f32(y[j]);
+          }
         }
       }
       asm volatile("barrier.cta.sync 1, 128;" ::: "memory");  // s_xs has been read
