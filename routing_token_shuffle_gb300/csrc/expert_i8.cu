@@ -756,15 +756,16 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
 
 // From this many rows per expert on average the wide tiles win: they read a weight byte once
 // per 160 rows and issue fewer MMAs for them; below, the weights' stream is the work, and the
-// narrow tiles keep more of it in flight. Measured (FFN, 160 experts of 5120 x 1536): 32 rows
-// 651 us narrow and 686 wide, 64 rows 845 and 736; 8 experts of 4096 x 14336: 279 and 292,
-// 368 and 325; 128 experts of 2048 x 768: 143 and 143, 189 and 182.
+// narrow tiles keep more of it in flight. Measured (FFN, narrow and wide, at 24, 40 and 64 rows):
+// 160 experts of 5120 x 1536 633 and 628, 670 and 647, 784 and 684 us; 8 experts of
+// 4096 x 14336 256 and 258, 264 and 263, 322 and 268; 128 experts of 2048 x 768 126 and 138,
+// 140 and 144, 166 and 159.
 constexpr int kWideRows = 40;
 // From this many on, 192-row tiles instead of 160 where the rows are in place: fewer MMAs a
-// row, against a third operand stage (FFN, 160 and 192 rows: 100 rows an expert 342 and 360
-// us, 175: 467 and 488, 250: 617 and 641; 307: 2440 and 2423, 512: 269 and 258, 1024: 2018 and
-// 1953).
-constexpr int kTallRows = 288;
+// row, against a third operand stage (FFN, 160 and 192 rows, 8 experts of 4096 x 14336: 100
+// rows an expert 288 and 309 us, 250: 535 and 569, 512: 975 and 980, 1024: 1706 and 1659; 160 of
+// 5120 x 1536, 307 rows: 2134 and 2156; 16 of 2048 x 2048, 512 rows: 211 and 204).
+constexpr int kTallRows = 400;
 bool wide(const smoe_desc& d) { return (long long)d.T * d.K >= (long long)kWideRows * d.E; }
 
 int i8_sm_count() {

@@ -375,6 +375,7 @@ MM = [
     (64, 6, 160, 1024, 264), (100, 8, 16, 2048, 768), (257, 2, 5, 272, 136), (7, 2, 3, 4096, 1032),
     (1000, 4, 8, 512, 640), (2000, 2, 4, 128, 256), (130, 1, 1, 1040, 3000), (513, 3, 31, 96, 200),
     (39, 1, 1, 80, 24), (40, 1, 1, 80, 24), (193, 1, 1, 208, 520), (385, 1, 1, 64, 8),
+    (900, 1, 2, 64, 1544),
 ]
 
 
@@ -505,7 +506,7 @@ def test_expert_matmul_i8_two_streams_at_once():
 
 # tokens and channels that take the narrow tiles, the wide ones that gather their rows, and
 # the wide ones whose rows are put in place (160 and 192 rows high)
-TILES = [(30, 32), (200, 32), (200, 1544), (600, 1544)]
+TILES = [(30, 32), (200, 32), (200, 1544), (600, 1544), (900, 1544)]
 
 
 @pytest.mark.parametrize("T,n_out", TILES)
@@ -590,7 +591,7 @@ FFN = [
     (1, 16, 1, 1, 16, 0), (1, 512, 8, 2, 768, 0), (5, 1024, 40, 6, 512, 2), (64, 640, 160, 6, 96, 2),
     (33, 272, 4, 3, 144, 1), (500, 256, 8, 2, 1040, 0), (300, 2048, 16, 8, 768, 0),
     (1000, 512, 4, 2, 256, 1), (193, 64, 1, 1, 48, 1), (65, 32, 2, 1, 16, 8), (150, 96, 3, 2, 784, 2),
-    (700, 128, 2, 1, 800, 0),
+    (700, 128, 2, 1, 800, 0), (900, 128, 2, 1, 800, 1),
 ]
 
 
