@@ -34,7 +34,8 @@
 // ms (6.2 TB/s of the touched weights, 0.93 of the measured copy rate), 3 tokens of 8 experts
 // of 4096 x 14336 242 us (6 TB/s), one token of 128 experts of 2048 x 768 29 us (75 MB: 11 us
 // of stream, 7 us until the routes are known, two barriers and the joining of sums). fp32, 13
-// tokens of 24 experts of 1000 x 1416 106 us: FMAs and shared memory, not HBM (53 us).
+// tokens of 24 experts of 1000 x 1416 86 us: 53 us of HBM, 11 until the routes are known, and
+// the shared expert's blocks, where FMAs and shared memory take twice the stream's time.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -74,8 +75,10 @@ struct FewArgs {
 // SM can stream twice its share of HBM's rate, so that many keep it busy, and no sums have to
 // be joined (one token of a 128-expert layer, 96 up tiles: 33 -> 30 us).
 // fp32: ranges of equal weight; a block takes longer the more tokens its expert has, and
-// equal ranges left the slowest CTA at 1.4 times the mean. Weight 2 + (groups of four
-// tokens), measured 900 clocks with one group and 1700 with four.
+// equal ranges left the slowest CTA at 1.4 times the mean. Up to 16 tokens kPackBlock + (the
+// expert's tokens): 4, 8 and 16 gave 93, 91 and 100 us with 13 tokens, 104, 98 and 105 with 16.
+// Above, 2 + (groups of four tokens): 900 clocks with one group and 1700 with four.
+constexpr int kPackBlock = 8;
 struct Range {
   int kper, unit, quot, rem;
   const int* table;  // fp32: first block of each CTA, in shared memory
@@ -302,6 +305,11 @@ constexpr int kSelectAll = kGateThreads / 32;
 // accumulator columns the epilogue adds to the first ones. Rounding H to bf16 alone made the
 // layer's error 1.4 to 1.6 times that of rounding its output; the second row is free up to 32
 // tokens (the stream from HBM is the time) and takes 64 tokens from 1.03 to 1.06 ms.
+// Floats between the rows of the exchange buffer: odd, or for 16-byte accesses an odd number
+// of them.
+template <typename TE>
+constexpr int few_xch() { return sizeof(TE) == 2 ? 17 : 20; }
+
 template <typename TE, int NP, int ND>
 __global__ void __launch_bounds__(kFewThreads, 1)
 moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
@@ -317,19 +325,27 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   constexpr uint32_t kCols = ND == 16 ? 64 : 2 * ND;
   // Consumer threads: 4 warps read the accumulators (bf16), 8 warps multiply (fp32): two
   // groups of four, which take every other block. A warp takes all 128 rows of its block, four
-  // to a lane, 16 tokens and a share of the contraction: shared memory returns 128 bytes a clock, broadcast or not, so a token's
-  // values have to serve four rows (one row a lane and all tokens: 512 clocks of shared
-  // memory for every four tokens of a block, against 712 that its load from HBM takes; now
-  // 128).
+  // to a lane, 16 tokens and a share of the contraction: shared memory returns 128 bytes a
+  // clock, broadcast or not, so a token's values have to serve four rows (one row a lane and
+  // all tokens: 512 clocks of shared memory for every four tokens of a block, against 712 that
+  // its load from HBM takes; now 128).
   constexpr int kCons = kTC ? 128 : 256;
   constexpr int kTokSplit = NP / 16, kKSplit = 8 / kTokSplit;
+  // fp32, up to 16 tokens: only the routed tokens of a block are multiplied. In the up product,
+  // whose tile is one expert's, they take the first accumulators, so that the unrolled code
+  // runs straight on and ends at the last of them: stepping over the other tokens' code, at
+  // every block, cost more than the FMAs (106 -> 91 us with 13 tokens of 3 from 24 experts).
+  // Rows of H that no routed token owns are then neither written nor read.
+  constexpr bool kPack = !kTC && NP == 16;
+  constexpr int kXch = few_xch<TE>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int S = p.stages;
   uint8_t* sA = base;
   uint8_t* sB = base + (size_t)S * kFewA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + (size_t)S * kB);
+  float* s_xch = reinterpret_cast<float*>(sB + (size_t)S * kB);  // [128][kXch], four of them for fp32
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_xch + (kTC ? 1 : 4) * 128 * kXch);
   uint64_t* empty = full + kFewMaxStages;
   uint64_t* tfull = empty + kFewMaxStages;
   uint64_t* tempty = tfull + 2;
@@ -340,10 +356,10 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   int* s_nact = s_abort + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_nact + 1);
   float* s_red = reinterpret_cast<float*>(s_tmem + 2);     // [10][32]
-  float* s_xch = s_red + kGateThreads;                     // [128][17], four of them for fp32
-  float* s_wcol = s_xch + (kTC ? 1 : 4) * 128 * 17;         // [64]
+  float* s_wcol = s_red + kGateThreads;                    // [64]
   int* s_use = reinterpret_cast<int*>(s_wcol + 64);        // [64]
-  int32_t* s_act = s_use + 64;                             // [E]
+  int* s_tok = s_use + 64;                                 // [64] token of each column (kPack)
+  int32_t* s_act = s_tok + 64;                             // [E]
   int32_t* s_idx = s_act + p.E;                            // [T K]
   float* s_w = reinterpret_cast<float*>(s_idx + p.T * p.K);
   int32_t* s_first = reinterpret_cast<int32_t*>(s_w + p.T * p.K);  // fp32: [2][kFewMaxCtas + 1]
@@ -624,11 +640,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
 #pragma unroll 1
               for (int q16 = 0; q16 < kTokSplit; ++q16) {
                 uint32_t g = (uint32_t)(m >> (16 * q16)) & 0xffffu;
-                g |= g >> 2;
-                g |= g >> 1;
-                most = max(most, __popc(g & 0x1111u));
+                if (!kPack) {
+                  g |= g >> 2;
+                  g |= g >> 1;
+                  g &= 0x1111u;
+                }
+                most = max(most, __popc(g));
               }
-              w = 2 + kTokSplit * most;
+              w = kPack ? kPackBlock + most : 2 + kTokSplit * most;
             }
             int incl = w;
 #pragma unroll
@@ -644,7 +663,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       }
       group_sync(2, kGateThreads);
       if (!kTC) {
-        const int every = 2 + kTokSplit * ((min(p.T, 16) + 3) / 4);
+        const int every = kPack ? kPackBlock + p.T : 2 + kTokSplit * ((min(p.T, 16) + 3) / 4);
         for (int i = gt; i < 2 * (nc + 1); i += kGateThreads) {
           if (i <= nc) s_first[i] = weighted_first(i, nc, 1, FB * nkd, p.S, every, s_pre, *s_nact);
           else s_first[kFewMaxCtas + i - nc] =
@@ -669,13 +688,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         for (int i = r.first(cta); i < end && ok;) {
           const int tile = i / r.kper, k0 = i - tile * r.kper;
           const int k1 = min(r.kper, k0 + end - i);
-          float acc[kTC ? 1 : 4][kTC ? 1 : 16] = {};  // [rows lane + 32 r][tokens 16 tq + t]
+          float acc[kTC ? 1 : 4][kTC ? 1 : 16] = {};  // [rows lane + 32 r][columns 16 tq + t]
           const uint32_t ta = tcount & 1u, taph = (tcount >> 1) & 1u;
           ++tcount;
           if (kTC) {
             ok = tc::mbar_wait_warp(&tfull[ta], taph, abort);
           } else {
-            // only the tokens of a block's expert: the others are not kept (up) or zero (down)
+            // only the tokens of a block's expert (above 16 tokens only their groups of four): the
+            // others are not kept (up) or zero (down)
             const unsigned long long every = ~0ull >> (64 - p.T);
             int slot = part == 2 ? k0 / nkf : slot1 + tile / FB;
             int left = part == 2 ? (slot + 1) * nkf - k0 : r.kper;
@@ -696,26 +716,48 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
               const uint8_t* b = sB + s * kB + tq * 16 * 128;
               const uint32_t on16 = (uint32_t)(on >> (16 * tq)) & 0xffffu;
 #pragma unroll
-              for (int cc = 0; cc < (kTC ? 0 : 16 / kKSplit); ++cc) {
-                if (on16 == 0) break;
-                const int c = ks % (kKSplit / 2) * (16 / kKSplit) + cc;
-                float4 av[4];
+              for (int c0 = 0; c0 < (kTC || on16 == 0 ? 0 : 16 / kKSplit); c0 += 2) {
+                const int c = ks % (kKSplit / 2) * (16 / kKSplit) + c0;
+                float4 av[2][4];
 #pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4)
-                  av[r4] = *reinterpret_cast<const float4*>(a + r4 * 4096 + ((c ^ (lane & 7)) << 4));
+                for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-                for (int t = 0; t < 16; t += 4) {
-                  if (((on16 >> t) & 15) == 0) continue;
+                  for (int r4 = 0; r4 < 4; ++r4)
+                    av[cc][r4] = *reinterpret_cast<const float4*>(a + r4 * 4096 + (((c + cc) ^ (lane & 7)) << 4));
+                auto token = [&](int j, int t) {  // accumulator j += A times row t of B
 #pragma unroll
-                  for (int u = 0; u < 4; ++u) {
-                    const float4 bv = *reinterpret_cast<const float4*>(b + (t + u) * 128 + ((c ^ ((t + u) & 7)) << 4));
+                  for (int cc = 0; cc < 2; ++cc) {
+                    const float4 bv = *reinterpret_cast<const float4*>(b + t * 128 + (((c + cc) ^ (t & 7)) << 4));
 #pragma unroll
                     for (int r4 = 0; r4 < 4; ++r4) {
-                      float& s4 = acc[kTC ? 0 : r4][kTC ? 0 : t + u];
-                      s4 = fmaf(av[r4].x, bv.x, s4);
-                      s4 = fmaf(av[r4].y, bv.y, s4);
-                      s4 = fmaf(av[r4].z, bv.z, s4);
-                      s4 = fmaf(av[r4].w, bv.w, s4);
+                      float& s4 = acc[kTC ? 0 : r4][kTC ? 0 : j];
+                      s4 = fmaf(av[cc][r4].x, bv.x, s4);
+                      s4 = fmaf(av[cc][r4].y, bv.y, s4);
+                      s4 = fmaf(av[cc][r4].z, bv.z, s4);
+                      s4 = fmaf(av[cc][r4].w, bv.w, s4);
+                    }
+                  }
+                };
+                if (kPack && part < 2) {
+                  uint32_t m = on16;
+#pragma unroll
+                  for (int j = 0; j < 16; j += 2) {
+                    if (m == 0) break;
+                    const int t0 = __ffs(m) - 1;
+                    m &= m - 1;
+                    const int t1 = m ? __ffs(m) - 1 : t0;
+                    m &= m - 1;
+                    token(j, t0);
+                    token(j + 1, t1);
+                  }
+                } else {
+#pragma unroll
+                  for (int t = 0; t < 16; t += 4) {
+                    if (((on16 >> t) & 15) == 0) continue;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                      if (kPack && ((on16 >> (t + u)) & 1) == 0) continue;
+                      token(t + u, t + u);
                     }
                   }
                 }
@@ -740,22 +782,26 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           const int li = tile / FB, fb = tile - li * FB, slot = (part == 0 ? 0 : slot1) + li;
           if (part < 2 && k0 == 0 && ct < 64) {  // the tokens of this expert and their weights
             float w = 1.0f;
-            int use = row < p.T;
+            int use = row < p.T, at = row;
             if (slot >= p.S) {
               const int e = s_act[slot - p.S];
-              use = (int)((s_mask[e] >> row) & 1);
+              const unsigned long long m = s_mask[e], before = (1ull << row) - 1;
+              use = (int)((m >> row) & 1);
 #pragma unroll 1
               for (int k = 0; k < p.K && use; ++k)
                 if (s_idx[row * p.K + k] == e) w = s_w[row * p.K + k];
+              if (kPack) at = use ? __popcll(m & before) : __popcll(m) + __popcll(~m & before);
             }
-            s_wcol[row] = w;
-            s_use[row] = use;
+            s_wcol[at] = w;
+            s_use[at] = use;
+            if (kPack) s_tok[at] = row;
           }
-          float* mine = s_xch + row * 17;
+          float* mine = s_xch + row * kXch;
+          const int cols = kPack && part < 2 && slot >= p.S ? __popcll(s_mask[s_act[slot - p.S]]) : p.T;
 #pragma unroll
           for (int c0 = 0; c0 < NP; c0 += 16) {
-            if (c0 >= p.T) break;
-            const int nt = min(16, p.T - c0);
+            if (c0 >= cols) break;
+            const int nt = min(16, cols - c0);
             if (kTC) {
               const uint32_t col = tmem + ((uint32_t)(q * 32) << 16) + ta * ND + c0;
               float v[16];
@@ -771,34 +817,43 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
             } else {
               if (c0) group_sync(1, kCons);  // the last 16 tokens' sums have been used
               // the contraction's shares: into min(kKSplit, 4) buffers, four more added to
-              // them, and the buffers' sum into the first
+              // them, and the buffers' sum into the first. By 16 bytes: this code runs once a
+              // tile, and fetching it costs as much as running it (4200 -> 1900 clocks)
               constexpr int kBuf = kKSplit < 4 ? kKSplit : 4;
-              float* buf = s_xch + (ks & 3) * 128 * 17 + lane * 17;
+              float* buf = s_xch + ((ks & 3) * 128 + lane) * kXch;
 #pragma unroll 1
               for (int k = 0; k < kKSplit; k += 4) {
                 if (tq == c0 / 16 && (ks & ~3) == k) {
 #pragma unroll
-                  for (int r4 = 0; r4 < (kTC ? 0 : 4); ++r4) {
-                    float* x = buf + 32 * r4 * 17;
-                    float old[16];
+                  for (int t = 0; t < (kTC ? 0 : 16); t += 4) {
+                    if (kPack && t >= nt) break;
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) old[t] = k == 0 ? 0.0f : x[t];
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) x[t] = old[t] + acc[kTC ? 0 : r4][kTC ? 0 : t];
+                    for (int r4 = 0; r4 < 4; ++r4) {
+                      float4* x = reinterpret_cast<float4*>(buf + 32 * r4 * kXch + t);
+                      float4 v = k == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *x;
+                      v.x += acc[kTC ? 0 : r4][kTC ? 0 : t];
+                      v.y += acc[kTC ? 0 : r4][kTC ? 0 : t + 1];
+                      v.z += acc[kTC ? 0 : r4][kTC ? 0 : t + 2];
+                      v.w += acc[kTC ? 0 : r4][kTC ? 0 : t + 3];
+                      *x = v;
+                    }
                   }
                 }
                 group_sync(1, kCons);
               }
-              {
-                float sum[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) sum[t] = mine[8 * half + t];
+              for (int t = 8 * half; t < 8 * half + 8; t += 4) {
+                if (kPack && t >= nt) break;
+                float4 sum = *reinterpret_cast<const float4*>(mine + t);
 #pragma unroll
-                for (int k = 1; k < kBuf; ++k)
-#pragma unroll
-                  for (int t = 0; t < 8; ++t) sum[t] += mine[k * 128 * 17 + 8 * half + t];
-#pragma unroll
-                for (int t = 0; t < 8; ++t) mine[8 * half + t] = sum[t];
+                for (int k = 1; k < kBuf; ++k) {
+                  const float4 v = *reinterpret_cast<const float4*>(mine + k * 128 * kXch + t);
+                  sum.x += v.x;
+                  sum.y += v.y;
+                  sum.z += v.z;
+                  sum.w += v.w;
+                }
+                *reinterpret_cast<float4*>(mine + t) = sum;
               }
               group_sync(1, kCons);
             }
@@ -822,20 +877,29 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
                 for (int c = 0; c < 16; ++c) v += in[c];
                 mine[0] = v;
               }
-            } else if (half == 0) {
+            } else {
+              constexpr int kT = kTC ? 16 : 8, kC = kPack ? 4 : 2;  // tokens of a thread, CTAs at a time
+              const int t0 = kT * half;
 #pragma unroll 1
-              for (int c = cta + 1; c < c1; c += 2) {
-                const float* src = partial + ((size_t)c * NP + c0) * 128 + row;
-                const bool one = r.any(c), two = c + 1 < c1 && r.any(c + 1);
-                float in[2][16], v[16];
+              for (int c = cta + 1; c < c1; c += kC) {
+                const float* src = partial + ((size_t)c * NP + c0 + t0) * 128 + row;
+                float in[kC][kT];
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                  in[0][t] = one && t < nt ? __ldcg(src + t * 128) : 0.0f;
-                  in[1][t] = two && t < nt ? __ldcg(src + (size_t)NP * 128 + t * 128) : 0.0f;
-                  v[t] = mine[t];
+                for (int k = 0; k < kC; ++k) {
+                  const bool on = c + k < c1 && r.any(c + k);
+#pragma unroll
+                  for (int t = 0; t < kT; ++t)
+                    in[k][t] = on && t0 + t < nt ? __ldcg(src + ((size_t)k * NP + t) * 128) : 0.0f;
                 }
+                float v[kT];
 #pragma unroll
-                for (int t = 0; t < 16; ++t) mine[t] = v[t] + in[0][t] + in[1][t];
+                for (int t = 0; t < kT; ++t) v[t] = mine[t0 + t];
+#pragma unroll
+                for (int k = 0; k < kC; ++k)
+#pragma unroll
+                  for (int t = 0; t < kT; ++t) v[t] += in[k][t];
+#pragma unroll
+                for (int t = 0; t < kT; ++t) mine[t0 + t] = v[t];
               }
             }
             if (!kTC) group_sync(1, kCons);
@@ -844,12 +908,13 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
 #pragma unroll 1
               for (int j = ct; j < 64 * nt; j += kCons) {
                 const int fr = j & 63, t = j >> 6, f = fb * 64 + fr;
-                const float g = s_xch[fr * 17 + t];
-                const float hv = g / (1.0f + expf(-g)) * s_xch[(64 + fr) * 17 + t] * s_wcol[c0 + t];
+                const float g = s_xch[fr * kXch + t];
+                const float hv = g / (1.0f + expf(-g)) * s_xch[(64 + fr) * kXch + t] * s_wcol[c0 + t];
                 if (f < p.F) {
                   const float use = s_use[c0 + t] ? hv : 0.0f;
                   const TE hi = Elem<TE>::from_f32(use);
-                  TE* out = static_cast<TE*>(p.h) + ((size_t)slot * (kTC ? 2 : 1) * p.T + c0 + t) * p.F + f;
+                  const int tok = kPack ? s_tok[t] : c0 + t;
+                  TE* out = static_cast<TE*>(p.h) + ((size_t)slot * (kTC ? 2 : 1) * p.T + tok) * p.F + f;
                   *out = hi;
                   if (kTC) {
                     const float back = Elem<TE>::to_f32(hi);
@@ -930,7 +995,7 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
             ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
             d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
   const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 +
-                      4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * 17 + 128) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K +
+                      4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * few_xch<TE>() + 192) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K +
                       (kF32 ? 4 * ((size_t)d.E + 1 + 2 * (kFewMaxCtas + 1)) : 0);
   p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + ND * 128));
   auto kern = moe_few_kernel<TE, NP, ND>;
