@@ -669,6 +669,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       TO* out = static_cast<TO*>(!UP && tl.shared ? p.out_sh : p.out) + (size_t)tl.orow * p.N + chan;
 #pragma unroll 1
       for (int c = 0; c < n32; ++c) {
+        __syncwarp();  // TMEM loads are a whole warp's: lanes that split (atomics, barriers) join
         auto read_out = [&] {  // after the last chunk another tile's MMAs may start
           if (c != n32 - 1) return;
           tc::fence_before_sync();
@@ -744,6 +745,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       if (++d == 2) { d = 0; dph ^= 1u; }
     }
   }
+  __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
   if (kPair) tc::cluster_sync();  // no signal or copy of the other CTA is on its way here

@@ -805,6 +805,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
             if (kTC) {
               const uint32_t col = tmem + ((uint32_t)(q * 32) << 16) + ta * ND + c0;
               float v[16];
+              __syncwarp();  // a whole warp's loads: lanes that split in waits and stores join
               tc::tmem_ld16(col, v);
               if (part == 2) {  // and the rests' products
                 float w[16];
@@ -950,6 +951,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
       }
     }
   }
+  __syncwarp();
   if (kTC) tc::fence_before_sync();
   __syncthreads();
   if (kTC) {
