@@ -416,7 +416,8 @@ SMOE_API int smoe_moe_forward_routed(const smoe_desc* desc, const void* x,
  *   q_out   nullable [T, d] int8: rint(n / q_scale), from n before x_out's rounding
  *   q_scale [T] fp32, needed with q_out: max |n| / 127 of the row. A row whose scale would
  *           be below the smallest normal fp32 number gets scale 0 and zeros; a row with an
- *           infinity or a NaN gets scale NaN and zeros.
+ *           infinity or a NaN, or whose sum of squares overflows fp32 (n is then 0), gets
+ *           scale NaN and zeros.
  * At least one of r_out, x_out and q_out is given. d <= 16384 (a row is held in
  * registers); else SMOE_ERR_SHAPE. No workspace.                                       */
 SMOE_API int smoe_add_rmsnorm(const smoe_desc* desc, const float* r, const void* y,

@@ -111,6 +111,19 @@ def test_add_rmsnorm_in_place():
 
 
 @pytest.mark.parametrize("d", [128, 5120])
+def test_add_rmsnorm_overflowing_row(d):
+    """A finite row whose squares overflow: n is 0 and the scale says so; its neighbour stays."""
+    g = gen(8)
+    r = randn(g, 2, d)
+    r[0] = 1e30
+    gamma = torch.ones(d, device="cuda")
+    out = norm_buffers(2, d, "f32")
+    smoe.smoe_add_rmsnorm(norm_desc(2, d, "f32"), r, gamma, eps=1e-6, **out)
+    assert (out["x_out"][0] == 0).all() and out["q_scale"][0].isnan() and (out["q_out"][0] == 0).all()
+    check_norm(norm_ref(r, None, gamma, 1e-6)[1][1:], {k: v[1:] for k, v in out.items()}, "f32")
+
+
+@pytest.mark.parametrize("d", [128, 5120])
 def test_add_rmsnorm_odd_rows(d):
     """Zero rows, tiny rows, rows with an infinity or a NaN; the rows beside them."""
     g = gen(7)
