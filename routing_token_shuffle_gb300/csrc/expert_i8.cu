@@ -23,10 +23,10 @@
 // The up product's A tile is 64 channels of W1 and the same 64 of W3.
 //
 // Measured: 384 rows over 160 experts of 5120 x 1536 188 us (6.1 TB/s of weights); 131072 rows
-// of 2048 over 128 experts of 768 channels 331 us, 1.25 PFLOP/s of fp16; the FFN of 8192
-// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.4 to 2.5 ms with the clock that
-// the power cap allows, 1.23 to 1.27 PFLOP/s; of 1001 tokens (2 of 8 experts of 4096 x 14336)
-// 578 us, 1.22 PFLOP/s.
+// of 2048 over 128 experts of 768 channels 326 us, 1.27 PFLOP/s of fp16; the FFN of 8192
+// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.3 to 2.4 ms with the clock that
+// the power cap allows, 1.27 to 1.35 PFLOP/s; of 1001 tokens (2 of 8 experts of 4096 x 14336)
+// 575 us, 1.23 PFLOP/s.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -55,7 +55,7 @@ constexpr int kMaxGroupTab = 2 * (kMaxGroups + 2);
 //     read), the pair 97; the limit is 128. 160 leaves TMEM for three operand stages, so
 //     that widening does not wait for the MMAs of the stage before last; 192 issues fewer
 //     MMAs a row (see kTallRows), and serves the gathering products, whose copies take as
-//     long for fewer rows (331 us, against 337 to 347 with 160).
+//     long for fewer rows (328 us, against 347 with 160).
 template <int NT> struct I8Cfg;
 template <> struct I8Cfg<64> { static constexpr int kW = 8, kOp = 4, kB = 0, kRows = 64; };
 template <> struct I8Cfg<160> { static constexpr int kW = 6, kOp = 3, kB = 5, kRows = 80; };
