@@ -40,16 +40,14 @@
 #include <cfloat>
 #include <climits>
 
+#include "few_ring.cuh"
 #include "tc_common.cuh"
 
 namespace smoe {
 namespace {
 
 constexpr int kFewThreads = 384;
-constexpr int kGateThreads = 320;          // warps 2-11 compute logits and select
-constexpr uint32_t kFewA = 128 * 128;      // A tile: 128 rows x 128 bytes
-constexpr int kFewMaxStages = 16;
-constexpr int kFewSmem = 227 * 1024;
+constexpr uint32_t kFewA = kFewStageA;
 
 struct FewArgs {
   const void* x;
@@ -305,11 +303,6 @@ constexpr int kSelectAll = kGateThreads / 32;
 // accumulator columns the epilogue adds to the first ones. Rounding H to bf16 alone made the
 // layer's error 1.4 to 1.6 times that of rounding its output; the second row is free up to 32
 // tokens (the stream from HBM is the time) and takes 64 tokens from 1.03 to 1.06 ms.
-// Floats between the rows of the exchange buffer: odd, or for 16-byte accesses an odd number
-// of them.
-template <typename TE>
-constexpr int few_xch() { return sizeof(TE) == 2 ? 17 : 20; }
-
 template <typename TE, int NP, int ND>
 __global__ void __launch_bounds__(kFewThreads, 1)
 moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
@@ -337,7 +330,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
   // every block, cost more than the FMAs (106 -> 91 us with 13 tokens of 3 from 24 experts).
   // Rows of H that no routed token owns are then neither written nor read.
   constexpr bool kPack = !kTC && NP == 16;
-  constexpr int kXch = few_xch<TE>();
+  constexpr int kXch = few_xch(!kTC);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -706,7 +699,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
                 left = nkf - 1;
                 on = slot < p.S ? every : s_mask[s_act[slot - p.S]];
               }
-              if (((kb - k0) & 1) != ks / (kKSplit / 2)) {  // the other group's block
+              if (few_group(kb - k0) != ks / (kKSplit / 2)) {  // the other group's block
                 if (++s == (uint32_t)S) { s = 0; ph ^= 1u; }
                 continue;
               }
@@ -996,10 +989,7 @@ cudaError_t run_few(const smoe_desc& d, const void* x, const void* w_gate, const
             ws_ptr<int32_t>(ws, L.ridx), ws_ptr<float>(ws, L.rw),
             ws_ptr<uint32_t>(ws, kFewCtl), ws_ptr<DeviceStatus>(ws, L.status),
             d.T, d.d, d.E, d.K, d.H, d.F, d.n_shared, d.renorm, 0};
-  const size_t misc = 1024 + (2 * kFewMaxStages + 6) * 8 + 8 * (size_t)d.E + 16 +
-                      4 * (kGateThreads + (kF32 ? 4 : 1) * 128 * few_xch<TE>() + 192) + 4 * (size_t)d.E + 8 * (size_t)d.T * d.K +
-                      (kF32 ? 4 * ((size_t)d.E + 1 + 2 * (kFewMaxCtas + 1)) : 0);
-  p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - misc) / (kFewA + ND * 128));
+  p.stages = few_stages(kF32, d.E, (size_t)d.T * d.K, ND);
   auto kern = moe_few_kernel<TE, NP, ND>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
   if (e != cudaSuccess) return e;

@@ -267,7 +267,6 @@ cudaError_t launch_add_rmsnorm(const smoe_desc& d, const float* r, const void* y
 // The few-token layer's own workspace (few.cu). Its grid-barrier counters live in the first
 // 256 bytes, behind the status word: they start at zero and the kernel leaves them at zero.
 constexpr int kFewMaxT = 64;
-constexpr int kFewMaxCtas = 160;   // one per SM
 constexpr size_t kFewCtl = 128;
 struct FewLayout {
   size_t status, flags, logits, ridx, rw, partial, h, total;

@@ -338,6 +338,25 @@ def test_moe_few_reads_nothing_of_an_old_workspace(dt):
         assert (ws[:256] == 0).all()  # as it was, for the next call
 
 
+# shapes whose shared memory would fit an odd number of stages
+@pytest.mark.parametrize("T,d,E,K,F", [(64, 1000, 24, 3, 712), (40, 520, 8, 2, 264), (24, 1000, 8, 2, 712),
+                                       (32, 264, 24, 3, 136), (13, 512, 160, 6, 264), (7, 256, 128, 8, 136)])
+def test_moe_few_fp32_repeats_its_bits(T, d, E, K, F):
+    """Two inputs in turn, a few hundred calls: the first call's bits every time."""
+    c = Few(T, d, E, K, 1, F, 1, "f32")
+    xs, want = [c.x, c.x.flip(1).contiguous() * 2], []
+    for c.x in xs:
+        c.run()
+        c.check()
+        want.append(c.y.clone())
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        c.x = xs[i & 1]
+        c.run()
+        wrong += (c.y != want[i & 1]).sum()
+    assert wrong.item() == 0
+
+
 def test_moe_few_two_streams_at_once():
     """Two calls with their own workspaces on two streams."""
     cs = [Few(3 + i, 768, 16, 2, 1, 384, i, "bf16", seed=i) for i in range(2)]
