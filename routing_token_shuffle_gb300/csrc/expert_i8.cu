@@ -354,6 +354,12 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     tc::tma_prefetch_map(&tmX48);
     tc::tma_prefetch_map(&tmX);
   }
+  __syncwarp();
+  if (kPair) tc::cluster_arrive();
+  if (warp == 3) group_table<NT>(p, s_ts, s_off, lane);
+  __syncwarp();
+  // the peer runs, and both CTAs' barriers are initialised before a remote signal
+  if (kPair) tc::cluster_wait();
   if (warp == 2) {
     if (kPair) {
       tc::tmem_alloc_pair(s_tmem, 512);
@@ -363,10 +369,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       tc::tmem_relinquish();
     }
   }
-  if (warp == 3) group_table<NT>(p, s_ts, s_off, lane);
   tc::fence_before_sync();
   __syncthreads();
-  if (kPair) tc::cluster_sync();  // both CTAs' barriers are initialised before a remote signal
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
   constexpr int kChan = (UP ? 64 : 128) * (kPair ? 2 : 1);

@@ -577,15 +577,19 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
     tc::tma_prefetch_map(&tmB1);
     tc::tma_prefetch_map(&tmB3);
   }
+  __syncwarp();
+  tc::cluster_arrive();
   for (int i = threadIdx.x; i <= p.G; i += kPairThreads) s_ts[i] = p.tile_start[i];
   for (int i = threadIdx.x; i <= p.E; i += kPairThreads) s_eo[i] = p.expert_off[i];
+  __syncwarp();
+  // the peer runs, and both CTAs' barriers are initialised before any remote signal
+  tc::cluster_wait();
   if (warp == 2) {
     tc::tmem_alloc_pair(s_tmem, 2 * kAccCols);
     tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();  // both CTAs' barriers are initialised before any remote signal
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
   const int total = s_ts[p.G] * p.NT;

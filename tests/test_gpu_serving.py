@@ -515,6 +515,26 @@ def test_expert_matmul_i8_scales_that_are_not_finite(T, n_out):
     assert torch.equal(out.isnan(), want)
 
 
+@pytest.mark.parametrize("T,n_out", [(6000, 1552), (2200, 1552)])
+def test_expert_matmul_i8_queued_in_place(T, n_out):
+    """Many calls queued one behind the other whose rows a kernel puts in place while the pairs of
+    the product behind it start (192 and 160 row tiles)."""
+    g = gen(14)
+    K, E, n_in = 8, 64, 1024
+    xq, wq = int8(g, T, n_in), int8(g, E, n_out, n_in)
+    src, off = rows_of(T, K, E, 3)
+    xs, sw = torch.rand(T, generator=g, device="cuda"), torch.rand(E, n_out, generator=g, device="cuda")
+    desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, "f32")
+    ws, out = smoe.workspace_i8(desc), torch.empty(T * K, n_out, device="cuda")
+    for _ in range(4):
+        for _ in range(500):
+            smoe.smoe_expert_matmul_i8(desc, xq, xs, off, wq, sw, out, ws, row_src=src)
+        smoe.smoe_get_status(ws)
+    ref, acc = matmul_ref(xq, xs, src, off, wq, sw)
+    assert acc.abs().max() < 2 ** 24
+    assert ((out.double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
+
+
 def test_expert_matmul_i8_two_streams_at_once():
     g = gen(11)
     cs = []
