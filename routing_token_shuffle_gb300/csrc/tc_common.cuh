@@ -169,6 +169,31 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same whose release covers shared memory alone, and mbar_test and mbar_wait_warp whose
+// success acquires as much: for shared memory that one CTA of the cluster wrote and another
+// reads, without waiting for the writer's stores to global memory.
+__device__ __forceinline__ void mbar_arrive_cluster_shared(uint32_t cluster_bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+      : "memory");
+}
+__device__ __forceinline__ bool mbar_test_shared(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "fence.acquire.sync_restrict::shared::cluster.cluster;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_warp_shared(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait_warp(bar, parity, abort) && __all_sync(0xffffffffu, mbar_test_shared(bar, parity));
+}
+
 // 16-byte load from another CTA of the cluster (shared::cluster address from cluster_addr).
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;

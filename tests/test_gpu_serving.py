@@ -535,6 +535,32 @@ def test_expert_matmul_i8_queued_in_place(T, n_out):
     assert ((out.double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
 
 
+@pytest.mark.parametrize("T,K,E,n_in,n_out", [(4000, 4, 8, 1024, 256), (700, 6, 20, 4096, 264),
+                                              (97, 2, 3, 272, 1536)])
+def test_expert_matmul_i8_gathered_rows_on_one_workspace(T, K, E, n_in, n_out):
+    """Calls with other rows and scales queued one behind the other on one workspace, the rows
+    gathered by pairs of CTAs: each call's output is what the call alone gives."""
+    g = gen(13)
+    wq, sw = int8(g, E, n_out, n_in), torch.rand(E, n_out, generator=g, device="cuda")
+    desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, "f32")
+    calls = []
+    for i in range(3):
+        src, off = rows_of(T, K, E, i)
+        xs = torch.rand(T, generator=g, device="cuda") * 10.0 ** i
+        calls.append((int8(g, T, n_in), xs, src, off, torch.empty(T * K, n_out, device="cuda")))
+    ws = smoe.workspace_i8(desc)
+    for _ in range(60):
+        for xq, xs, src, off, out in calls:
+            out.fill_(7.0)
+        for xq, xs, src, off, out in calls:
+            smoe.smoe_expert_matmul_i8(desc, xq, xs, off, wq, sw, out, ws, row_src=src)
+    smoe.smoe_get_status(ws)
+    for xq, xs, src, off, out in calls:
+        ref, acc = matmul_ref(xq, xs, src, off, wq, sw)
+        assert acc.abs().max() < 2 ** 24
+        assert ((out.double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
+
+
 def test_expert_matmul_i8_two_streams_at_once():
     g = gen(11)
     cs = []
