@@ -179,6 +179,8 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// (What an earlier kernel of the stream may still be writing when a kernel here starts is read
+// through L2: loads through the read-only path may be moved above the wait for that kernel.)
 // One row of the product's operand, by a warp. Token rows: row r < TK is xq[map[r]] (or
 // xq[r]), row TK + t the token t (shared experts); rows outside the segments [begin, end)
 // belong to nobody. Hidden rows: s = max |h| / 127, rint(h / s), an integer that fp16 holds;
@@ -201,7 +203,7 @@ __device__ __forceinline__ void make_row(const RowSource& p, int r, int begin, i
       uint2 b[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        b[u] = in && v + 32 * u < vecs ? __ldg(from + v + 32 * u) : make_uint2(0u, 0u);
+        b[u] = in && v + 32 * u < vecs ? __ldcg(from + v + 32 * u) : make_uint2(0u, 0u);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         uint4 o;
@@ -243,8 +245,8 @@ __device__ __forceinline__ void make_row(const RowSource& p, int r, int begin, i
 // token of each dispatched row, the zero row where it is out of range. Also clears the maxima
 // of the hidden rows that the product will write.
 __global__ void __launch_bounds__(256)
-i8_tokens_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E, int KD,
-                 int32_t* __restrict__ row_tok, uint32_t* __restrict__ clear, int nclear,
+i8_tokens_kernel(const RowSource p, const int32_t* expert_off, int E, int KD,
+                 int32_t* row_tok, uint32_t* clear, int nclear,
                  DeviceStatus* st) {
   pdl_wait_and_trigger();
   const int begin = expert_off[0], end = expert_off[E], T = p.n_src;
@@ -275,8 +277,8 @@ i8_tokens_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int 
 // behind completion counters, 131072 rows of 2048 took 401 us with their product, against
 // 376.) Also clears the maxima of the hidden rows that the product will write.
 __global__ void __launch_bounds__(256)
-i8_rows_kernel(const RowSource p, const int32_t* __restrict__ expert_off, int E, int KD,
-               uint32_t* __restrict__ clear, int nclear, DeviceStatus* st) {
+i8_rows_kernel(const RowSource p, const int32_t* expert_off, int E, int KD,
+               uint32_t* clear, int nclear, DeviceStatus* st) {
   pdl_wait_and_trigger();
   for (int i = blockIdx.x * 256 + threadIdx.x; i < nclear; i += gridDim.x * 256) clear[i] = 0u;
   const int begin = p.h ? 0 : expert_off[0], end = p.h ? p.rows : expert_off[E];
@@ -428,7 +430,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       __syncwarp();
       for (int i = 16 * cw + lane; i < mine && lane < 16; i += 16 * kCopyWarps) {
         const int r = (int)rank * mine + i;  // row of the tile
-        s_row[i] = r >= tl.rows ? p.T : tl.shared ? tl.r0 + r : __ldg(p.row_tok + tl.brow + r);
+        s_row[i] = r >= tl.rows ? p.T : tl.shared ? tl.r0 + r : __ldcg(p.row_tok + tl.brow + r);
       }
       __syncwarp();
       for (int kb = 0; kb < nk; ++kb) {
@@ -461,8 +463,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
     // The copies wrote through the generic proxy, the MMA reads through the async proxy, and the
     // leader issues it for both CTAs' rows: the proxy fence, then a release at cluster scope of
     // what is in shared memory, which the MMA warp acquires. (131072 rows of 2048 to 768
-    // channels: 327 us, 324 without the order. A release of everything waits for the epilogue's stores: 446 us,
-    // and 356 with a warp for each stage of the ring.)
+    // channels: 327 us, 324 without the order. A release of everything waits for the epilogue's
+    // stores: 446 us, and 356 with a warp for each stage of the ring.)
     const int stages = total > first ? (total - first + stride - 1) / stride * nk : 0;
     uint32_t bs = 0, ph = 0;
     bool ok = true;
@@ -658,8 +660,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
       // the tile's scales, ahead of its accumulator
       for (int i = row; i < NT; i += 128) {
         int r = tl.brow + i;
-        if (GATHER && i < nt) r = tl.shared ? tl.r0 + i : __ldg(p.row_tok + r);
-        s_xs[i] = i < nt ? __ldg(p.xs + r) : 0.0f;
+        if (GATHER && i < nt) r = tl.shared ? tl.r0 + i : __ldcg(p.row_tok + r);
+        s_xs[i] = i < nt ? __ldcg(p.xs + r) : 0.0f;
       }
       const float sc = has ? __ldg(p.sa + (size_t)tl.g * p.N + chan) : 0.0f;
       const float sc3 = UP && has ? __ldg(p.sb + (size_t)tl.g * p.N + chan) : 0.0f;

@@ -195,7 +195,7 @@ __device__ __forceinline__ void gate_logits(const FewArgs& p, float* red, int gt
       for (int j = 0; j < 4; ++j) wv[j] = __ldg(w + (size_t)min(e0 + j, p.E - 1) * nv + v);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < nt) xv[i] = __ldg(x + (size_t)(t0 + i) * nv + v);
+        if (i < nt) xv[i] = __ldcg(x + (size_t)(t0 + i) * nv + v);  // y may be the same buffer
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < nt) {

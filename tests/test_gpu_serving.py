@@ -270,6 +270,19 @@ def test_moe_few_over_its_input():
     assert torch.equal(c.x, c.y)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 30, 64])
+def test_moe_few_over_its_input_again(T, dt):
+    """The layer applied to its own output, call after call, as with separate buffers."""
+    c = Few(T, 640, 12, 2, 1, 192, 1, dt)
+    x = c.x.clone()
+    for _ in range(8):
+        c.run()
+        smoe.smoe_moe_forward_few(c.desc, x, c.w_gate, c.w1, c.w3, c.w2, x, c.ws)
+        assert torch.equal(x, c.y)
+        c.x.copy_(c.y)
+
+
 def test_moe_few_keeps_other_tokens_out():
     """A token whose states overflow its experts does not reach the other tokens."""
     c = Few(4, 256, 8, 2, 1, 128, 1, "bf16")
@@ -757,6 +770,34 @@ def test_norm_route_dispatch_ffn_combine():
     ref = c.ysh[0].double() + (w.double()[..., None] * c.y[pair_row.long()].double()).sum(1)
     mag = c.ysh[0].double().abs() + (w.double()[..., None] * c.y[pair_row.long()].double().abs()).sum(1)
     assert ((out.double() - ref).abs() <= HALF["bf16"] * ref.abs() + 8 * HALF["f32"] * mag).all()
+
+
+@pytest.mark.parametrize("T,n_out", [(40, 264), (900, 264), (900, 1608)])
+def test_norm_then_product_queued(T, n_out):
+    """Norms and the products of their rows queued one behind the other on the same buffers, two
+    inputs in turn: each product is that of its own norm's rows."""
+    g = gen(15)
+    K, E, d = 2, 3, 1024
+    wq, sw = int8(g, E, n_out, d), torch.rand(E, n_out, generator=g, device="cuda")
+    src, off = rows_of(T, K, E, 6)
+    desc = smoe.make_desc(T, d, E, K, 1, n_out, 0, 1, 1, "f32")
+    rs, gamma = [randn(g, T, d), 50 * randn(g, T, d)], 1 + 0.1 * randn(g, d)
+    q, qs = torch.empty(T, d, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    qd, qsd = torch.empty(T * K, d, dtype=torch.int8, device="cuda"), torch.empty(T * K, device="cuda")
+    ddesc = smoe.make_desc(T * K, d, E, 1, 1, n_out, 0, 1, 1, "f32")
+    ws, outs = smoe.workspace_i8(desc), torch.empty(20, 2, T * K, n_out, device="cuda")
+    rd = [r[src.long()].contiguous() for r in rs]
+    for i in range(20):
+        r = i & 1
+        smoe.smoe_add_rmsnorm(desc, rs[r], gamma, q_out=q, q_scale=qs)
+        smoe.smoe_expert_matmul_i8(desc, q, qs, off, wq, sw, outs[i, 0], ws, row_src=src)
+        smoe.smoe_add_rmsnorm(ddesc, rd[r], gamma, q_out=qd, q_scale=qsd)
+        smoe.smoe_expert_matmul_i8(desc, qd, qsd, off, wq, sw, outs[i, 1], ws)
+    smoe.smoe_get_status(ws)
+    for r in (0, 1):
+        smoe.smoe_add_rmsnorm(desc, rs[r], gamma, q_out=q, q_scale=qs)
+        ref, _ = matmul_ref(q, qs, src, off, wq, sw)
+        assert ((outs[r::2].double() - ref).abs() <= 2.1 * HALF["f32"] * ref.abs()).all()
 
 
 def test_the_8bit_layer_captured():
