@@ -410,7 +410,7 @@ SMOE_API int smoe_moe_forward_routed(const smoe_desc* desc, const void* x,
  * counterpart): h = r + y, n = h gamma / sqrt(mean(h^2) + eps) over each row, in fp32.
  *   r       [T, d] fp32 residual (as in smoe_prefetch_predict)
  *   y       nullable [T, d] dtype: what is added to it (a layer output)
- *   gamma   [d] fp32;  eps >= 0
+ *   gamma   [d] fp32;  0 <= eps <= 1 (eps = 0: a row of zeros gives zeros)
  *   r_out   nullable [T, d] fp32: h (may be the same buffer as r)
  *   x_out   nullable [T, d] dtype: n (may be the same buffer as y)
  *   q_out   nullable [T, d] int8: rint(n / q_scale), from n before x_out's rounding

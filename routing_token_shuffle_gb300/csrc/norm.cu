@@ -18,6 +18,11 @@ namespace {
 // Rows of at most 1024 elements take one warp each (8 rows per block), longer ones a block.
 constexpr int kWarpRowMax = 1024;
 
+// An eps below this does not hide what a sum of squares below it has lost to underflow: such
+// calls take a form of the kernel with a second pass over such rows (kNoEps). In every call its
+// registers would cost 8192 rows of 5120 134 us, against 85.
+constexpr float kNoEpsBelow = 0x1p-100f;
+
 struct NormArgs {
   const float* r;
   const void* y;       // nullable
@@ -49,7 +54,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
 
 // One row per group of kThreads threads (a warp or the block); thread i holds the 8-element
 // chunks i, i + kThreads, ... of it.
-template <typename TE, int kChunks, bool kWarp>
+template <typename TE, int kChunks, bool kWarp, bool kNoEps>
 __global__ void __launch_bounds__(1024)
 add_rmsnorm_kernel(const NormArgs p) {
   pdl_wait_and_trigger();
@@ -63,59 +68,81 @@ add_rmsnorm_kernel(const NormArgs p) {
        row += (long long)gridDim.x * rows_per_block) {
     const size_t base = (size_t)row * p.d;
     float h[kChunks][8];
-    float sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int ch = me + c * nthr;
-      if (ch >= nchunk) continue;
-      load8(p.r + base + ch * 8, h[c]);
-      if (p.y) {
-        float v[8];
-        load8(static_cast<const TE*>(p.y) + base + ch * 8, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[c][i] += v[i];
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int ch = me + c * nthr;
-      if (ch >= nchunk) continue;
-      if (p.r_out) store8(p.r_out + base + ch * 8, h[c]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
-    }
-    // |h gamma| is compared as an unsigned integer: the order of the magnitudes, and a NaN
-    // is above every number, so a row that holds one does not pass for a finite row
-    uint32_t big = 0;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int ch = me + c * nthr;
-      if (ch >= nchunk) continue;
-      float g[8];
-      load8(p.gamma + ch * 8, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[c][i] *= g[i];
-        big = max(big, __float_as_uint(h[c][i]) & 0x7fffffffu);
-      }
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    big = __reduce_max_sync(0xffffffffu, big);
-    if (!kWarp) {
-      __syncthreads();  // the previous row's sums have been read
-      if (lane == 0) {
-        s_sum[warp] = sum;
-        s_max[warp] = big;
-      }
-      __syncthreads();
+    float sum, eps = p.eps, up = 1.0f;
+    uint32_t big;
+    const float* r = p.r;
+    const void* y = p.y;
+    // kNoEps: a row whose squares fp32 holds with few bits or not at all is taken twice, the
+    // second time 2^100 times as large, which is exact (its values are below 2^-50). r_out has
+    // been written by then and is read back, as it may be r.
+#pragma unroll 1
+    for (;;) {
       sum = 0.0f;
-      for (int w = 0; w < (int)blockDim.x >> 5; ++w) {
-        sum += s_sum[w];
-        big = max(big, s_max[w]);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int ch = me + c * nthr;
+        if (ch >= nchunk) continue;
+        load8(r + base + ch * 8, h[c]);
+        if (y) {
+          float v[8];
+          load8(static_cast<const TE*>(y) + base + ch * 8, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[c][i] += v[i];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int ch = me + c * nthr;
+        if (ch >= nchunk) continue;
+        if (p.r_out && (!kNoEps || up == 1.0f)) store8(p.r_out + base + ch * 8, h[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (kNoEps) h[c][i] *= up;
+          sum = fmaf(h[c][i], h[c][i], sum);
+        }
+      }
+      // |h gamma| is compared as an unsigned integer: the order of the magnitudes, and a NaN
+      // is above every number, so a row that holds one does not pass for a finite row
+      big = 0;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int ch = me + c * nthr;
+        if (ch >= nchunk) continue;
+        float g[8];
+        load8(p.gamma + ch * 8, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[c][i] *= g[i];
+          big = max(big, __float_as_uint(h[c][i]) & 0x7fffffffu);
+        }
+      }
+#pragma unroll
+      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      big = __reduce_max_sync(0xffffffffu, big);
+      if (!kWarp) {
+        __syncthreads();  // the previous sums have been read
+        if (lane == 0) {
+          s_sum[warp] = sum;
+          s_max[warp] = big;
+        }
+        __syncthreads();
+        sum = 0.0f;
+        for (int w = 0; w < (int)blockDim.x >> 5; ++w) {
+          sum += s_sum[w];
+          big = max(big, s_max[w]);
+        }
+      }
+      if (!kNoEps || up != 1.0f || !(sum < kNoEpsBelow)) break;
+      up = 0x1p100f;
+      eps = eps * 0x1p100f * 0x1p100f;
+      if (p.r_out) {
+        r = p.r_out;
+        y = nullptr;
       }
     }
-    const float rs = 1.0f / sqrtf(sum / (float)p.d + p.eps);
+    // (a row of zeros without an eps: zeros)
+    const float mean = sum / (float)p.d + eps;
+    const float rs = kNoEps && mean == 0.0f ? 0.0f : 1.0f / sqrtf(mean);
     const float amax = __uint_as_float(big) * rs;
     // a row whose scale would be subnormal counts as zero; a row with an infinity or a NaN
     // gets the scale NaN and zeros, so that what is computed from it shows it
@@ -152,22 +179,27 @@ add_rmsnorm_kernel(const NormArgs p) {
   }
 }
 
-template <typename TE>
+template <typename TE, bool kNoEps>
 cudaError_t run_norm(const NormArgs& p, cudaStream_t s) {
   const int nchunk = p.d >> 3;
   if (p.d <= kWarpRowMax) {
     const int grid = ceil_div(p.T, 8);
-    if (nchunk <= 32) SMOE_LAUNCH((add_rmsnorm_kernel<TE, 1, true>), grid, 256, 0, s, p);
-    else SMOE_LAUNCH((add_rmsnorm_kernel<TE, 4, true>), grid, 256, 0, s, p);
+    if (nchunk <= 32) SMOE_LAUNCH((add_rmsnorm_kernel<TE, 1, true, kNoEps>), grid, 256, 0, s, p);
+    else SMOE_LAUNCH((add_rmsnorm_kernel<TE, 4, true, kNoEps>), grid, 256, 0, s, p);
     return cudaGetLastError();
   }
   // one chunk a thread: 3.6 us for 64 rows of 5120, against 4.4 with two; two where a block
   // of one would pass 768 threads (4096 rows of 8192: 79 us, against 84)
   const int per = p.d <= 6144 ? 1 : 2;
   const int threads = (ceil_div(nchunk, per) + 31) / 32 * 32;
-  if (per == 1) SMOE_LAUNCH((add_rmsnorm_kernel<TE, 1, false>), p.T, threads, 0, s, p);
-  else SMOE_LAUNCH((add_rmsnorm_kernel<TE, 2, false>), p.T, threads, 0, s, p);
+  if (per == 1) SMOE_LAUNCH((add_rmsnorm_kernel<TE, 1, false, kNoEps>), p.T, threads, 0, s, p);
+  else SMOE_LAUNCH((add_rmsnorm_kernel<TE, 2, false, kNoEps>), p.T, threads, 0, s, p);
   return cudaGetLastError();
+}
+
+template <typename TE>
+cudaError_t run_norm_t(const NormArgs& p, cudaStream_t s) {
+  return p.eps < kNoEpsBelow ? run_norm<TE, true>(p, s) : run_norm<TE, false>(p, s);
 }
 
 }  // namespace
@@ -176,7 +208,7 @@ cudaError_t launch_add_rmsnorm(const smoe_desc& d, const float* r, const void* y
                                const float* gamma, float eps, float* r_out, void* x_out,
                                int8_t* q_out, float* q_scale, cudaStream_t s) {
   const NormArgs p{r, y, gamma, r_out, x_out, q_out, q_scale, d.T, d.d, eps};
-  return d.dtype == SMOE_F32 ? run_norm<float>(p, s) : run_norm<__nv_bfloat16>(p, s);
+  return d.dtype == SMOE_F32 ? run_norm_t<float>(p, s) : run_norm_t<__nv_bfloat16>(p, s);
 }
 
 }  // namespace smoe

@@ -110,6 +110,43 @@ def test_add_rmsnorm_in_place():
     assert torch.equal(r, a["r_out"]) and torch.equal(y, a["x_out"])
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-31, 1e-29])
+@pytest.mark.parametrize("d", [128, 1000, 5120, 8200])
+def test_add_rmsnorm_tiny_rows(d, eps):
+    """Rows whose squares fp32 does not hold, with an eps of zero or as small: the norm all the
+    same; a row of zeros gives zeros. Each combination of outputs, and r_out over r."""
+    g = gen(16)
+    r = randn(g, 7, d)
+    r[1] = 0.0
+    for i, s in ((2, 1e-15), (3, 1e-20), (4, 1e-30), (5, 3e-41)):
+        r[i] *= s
+    r[6] *= 1e-30
+    r[6, 5] = 1e-19
+    gamma = 1 + 0.3 * randn(g, d)
+    n = norm_ref(r, None, gamma, eps)[1]
+    if eps == 0:
+        n[1] = 0.0
+    desc = norm_desc(7, d, "f32")
+    first = norm_buffers(7, d, "f32")
+    smoe.smoe_add_rmsnorm(desc, r, gamma, eps=eps, **first)
+    # above eps = 2^-100 h gamma is not scaled: row 5's products are below fp32's normal numbers
+    good = [0, 1, 2, 3, 4, 6] + ([5] if eps < 2.0 ** -100 else [])
+    check_norm(n[good], {k: v[good] for k, v in first.items()}, "f32")
+    assert first["q_scale"][1] == 0 and (first["q_out"][1] == 0).all() and (first["x_out"][1] == 0).all()
+    out = norm_buffers(7, d, "f32", r=False)
+    smoe.smoe_add_rmsnorm(desc, r, gamma, eps=eps, **out)
+    y = r * 0.5  # r / 2 + r / 2 is r, but for the smallest values' last bit
+    keep = [0, 1, 2, 3, 4, 6]
+    summed = norm_buffers(7, d, "f32", r=False)
+    smoe.smoe_add_rmsnorm(desc, r - y, gamma, y=y, eps=eps, **summed)
+    for k in ("x_out", "q_out", "q_scale"):
+        assert torch.equal(out[k], first[k]) and torch.equal(summed[k][keep], first[k][keep]), k
+    x = torch.empty_like(r)
+    r2 = r.clone()
+    smoe.smoe_add_rmsnorm(desc, r2, gamma, r_out=r2, x_out=x, eps=eps)
+    assert torch.equal(r2, r) and torch.equal(x, first["x_out"])
+
+
 @pytest.mark.parametrize("d", [128, 5120])
 def test_add_rmsnorm_overflowing_row(d):
     """A finite row whose squares overflow: n is 0 and the scale says so; its neighbour stays."""

@@ -134,3 +134,9 @@ def test_binding_refuses_weights_of_another_expert_count(lib):
     z = torch.zeros(16)
     with pytest.raises(ValueError, match="7 experts"):
         B.smoe_expert_matmul_i8(desc(), z, z, z, torch.zeros(7, 16, 16, dtype=torch.int8), z, z, z, stream=0)
+
+
+def test_norm_eps_is_at_most_one(lib):
+    f, d = lib.smoe_add_rmsnorm, desc(T=0)
+    for eps, code in ((0.0, 0), (1.0, 0), (1.5, -1), (float("inf"), -1)):
+        assert f(ref(d), 16, None, 16, eps, 16, None, None, None, None) == code, eps
