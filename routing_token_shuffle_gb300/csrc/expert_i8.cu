@@ -403,10 +403,13 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         if (++ws == C::kW) { ws = 0; wph ^= 1u; }
       }
     }
-    if (!ok && lead) {
-      *abort = 1;
-      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      // let the copies already issued land before the CTA's shared memory goes away
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // the copies in flight land before the CTA's shared memory goes away, also where it was
+      // another role that gave up
       volatile int never = 0;
       for (uint32_t j = wit > C::kW ? wit - C::kW : 0; j < wit; ++j)
         tc::mbar_wait(&wfull[j % C::kW], (j / C::kW) & 1u, &never);
@@ -520,13 +523,21 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
         if (++bs == kRing) { bs = 0; bph ^= 1u; }
       }
     }
-    if (!ok && lead) {
-      *abort = 1;
-      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      // as above; a barrier that others share may never complete: wait out the limit once
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // as above, the leader for both CTAs' copies; a barrier that others share may never
+      // complete: then the limit is waited out once. So does a peer where a role gave up: its
+      // copies may be of stages that the leader did not get to.
       volatile int never = 0;
-      for (uint32_t j = bit > kRing ? bit - kRing : 0; j < bit && rank == 0; ++j)
-        if (!tc::mbar_wait(&bar[j % kRing], (j / kRing) & 1u, &never)) break;
+      if (rank == 0) {
+        for (uint32_t j = bit > kRing ? bit - kRing : 0; j < bit; ++j)
+          if (!tc::mbar_wait(&bar[j % kRing], (j / kRing) & 1u, &never)) break;
+      } else if (*abort) {
+        tc::wait_out();
+      }
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {

@@ -145,12 +145,12 @@ __device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
 __device__ __forceinline__ void add_release(uint32_t* p) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
-// bounded wait for *p >= want
-__device__ __forceinline__ bool wait_ge(const uint32_t* p, uint32_t want, volatile int* abort) {
-  if (ld_acquire(p) >= want) return true;
+// bounded wait for *p >= want (signed: a counter that starts below zero is that much short)
+__device__ __forceinline__ bool wait_ge(const uint32_t* p, int want, volatile int* abort) {
+  if ((int)ld_acquire(p) >= want) return true;
   const unsigned long long t0 = tc::globaltimer();
   for (uint32_t i = 1;; ++i) {
-    if (ld_acquire(p) >= want) return true;
+    if ((int)ld_acquire(p) >= want) return true;
     if ((i & 63u) == 0 && (*abort || tc::globaltimer() - t0 > tc::kWaitTimeoutNs)) return false;
   }
 }
@@ -481,7 +481,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           step(part, r, ahead);
           next_stage();
         }
-        if (ok) ok = __all_sync(0xffffffffu, !lead || wait_ge(p.ctl + 1, (uint32_t)nc, abort));
+        if (ok) ok = __all_sync(0xffffffffu, !lead || wait_ge(p.ctl + 1, nc, abort));
         // H was written by other SMs through the generic proxy
         asm volatile("fence.proxy.async.global;" ::: "memory");
         // (also after a wait that gave up: the stages' byte counts must complete)
@@ -502,10 +502,13 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         next_stage();
       }
     }
-    if (!ok && lead) {
-      *abort = 1;
-      record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
-      // let the copies already issued land before the CTA's shared memory goes away
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutFew, cta);
+      }
+      // the copies in flight land before the CTA's shared memory goes away, also where it was
+      // another role that gave up
       volatile int never = 0;
       const uint32_t firstj = it > (uint32_t)S ? it - S : 0;
       for (uint32_t j = firstj; j < it; ++j) tc::mbar_wait(&full[j % S], (j / S) & 1u, &never);
@@ -568,7 +571,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
     if (gt == 0) {
       for (int q = 0; q < 3; ++q) p.flags[q * kFewMaxCtas + cta] = 0;
       add_release(p.ctl);  // after every write of this CTA that the barrier ordered before it
-      ok = wait_ge(p.ctl, (uint32_t)nc, abort);
+      ok = wait_ge(p.ctl, nc, abort);
     }
     ok = group_and(2, kGateThreads, ok);
     if (ok) {
@@ -596,7 +599,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
         if (p.T > kSelectAll && lane == 0) add_release(p.ctl + 2);
       }
       if (p.T > kSelectAll) {
-        if (gt == 0) ok = wait_ge(p.ctl + 2, (uint32_t)p.T, abort);
+        if (gt == 0) ok = wait_ge(p.ctl + 2, p.T, abort);
         ok = group_and(2, kGateThreads, ok);
         for (int i = gt; ok && i < p.T * p.K; i += kGateThreads) {
           s_idx[i] = __ldcg(p.ridx + i);
@@ -765,7 +768,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmX,   // [T, d], NP-row box
           if (k0 == 0 && k1 != r.kper) {
             while (r.first(c1) < (tile + 1) * r.kper) ++c1;  // cta + 1 .. c1 - 1 hold the rest
             for (int c = cta + 1 + ct; c < c1; c += kCons)
-              if (r.any(c)) ok = ok && wait_ge(flags + c, 1u, abort);
+              if (r.any(c)) ok = ok && wait_ge(flags + c, 1, abort);
           }
           // one outcome for the consumer warps, which go on to barriers together
           ok = group_and(1, kCons, ok);

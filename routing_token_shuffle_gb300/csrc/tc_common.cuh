@@ -84,6 +84,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The limit of a wait, for copies whose completion this thread cannot see.
+__device__ __forceinline__ void wait_out() {
+  const unsigned long long t0 = globaltimer();
+  while (globaltimer() - t0 <= kWaitTimeoutNs) __nanosleep(1000);
+}
+
 // True in one lane of a converged warp. A role that issues TMA or tcgen05.mma runs as a
 // whole warp and issues under this predicate: their operands are warp-uniform registers,
 // and inside a branch on the lane number moving them there cost 119 clocks per

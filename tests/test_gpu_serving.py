@@ -407,6 +407,30 @@ def test_moe_few_fp32_repeats_its_bits(T, d, E, K, F):
     assert wrong.item() == 0
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,counter", [(4, 0), (4, 1), (24, 0), (24, 1), (24, 2)])
+def test_moe_few_a_wait_that_runs_out(T, counter, dt):
+    """A counter of the kernel's (first barrier, second barrier, selected tokens) that starts one
+    short: every wait for it runs into its limit, the status says so, and the workspace serves
+    the next call as before."""
+    c = Few(T, 512, 16, 2, 1, 320, 1, dt)
+    c.run()
+    c.check()
+    want = c.y.clone()
+    words = c.ws[:256].view(torch.int32)
+    words[32 + counter] = -1
+    c.run()
+    with pytest.raises(smoe.SmoeError) as e:
+        smoe.smoe_get_status(c.ws)
+    assert e.value.code == -7
+    assert (words == 0).all()
+    for _ in range(3):
+        c.y.fill_(3.0)
+        c.run()
+        smoe.smoe_get_status(c.ws)
+        assert torch.equal(c.y, want)
+
+
 def test_moe_few_two_streams_at_once():
     """Two calls with their own workspaces on two streams."""
     cs = [Few(3 + i, 768, 16, 2, 1, 384, i, "bf16", seed=i) for i in range(2)]
