@@ -3,8 +3,8 @@
 // and the SwiGLU FFN made of three of them, its hidden rows requantised in between.
 //
 // GB300's tensor cores have no fast 8-bit integer rate, but every int8 value is exact in
-// fp16, every product of two is below 2^14, and the accumulator is fp32: the fp16 products
-// give the integer sum exactly while it stays below 2^24. So the rows are widened to fp16
+// fp16, every product of two is at most 2^14, and the accumulator is fp32: the fp16 products
+// give the integer sum exactly while it stays within 2^24. So the rows are widened to fp16
 // once (they are small), the weights travel and are staged as bytes (what bounds a decode
 // batch is their stream from HBM) and are widened on the way into the tensor core: warps
 // read the staged bytes, turn them into fp16 pairs (1.25 instructions a value: the byte with

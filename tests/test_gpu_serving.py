@@ -320,6 +320,28 @@ def test_moe_few_over_its_input_again(T, dt):
         c.x.copy_(c.y)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [5, 20])
+def test_moe_few_weights_that_are_not_finite(T, dt):
+    """A weight of W2 that is not finite: its expert's tokens get it at its channel; the other
+    channels keep their bits, and an expert that no token is routed to changes nothing."""
+    c = Few(T, 256, 64, 2, 1, 96, 0, dt)
+    c.run()
+    clean = c.y.clone()
+    touched = sorted(set(c.idx.flatten().tolist()))
+    e, other = touched[1], next(i for i in range(64) if i not in touched)
+    c.w2[other] = math.nan
+    c.run()
+    assert torch.equal(c.y, clean)
+    c.w2[e, 77, 5] = math.inf
+    c.run()
+    keep = [i for i in range(256) if i != 77]
+    assert torch.equal(c.y[:, keep], clean[:, keep])
+    routed = (c.idx == e).any(1)
+    assert not c.y[routed, 77].isfinite().any()
+    smoe.smoe_get_status(c.ws)
+
+
 def test_moe_few_keeps_other_tokens_out():
     """A token whose states overflow its experts does not reach the other tokens."""
     c = Few(4, 256, 8, 2, 1, 128, 1, "bf16")
@@ -757,6 +779,30 @@ def test_expert_ffn_i8(T, d, E, K, F, S, dt):
     c.y.fill_(3.0)
     c.run()
     assert torch.equal(first, c.y)
+
+
+# tokens (of 2 experts each, of 3) and hidden channels that take the narrow tiles, the wide ones
+# that gather their rows, and the wide ones whose rows are put in place (160 and 192 rows high)
+@pytest.mark.parametrize("S", [0, 1])
+@pytest.mark.parametrize("T,F", [(20, 64), (300, 64), (300, 800), (1000, 800)])
+def test_expert_ffn_i8_padded_batch(T, F, S):
+    """Rows in front of the first segment and behind the last one name no token: they are neither
+    read nor written, whatever an old workspace holds."""
+    c = Ffn8(T, 128, 3, 2, F, S, "f32")
+    n, lead = T * 2, 7
+    e = torch.sort(torch.randint(0, 3, (n - lead - 11,), generator=torch.Generator().manual_seed(T))).values
+    src = torch.randint(0, T, (len(e),), generator=torch.Generator().manual_seed(T + 1)).int().cuda()
+    c.src = torch.cat([torch.full((lead,), T, dtype=torch.int32, device="cuda"), src,
+                       torch.full((11,), -1, dtype=torch.int32, device="cuda")])
+    off = torch.zeros(4, dtype=torch.int64)
+    off[1:] = torch.cumsum(torch.bincount(e, minlength=3), 0)
+    c.off = (off + lead).int().cuda()
+    c.ws[256:] = 0xFF
+    for _ in range(2):  # the second call on what the first one left
+        c.y.fill_(7.0)
+        c.run()
+        c.check()
+        assert (c.y[:lead] == 7.0).all() and (c.y[n - 11:] == 7.0).all()
 
 
 def test_expert_ffn_i8_rows_in_dispatched_order():
