@@ -279,12 +279,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     if (!ok) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      // let the copies already issued land before the CTA's shared memory goes away
-      volatile int never = 0;
-      const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0;
-      for (uint32_t j = first; j < it; ++j)
-        tc::mbar_wait(&full[j % kStages], (j / kStages) & 1u, &never);
     }
+    // the copies in flight land before shared memory goes away, whichever role gave up
+    volatile int never = 0;
+    const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0;
+    for (uint32_t j = first; j < it; ++j)
+      tc::mbar_wait(&full[j % kStages], (j / kStages) & 1u, &never);
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
     uint32_t it = 0, tcount = 0;
@@ -631,6 +631,16 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
     if (!ok) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+    // The copies in flight land before shared memory goes away, whichever role gave up: the
+    // leader waits for both CTAs' (a barrier that the peer did not get to never completes: then
+    // the limit is waited out once), the peer cannot see its own complete.
+    volatile int never = 0;
+    if (rank == 0) {
+      for (uint32_t j = it > (uint32_t)kPairStages ? it - kPairStages : 0; j < it; ++j)
+        if (!tc::mbar_wait(&full[j % kPairStages], (j / kPairStages) & 1u, &never)) break;
+    } else if (*abort) {
+      tc::wait_out();
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---------------------------------------------------------------- MMA issuer (leader)

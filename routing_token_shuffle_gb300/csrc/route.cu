@@ -479,11 +479,11 @@ gate_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     if (!ok) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      volatile int never = 0;
-      const uint32_t first = it > nst ? it - nst : 0;
-      for (uint32_t j = first; j < it; ++j)
-        tc::mbar_wait(&full[j % nst], (j / nst) & 1u, &never);
     }
+    // the copies in flight land before shared memory goes away, whichever role gave up
+    volatile int never = 0;
+    const uint32_t first = it > nst ? it - nst : 0;
+    for (uint32_t j = first; j < it; ++j) tc::mbar_wait(&full[j % nst], (j / nst) & 1u, &never);
   } else if (warp == 1 && lane == 0) {
     uint32_t it = 0;
     bool ok = true;
@@ -664,10 +664,11 @@ route_fused_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     if (!ok) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
-      volatile int never = 0;
-      const uint32_t first = it > nst ? it - nst : 0;
-      for (uint32_t j = first; j < it; ++j) tc::mbar_wait(&full[j % nst], (j / nst) & 1u, &never);
     }
+    // the copies in flight land before shared memory goes away, whichever role gave up
+    volatile int never = 0;
+    const uint32_t first = it > nst ? it - nst : 0;
+    for (uint32_t j = first; j < it; ++j) tc::mbar_wait(&full[j % nst], (j / nst) & 1u, &never);
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
     uint32_t it = 0;
