@@ -413,7 +413,9 @@ SMOE_API int smoe_moe_forward_routed(const smoe_desc* desc, const void* x,
  *   gamma   [d] fp32;  0 <= eps <= 1 (eps = 0: a row of zeros gives zeros)
  *   r_out   nullable [T, d] fp32: h (may be the same buffer as r)
  *   x_out   nullable [T, d] dtype: n (may be the same buffer as y)
- *   q_out   nullable [T, d] int8: rint(n / q_scale), from n before x_out's rounding
+ *   q_out   nullable [T, d] int8: n / q_scale rounded to an integer, from n before x_out's
+ *           rounding; computed as n times 1 / q_scale, so that a value within 2^-22 of half-way
+ *           between two integers (relative to it) may go to either
  *   q_scale [T] fp32, needed with q_out: max |n| / 127 of the row. A row whose scale would
  *           be below the smallest normal fp32 number gets scale 0 and zeros; a row with an
  *           infinity or a NaN, or whose sum of squares overflows fp32 (n is then 0), gets
@@ -437,8 +439,8 @@ SMOE_API size_t smoe_few_workspace_size(const smoe_desc* desc);
  * it is and in bf16 layers as the sum of two bf16 values (16 bits of it), and its sum over the
  * experts stays in fp32 until y: y's rounding is the layer's error. fp32 layers multiply in
  * fp32 (not tf32). The result does not depend on timing. A token's products stay apart from
- * the other tokens', but the weights of W2 have to be finite: one that is not reaches every
- * token of the call.
+ * the other tokens', but the weights of W2 of the touched experts have to be finite: one that
+ * is not reaches every token of the call, at its output channel.
  *   x [T, d] dtype; w_gate [E, d] dtype; w1, w3 [E+n_shared, F, d], w2 [E+n_shared, d, F]
  *   dtype; y [T, d] dtype (may be the same buffer as x)
  *   logits nullable [T, E] fp32; topk_idx nullable [T, K] int32, topk_w nullable [T, K]
@@ -463,7 +465,8 @@ typedef struct smoe_i8_weights {
 } smoe_i8_weights;
 
 /* Bytes of the workspace of smoe_expert_matmul_i8 and smoe_expert_ffn_i8 for this shape
- * (of the same manner as every workspace). Returns 0 if the descriptor is invalid. */
+ * (of the same manner as every workspace). One size for both: it holds the FFN's hidden rows
+ * also where a program calls the product alone. Returns 0 if the descriptor is invalid. */
 SMOE_API size_t smoe_i8_workspace_size(const smoe_desc* desc);
 
 /* Grouped product in 8-bit integers with a scale per row and per output channel: for every
@@ -488,7 +491,9 @@ SMOE_API int smoe_expert_matmul_i8(const smoe_desc* desc, int n_out, int n_in, c
 
 /* The grouped SwiGLU expert FFN of smoe_expert_ffn in 8-bit integers: products as
  * smoe_expert_matmul_i8; the hidden row h = silu(g) u, in fp32, is requantised with its own
- * scale max |h| / 127 (and smoe_add_rmsnorm's rules for zero and non-finite rows).
+ * scale max |h| / 127 (and smoe_add_rmsnorm's rules for half-way values and for zero and
+ * non-finite rows). silu divides with an error of up to 2 units in the last place, and gives 0
+ * for gates below -87.3, where silu is above -1.1e-36.
  *   xq, x_scale, row_src, expert_off as in smoe_expert_matmul_i8 with n_in = d; row_src is
  *   needed when n_shared > 0 (shared expert j runs on all T rows of xq)
  *   y_disp   [T K, d] dtype

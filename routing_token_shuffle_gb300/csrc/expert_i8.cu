@@ -22,11 +22,11 @@
 //               magnitude, by an integer atomicMax, whose result has no order)
 // The up product's A tile is 64 channels of W1 and the same 64 of W3.
 //
-// Measured: 384 rows over 160 experts of 5120 x 1536 188 us (6.1 TB/s of weights); 131072 rows
-// of 2048 over 128 experts of 768 channels 326 us, 1.27 PFLOP/s of fp16; the FFN of 8192
-// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.3 to 2.4 ms with the clock that
-// the power cap allows, 1.27 to 1.35 PFLOP/s; of 1001 tokens (2 of 8 experts of 4096 x 14336)
-// 575 us, 1.23 PFLOP/s.
+// Measured: 384 rows over 160 experts of 5120 x 1536 184 to 187 us (6.2 TB/s of weights); 131072
+// rows of 2048 over 128 experts of 768 channels 326 us, 1.26 PFLOP/s of fp16; the FFN of 8192
+// tokens (6 of 160 experts and two shared ones, 5120 x 1536) 2.26 to 2.4 ms with the clock that
+// the power cap allows, 1.29 to 1.37 PFLOP/s; of 1001 tokens (2 of 8 experts of 4096 x 14336)
+// 547 to 580 us, 1.22 to 1.29 PFLOP/s.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -735,6 +735,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmWa,   // weights as 16-bit 
               for (int j = 0; j < 4; ++j, o += p.N) {
                 const float g = gate[i + j] * x[j] * sc;
                 const float u = up[i + j] * x[j] * sc3;
+                // (the fast division: 2 units in the last place, and 7 bits are kept of h)
                 const float h = has ? __fdividef(g, 1.0f + expf(-g)) * u : 0.0f;
                 if (i + j < stop) *o = Elem<TO>::from_f32(h);
                 const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
@@ -854,9 +855,9 @@ cudaError_t run_rows(const RowSource& r, const int32_t* expert_off, int E, int K
 // Up to this many output channels a product of wide tiles gathers its rows from the widened
 // tokens; above, a kernel puts them in place and TMA loads them. Gathering spares writing
 // every row (K times the tokens) and slows the product by about a tenth, which more channels
-// make dearer. Measured (in place, gathered): 131072 rows of 2048: 256 channels 226, 127 us;
-// 768: 366, 318; 1536: 595, 601. 49152 rows of 5120: 1024 channels 465, 417; 1536: 627, 593.
-// 16384 rows of 4096: 1024 channels 112, 109; 2048: 185, 194; 4096: 318, 347.
+// make dearer. Measured (in place, gathered): 131072 rows of 2048: 256 channels 230, 129 us;
+// 768: 372, 326; 1536: 628, 616; 2048: 813, 816. 49152 rows of 5120: 768 channels 383, 340; 1536:
+// 647, 646; 2048: 819, 844. 16384 rows of 4096: 768 channels 96, 92; 1536: 152, 158; 2048: 185, 197.
 constexpr int kGatherChannels = 1536;
 
 // Token rows for the product `p`: gathered by it (wide tiles), or put in place for it.
