@@ -342,6 +342,15 @@ def test_moe_few_weights_that_are_not_finite(T, dt):
     smoe.smoe_get_status(c.ws)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 16, 32, 64])
+def test_moe_few_most_experts(T, dt):
+    """512 experts of which each token takes 32, 8 shared ones: the largest tables in shared memory."""
+    c = Few(T, 72, 512, 32, 4, 40, 8, dt, renorm=1)
+    c.run()
+    c.check()
+
+
 def test_moe_few_keeps_other_tokens_out():
     """A token whose states overflow its experts does not reach the other tokens."""
     c = Few(4, 256, 8, 2, 1, 128, 1, "bf16")
@@ -803,6 +812,23 @@ def test_expert_ffn_i8_padded_batch(T, F, S):
         c.run()
         c.check()
         assert (c.y[:lead] == 7.0).all() and (c.y[n - 11:] == 7.0).all()
+
+
+@pytest.mark.parametrize("T,K", [(9, 4), (300, 32), (700, 32), (6400, 32)])
+def test_expert_ffn_i8_most_experts(T, K):
+    """512 experts and 8 shared ones, in each tile form."""
+    c = Ffn8(T, 32, 512, K, 16, 8, "f32", empty=(0, 200, 511))
+    c.run()
+    smoe.smoe_get_status(c.ws)
+    off = c.off.tolist()
+    for e in range(0, 512, 37):
+        if off[e + 1] > off[e]:
+            out, tol = c.expert(c.src[off[e]:off[e + 1]].long(), e)
+            assert ((c.y[off[e]:off[e + 1]].double() - out).abs() <= tol).all(), e
+    assert not (c.y == 7.0).all(1).any()
+    for j in range(8):
+        out, tol = c.expert(torch.arange(T, device="cuda"), 512 + j)
+        assert ((c.ysh[j].double() - out).abs() <= tol).all(), j
 
 
 def test_expert_ffn_i8_rows_in_dispatched_order():
