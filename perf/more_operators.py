@@ -176,7 +176,8 @@ def _block_scale(x, pow2):
     T, d = x.shape
     pad = torch.zeros(T, _blocks(d) * BLOCK, dtype=x.dtype, device=x.device)
     pad[:, :d] = x.abs()
-    s = pad.view(T, -1, BLOCK).amax(-1) / F8_MAX
+    s = pad.view(T, -1, BLOCK).amax(-1)
+    s = s / torch.full_like(s, F8_MAX)  # (by a number torch would multiply with its inverse)
     if pow2:
         m, e = torch.frexp(s)
         s = torch.ldexp(torch.ones_like(s), torch.where(m == 0.5, e - 1, e))
