@@ -19,6 +19,10 @@
  *   residual add + RMS norm, with 8-bit rows        -> smoe_add_rmsnorm
  *   the whole layer for at most 64 tokens           -> smoe_moe_forward_few
  *   expert products / FFN in 8-bit integers         -> smoe_expert_matmul_i8, smoe_expert_ffn_i8
+ *   rows / expert products in 8-bit floating point  -> smoe_rows_f8, smoe_expert_matmul_f8
+ * and, when its experts are trained,
+ *   one grouped product, its two gradients          -> smoe_expert_matmul, _dx, _dw, _dw_f8
+ *   SwiGLU kept in 8 bits, and its backward pass    -> smoe_swiglu_f8, smoe_swiglu_grad_f8
  *
  * Sources (page title, section):
  *   "Speculative MoE" (research-notes page): §1 top-K gating and EP
@@ -33,8 +37,8 @@
  * Conventions shared by every entry point
  *   - Memory: every pointer is a caller-owned DEVICE pointer unless the argument
  *     says host. The library allocates nothing; scratch space is the caller's
- *     workspace (size from smoe_workspace_size; smoe_moe_forward_few and the 8-bit entry
- *     points have size functions of their own). Pointers must be 16-byte aligned
+ *     workspace (size from smoe_workspace_size; smoe_moe_forward_few, the 8-bit integer entry
+ *     points and the single products have size functions of their own). Pointers must be 16-byte aligned
  *     (SMOE_ERR_ALIGN otherwise). Matrices are row-major and dense.
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream). Every call is asynchronous on that stream; the return value covers
@@ -95,7 +99,8 @@ typedef struct smoe_desc {
 } smoe_desc;
 
 /* Bytes of workspace that every entry point below accepts for this shape (one
- * buffer serves all of them, but for smoe_moe_forward_few and the 8-bit entry points).
+ * buffer serves all of them, but for smoe_moe_forward_few, the 8-bit entry points and the
+ * single products smoe_expert_matmul*).
  * Returns 0 if the descriptor is invalid. */
 SMOE_API size_t smoe_workspace_size(const smoe_desc* desc);
 
@@ -503,6 +508,108 @@ SMOE_API int smoe_expert_ffn_i8(const smoe_desc* desc, const int8_t* xq, const f
                                 const int32_t* row_src, const int32_t* expert_off,
                                 const smoe_i8_weights* weights, void* y_disp, void* y_shared,
                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Rows in 8-bit floating point (e4m3) with a scale per row and block of 128 channels (the last
+ * block may be shorter):
+ *   scale = max |x| / 448 over the block, in fp32; pow2 = 1: the power of two that is not below
+ *   it;  q = x / scale rounded to e4m3 (to nearest, ties to even).
+ * A power of two costs precision at the smallest magnitudes alone, since e4m3 has an exponent
+ * of its own, and what it stands for, q * scale, is exact in bf16. A block that is zero, or
+ * whose scale would be below the smallest normal fp32 number, gets scale 0 and zeros; a block
+ * with an infinity or a NaN gets scale NaN and zeros.
+ *   x [rows, cols] desc->dtype (nothing else of desc is used, but it has to be valid)
+ *   q [rows, cols] e4m3 bytes; scale [rows, ceil(cols / 128)] fp32
+ * cols is a multiple of 8 (of 16 for rows that go to a product). rows = 0 is a no-op. No
+ * workspace.                                                                            */
+SMOE_API int smoe_rows_f8(const smoe_desc* desc, int rows, int cols, const void* x, int pow2,
+                          uint8_t* q, float* scale, void* stream);
+
+/* Bytes of the workspace of smoe_expert_matmul_f8, smoe_expert_matmul, _dx, _dw and _dw_f8 for
+ * this shape (of the same manner as every workspace). One size for all: it holds the widened
+ * rows of _dw_f8 also where a program does not call that. 0 if the descriptor is invalid. */
+SMOE_API size_t smoe_product_workspace_size(const smoe_desc* desc);
+
+/* Grouped product in 8-bit floating point with block scales: for every expert e and each of
+ * its dispatched rows r, with s = row_src[r] and blocks b of 128 of the n_in channels,
+ *   out[r, n] = sum_b x_scale[s, b] w_scale[e, n / 128, b] sum_{k in b} xq[s, k] wq[e, n, k],
+ * a block's sum in the tensor core's fp32 accumulator, the rest in fp32. Scales are any fp32
+ * values (smoe_rows_f8's of either kind).
+ *   xq         [T, n_in] e4m3 token rows when row_src is given, else [T K, n_in] rows already
+ *              in dispatched order
+ *   x_scale    [T or T K, ceil(n_in / 128)] fp32
+ *   row_src    nullable [T K] int32 in [0, T) (smoe_dispatch's row_token)
+ *   expert_off [E+1] int32 (from smoe_dispatch); rows outside the segments are not written
+ *   wq         [E, n_out, n_in] e4m3;  w_scale [E, ceil(n_out / 128), ceil(n_in / 128)] fp32
+ *   out        [T K, n_out] dtype
+ * n_in is a multiple of 16, n_out of 8. A row_src entry out of range gives a zero row and
+ * SMOE_ERR_DATA.                                                                       */
+SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, const uint8_t* xq,
+                                   const float* x_scale, const int32_t* row_src,
+                                   const int32_t* expert_off, const uint8_t* wq,
+                                   const float* w_scale, void* out, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Grouped product: for every expert e and each of its dispatched rows r,
+ *   out[r, n] = sum_k x[r, k] w[e, n, k],
+ * fp32 accumulation. fp32 layers multiply in fp32 (not tf32).
+ *   x [T K, n_in] dtype in dispatched order; expert_off [E+1] int32; w [E, n_out, n_in] dtype;
+ *   out [T K, n_out] dtype, rows outside the segments are not written
+ * n_in and n_out are multiples of 8 (of this product and its two gradients). Descriptors of
+ * these entry points name T, K, E and the dtype; d and F are the layer's.               */
+SMOE_API int smoe_expert_matmul(const smoe_desc* desc, int n_out, int n_in, const void* x,
+                                const int32_t* expert_off, const void* w, void* out, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Its gradient with respect to the rows:
+ *   dx[r, k] = sum_n dy[r, n] w[e, n, k]  (+ sum_n dy2[r, n] w2[e, n, k]),
+ * one sum in fp32, rounded once: a SwiGLU layer's gate and up product are taken together.
+ *   dy, dy2 [T K, n_out] dtype; w, w2 [E, n_out, n_in] dtype as in smoe_expert_matmul (dy2 and w2
+ *   nullable, together); dx [T K, n_in] dtype, rows outside the segments are not written */
+SMOE_API int smoe_expert_matmul_dx(const smoe_desc* desc, int n_out, int n_in, const void* dy,
+                                   const void* w, const void* dy2, const void* w2,
+                                   const int32_t* expert_off, void* dx, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Its gradient with respect to the weights, in fp32:
+ *   dw[e, n, k] = add[e, n, k] + sum_{r of e} dy[r, n] x[r, k].
+ *   dy [T K, n_out] dtype; x [T K, n_in] dtype; add nullable [E, n_out, n_in] fp32: the gradient
+ *   of earlier batches (may be the same buffer as dw); dw [E, n_out, n_in] fp32, every expert
+ *   written: one without rows gets add, or zeros. Rows outside the segments are not read into
+ *   any sum. With T = 0 nothing is written. A bad expert_off (SMOE_ERR_DATA) writes nothing. */
+SMOE_API int smoe_expert_matmul_dw(const smoe_desc* desc, int n_out, int n_in, const void* dy,
+                                   const void* x, const int32_t* expert_off, const float* add,
+                                   float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* The same from rows kept in 8 bits (smoe_rows_f8, smoe_swiglu_f8): x[r] = xq[s] times its
+ * scales, s = row_src[r], in the layer's type: exact for scales that are powers of two, rounded
+ * to bf16 otherwise in bf16 layers.
+ *   xq [T, n_in] e4m3 token rows when row_src is given, else [T K, n_in]; x_scale [T or T K,
+ *   ceil(n_in / 128)] fp32; row_src nullable [T K] int32 in [0, T): an entry out of range
+ *   counts as a zero row and is recorded as SMOE_ERR_DATA
+ * n_in is a multiple of 16 and at most the larger of desc->d and desc->F.               */
+SMOE_API int smoe_expert_matmul_dw_f8(const smoe_desc* desc, int n_out, int n_in, const void* dy,
+                                      const uint8_t* xq, const float* x_scale,
+                                      const int32_t* row_src, const int32_t* expert_off,
+                                      const float* add, float* dw, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* h = g sig(g) u, and what the backward pass needs of g and u in 8 bits (blocks and scales as
+ * smoe_rows_f8). A quarter to a half of the bytes that g and u would keep.
+ *   g, u [rows, cols] dtype; h nullable [rows, cols] dtype (may be the same buffer as g or u);
+ *   h8, h8_scale nullable: h in 8 bits, from its fp32 value, for an 8-bit product;
+ *   g8, g8_scale, u8, u8_scale nullable: the kept inputs
+ * At least one of h, h8, g8, u8 is given. cols is a multiple of 8. No workspace.        */
+SMOE_API int smoe_swiglu_f8(const smoe_desc* desc, int rows, int cols, const void* g, const void* u,
+                            int pow2, void* h, uint8_t* h8, float* h8_scale, uint8_t* g8,
+                            float* g8_scale, uint8_t* u8, float* u8_scale, void* stream);
+
+/* Its backward pass, from what was kept: with g and u as g8 and u8 stand for,
+ *   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh g sig(g),  h = g sig(g) u.
+ *   dh [rows, cols] dtype; dg, du [rows, cols] dtype; h nullable [rows, cols] dtype: the input of
+ *   the down product's weight gradient. One of dg, du and h may be the same buffer as dh.   */
+SMOE_API int smoe_swiglu_grad_f8(const smoe_desc* desc, int rows, int cols, const void* dh,
+                                 const uint8_t* g8, const float* g8_scale, const uint8_t* u8,
+                                 const float* u8_scale, void* dg, void* du, void* h, void* stream);
 
 /* Synchronises `stream`, returns SMOE_OK, SMOE_ERR_DATA or SMOE_ERR_DEVICE_TIMEOUT from
  * the workspace status word, and clears it. */

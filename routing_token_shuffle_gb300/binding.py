@@ -50,6 +50,7 @@ class I8Weights(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
+_I = ctypes.c_int
 _D = ctypes.POINTER(SmoeDesc)
 
 SIGNATURES = {
@@ -86,6 +87,15 @@ SIGNATURES = {
                                              _P, _P, _SZ, _P]),
     "smoe_expert_ffn_i8": (ctypes.c_int, [_D, _P, _P, _P, _P, ctypes.POINTER(I8Weights), _P, _P, _P,
                                           _SZ, _P]),
+    "smoe_rows_f8": (ctypes.c_int, [_D, _I, _I, _P, _I, _P, _P, _P]),
+    "smoe_product_workspace_size": (_SZ, [_D]),
+    "smoe_expert_matmul_f8": (ctypes.c_int, [_D, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_expert_matmul": (ctypes.c_int, [_D, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_expert_matmul_dx": (ctypes.c_int, [_D, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_expert_matmul_dw": (ctypes.c_int, [_D, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_expert_matmul_dw_f8": (ctypes.c_int, [_D, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "smoe_swiglu_f8": (ctypes.c_int, [_D, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "smoe_swiglu_grad_f8": (ctypes.c_int, [_D, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "smoe_get_status": (ctypes.c_int, [_P, _P]),
     "smoe_selftest_device_timeout": (ctypes.c_int, [_P, _SZ, _P]),
     "smoe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -177,6 +187,11 @@ def workspace_few(desc: SmoeDesc, device="cuda"):
 def workspace_i8(desc: SmoeDesc, device="cuda"):
     """A zeroed workspace tensor for smoe_expert_matmul_i8 and smoe_expert_ffn_i8."""
     return _zeroed(desc, "smoe_i8_workspace_size", device)
+
+
+def workspace_products(desc: SmoeDesc, device="cuda"):
+    """A zeroed workspace tensor for smoe_expert_matmul_f8, smoe_expert_matmul and its gradients."""
+    return _zeroed(desc, "smoe_product_workspace_size", device)
 
 
 def smoe_route(desc, x, w_gate, topk_idx, topk_w, logits_in=None, logits_out=None, ws=None,
@@ -367,6 +382,95 @@ def smoe_expert_ffn_i8(desc, xq, x_scale, expert_off, weights: I8Weights, y_disp
                                     _ptr(expert_off), ctypes.byref(weights), _ptr(y_disp),
                                     _ptr(y_shared), _ptr(ws), ws.numel(), _stream(stream)),
            "smoe_expert_ffn_i8")
+
+
+def _matrix(desc, w, name):
+    """(n_out, n_in) of expert weights [E, n_out, n_in]."""
+    E, n_out, n_in = w.shape
+    if E != desc.E:
+        raise ValueError(f"{name} holds {E} experts, the descriptor {desc.E}")
+    return n_out, n_in
+
+
+def _same(name, a, like):
+    if a is not None and a.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(a.shape)}, not {tuple(like.shape)}")
+
+
+def smoe_rows_f8(desc, x, q, scale, pow2=0, stream=None):
+    """x [rows, cols] in desc's dtype to q (e4m3) and scale [rows, ceil(cols / 128)]."""
+    rows, cols = x.shape
+    _same("q", q, x)
+    _check(lib().smoe_rows_f8(ctypes.byref(desc), rows, cols, _ptr(x), int(pow2), _ptr(q), _ptr(scale),
+                              _stream(stream)), "smoe_rows_f8")
+
+
+def smoe_expert_matmul_f8(desc, xq, x_scale, expert_off, wq, w_scale, out, ws, row_src=None,
+                          stream=None):
+    """wq [E, n_out, n_in]; n_out and n_in are taken from its shape; ws from workspace_products."""
+    n_out, n_in = _matrix(desc, wq, "wq")
+    _check(lib().smoe_expert_matmul_f8(ctypes.byref(desc), n_out, n_in, _ptr(xq), _ptr(x_scale),
+                                       _ptr(row_src), _ptr(expert_off), _ptr(wq), _ptr(w_scale),
+                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_expert_matmul_f8")
+
+
+def smoe_expert_matmul(desc, x, expert_off, w, out, ws, stream=None):
+    """out = x w^T by expert; w [E, n_out, n_in]; ws from workspace_products."""
+    n_out, n_in = _matrix(desc, w, "w")
+    _check(lib().smoe_expert_matmul(ctypes.byref(desc), n_out, n_in, _ptr(x), _ptr(expert_off),
+                                    _ptr(w), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_expert_matmul")
+
+
+def smoe_expert_matmul_dx(desc, dy, w, expert_off, dx, ws, dy2=None, w2=None, stream=None):
+    """dx = dy w (+ dy2 w2) by expert; w, w2 [E, n_out, n_in]; ws from workspace_products."""
+    n_out, n_in = _matrix(desc, w, "w")
+    _same("w2", w2, w)
+    _check(lib().smoe_expert_matmul_dx(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(w), _ptr(dy2),
+                                       _ptr(w2), _ptr(expert_off), _ptr(dx), _ptr(ws), ws.numel(),
+                                       _stream(stream)), "smoe_expert_matmul_dx")
+
+
+def smoe_expert_matmul_dw(desc, dy, x, expert_off, dw, ws, add=None, stream=None):
+    """dw = (add +) dy^T x by expert, fp32 [E, n_out, n_in]; ws from workspace_products."""
+    n_out, n_in = _matrix(desc, dw, "dw")
+    _same("add", add, dw)
+    _check(lib().smoe_expert_matmul_dw(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(x),
+                                       _ptr(expert_off), _ptr(add), _ptr(dw), _ptr(ws), ws.numel(),
+                                       _stream(stream)), "smoe_expert_matmul_dw")
+
+
+def smoe_expert_matmul_dw_f8(desc, dy, xq, x_scale, expert_off, dw, ws, row_src=None, add=None,
+                             stream=None):
+    """smoe_expert_matmul_dw from rows kept in 8 bits (token rows when row_src is given)."""
+    n_out, n_in = _matrix(desc, dw, "dw")
+    _same("add", add, dw)
+    _check(lib().smoe_expert_matmul_dw_f8(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(xq),
+                                          _ptr(x_scale), _ptr(row_src), _ptr(expert_off), _ptr(add),
+                                          _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_expert_matmul_dw_f8")
+
+
+def smoe_swiglu_f8(desc, g, u, h=None, h8=None, h8_scale=None, g8=None, g8_scale=None, u8=None,
+                   u8_scale=None, pow2=1, stream=None):
+    """h = silu(g) u, and h, g, u in 8 bits, each where its buffers are given."""
+    rows, cols = g.shape
+    for name, t in (("u", u), ("h", h), ("h8", h8), ("g8", g8), ("u8", u8)):
+        _same(name, t, g)
+    _check(lib().smoe_swiglu_f8(ctypes.byref(desc), rows, cols, _ptr(g), _ptr(u), int(pow2), _ptr(h),
+                                _ptr(h8), _ptr(h8_scale), _ptr(g8), _ptr(g8_scale), _ptr(u8),
+                                _ptr(u8_scale), _stream(stream)), "smoe_swiglu_f8")
+
+
+def smoe_swiglu_grad_f8(desc, dh, g8, g8_scale, u8, u8_scale, dg, du, h=None, stream=None):
+    """dg, du (and h again) from dh and what smoe_swiglu_f8 kept."""
+    rows, cols = dh.shape
+    for name, t in (("g8", g8), ("u8", u8), ("dg", dg), ("du", du), ("h", h)):
+        _same(name, t, dh)
+    _check(lib().smoe_swiglu_grad_f8(ctypes.byref(desc), rows, cols, _ptr(dh), _ptr(g8),
+                                     _ptr(g8_scale), _ptr(u8), _ptr(u8_scale), _ptr(dg), _ptr(du),
+                                     _ptr(h), _stream(stream)), "smoe_swiglu_grad_f8")
 
 
 def kernel_launches() -> int:

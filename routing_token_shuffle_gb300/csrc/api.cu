@@ -852,6 +852,208 @@ SMOE_API int smoe_selftest_device_timeout(void* ws, size_t ws_bytes, void* strea
   return SMOE_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit rows, products, gradients
+static int check_rows_f8(const smoe_desc* d, int rows, int cols) {
+  SMOE_CHECK(check_desc(d));
+  SMOE_REQUIRE(rows >= 0 && cols > 0 && cols % 8 == 0 &&
+                   (long long)rows * ((cols + 127LL) / 128) <= INT_MAX / 2,
+               SMOE_ERR_SHAPE, "rows=%d, cols=%d: cols must be a multiple of 8, rows * cols / 128 below 2^30",
+               rows, cols);
+  return SMOE_OK;
+}
+
+// 8-bit rows and their scales go together
+#define SMOE_F8_PAIR(q, s) \
+  do { \
+    SMOE_OPT_PTR(q); \
+    SMOE_OPT_PTR(s); \
+    SMOE_REQUIRE(!(q) == !(s), SMOE_ERR_ARG, "%s and %s go together", #q, #s); \
+  } while (0)
+
+SMOE_API int smoe_rows_f8(const smoe_desc* desc, int rows, int cols, const void* x, int pow2,
+                          uint8_t* q, float* scale, void* stream) {
+  SMOE_CHECK(check_rows_f8(desc, rows, cols));
+  SMOE_REQUIRE(pow2 == 0 || pow2 == 1, SMOE_ERR_ARG, "pow2 must be 0 or 1");
+  SMOE_PTR(x);
+  SMOE_PTR(q);
+  SMOE_PTR(scale);
+  if (rows == 0) return SMOE_OK;
+  SMOE_CHECK(check_device());
+  cudaError_t e = launch_rows_f8(*desc, rows, cols, x, pow2, q, scale, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit rows launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_swiglu_f8(const smoe_desc* desc, int rows, int cols, const void* g, const void* u,
+                            int pow2, void* h, uint8_t* h8, float* h8_scale, uint8_t* g8,
+                            float* g8_scale, uint8_t* u8, float* u8_scale, void* stream) {
+  SMOE_CHECK(check_rows_f8(desc, rows, cols));
+  SMOE_REQUIRE(pow2 == 0 || pow2 == 1, SMOE_ERR_ARG, "pow2 must be 0 or 1");
+  SMOE_PTR(g);
+  SMOE_PTR(u);
+  SMOE_OPT_PTR(h);
+  SMOE_F8_PAIR(h8, h8_scale);
+  SMOE_F8_PAIR(g8, g8_scale);
+  SMOE_F8_PAIR(u8, u8_scale);
+  SMOE_REQUIRE(h || h8 || g8 || u8, SMOE_ERR_ARG, "no output is given");
+  if (rows == 0) return SMOE_OK;
+  SMOE_CHECK(check_device());
+  cudaError_t e = launch_swiglu_f8(*desc, rows, cols, g, u, pow2, h, F8Rows{h8, h8_scale},
+                                   F8Rows{g8, g8_scale}, F8Rows{u8, u8_scale},
+                                   static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "SwiGLU launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_swiglu_grad_f8(const smoe_desc* desc, int rows, int cols, const void* dh,
+                                 const uint8_t* g8, const float* g8_scale, const uint8_t* u8,
+                                 const float* u8_scale, void* dg, void* du, void* h, void* stream) {
+  SMOE_CHECK(check_rows_f8(desc, rows, cols));
+  SMOE_PTR(dh);
+  SMOE_PTR(g8);
+  SMOE_PTR(g8_scale);
+  SMOE_PTR(u8);
+  SMOE_PTR(u8_scale);
+  SMOE_PTR(dg);
+  SMOE_PTR(du);
+  SMOE_OPT_PTR(h);
+  if (rows == 0) return SMOE_OK;
+  SMOE_CHECK(check_device());
+  cudaError_t e = launch_swiglu_grad_f8(*desc, rows, cols, dh, g8, g8_scale, u8, u8_scale, dg, du, h,
+                                        static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "SwiGLU gradient launch");
+  return SMOE_OK;
+}
+
+static int check_products(const smoe_desc* d) {
+  SMOE_CHECK(check_desc(d));
+  SMOE_REQUIRE((long long)d->T * d->K <= INT_MAX / 2, SMOE_ERR_SHAPE, "batch too large");
+  return SMOE_OK;
+}
+
+// The checks that the five products share; step: what n_in is a multiple of.
+static int check_product(const smoe_desc* d, int n_out, int n_in, int step, const void* ws,
+                         size_t ws_bytes) {
+  SMOE_CHECK(check_products(d));
+  SMOE_REQUIRE(n_in > 0 && n_in % step == 0, SMOE_ERR_SHAPE, "n_in=%d must be a multiple of %d", n_in, step);
+  SMOE_REQUIRE(n_out > 0 && n_out % 8 == 0, SMOE_ERR_SHAPE, "n_out=%d must be a multiple of 8", n_out);
+  // matrix rows and tiles are numbered in 32 bits
+  const long long tiles = (long long)d->T * d->K / 16 + 2LL * d->E;
+  SMOE_REQUIRE((long long)d->E * n_out <= kMaxMatrixRows &&
+                   tiles * ((std::max(n_out, n_in) + 127LL) / 128) <= INT_MAX / 2 &&
+                   (long long)d->E * ((n_out + 63LL) / 64) * ((n_in + 127LL) / 128) <= INT_MAX / 2,
+               SMOE_ERR_SHAPE, "expert matrices or batch too large");
+  ProductLayout L;
+  product_ws_layout(*d, &L);
+  return check_ws_bytes(L.total, const_cast<void*>(ws), ws_bytes);
+}
+
+SMOE_API size_t smoe_product_workspace_size(const smoe_desc* desc) {
+  if (check_products(desc) != SMOE_OK) return 0;
+  ProductLayout L;
+  product_ws_layout(*desc, &L);
+  return L.total;
+}
+
+SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, const uint8_t* xq,
+                                   const float* x_scale, const int32_t* row_src,
+                                   const int32_t* expert_off, const uint8_t* wq,
+                                   const float* w_scale, void* out, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  SMOE_CHECK(check_product(desc, n_out, n_in, 16, ws, ws_bytes));
+  SMOE_PTR(xq);
+  SMOE_PTR(x_scale);
+  SMOE_OPT_PTR(row_src);
+  SMOE_PTR(expert_off);
+  SMOE_PTR(wq);
+  SMOE_PTR(w_scale);
+  SMOE_PTR(out);
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_expert_matmul_f8(*desc, n_out, n_in, xq, x_scale, row_src, expert_off, wq,
+                                          w_scale, out, ws, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit floating-point product launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_expert_matmul(const smoe_desc* desc, int n_out, int n_in, const void* x,
+                                const int32_t* expert_off, const void* w, void* out, void* ws,
+                                size_t ws_bytes, void* stream) {
+  SMOE_CHECK(check_product(desc, n_out, n_in, 8, ws, ws_bytes));
+  SMOE_PTR(x);
+  SMOE_PTR(expert_off);
+  SMOE_PTR(w);
+  SMOE_PTR(out);
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_expert_rows(*desc, n_out, n_in, x, w, nullptr, nullptr, false, expert_off, out,
+                                     ws, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_expert_matmul_dx(const smoe_desc* desc, int n_out, int n_in, const void* dy,
+                                   const void* w, const void* dy2, const void* w2,
+                                   const int32_t* expert_off, void* dx, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  SMOE_CHECK(check_product(desc, n_out, n_in, 8, ws, ws_bytes));
+  SMOE_PTR(dy);
+  SMOE_PTR(w);
+  SMOE_OPT_PTR(dy2);
+  SMOE_OPT_PTR(w2);
+  SMOE_REQUIRE(!dy2 == !w2, SMOE_ERR_ARG, "dy2 and w2 go together");
+  SMOE_PTR(expert_off);
+  SMOE_PTR(dx);
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_expert_rows(*desc, n_out, n_in, dy, w, dy2, w2, true, expert_off, dx, ws,
+                                     static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "row gradient launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_expert_matmul_dw(const smoe_desc* desc, int n_out, int n_in, const void* dy,
+                                   const void* x, const int32_t* expert_off, const float* add,
+                                   float* dw, void* ws, size_t ws_bytes, void* stream) {
+  SMOE_CHECK(check_product(desc, n_out, n_in, 8, ws, ws_bytes));
+  SMOE_PTR(expert_off);
+  SMOE_OPT_PTR(add);
+  SMOE_PTR(dw);
+  SMOE_PTR(dy);
+  SMOE_PTR(x);
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaError_t e = launch_expert_dw(*desc, n_out, n_in, dy, x, expert_off, add, dw, ws,
+                                   static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+  return SMOE_OK;
+}
+
+SMOE_API int smoe_expert_matmul_dw_f8(const smoe_desc* desc, int n_out, int n_in, const void* dy,
+                                      const uint8_t* xq, const float* x_scale,
+                                      const int32_t* row_src, const int32_t* expert_off,
+                                      const float* add, float* dw, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  SMOE_CHECK(check_product(desc, n_out, n_in, 16, ws, ws_bytes));
+  SMOE_REQUIRE(n_in <= std::max(desc->d, desc->F), SMOE_ERR_SHAPE, "n_in=%d must be at most max(d, F)=%d",
+               n_in, std::max(desc->d, desc->F));
+  SMOE_PTR(dy);
+  SMOE_PTR(xq);
+  SMOE_PTR(x_scale);
+  SMOE_OPT_PTR(row_src);
+  SMOE_PTR(expert_off);
+  SMOE_OPT_PTR(add);
+  SMOE_PTR(dw);
+  SMOE_CHECK(check_device());
+  if (desc->T == 0) return SMOE_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const void* rows = nullptr;
+  cudaError_t e = launch_widen_rows(*desc, n_in, xq, x_scale, row_src, expert_off, ws, &rows, s);
+  if (e == cudaSuccess) e = launch_expert_dw(*desc, n_out, n_in, dy, rows, expert_off, add, dw, ws, s);
+  if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+  return SMOE_OK;
+}
+
 SMOE_API int smoe_get_status(void* ws, void* stream) {
   SMOE_REQUIRE(ws != nullptr, SMOE_ERR_ARG, "workspace must not be NULL");
   cudaStream_t s = static_cast<cudaStream_t>(stream);

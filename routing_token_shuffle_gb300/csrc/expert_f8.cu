@@ -1,0 +1,483 @@
+// Expert products in 8-bit floating point (e4m3) with a scale for each block of 128 contraction
+// channels, one per row on the token side and one per 128 output channels on the weight side:
+//   out[r, n] = sum_b xs[s(r), b] ws[e(r), n / 128, b] sum_{k in b} xq[s(r), k] wq[e(r), n, k].
+//
+// The scales are fp32 of any value, so a block's sum leaves the tensor core before it is
+// scaled: tcgen05.mma (kind::f8f6f4) gives each block of 128 in a TMEM buffer of its own, and
+// the epilogue warps multiply it by its two scales and add it to accumulators in registers
+// while the next blocks' MMAs run into the other buffers. One block costs the epilogue one TMEM
+// read and one FMA a value, less than the MMAs' own time.
+//
+// One persistent CTA per SM walks the tiles (expert, channel tile, row tile), row tiles fastest
+// so that neighbours share the weights through L2. The token rows are gathered through row_src by
+// 16-byte asynchronous copies, so no dispatched copy of them is made; weights come by TMA.
+//   wide   128 rows x 256 channels: the rows are the MMA's M, so that a thread of the epilogue
+//          holds one row and a block's scale is one number for it
+//   narrow 128 channels x at most 64 rows: for batches that do not fill an expert's tile the
+//          weights' stream is the work; the channels are the MMA's M, its N the rows rounded up
+//          to 16, and the row scales are read from shared memory
+#include <algorithm>
+
+#include "tc_common.cuh"
+
+namespace smoe {
+namespace {
+
+template <bool WIDE> struct F8Cfg;
+// Registers hold the accumulators: 128 a thread in the wide form (8 epilogue warps), 64 in the
+// narrow one (4 warps).
+template <> struct F8Cfg<true> {
+  static constexpr int kThreads = 384, kStages = 4, kChan = 256, kRows = 128, kBufs = 2, kCols = 256;
+  static constexpr int kStage = 48 * 1024, kEpiWarps = 8, kEpiSmem = 8 * 2048;
+};
+template <> struct F8Cfg<false> {
+  static constexpr int kThreads = 256, kStages = 8, kChan = 128, kRows = 64, kBufs = 8, kCols = 64;
+  static constexpr int kStage = 24 * 1024, kEpiWarps = 4, kEpiSmem = 4 * 256;
+};
+
+template <bool WIDE>
+constexpr size_t f8_smem() {
+  using C = F8Cfg<WIDE>;
+  return 1024 + (size_t)C::kStages * C::kStage + C::kEpiSmem + 8 * (2 * C::kStages + 2 * C::kBufs + 1) + 16 +
+         4 * 2 * (kMaxGroups + 2);
+}
+
+struct F8Args {
+  const uint8_t* xq;
+  const float* xs;
+  const int32_t* row_src;     // nullable
+  const int32_t* expert_off;
+  const float* ws;
+  void* out;
+  DeviceStatus* st;
+  int E, TK, n_src, N, KD;    // n_src: rows of xq
+};
+
+struct F8Tile {
+  int g, n0, rows;            // expert, first channel, rows of the tile
+  int row0;                   // first dispatched row
+};
+
+// Row tiles of each expert (s_ts, prefix) and their first rows (s_off), by one warp. A bad
+// expert_off schedules nothing.
+template <int ROWS>
+__device__ __forceinline__ void f8_table(const F8Args& p, int32_t* s_ts, int32_t* s_off, int lane) {
+  bool bad = false;
+  for (int g = lane; g <= p.E; g += 32) {
+    const int lo = p.expert_off[g], hi = g < p.E ? p.expert_off[g + 1] : lo;
+    bad |= lo < 0 || hi < lo || hi > p.TK;
+    s_off[g] = lo;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && lane == 0) record_error(p.st, kStatusData, kBadPairRow, -1);
+  __syncwarp();
+  int carry = 0;
+  for (int g0 = 0; g0 < p.E; g0 += 32) {
+    const int g = g0 + lane;
+    const int n = !bad && g < p.E ? (s_off[g + 1] - s_off[g] + ROWS - 1) / ROWS : 0;
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (g < p.E) s_ts[g] = carry + incl - n;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) s_ts[p.E] = carry;
+}
+
+// Tile t of a walk whose tiles ascend; g: the last one's expert. Narrow: an expert's row tiles
+// are equally long, not 64 rows and a rest.
+template <bool WIDE>
+__device__ __forceinline__ F8Tile f8_decode(const F8Args& p, const int32_t* ts, const int32_t* off,
+                                            int ntile, int t, int& g) {
+  using C = F8Cfg<WIDE>;
+  while (ts[g + 1] * ntile <= t) ++g;
+  const int mt = ts[g + 1] - ts[g], local = t - ts[g] * ntile;
+  const int n_tile = local / mt, m_tile = local - n_tile * mt;
+  const int rows = off[g + 1] - off[g];
+  const int step = WIDE ? C::kRows : ((rows + mt - 1) / mt + 15) & ~15;
+  F8Tile r;
+  r.g = g;
+  r.n0 = n_tile * C::kChan;
+  r.rows = min(step, rows - m_tile * step);
+  r.row0 = off[g] + m_tile * step;
+  return r;
+}
+
+template <bool WIDE, typename TO>
+__global__ void __launch_bounds__(F8Cfg<WIDE>::kThreads, 1)
+f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pairs, 128-row box
+               const F8Args p) {
+  using C = F8Cfg<WIDE>;
+  constexpr int kWBytes = C::kChan * 128, kXBytes = C::kRows * 128;
+  constexpr int kGatherWarps = 2, kGatherRows = C::kRows / kGatherWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sW = base;                                  // [kStages][kChan x 128 bytes]
+  uint8_t* sX = sW + C::kStages * kWBytes;             // [kStages][kRows x 128 bytes]
+  uint8_t* sE = sX + C::kStages * kXBytes;             // epilogue warps' own space
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + C::kEpiSmem);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* dfull = empty + C::kStages;
+  uint64_t* dempty = dfull + C::kBufs;
+  uint64_t* drain = dempty + C::kBufs;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  int32_t* s_ts = reinterpret_cast<int32_t*>(s_abort + 3);
+  int32_t* s_off = s_ts + kMaxGroups + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      tc::mbar_init(&full[s], 1 + 32 * kGatherWarps);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      tc::mbar_init(&dfull[b], 1);
+      tc::mbar_init(&dempty[b], C::kEpiWarps);
+    }
+    tc::mbar_init(drain, 1);
+    *s_abort = 0;
+    tc::mbar_init_fence();
+    tc::tma_prefetch_map(&tmW);
+  }
+  pdl_wait_and_trigger();
+  __syncwarp();
+  if (warp == 3) f8_table<C::kRows>(p, s_ts, s_off, lane);
+  if (warp == 2) {
+    tc::tmem_alloc(s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  const int ntile = (p.N + C::kChan - 1) / C::kChan;
+  const int total = s_ts[p.E] * ntile;
+  const int nk = (p.KD + 127) / 128;
+  volatile int* abort = s_abort;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- weights
+    const bool lead = tc::elect_one();
+    uint32_t s = 0, ph = 1, it = 0;
+    bool ok = true;
+    int g = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      const int wrow = tl.g * p.N + tl.n0;
+      // the tile's second 128 channels, where the matrix has them
+      const bool two = WIDE && tl.n0 + 128 < p.N;
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = tc::mbar_wait_warp(&empty[s], ph, abort);
+        if (!ok) break;
+        if (lead) {
+          tc::mbar_expect_tx(&full[s], two ? 2 * 128 * 128 : 128 * 128);
+          tc::tma_load_2d(sW + s * kWBytes, &tmW, &full[s], kb * 64, wrow);
+          if (two) tc::tma_load_2d(sW + s * kWBytes + 128 * 128, &tmW, &full[s], kb * 64, wrow + 128);
+        }
+        __syncwarp();
+        ++it;
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // The copies in flight land before shared memory goes away, whichever role gave up. A
+      // stage that the gathering warps did not get to never completes: then the limit is
+      // waited out once.
+      volatile int never = 0;
+      for (uint32_t j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+        if (!tc::mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1u, &never)) break;
+    }
+    __syncwarp();
+  } else if (warp == 2 || warp == 3) {
+    // ---------------------------------------------------------------- rows
+    // Four rows of 128 bytes an instruction, into the 128-byte-swizzled stage. Rows past the
+    // tile's are zeros (narrow: up to the MMA's columns).
+    const int c = lane & 7, sub = (warp - 2) * kGatherRows + (lane >> 3);
+    constexpr int kIter = kGatherRows / 4;
+    uint32_t s = 0, ph = 1;
+    bool ok = true;
+    int g = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      const int used = WIDE ? C::kRows : (tl.rows + 15) & ~15;
+      int id[kIter];
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int r = sub + 4 * i;
+        id[i] = -1;
+        if (r < tl.rows) {
+          const int row = tl.row0 + r, src = p.row_src ? __ldcg(p.row_src + row) : row;
+          if ((unsigned)src < (unsigned)p.n_src) id[i] = src;
+          else if (tl.n0 == 0 && c == 0) record_error(p.st, kStatusData, kBadPerm, row);
+        }
+      }
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = tc::mbar_wait_warp(&empty[s], ph, abort);
+        if (!ok) break;
+        const uint32_t dst = tc::smem_u32(sX + s * kXBytes);
+        const int at = kb * 128 + c * 16;
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int r = sub + 4 * i;
+          const bool in = id[i] >= 0 && at < p.KD;
+          if (r < used)
+            tc::cp_async16(dst + r * 128 + ((c ^ (r & 7)) << 4),
+                           p.xq + (in ? (size_t)id[i] * p.KD + at : 0), in ? 16u : 0u);
+        }
+        tc::cp_async_arrive(&full[s]);
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    tc::cp_async_wait_all();
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const bool lead = tc::elect_one();
+    uint32_t s = 0, ph = 0, b = 0, bph = 1;
+    bool ok = true, in = false, free = false;
+    int g = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      const uint32_t idesc =
+          WIDE ? tc::instr_desc_f8(128, tl.n0 + 128 < p.N ? 256 : 128) : tc::instr_desc_f8(128, (tl.rows + 15) & ~15);
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!in) ok = tc::mbar_wait_warp(&full[s], ph, abort);
+        if (!free && ok) ok = tc::mbar_wait_warp(&dempty[b], bph, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        // the gathered rows were written through the generic proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        const uint64_t wd = tc::sw128_kmajor_desc(tc::smem_u32(sW + s * kWBytes));
+        const uint64_t xd = tc::sw128_kmajor_desc(tc::smem_u32(sX + s * kXBytes));
+        const uint32_t acc = tmem + b * C::kCols;
+        uint64_t *e_bar = &empty[s], *d_bar = &dfull[b];
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+        if (++b == C::kBufs) { b = 0; bph ^= 1u; }
+        // the next stage's barriers are asked for while this stage's MMAs are issued
+        const bool in_next = tc::mbar_test(&full[s], ph), free_next = tc::mbar_test(&dempty[b], bph);
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f8(acc, (WIDE ? xd : wd) + 2 * k, (WIDE ? wd : xd) + 2 * k, idesc, k > 0);
+          tc::commit(e_bar);
+          tc::commit(d_bar);
+        }
+        in = __all_sync(0xffffffffu, in_next);
+        free = __all_sync(0xffffffffu, free_next);
+      }
+    }
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // wait for every MMA this thread issued before TMEM is released
+      volatile int never = 0;
+      tc::commit(drain);
+      tc::mbar_wait(drain, 0, &never);
+    }
+    __syncwarp();
+  } else if (WIDE) {
+    // ---------------------------------------------------------------- epilogue, wide
+    // warps 4-7 the tile's first 128 channels, 8-11 the other 128; a thread holds one row
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* buf = sE + (warp - 4) * 2048;
+    uint32_t b = 0, bph = 0;
+    bool ok = true;
+    int g = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      const int n0 = tl.n0 + 128 * half, r = q * 32 + lane;
+      const bool has = n0 < p.N;  // (its last channels may lie past the matrix: they are not stored)
+      int src = -1;
+      if (r < tl.rows) {
+        src = p.row_src ? __ldcg(p.row_src + tl.row0 + r) : tl.row0 + r;
+        if ((unsigned)src >= (unsigned)p.n_src) src = -1;
+      }
+      const float* xs = p.xs + (size_t)max(src, 0) * nk;
+      const float* ws = p.ws + ((size_t)tl.g * ((p.N + 127) / 128) + (has ? n0 / 128 : 0)) * nk;
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      float sc = src >= 0 ? __ldcg(xs) * __ldcg(ws) : 0.0f;
+      for (int kb = 0; kb < nk; ++kb) {
+        const float now = sc;
+        if (kb + 1 < nk) sc = src >= 0 ? __ldcg(xs + kb + 1) * __ldcg(ws + kb + 1) : 0.0f;
+        ok = tc::mbar_wait_warp(&dfull[b], bph, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (has) {
+          const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + b * C::kCols + half * 128;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            tc::tmem_ld32(taddr + c, v);
+            tc::tmem_ld_wait();
+            if (c == 96) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&dempty[b]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), now, acc[c + i]);
+          }
+        } else if (lane == 0) {
+          tc::mbar_arrive(&dempty[b]);
+        }
+        if (++b == C::kBufs) { b = 0; bph ^= 1u; }
+      }
+      if (!ok) break;
+      if (!has) continue;
+      // 32 rows x 64 bytes at a time through the warp's own 2 KB (16-byte chunks swizzled by
+      // pairs of rows: no bank conflicts either way), stored as segments of 64 bytes
+      constexpr int kVec = 16 / (int)sizeof(TO), kWin = 4 * kVec;
+      TO* out = static_cast<TO*>(p.out) + (size_t)tl.row0 * p.N;
+#pragma unroll
+      for (int c = 0; c < 128; c += kWin) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+              pack16(acc + c + j * kVec, (const TO*)nullptr);
+        __syncwarp();
+        const int ch = lane & 3, col = n0 + c + ch * kVec;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2);
+          const uint4 v = *reinterpret_cast<const uint4*>(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+          if (q * 32 + rr < tl.rows && col < p.N)
+            *reinterpret_cast<uint4*>(out + (size_t)(q * 32 + rr) * p.N + col) = v;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue, narrow
+    // a thread holds one channel; each warp keeps the block's 64 row scales for itself
+    const int q = warp & 3;
+    float* s_sc = reinterpret_cast<float*>(sE) + q * 64;
+    uint32_t b = 0, bph = 0;
+    bool ok = true;
+    int g = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      const int chan = tl.n0 + q * 32 + lane, used = (tl.rows + 15) & ~15;
+      const float* xs[2];
+      bool has[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = lane + 32 * u;
+        int src = -1;
+        if (r < tl.rows) src = p.row_src ? __ldcg(p.row_src + tl.row0 + r) : tl.row0 + r;
+        has[u] = (unsigned)src < (unsigned)p.n_src;
+        xs[u] = p.xs + (has[u] ? (size_t)src * nk : 0);
+      }
+      const float* ws = p.ws + ((size_t)tl.g * ((p.N + 127) / 128) + tl.n0 / 128) * nk;
+      float acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+      float w = __ldcg(ws), s0 = has[0] ? __ldcg(xs[0]) * w : 0.0f, s1 = has[1] ? __ldcg(xs[1]) * w : 0.0f;
+      for (int kb = 0; kb < nk; ++kb) {
+        __syncwarp();
+        s_sc[lane] = s0;
+        s_sc[lane + 32] = s1;
+        if (kb + 1 < nk) {
+          w = __ldcg(ws + kb + 1);
+          s0 = has[0] ? __ldcg(xs[0] + kb + 1) * w : 0.0f;
+          s1 = has[1] ? __ldcg(xs[1] + kb + 1) * w : 0.0f;
+        }
+        ok = tc::mbar_wait_warp(&dfull[b], bph, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + b * C::kCols;
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
+          if (c >= used) break;
+          float v[16];
+          tc::tmem_ld16(taddr + c, v);
+          if (c + 16 >= used) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&dempty[b]);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(s_sc + c + i);
+            acc[c + i] = fmaf(v[i], f.x, acc[c + i]);
+            acc[c + i + 1] = fmaf(v[i + 1], f.y, acc[c + i + 1]);
+            acc[c + i + 2] = fmaf(v[i + 2], f.z, acc[c + i + 2]);
+            acc[c + i + 3] = fmaf(v[i + 3], f.w, acc[c + i + 3]);
+          }
+        }
+        if (++b == C::kBufs) { b = 0; bph ^= 1u; }
+      }
+      if (!ok) break;
+      if (chan < p.N) {
+        TO* out = static_cast<TO*>(p.out) + (size_t)tl.row0 * p.N + chan;
+#pragma unroll
+        for (int i = 0; i < 64; ++i, out += p.N)
+          if (i < tl.rows) *out = Elem<TO>::from_f32(acc[i]);
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+}
+
+// From this many rows an expert on average the wide tiles.
+constexpr int kWideRows = 48;
+
+template <bool WIDE, typename TO>
+cudaError_t run_f8(const F8Args& p, const void* wq, long long tile_bound, cudaStream_t s) {
+  alignas(64) CUtensorMap tw;
+  if (!encode_tmap_2d(&tw, wq, false, (uint64_t)p.E * p.N, p.KD / 2, 128, 64)) return cudaErrorInvalidValue;
+  auto kern = f8_gemm_kernel<WIDE, TO>;
+  const int smem = (int)f8_smem<WIDE>();
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<long long>(device_sms(), std::max<long long>(tile_bound, 1));
+  SMOE_LAUNCH(kern, grid, F8Cfg<WIDE>::kThreads, smem, s, tw, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_expert_matmul_f8(const smoe_desc& d, int n_out, int n_in, const void* xq,
+                                    const float* xs, const int32_t* row_src,
+                                    const int32_t* expert_off, const void* wq, const float* w_scale,
+                                    void* out, void* ws, cudaStream_t s) {
+  const int TK = d.T * d.K;
+  const F8Args p{static_cast<const uint8_t*>(xq), xs, row_src, expert_off, w_scale, out,
+                 static_cast<DeviceStatus*>(ws), d.E, TK, row_src ? d.T : TK, n_out, n_in};
+  const bool wide = (long long)TK >= (long long)kWideRows * d.E;
+  // no more tiles than this, whatever the rows' spread over the experts
+  const long long bound = ((long long)ceil_div(TK, wide ? 128 : 64) + std::min(TK, d.E)) *
+                          ceil_div(n_out, wide ? 256 : 128);
+  if (d.dtype == SMOE_F32) return wide ? run_f8<true, float>(p, wq, bound, s) : run_f8<false, float>(p, wq, bound, s);
+  return wide ? run_f8<true, __nv_bfloat16>(p, wq, bound, s) : run_f8<false, __nv_bfloat16>(p, wq, bound, s);
+}
+
+}  // namespace smoe

@@ -1,0 +1,603 @@
+// Weight gradients of the experts' products, each over its expert's ragged rows,
+//   dw[e, n, k] = add[e, n, k] + sum_{r of e} dy[r, n] x[r, k]   (fp32),
+// x as it is or widened from 8-bit rows first.
+//
+// bf16: the contraction runs over rows, which neither operand is contiguous in, so both are
+// staged by TMA as they lie (boxes of 64 channels x 64 rows) and read MN-major by tcgen05.mma:
+// nothing is transposed. A segment ends anywhere: an MMA takes 16 rows, those of the last one
+// that belong to the next expert (or to nobody) are set to zero in shared memory, in both
+// operands, before it runs, so that neither their values nor their infinities reach the sum.
+// One persistent CTA per SM walks 128 x 256 tiles of the gradients:
+//   warp 0  TMA;  warp 1  the last rows' zeros, tcgen05.mma into one of two TMEM accumulators;
+//   warps 4-11  add and store, while the next tile's MMAs run.
+// An expert's R rows give 2 R flops per element of 4 bytes (8 with add): below about 550 rows an
+// expert the stores bound it, not the tensor cores.
+#include <algorithm>
+#include <cuda_fp8.h>
+
+#include "tc_common.cuh"
+
+namespace smoe {
+namespace {
+
+constexpr int kDwThreads = 384, kDwStages = 4, kDwWarps = 8;
+constexpr int kDwA = 128 * 128, kDwB = 256 * 128;  // bytes of a stage: 64 rows of 128 and 256 channels
+constexpr size_t kDwSmem = 1024 + kDwStages * (kDwA + kDwB) + kDwWarps * 2048 +
+                           8 * (2 * kDwStages + 2 * 2 + 1) + 16 + 4 * (kMaxGroups + 2);
+
+struct DwArgs {
+  const int32_t* expert_off;
+  const float* add;   // nullable
+  float* dw;
+  DeviceStatus* st;
+  int E, TK, M, N;    // M = n_out, N = n_in
+  int mt, nt;         // tiles of each
+};
+
+struct DwTile {
+  int e, m0, n0, row0, rows;
+};
+
+__device__ __forceinline__ DwTile dw_decode(const DwArgs& p, const int32_t* off, int t) {
+  DwTile r;
+  const int per = p.mt * p.nt;
+  r.e = t / per;
+  const int in = t - r.e * per, n = in / p.mt;
+  r.m0 = (in - n * p.mt) * 128;
+  r.n0 = n * 256;
+  r.row0 = off[r.e];
+  r.rows = off[r.e + 1] - r.row0;
+  return r;
+}
+
+__global__ void __launch_bounds__(kDwThreads, 1)
+dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+          const DwArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = base;
+  uint8_t* sB = sA + kDwStages * kDwA;
+  uint8_t* sE = sB + kDwStages * kDwB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + kDwWarps * 2048);
+  uint64_t* empty = full + kDwStages;
+  uint64_t* dfull = empty + kDwStages;
+  uint64_t* dempty = dfull + 2;
+  uint64_t* drain = dempty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  int* s_bad = s_abort + 1;
+  int32_t* s_off = s_bad + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kDwStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(&dfull[a], 1);
+      tc::mbar_init(&dempty[a], kDwWarps);
+    }
+    tc::mbar_init(drain, 1);
+    *s_abort = 0;
+    tc::mbar_init_fence();
+    tc::tma_prefetch_map(&tmA);
+    tc::tma_prefetch_map(&tmB);
+  }
+  pdl_wait_and_trigger();
+  __syncwarp();
+  if (warp == 3) {  // a bad expert_off schedules nothing
+    bool bad = false;
+    for (int g = lane; g <= p.E; g += 32) {
+      const int lo = p.expert_off[g], hi = g < p.E ? p.expert_off[g + 1] : lo;
+      bad |= lo < 0 || hi < lo || hi > p.TK;
+      s_off[g] = lo;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      *s_bad = bad;
+      if (bad) record_error(p.st, kStatusData, kBadPairRow, -1);
+    }
+  }
+  if (warp == 2) {
+    tc::tmem_alloc(s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  const int total = *s_bad ? 0 : p.E * p.mt * p.nt;
+  volatile int* abort = s_abort;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    const bool lead = tc::elect_one();
+    uint32_t s = 0, ph = 1, it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const DwTile tl = dw_decode(p, s_off, t);
+      const int na = tl.m0 + 64 < p.M ? 2 : 1, nb = min(4, (p.N - tl.n0 + 63) / 64);
+      for (int r = 0; r < tl.rows; r += 64) {
+        ok = tc::mbar_wait_warp(&empty[s], ph, abort);
+        if (!ok) break;
+        if (lead) {
+          tc::mbar_expect_tx(&full[s], (na + nb) * 8192);
+          for (int j = 0; j < na; ++j)
+            tc::tma_load_2d(sA + s * kDwA + j * 8192, &tmA, &full[s], tl.m0 + 64 * j, tl.row0 + r);
+          for (int j = 0; j < nb; ++j)
+            tc::tma_load_2d(sB + s * kDwB + j * 8192, &tmB, &full[s], tl.n0 + 64 * j, tl.row0 + r);
+        }
+        __syncwarp();
+        ++it;
+        if (++s == kDwStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // the copies in flight land before shared memory goes away, whichever role gave up
+      volatile int never = 0;
+      for (uint32_t j = it > kDwStages ? it - kDwStages : 0; j < it; ++j)
+        tc::mbar_wait(&full[j % kDwStages], (j / kDwStages) & 1u, &never);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const bool lead = tc::elect_one();
+    uint32_t s = 0, ph = 0, d = 0, dph = 1;
+    bool ok = true, in = false;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const DwTile tl = dw_decode(p, s_off, t);
+      if (tl.rows == 0) continue;
+      const uint32_t idesc = tc::instr_desc(false, 128, 64 * min(4, (p.N - tl.n0 + 63) / 64)) |
+                             tc::kIdescTransA | tc::kIdescTransB;
+      ok = tc::mbar_wait_warp(&dempty[d], dph, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t acc = tmem + d * 256;
+      for (int r = 0; r < tl.rows; r += 64) {
+        if (!in) ok = tc::mbar_wait_warp(&full[s], ph, abort);
+        if (!ok) break;
+        const int left = min(64, tl.rows - r);
+        if (left & 15) {  // the rows past the segment, up to the 16th, become zeros
+          const int n = 16 - (left & 15);
+          for (int i = lane; i < 6 * 8 * n; i += 32) {
+            const int box = i / (8 * n), in = i - box * 8 * n;
+            uint8_t* b = box < 2 ? sA + s * kDwA + box * 8192 : sB + s * kDwB + (box - 2) * 8192;
+            *reinterpret_cast<uint4*>(b + left * 128 + in * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        tc::fence_after_sync();
+        const uint64_t ad = tc::sw128_mnmajor_desc(tc::smem_u32(sA + s * kDwA));
+        const uint64_t bd = tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kDwB));
+        uint64_t* e_bar = &empty[s];
+        if (++s == kDwStages) { s = 0; ph ^= 1u; }
+        const bool in_next = tc::mbar_test(&full[s], ph);
+        if (lead) {
+          const int steps = (left + 15) >> 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) tc::mma_bf16(acc, ad + 128 * k, bd + 128 * k, idesc, r > 0 || k > 0);
+          tc::commit(e_bar);
+        }
+        in = __all_sync(0xffffffffu, in_next);
+      }
+      if (!ok) break;
+      if (lead) tc::commit(&dfull[d]);
+      __syncwarp();
+      if (++d == 2) { d = 0; dph ^= 1u; }
+    }
+    if (lead) {
+      if (!ok) {
+        *abort = 1;
+        record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+      }
+      // wait for every MMA this thread issued before TMEM is released
+      volatile int never = 0;
+      tc::commit(drain);
+      tc::mbar_wait(drain, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- epilogue
+    // warps 4-7 the tile's first 128 columns, 8-11 the other 128, 32 rows each; 32 rows x 64
+    // bytes at a time through the warp's own 2 KB, added to and stored as segments of 64 bytes.
+    // What is added is loaded two such windows ahead.
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* buf = sE + (warp - 4) * 2048;
+    const int ch = lane & 3, sub = lane >> 2;
+    uint32_t d = 0, dph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const DwTile tl = dw_decode(p, s_off, t);
+      const int m0 = tl.m0 + q * 32, n0 = tl.n0 + half * 128;
+      const size_t at = ((size_t)tl.e * p.M + m0) * p.N + n0;
+      const int mrows = min(32, p.M - m0), ncols = min(128, p.N - n0);  // may be below 1
+      const int nwin = mrows > 0 && ncols > 0 ? (ncols + 15) >> 4 : 0;
+      float4 add[2][4];
+      auto load = [&](int w, float4 (&a)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + sub, col = w * 16 + ch * 4;
+          a[i] = rr < mrows && col < ncols
+                     ? __ldcs(reinterpret_cast<const float4*>(p.add + at + (size_t)rr * p.N + col))
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+      };
+      if (p.add) {
+        load(0, add[0]);
+        load(1, add[1]);
+      }
+      if (tl.rows > 0) {
+        ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + d * 256 + half * 128;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w >= nwin) break;
+        __syncwarp();  // TMEM loads are a whole warp's
+        float v[16];
+        if (tl.rows > 0) {
+          tc::tmem_ld16(taddr + 16 * w, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + sub, col = w * 16 + ch * 4;
+          float4 o = *reinterpret_cast<const float4*>(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+          if (p.add) {
+            const float4 a = add[w & 1][i];
+            o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
+          }
+          if (rr < mrows && col < ncols)
+            __stcs(reinterpret_cast<float4*>(p.dw + at + (size_t)rr * p.N + col), o);
+        }
+        if (p.add && w + 2 < 8) load(w + 2, add[w & 1]);
+      }
+      if (tl.rows > 0) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&dempty[d]);
+        if (++d == 2) { d = 0; dph ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ kept rows
+// dst[r] = q[map[r]] times its scales, in the layer's type; a map entry out of range gives a row
+// of zeros. 16 values a thread.
+template <typename TE>
+__global__ void __launch_bounds__(256)
+widen_rows_kernel(const uint4* q, const float* scale, const int32_t* map, const int32_t* expert_off,
+                  int E, int rows, int n_src, int cols, TE* dst, DeviceStatus* st) {
+  pdl_wait_and_trigger();
+  const int vecs = cols >> 4, nblk = (cols + 127) >> 7, lane = threadIdx.x & 31;
+  const int begin = max(expert_off[0], 0), end = min(expert_off[E], rows);
+  for (int r = begin + blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
+    const int src = map ? map[r] : r;
+    const bool in = (unsigned)src < (unsigned)n_src;
+    if (!in && lane == 0) record_error(st, kStatusData, kBadPerm, r);
+    for (int v0 = lane; v0 < vecs; v0 += 128) {
+      uint4 w[4];
+      float s[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int v = v0 + 32 * u;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        s[u] = 0.0f;
+        if (in && v < vecs) {
+          w[u] = q[(size_t)src * vecs + v];
+          s[u] = scale[(size_t)src * nblk + (v >> 3)];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int v = v0 + 32 * u;
+        if (v >= vecs) break;
+        const uint32_t b[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+              (__nv_fp8x2_storage_t)(b[i >> 1] >> (16 * (i & 1)) & 0xffffu), __NV_E4M3)));
+          f[2 * i] = h.x * s[u];
+          f[2 * i + 1] = h.y * s[u];
+        }
+        uint4* out = reinterpret_cast<uint4*>(dst + (size_t)r * cols + v * 16);
+        constexpr int kVec = 16 / (int)sizeof(TE);
+#pragma unroll
+        for (int i = 0; i < 16 / kVec; ++i) out[i] = pack16(f + i * kVec, (const TE*)nullptr);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ fp32
+// fp32 layers multiply in fp32 on the CUDA cores (the tensor cores' tf32 keeps 11 bits):
+//   kind 0  y[r, n] = sum_k x[r, k] w[e, n, k]           rows x n_out, over n_in
+//   kind 1  dx[r, k] = sum_n dy[r, n] w[e, n, k] (twice) rows x n_in, over n_out
+//   kind 2  dw[e, n, k] = sum_r dy[r, n] x[r, k] (+ add)  n_out x n_in, over the rows
+// Tiles of BM x 128, 256 threads with BM / 16 x 8 sums each (16 x 128: 2 x 4), 16 of the contraction at
+// a time through shared memory, the next 16 in registers meanwhile.
+struct F32Args {
+  const float *a, *b, *a2, *b2, *add;
+  float* out;
+  const int32_t* expert_off;
+  DeviceStatus* st;
+  int E, TK, n_out, n_in;
+};
+
+template <int KIND, int BM>
+__global__ void __launch_bounds__(256)
+grouped_f32_kernel(const F32Args p) {
+  constexpr int BN = 128, BK = 16, TM = BM == 16 ? 2 : BM / 16, TN = BM == 16 ? 4 : 8;
+  constexpr int kTx = BN / TN;                  // threads along N
+  __shared__ alignas(16) float As[BK][BM + 4];
+  __shared__ alignas(16) float Bs[BK][BN + 4];
+  __shared__ int32_t s_ts[kMaxGroups + 2], s_off[kMaxGroups + 2];
+  pdl_wait_and_trigger();
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    bool bad = false;
+    for (int g = lane; g <= p.E; g += 32) {
+      const int lo = p.expert_off[g], hi = g < p.E ? p.expert_off[g + 1] : lo;
+      bad |= lo < 0 || hi < lo || hi > p.TK;
+      s_off[g] = lo;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && lane == 0) record_error(p.st, kStatusData, kBadPairRow, -1);
+    __syncwarp();
+    int carry = 0;
+    for (int g0 = 0; g0 < p.E; g0 += 32) {
+      const int g = g0 + lane;
+      int n = 0;
+      if (!bad && g < p.E) n = KIND == 2 ? (p.n_out + BM - 1) / BM : (s_off[g + 1] - s_off[g] + BM - 1) / BM;
+      int incl = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      if (g < p.E) s_ts[g] = carry + incl - n;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s_ts[p.E] = carry;
+  }
+  __syncthreads();
+  const int N = KIND == 0 ? p.n_out : p.n_in, ntile = (N + BN - 1) / BN;
+  const int total = s_ts[p.E] * ntile;
+  const int tx = tid % kTx, ty = tid / kTx;
+  int g = 0;
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    while (s_ts[g + 1] * ntile <= t) ++g;
+    const int mt = s_ts[g + 1] - s_ts[g], local = t - s_ts[g] * ntile;
+    const int n_tile = local / mt, n0 = n_tile * BN, m0 = (local - n_tile * mt) * BM;
+    const int row0 = s_off[g], rows = s_off[g + 1] - row0;
+    const int M = KIND == 2 ? p.n_out : rows;
+    const int K1 = KIND == 0 ? p.n_in : KIND == 1 ? p.n_out : rows;
+    const int nk1 = (K1 + BK - 1) / BK, nk = KIND == 1 && p.a2 ? 2 * nk1 : nk1;
+    float acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
+
+    constexpr int kA = (BM * BK / 4 + 255) / 256, kB = BN * BK / 4 / 256;
+    float4 ra[kA], rb[kB];
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto fetch = [&](int kb) {
+      const bool second = kb >= nk1;
+      const float* a = second ? p.a2 : p.a;
+      const float* b = second ? p.b2 : p.b;
+      const int k0 = (second ? kb - nk1 : kb) * BK;
+#pragma unroll
+      for (int i = 0; i < kA; ++i) {
+        const int v = tid + i * 256;
+        ra[i] = zero;
+        if (v >= BM * BK / 4) continue;
+        if (KIND == 2) {  // [row][n_out]
+          const int k = v / (BM / 4), m = (v - k * (BM / 4)) * 4;
+          if (k0 + k < K1 && m0 + m < M)
+            ra[i] = *reinterpret_cast<const float4*>(a + (size_t)(row0 + k0 + k) * p.n_out + m0 + m);
+        } else {
+          const int m = v >> 2, k = (v & 3) * 4;
+          if (m0 + m < M && k0 + k < K1)
+            ra[i] = *reinterpret_cast<const float4*>(a + (size_t)(row0 + m0 + m) * K1 + k0 + k);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        const int v = tid + i * 256;
+        rb[i] = zero;
+        if (KIND == 0) {  // [n_out][n_in]
+          const int n = v >> 2, k = (v & 3) * 4;
+          if (n0 + n < N && k0 + k < K1)
+            rb[i] = *reinterpret_cast<const float4*>(b + ((size_t)g * p.n_out + n0 + n) * p.n_in + k0 + k);
+        } else {
+          const int k = v >> 5, n = (v & 31) * 4;
+          const size_t row = KIND == 1 ? (size_t)g * p.n_out + k0 + k : (size_t)row0 + k0 + k;
+          if (k0 + k < K1 && n0 + n < N)
+            rb[i] = *reinterpret_cast<const float4*>(b + row * p.n_in + n0 + n);
+        }
+      }
+    };
+    if (nk > 0) fetch(0);
+    for (int kb = 0; kb < nk; ++kb) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kA; ++i) {
+        const int v = tid + i * 256;
+        if (v >= BM * BK / 4) continue;
+        const float f[4] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w};
+        if (KIND == 2) {
+          const int k = v / (BM / 4), m = (v - k * (BM / 4)) * 4;
+          *reinterpret_cast<float4*>(&As[k][m]) = ra[i];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) As[(v & 3) * 4 + j][v >> 2] = f[j];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        const int v = tid + i * 256;
+        const float f[4] = {rb[i].x, rb[i].y, rb[i].z, rb[i].w};
+        if (KIND == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) Bs[(v & 3) * 4 + j][v >> 2] = f[j];
+        } else {
+          *reinterpret_cast<float4*>(&Bs[v >> 5][(v & 31) * 4]) = rb[i];
+        }
+      }
+      __syncthreads();
+      if (kb + 1 < nk) fetch(kb + 1);
+#pragma unroll
+      for (int k = 0; k < BK; ++k) {
+        float a[TM], b[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = As[k][ty * TM + i];
+#pragma unroll
+        for (int j = 0; j < TN; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&Bs[k][tx * 4 + j * kTx]);
+          b[j] = f.x; b[j + 1] = f.y; b[j + 2] = f.z; b[j + 3] = f.w;
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = m0 + ty * TM + i;
+      if (m >= M) continue;
+      const size_t row = (KIND == 2 ? (size_t)g * p.n_out : (size_t)row0) + m;
+#pragma unroll
+      for (int j = 0; j < TN; j += 4) {
+        const int n = n0 + tx * 4 + j * kTx;
+        if (n >= N) continue;
+        float4 o = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+        if (KIND == 2 && p.add) {
+          const float4 f = *reinterpret_cast<const float4*>(p.add + row * N + n);
+          o.x += f.x; o.y += f.y; o.z += f.z; o.w += f.w;
+        }
+        *reinterpret_cast<float4*>(p.out + row * N + n) = o;
+      }
+    }
+  }
+}
+
+template <int KIND, int BM>
+cudaError_t run_f32(const F32Args& p, long long tiles, cudaStream_t s) {
+  const int grid = (int)std::min<long long>(std::max<long long>(tiles, 1), (long long)device_sms() * 4);
+  SMOE_LAUNCH((grouped_f32_kernel<KIND, BM>), grid, 256, 0, s, p);
+  return cudaGetLastError();
+}
+
+// Rows an expert from which the 64-row tiles take over from the 16-row ones.
+constexpr int kF32Rows = 24;
+
+}  // namespace
+
+int device_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 148;
+}
+
+void product_ws_layout(const smoe_desc& d, ProductLayout* L) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  L->status = take(256);
+  L->tiles = take(4 * (kMaxGroups + 2));
+  L->rows = take((size_t)d.T * d.K * std::max(d.d, d.F) * elem_size(d));
+  L->total = off;
+}
+
+cudaError_t launch_expert_rows(const smoe_desc& d, int n_out, int n_in, const void* a, const void* w,
+                               const void* a2, const void* w2, bool transposed,
+                               const int32_t* expert_off, void* out, void* ws, cudaStream_t s) {
+  if (d.dtype != SMOE_F32)
+    return launch_expert_rows_bf16(d, n_out, n_in, a, w, a2, w2, transposed, expert_off, out, ws, s);
+  const int TK = d.T * d.K;
+  const F32Args p{static_cast<const float*>(a), static_cast<const float*>(w),
+                  static_cast<const float*>(a2), static_cast<const float*>(w2), nullptr,
+                  static_cast<float*>(out), expert_off, static_cast<DeviceStatus*>(ws), d.E, TK, n_out, n_in};
+  const bool few = (long long)TK < (long long)kF32Rows * d.E;
+  const long long tiles = ((long long)ceil_div(TK, few ? 16 : 64) + std::min(TK, d.E)) *
+                          ceil_div(transposed ? n_in : n_out, 128);
+  if (transposed) return few ? run_f32<1, 16>(p, tiles, s) : run_f32<1, 64>(p, tiles, s);
+  return few ? run_f32<0, 16>(p, tiles, s) : run_f32<0, 64>(p, tiles, s);
+}
+
+cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void* dy, const void* x,
+                             const int32_t* expert_off, const float* add, float* dw, void* ws,
+                             cudaStream_t s) {
+  const int TK = d.T * d.K;
+  DeviceStatus* st = static_cast<DeviceStatus*>(ws);
+  if (d.dtype == SMOE_F32) {
+    const F32Args p{static_cast<const float*>(dy), static_cast<const float*>(x), nullptr, nullptr, add,
+                    dw, expert_off, st, d.E, TK, n_out, n_in};
+    return run_f32<2, 64>(p, (long long)d.E * ceil_div(n_out, 64) * ceil_div(n_in, 128), s);
+  }
+  alignas(64) CUtensorMap A, B;
+  if (!encode_tmap_2d(&A, dy, false, TK, n_out, 64, 64) || !encode_tmap_2d(&B, x, false, TK, n_in, 64, 64))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDwSmem);
+  if (e != cudaSuccess) return e;
+  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 128), ceil_div(n_in, 256)};
+  const int grid = (int)std::min<long long>(device_sms(), (long long)d.E * p.mt * p.nt);
+  SMOE_LAUNCH(dw_kernel, grid, kDwThreads, kDwSmem, s, A, B, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,
+                              const int32_t* row_src, const int32_t* expert_off, void* ws,
+                              const void** rows_out, cudaStream_t s) {
+  ProductLayout L;
+  product_ws_layout(d, &L);
+  const int TK = d.T * d.K;
+  DeviceStatus* st = ws_ptr<DeviceStatus>(ws, L.status);
+  void* dst = ws_ptr<char>(ws, L.rows);
+  *rows_out = dst;
+  const int grid = std::min(ceil_div(TK, 8), 152 * 8);
+  auto run = [&](auto* out) -> cudaError_t {
+    using TE = std::remove_pointer_t<decltype(out)>;
+    SMOE_LAUNCH((widen_rows_kernel<TE>), grid, 256, 0, s, static_cast<const uint4*>(xq), scale, row_src,
+                expert_off, d.E, TK, row_src ? d.T : TK, cols, out, st);
+    return cudaGetLastError();
+  };
+  return d.dtype == SMOE_F32 ? run(static_cast<float*>(dst)) : run(static_cast<__nv_bfloat16*>(dst));
+}
+
+}  // namespace smoe

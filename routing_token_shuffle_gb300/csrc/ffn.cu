@@ -146,6 +146,8 @@ struct GemmArgs {
   int32_t* g_ticket;
   int32_t* g_counts;
   int g_vec, g_nsrc, g_nchunks, g_chunk;
+  // transposed weights (TW): a second pair of operands, added to the first's product
+  bool two;
 };
 
 struct Tile {
@@ -193,7 +195,10 @@ __device__ __forceinline__ void decode_tile(const int32_t* ts, const int32_t* eo
   }
 }
 
-template <bool UP, bool F32>
+// TW: Y[r, n] = sum_k A[r, k] W[g, k, n] (a row gradient): the weights' rows are the contraction,
+// B is staged as boxes of 64 columns x 64 rows and read MN-major. With p.two the contraction goes on
+// over a second A (tmA_sh) and W (tmB3).
+template <bool UP, bool F32, bool TW = false>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     const __grid_constant__ CUtensorMap tmA_sh,
@@ -205,7 +210,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   constexpr int BK = F32 ? 32 : 64;           // elements per 128-byte row
   constexpr int kMmaK = F32 ? 8 : 16;          // elements per MMA
   constexpr int kMmaPerStage = BK / kMmaK;     // 4
-  constexpr uint32_t kIdesc = tc::instr_desc(F32, kBM, 256);
+  constexpr uint32_t kIdesc = tc::instr_desc(F32, kBM, 256) | (TW ? tc::kIdescTransB : 0u);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -252,7 +257,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
   const int total = s_ts[p.G] * p.NT;
-  const int nkb = (p.KD + BK - 1) / BK;
+  const int nkb1 = (p.KD + BK - 1) / BK, nkb = TW && p.two ? 2 * nkb1 : nkb1;
   volatile int* abort = s_abort;
 
   if (warp == 0 && lane == 0) {
@@ -267,6 +272,15 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
         if (!tc::mbar_wait(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
         tc::mbar_expect_tx(&full[s], kStageA + kStageB);
+        if (TW) {
+          const bool second = kb >= nkb1;
+          const int k0 = (second ? kb - nkb1 : kb) * BK;
+          tc::tma_load_2d(sA + s * kStageA, second ? &tmA_sh : &tmA, &full[s], k0, tl.a_row);
+          for (int j = 0; j < 4; ++j)
+            tc::tma_load_3d(sB + s * kStageB + j * 8192, second ? &tmB3 : &tmB1, &full[s],
+                            tl.n0 + 64 * j, k0, tl.g);
+          continue;
+        }
         tc::tma_load_2d(sA + s * kStageA, amap, &full[s], kb * BK, tl.a_row);
         if (UP) {
           tc::tma_load_2d(sB + s * kStageB, &tmB1, &full[s], kb * BK, tl.b_row);
@@ -299,11 +313,14 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
         tc::fence_after_sync();
         const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kStageA));
-        const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kStageB));
+        const uint64_t bdesc = TW ? tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kStageB))
+                                  : tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kStageB));
 #pragma unroll
         for (int k = 0; k < kMmaPerStage; ++k) {
           const uint32_t acc = (kb > 0 || k > 0) ? 1u : 0u;
-          if (F32)
+          if (TW)
+            tc::mma_bf16(d_tmem, adesc + 2 * k, bdesc + 128 * k, kIdesc, acc);
+          else if (F32)
             tc::mma_tf32(d_tmem, adesc + 2 * k, bdesc + 2 * k, kIdesc, acc);
           else
             tc::mma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, kIdesc, acc);
@@ -526,7 +543,8 @@ __device__ __forceinline__ void decode_pair_tile(const int32_t* ts, const int32_
   }
 }
 
-template <bool UP>
+// TW: as in the single-SM kernel; the second A in tmA_sh and tmA_sh64, the second W in tmB3.
+template <bool UP, bool TW = false>
 __global__ void __launch_bounds__(kPairThreads, 1)
 grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row box
                          const __grid_constant__ CUtensorMap tmA_sh,  // 128-row box
@@ -537,7 +555,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
   // the down GEMM lets the combine be scheduled only as its CTAs finish (see the end)
   if (UP) pdl_wait_and_trigger(); else pdl_wait();
   using TE = __nv_bfloat16;
-  constexpr uint32_t kIdesc = tc::instr_desc(false, 256, 256);
+  constexpr uint32_t kIdesc = tc::instr_desc(false, 256, 256) | (TW ? tc::kIdescTransB : 0u);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -593,7 +611,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
   const int total = s_ts[p.G] * p.NT;
-  const int nkb = (p.KD + 63) / 64;
+  const int nkb1 = (p.KD + 63) / 64, nkb = TW && p.two ? 2 * nkb1 : nkb1;
   volatile int* abort = s_abort;
 
   if (warp == 0 && lane == 0) {
@@ -622,6 +640,16 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
         for (int j = 0; j < nj; ++j) {
           const int kb = kb2 + j;
           uint8_t* b = sB + (s * 2 + j) * kPairStage;
+          if (TW) {
+            const bool second = kb >= nkb1;
+            const int k0 = (second ? kb - nkb1 : kb) * 64, n0 = tl.n0 + (int)rank * 128;
+            const CUtensorMap* a = second ? (box64 ? &tmA_sh64 : &tmA_sh) : (box64 ? &tmA64 : &tmA);
+            const CUtensorMap* w = second ? &tmB3 : &tmB1;
+            tc::tma_load_2d_pair(sA + (s * 2 + j) * kPairStage, a, leader_full, k0, tl.a_row);
+            tc::tma_load_3d_pair(b, w, leader_full, n0, k0, tl.g);
+            tc::tma_load_3d_pair(b + 8192, w, leader_full, n0 + 64, k0, tl.g);
+            continue;
+          }
           tc::tma_load_2d_pair(sA + (s * 2 + j) * kPairStage, amap, leader_full, kb * 64, tl.a_row);
           tc::tma_load_2d_pair(b, &tmB1, leader_full, kb * 64, tl.b_row);
           if (UP) tc::tma_load_2d_pair(b + kPairStage / 2, &tmB3, leader_full, kb * 64, tl.b_row);
@@ -650,7 +678,8 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
       Tile tl;
       decode_pair_tile<UP>(s_ts, s_eo, p, t, rank, tl);
       // swapped tile: the weight rows (B stage) are the MMA's A, the tokens its B
-      const uint32_t idesc = tl.swap ? tc::instr_desc(false, 256, tl.N) : kIdesc;
+      const uint32_t idesc =
+          tl.swap ? tc::instr_desc(false, 256, tl.N) | (TW ? tc::kIdescTransA : 0u) : kIdesc;
       const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
       if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
       tc::fence_after_sync();
@@ -662,12 +691,14 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
         tc::fence_after_sync();
         for (int j = 0; j < nj; ++j) {
           const uint64_t tok_desc = tc::sw128_kmajor_desc(tc::smem_u32(sA + (s * 2 + j) * kPairStage));
-          const uint64_t w_desc = tc::sw128_kmajor_desc(tc::smem_u32(sB + (s * 2 + j) * kPairStage));
+          const uint32_t w_addr = tc::smem_u32(sB + (s * 2 + j) * kPairStage);
+          const uint64_t w_desc = TW ? tc::sw128_mnmajor_desc(w_addr) : tc::sw128_kmajor_desc(w_addr);
           const uint64_t adesc = tl.swap ? w_desc : tok_desc;
           const uint64_t bdesc = tl.swap ? tok_desc : w_desc;
+          const uint32_t a_step = TW && tl.swap ? 128 : 2, b_step = TW && !tl.swap ? 128 : 2;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc,
+            tc::mma_bf16_pair(d_tmem, adesc + a_step * k, bdesc + b_step * k, idesc,
                               (kb2 + j > 0 || k > 0) ? 1u : 0u);
         }
         tc::commit_pair(&empty[s], 0x3);
@@ -825,12 +856,6 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
   if (warp == 2) tc::tmem_dealloc_pair(tmem, 2 * kAccCols);
 }
 
-template <bool UP>
-cudaError_t launch_gemm_pair(const CUtensorMap& A, const CUtensorMap& Ash, const CUtensorMap& A64,
-                             const CUtensorMap& Ash64, const CUtensorMap& B1,
-                             const CUtensorMap& B3, const GemmArgs& args, long long tile_bound,
-                             cudaStream_t s);
-
 int sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -838,11 +863,11 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
-template <bool UP, bool F32>
+template <bool UP, bool F32, bool TW = false>
 cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& Ash, const CUtensorMap& B1,
                         const CUtensorMap& B3, const GemmArgs& args, long long tile_bound,
                         cudaStream_t s) {
-  auto kern = grouped_gemm_kernel<UP, F32>;
+  auto kern = grouped_gemm_kernel<UP, F32, TW>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -851,12 +876,12 @@ cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& Ash, const CUte
   return cudaGetLastError();
 }
 
-template <bool UP>
+template <bool UP, bool TW = false>
 cudaError_t launch_gemm_pair(const CUtensorMap& A, const CUtensorMap& Ash, const CUtensorMap& A64,
                              const CUtensorMap& Ash64, const CUtensorMap& B1,
                              const CUtensorMap& B3, const GemmArgs& args, long long tile_bound,
                              cudaStream_t s) {
-  auto kern = grouped_gemm_pair_kernel<UP>;
+  auto kern = grouped_gemm_pair_kernel<UP, TW>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kPairSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1010,20 +1035,18 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-bool encode_tmap_2d(CUtensorMap* map, const void* base, bool fp32, uint64_t rows, uint64_t cols,
-                    uint32_t box_rows, uint32_t box_cols) {
+namespace {
+
+bool encode_tmap(CUtensorMap* map, const void* base, bool fp32, int rank, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) {
     set_last_error(SMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     return false;
   }
-  const uint32_t esz = fp32 ? 4 : 2;
-  cuuint64_t dims[2] = {cols, rows > 0 ? rows : 1};
-  cuuint64_t strides[1] = {cols * esz};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                  2, const_cast<void*>(base), dims, strides, box, estr,
+                  rank, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -1033,6 +1056,23 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, bool fp32, uint64_t rows
   return true;
 }
 
+}  // namespace
+
+bool encode_tmap_2d(CUtensorMap* map, const void* base, bool fp32, uint64_t rows, uint64_t cols,
+                    uint32_t box_rows, uint32_t box_cols) {
+  const cuuint64_t dims[2] = {cols, rows > 0 ? rows : 1};
+  const cuuint64_t strides[1] = {cols * (fp32 ? 4 : 2)};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return encode_tmap(map, base, fp32, 2, dims, strides, box);
+}
+
+bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t rows, uint64_t cols) {
+  const cuuint64_t dims[3] = {cols, rows, outer};
+  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  const cuuint32_t box[3] = {64, 64, 1};
+  return encode_tmap(map, base, false, 3, dims, strides, box);
+}
+
 cudaError_t launch_expert_ffn(const smoe_desc& d, const void* x_disp, const void* x,
                               const int32_t* expert_off, const void* w1, const void* w3,
                               const void* w2, void* y_disp, void* y_sh, void* ws,
@@ -1040,6 +1080,45 @@ cudaError_t launch_expert_ffn(const smoe_desc& d, const void* x_disp, const void
   if (d.dtype == SMOE_F32)
     return run_ffn<true>(d, x_disp, x, expert_off, w1, w3, w2, y_disp, y_sh, ws, s, gather);
   return run_ffn<false>(d, x_disp, x, expert_off, w1, w3, w2, y_disp, y_sh, ws, s, gather);
+}
+
+// Both products of rows, on the kernels of the FFN's down product. (A pair's a_row maps need no
+// shared experts' rows: the second operands of a row gradient take their place.)
+cudaError_t launch_expert_rows_bf16(const smoe_desc& d, int n_out, int n_in, const void* a,
+                                    const void* w, const void* a2, const void* w2, bool transposed,
+                                    const int32_t* expert_off, void* out, void* ws, cudaStream_t s) {
+  ProductLayout L;
+  product_ws_layout(d, &L);
+  DeviceStatus* st = ws_ptr<DeviceStatus>(ws, L.status);
+  int32_t* tiles = ws_ptr<int32_t>(ws, L.tiles);
+  const int TK = d.T * d.K, N = transposed ? n_in : n_out, KD = transposed ? n_out : n_in;
+  const bool pairs = use_pair_tiles(d);
+  const int bm = pairs ? 256 : kBM;
+  SMOE_LAUNCH(tile_table_kernel, 1, 32, 0, s, expert_off, d.E, 0, d.T, TK, bm, tiles, st,
+              (int32_t*)nullptr, 0);
+  GemmArgs p{expert_off, tiles, out, nullptr, st, d.E, d.E, d.T, TK, N, KD, ceil_div(N, 256)};
+  p.two = a2 != nullptr;
+  if (a2 == nullptr) {
+    a2 = a;
+    w2 = w;
+  }
+  alignas(64) CUtensorMap A, A2, A64, A264, B, B2;
+  if (!encode_tmap_2d(&A, a, false, TK, KD, 128, 64) || !encode_tmap_2d(&A2, a2, false, TK, KD, 128, 64))
+    return cudaErrorInvalidValue;
+  if (transposed) {
+    if (!encode_tmap_3d(&B, w, d.E, n_out, n_in) || !encode_tmap_3d(&B2, w2, d.E, n_out, n_in))
+      return cudaErrorInvalidValue;
+  } else if (!encode_tmap_2d(&B, w, false, (uint64_t)d.E * N, KD, pairs ? 128 : 256, 64)) {
+    return cudaErrorInvalidValue;
+  }
+  const long long bound = ((long long)ceil_div(TK, bm) + d.E) * p.NT;
+  if (!pairs)
+    return transposed ? launch_gemm<false, false, true>(A, A2, B, B2, p, bound, s)
+                      : launch_gemm<false, false>(A, A, B, B, p, bound, s);
+  if (!encode_tmap_2d(&A64, a, false, TK, KD, 64, 64) || !encode_tmap_2d(&A264, a2, false, TK, KD, 64, 64))
+    return cudaErrorInvalidValue;
+  return transposed ? launch_gemm_pair<false, true>(A, A2, A64, A264, B, B2, p, bound, s)
+                    : launch_gemm_pair<false>(A, A, A64, A64, B, B, p, bound, s);
 }
 
 }  // namespace smoe

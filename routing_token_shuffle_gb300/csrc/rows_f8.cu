@@ -1,0 +1,298 @@
+// Rows in 8-bit floating point (e4m3) with a scale per row and 128 channels, and the SwiGLU
+// activation that keeps its inputs so between the forward and the backward pass:
+//   s = max |x| / 448 over a block (or the power of two that is not below it), q = rn(x / s);
+//   h = g sig(g) u, keeping g and u as such blocks;
+//   dg = dh u sig(g) (1 + g (1 - sig(g))), du = dh g sig(g), h again, from what was kept.
+// Every element is read once and written once, so HBM is the bound. A block of 128 channels is
+// 16 lanes of 8 values (16 bytes of bf16, 8 of the 8-bit values: full sectors both ways); its
+// largest magnitude takes four shuffles, and nothing is kept in shared memory. A power-of-two
+// scale costs no precision but at the smallest magnitudes (the format has its own exponent), its
+// division is exact, and what it stands for is exact in bf16, so that a product of bf16 rows
+// reads the kept values without another rounding.
+#include <algorithm>
+#include <cfloat>
+#include <cuda_fp8.h>
+
+#include "smoe_internal.cuh"
+
+namespace smoe {
+namespace {
+
+constexpr int kRowsThreads = 256;                 // 16 blocks of 128 channels at a time
+constexpr int kRowsGroups = kRowsThreads / 16;
+
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  unpack16(*reinterpret_cast<const uint4*>(p), v, (const __nv_bfloat16*)nullptr);
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = pack16(v, (const __nv_bfloat16*)nullptr);
+}
+
+// The block's 16 lanes hold 8 values each (zeros past the row's end). Magnitudes are compared as
+// unsigned integers: a NaN is above every number, so its block does not pass for a finite one.
+// A block whose scale would be subnormal gets scale 0 and zeros, one with an infinity or a NaN
+// scale NaN and zeros.
+__device__ __forceinline__ uint2 quantise8(const float* v, bool pow2, float* scale) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int off = 8; off; off >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, off));
+  const float amax = __uint_as_float(big);
+  const bool finite = big <= 0x7f7fffffu;
+  float s = amax / 448.0f;
+  const bool zero = !finite || s < FLT_MIN;
+  if (zero) s = finite ? 0.0f : __int_as_float(0x7fc00000);
+  else if (pow2) s = __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
+  *scale = s;
+  uint2 q = make_uint2(0u, 0u);
+  if (!zero) {
+    const float inv = 1.0f / s;  // exact for a power of two (between 2^-126 and 2^120)
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = pow2 ? v[2 * i] * inv : v[2 * i] / s;
+      const float b = pow2 ? v[2 * i + 1] * inv : v[2 * i + 1] / s;
+      w[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    }
+    q = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
+  return q;
+}
+
+// 8 kept values times their block's scale
+__device__ __forceinline__ void widen8(const uint2& q, float s, float* v) {
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)) & 0xffffu), __NV_E4M3));
+    const float2 f = __half22float2(h);
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+}
+
+// sig(x): for bf16 results with the fast exponential and division (2^-20), for fp32 ones with
+// the accurate forms
+template <typename TE>
+__device__ __forceinline__ float sigmoid(float x) {
+  if (sizeof(TE) == 2) return __fdividef(1.0f, 1.0f + __expf(-x));
+  return 1.0f / (1.0f + expf(-x));
+}
+
+// This thread's place: item `it` of `items` is 128 channels of a row.
+struct Place {
+  bool in, lead;   // inside the row; the block's first lane
+  int col;
+  size_t at, block;  // element and scale index
+};
+__device__ __forceinline__ Place place(uint32_t it, uint32_t items, int cols, uint32_t nblk) {
+  Place p;
+  const uint32_t row = it / nblk, b = it - row * nblk;
+  const int l = threadIdx.x & 15;
+  p.col = (int)b * 128 + l * 8;
+  p.in = it < items && p.col < cols;
+  p.lead = it < items && l == 0;
+  p.at = (size_t)row * cols + p.col;
+  p.block = (size_t)row * nblk + b;
+  return p;
+}
+
+// U blocks a thread, their loads ahead of the rest.
+template <typename TE, int U>
+__global__ void __launch_bounds__(kRowsThreads)
+rows_f8_kernel(const TE* x, uint2* q, float* scale, uint32_t items, int cols, uint32_t nblk,
+               int pow2) {
+  pdl_wait_and_trigger();
+  const uint32_t first = blockIdx.x * (kRowsGroups * U) + (threadIdx.x >> 4);
+  float v[U][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place p = place(first + u * kRowsGroups, items, cols, nblk);
+    if (p.in) load8(x + p.at, v[u]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place p = place(first + u * kRowsGroups, items, cols, nblk);
+    float s;
+    const uint2 w = quantise8(v[u], pow2 != 0, &s);
+    if (p.in) q[p.at >> 3] = w;
+    if (p.lead) scale[p.block] = s;
+  }
+}
+
+template <typename TE>
+struct SwigluArgs {
+  const TE *g, *u;
+  TE* h;               // each output nullable
+  uint2 *h8, *g8, *u8;
+  float *hs, *gs, *us;
+  uint32_t items, nblk;
+  int cols, pow2;
+};
+
+template <typename TE, int U>
+__global__ void __launch_bounds__(kRowsThreads)
+swiglu_f8_kernel(const SwigluArgs<TE> a) {
+  pdl_wait_and_trigger();
+  const uint32_t first = blockIdx.x * (kRowsGroups * U) + (threadIdx.x >> 4);
+  float g[U][8], up[U][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place p = place(first + u * kRowsGroups, a.items, a.cols, a.nblk);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[u][i] = up[u][i] = 0.0f;
+    if (p.in) {
+      load8(a.g + p.at, g[u]);
+      load8(a.u + p.at, up[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place p = place(first + u * kRowsGroups, a.items, a.cols, a.nblk);
+    float s;
+    if (a.g8) {
+      const uint2 w = quantise8(g[u], a.pow2 != 0, &s);
+      if (p.in) a.g8[p.at >> 3] = w;
+      if (p.lead) a.gs[p.block] = s;
+    }
+    if (a.u8) {
+      const uint2 w = quantise8(up[u], a.pow2 != 0, &s);
+      if (p.in) a.u8[p.at >> 3] = w;
+      if (p.lead) a.us[p.block] = s;
+    }
+    if (a.h == nullptr && a.h8 == nullptr) continue;
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = g[u][i] * sigmoid<TE>(g[u][i]) * up[u][i];
+    if (a.h && p.in) store8(a.h + p.at, h);
+    if (a.h8) {
+      const uint2 w = quantise8(h, a.pow2 != 0, &s);
+      if (p.in) a.h8[p.at >> 3] = w;
+      if (p.lead) a.hs[p.block] = s;
+    }
+  }
+}
+
+template <typename TE>
+struct SwigluGradArgs {
+  const TE* dh;
+  const uint2 *g8, *u8;
+  const float *gs, *us;
+  TE *dg, *du, *h;     // h nullable
+  uint32_t items, nblk;
+  int cols;
+};
+
+template <typename TE, int U>
+__global__ void __launch_bounds__(kRowsThreads)
+swiglu_grad_f8_kernel(const SwigluGradArgs<TE> a) {
+  pdl_wait_and_trigger();
+  const uint32_t first = blockIdx.x * (kRowsGroups * U) + (threadIdx.x >> 4);
+  float dh[U][8], gs[U], us[U];
+  uint2 g8[U], u8[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place p = place(first + u * kRowsGroups, a.items, a.cols, a.nblk);
+    if (!p.in) continue;
+    load8(a.dh + p.at, dh[u]);
+    g8[u] = a.g8[p.at >> 3];
+    u8[u] = a.u8[p.at >> 3];
+    gs[u] = a.gs[p.block];
+    us[u] = a.us[p.block];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place p = place(first + u * kRowsGroups, a.items, a.cols, a.nblk);
+    if (!p.in) continue;
+    float g[8], up[8], h[8];
+    widen8(g8[u], gs[u], g);
+    widen8(u8[u], us[u], up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float sig = sigmoid<TE>(g[i]), silu = g[i] * sig, d = dh[u][i];
+      h[i] = silu * up[i];
+      g[i] = d * up[i] * (sig * (1.0f + g[i] * (1.0f - sig)));
+      up[i] = d * silu;
+    }
+    store8(a.dg + p.at, g);
+    store8(a.du + p.at, up);
+    if (a.h) store8(a.h + p.at, h);
+  }
+}
+
+// Four blocks a thread once the grid fills the GPU all the same.
+constexpr uint32_t kManyItems = 152 * 8 * kRowsGroups * 4;
+
+}  // namespace
+
+cudaError_t launch_rows_f8(const smoe_desc& d, int rows, int cols, const void* x, int pow2, void* q,
+                           float* scale, cudaStream_t s) {
+  const uint32_t nblk = ceil_div(cols, 128), items = (uint32_t)rows * nblk;
+  auto run = [&](auto* xt) -> cudaError_t {
+    using TE = std::remove_const_t<std::remove_pointer_t<decltype(xt)>>;
+    if (items >= kManyItems)
+      SMOE_LAUNCH((rows_f8_kernel<TE, 4>), ceil_div(items, kRowsGroups * 4), kRowsThreads, 0, s, xt,
+                  static_cast<uint2*>(q), scale, items, cols, nblk, pow2);
+    else
+      SMOE_LAUNCH((rows_f8_kernel<TE, 1>), ceil_div(items, kRowsGroups), kRowsThreads, 0, s, xt,
+                  static_cast<uint2*>(q), scale, items, cols, nblk, pow2);
+    return cudaGetLastError();
+  };
+  return d.dtype == SMOE_F32 ? run(static_cast<const float*>(x))
+                             : run(static_cast<const __nv_bfloat16*>(x));
+}
+
+cudaError_t launch_swiglu_f8(const smoe_desc& d, int rows, int cols, const void* g, const void* u,
+                             int pow2, void* h, const F8Rows& h8, const F8Rows& g8, const F8Rows& u8,
+                             cudaStream_t s) {
+  const uint32_t nblk = ceil_div(cols, 128), items = (uint32_t)rows * nblk;
+  auto run = [&](auto* gt) -> cudaError_t {
+    using TE = std::remove_const_t<std::remove_pointer_t<decltype(gt)>>;
+    const SwigluArgs<TE> a{gt, static_cast<const TE*>(u), static_cast<TE*>(h),
+                           static_cast<uint2*>(h8.q), static_cast<uint2*>(g8.q),
+                           static_cast<uint2*>(u8.q), h8.scale, g8.scale, u8.scale,
+                           items, nblk, cols, pow2};
+    if (items >= kManyItems)
+      SMOE_LAUNCH((swiglu_f8_kernel<TE, 2>), ceil_div(items, kRowsGroups * 2), kRowsThreads, 0, s, a);
+    else
+      SMOE_LAUNCH((swiglu_f8_kernel<TE, 1>), ceil_div(items, kRowsGroups), kRowsThreads, 0, s, a);
+    return cudaGetLastError();
+  };
+  return d.dtype == SMOE_F32 ? run(static_cast<const float*>(g))
+                             : run(static_cast<const __nv_bfloat16*>(g));
+}
+
+cudaError_t launch_swiglu_grad_f8(const smoe_desc& d, int rows, int cols, const void* dh,
+                                  const void* g8, const float* gs, const void* u8, const float* us,
+                                  void* dg, void* du, void* h, cudaStream_t s) {
+  const uint32_t nblk = ceil_div(cols, 128), items = (uint32_t)rows * nblk;
+  auto run = [&](auto* dt) -> cudaError_t {
+    using TE = std::remove_const_t<std::remove_pointer_t<decltype(dt)>>;
+    const SwigluGradArgs<TE> a{dt, static_cast<const uint2*>(g8), static_cast<const uint2*>(u8), gs, us,
+                               static_cast<TE*>(dg), static_cast<TE*>(du), static_cast<TE*>(h),
+                               items, nblk, cols};
+    if (items >= kManyItems)
+      SMOE_LAUNCH((swiglu_grad_f8_kernel<TE, 2>), ceil_div(items, kRowsGroups * 2), kRowsThreads, 0, s, a);
+    else
+      SMOE_LAUNCH((swiglu_grad_f8_kernel<TE, 1>), ceil_div(items, kRowsGroups), kRowsThreads, 0, s, a);
+    return cudaGetLastError();
+  };
+  return d.dtype == SMOE_F32 ? run(static_cast<const float*>(dh))
+                             : run(static_cast<const __nv_bfloat16*>(dh));
+}
+
+}  // namespace smoe

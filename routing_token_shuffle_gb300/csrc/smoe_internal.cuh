@@ -291,4 +291,44 @@ cudaError_t launch_expert_ffn_i8(const smoe_desc& d, const int8_t* xq, const flo
                                  const smoe_i8_weights& W, void* y_disp, void* y_sh, void* ws,
                                  cudaStream_t s);
 
+// Rows in 8-bit floating point with a scale per 128 channels (rows_f8.cu).
+struct F8Rows {
+  void* q;
+  float* scale;
+};
+cudaError_t launch_rows_f8(const smoe_desc& d, int rows, int cols, const void* x, int pow2, void* q,
+                           float* scale, cudaStream_t s);
+cudaError_t launch_swiglu_f8(const smoe_desc& d, int rows, int cols, const void* g, const void* u,
+                             int pow2, void* h, const F8Rows& h8, const F8Rows& g8, const F8Rows& u8,
+                             cudaStream_t s);
+cudaError_t launch_swiglu_grad_f8(const smoe_desc& d, int rows, int cols, const void* dh,
+                                  const void* g8, const float* gs, const void* u8, const float* us,
+                                  void* dg, void* du, void* h, cudaStream_t s);
+
+// Expert products in 8-bit floating point (expert_f8.cu), and in the layer's type with their
+// gradients (ffn.cu, expert_grad.cu). One workspace for all of them.
+struct ProductLayout {
+  size_t status, tiles, rows, total;  // rows: widened rows of a weight gradient
+};
+void product_ws_layout(const smoe_desc& d, ProductLayout* out);
+int device_sms();  // of the current device
+cudaError_t launch_expert_matmul_f8(const smoe_desc& d, int n_out, int n_in, const void* xq,
+                                    const float* xs, const int32_t* row_src,
+                                    const int32_t* expert_off, const void* wq, const float* w_scale,
+                                    void* out, void* ws, cudaStream_t s);
+// out = a w^T, or (transposed) a w + a2 w2; a2, w2 nullable
+cudaError_t launch_expert_rows(const smoe_desc& d, int n_out, int n_in, const void* a, const void* w,
+                               const void* a2, const void* w2, bool transposed,
+                               const int32_t* expert_off, void* out, void* ws, cudaStream_t s);
+cudaError_t launch_expert_rows_bf16(const smoe_desc& d, int n_out, int n_in, const void* a,
+                                    const void* w, const void* a2, const void* w2, bool transposed,
+                                    const int32_t* expert_off, void* out, void* ws, cudaStream_t s);
+cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void* dy, const void* x,
+                             const int32_t* expert_off, const float* add, float* dw, void* ws,
+                             cudaStream_t s);
+// the workspace's rows = kept rows in the layer's type
+cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,
+                              const int32_t* row_src, const int32_t* expert_off, void* ws,
+                              const void** rows_out, cudaStream_t s);
+
 }  // namespace smoe

@@ -124,6 +124,16 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// The same of a 3-D tensor (c2: its outermost index).
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 16 bytes to shared memory without a register between; bytes past `valid` are zeros.
 __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, uint32_t valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(valid)
@@ -221,6 +231,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map,
+                                                 uint32_t cluster_bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
+      : "memory");
+}
+
 // A warp of each CTA of the pair allocates, and the peer CTA has to be running by then: call it
 // behind a cluster barrier. (The allocation has no limit to its wait. In front of the barrier,
 // with the pair's CTAs started apart because the kernel before still held one of the two SMs,
@@ -314,6 +333,16 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// 8-bit floating-point operands (32 of K an instruction).
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // The same with fp16 operands, A from TMEM: lane = row, two consecutive K elements in each
 // 32-bit column (8 columns per K = 16 instruction).
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
@@ -402,6 +431,21 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
   return d;
 }
 
+// The same of a 16-bit operand whose K is the row index in memory (MN-major): TMA boxes of 64
+// columns (128 bytes) x 64 rows of K, 8192 bytes each, side by side along M or N. Eight rows of
+// K are 1024 bytes (stride byte offset), the next 64 columns 8192 bytes on (leading byte
+// offset). Advancing K by 16 rows adds 2048 bytes: 128 to the address field.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+  uint64_t d = (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(8192u >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+// Bits of the instruction descriptor that say so of A and of B.
+constexpr uint32_t kIdescTransA = 1u << 15, kIdescTransB = 1u << 16;
+
 // Instruction descriptor of tcgen05.mma kind::f16 (bf16 inputs) / kind::tf32 with an
 // fp32 accumulator, both operands K-major: D format bits 4-5 = 1 (f32), A and B
 // formats bits 7-9 / 10-12 (bf16 = 1, tf32 = 2), N >> 3 in bits 17-22, M >> 4 in
@@ -416,11 +460,19 @@ __host__ __device__ constexpr uint32_t instr_desc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The same of kind::f8f6f4 with e4m3 operands (formats 0).
+__host__ __device__ constexpr uint32_t instr_desc_f8(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 }  // namespace tc
 
 // Host: encode a 2-D row-major tensor map [rows, cols] with a (box_cols x box_rows)
 // box and 128-byte swizzle. Returns false (and sets the last error) on failure.
 bool encode_tmap_2d(CUtensorMap* map, const void* base, bool fp32, uint64_t rows, uint64_t cols,
                     uint32_t box_rows, uint32_t box_cols);
+// The same of a 3-D bf16 tensor [outer, rows, cols] with a (64 x 64) box of one outer index: rows
+// and columns past a matrix' own read as zeros, not as the next matrix.
+bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t rows, uint64_t cols);
 
 }  // namespace smoe

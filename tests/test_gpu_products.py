@@ -1,0 +1,425 @@
+"""The 8-bit floating-point rows and products, the grouped products with their gradients and the
+8-bit activation checkpoints on the GPU, against plain formulas in 64 bits.
+
+Tolerances. A rounding is off by at most half a step of its type (bf16 2^-8, fp32 2^-24, e4m3
+2^-4, relative to the value). A sum of n products in fp32, each addition off by at most a step of
+the running sum (2^-23: a tensor core may cut off instead of rounding), is off by at most n 2^-23
+sum |a b|; a tensor core adds 16 (32) products at once, so n is the count of its additions."""
+import math
+
+import pytest
+import torch
+
+import routing_token_shuffle_gb300 as smoe
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+F8 = torch.float8_e4m3fn
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    assert torch.cuda.is_available()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def within(x, ref, tol):
+    """|x - ref| <= tol everywhere (a NaN is not)."""
+    err = (x.double() - ref.double()).abs()
+    bad = ~(err <= tol)
+    n = int(bad.sum())
+    assert n == 0, (n, float(err[bad].max()), bad.nonzero()[0].tolist())
+
+
+def same(a, b):
+    n = int((a != b).sum())
+    assert n == 0, (n, a.numel(), (a != b).nonzero()[0].tolist())
+
+
+def f8(x):
+    """e4m3, with zeros for values past the largest (only magnitudes up to 448 are passed)."""
+    return x.to(F8)
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+def spread(s, n):
+    return s.double().repeat_interleave(128, -1)[..., :n]
+
+
+# ------------------------------------------------------------------ rows in 8 bits
+def rows_desc(dt):
+    return smoe.make_desc(1, 8, 1, 1, 1, 8, 0, 1, 1, dt)
+
+
+def rows_ref(x, pow2):
+    """(scale, x / scale) by block, in fp32 as it is documented."""
+    T, d = x.shape
+    pad = torch.zeros(T, blocks(d) * 128, device=x.device)
+    pad[:, :d] = x.float().abs()
+    s = pad.view(T, -1, 128).amax(-1)
+    s = s / torch.full_like(s, 448.0)  # (by a number torch would multiply with its inverse)
+    if pow2:
+        m, e = torch.frexp(s)
+        s = torch.where(s > 0, torch.ldexp(torch.ones_like(s), torch.where(m == 0.5, e - 1, e)), s)
+    return s, x.float() / s.repeat_interleave(128, 1)[:, :d]
+
+
+@pytest.mark.parametrize("pow2", [0, 1])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 8), (3, 128), (1, 136), (17, 120), (64, 5120), (2049, 2048),
+                                 (33, 8200), (700, 1000), (40000, 128)])
+def test_rows_f8(T, d, dt, pow2):
+    x = (randn(gen(T + d), T, d) * 3).to(DT[dt])
+    q = torch.full((T, d), 7, dtype=torch.uint8, device="cuda")
+    s = torch.full((T, blocks(d)), 7.0, device="cuda")
+    smoe.smoe_rows_f8(rows_desc(dt), x, q, s, pow2=pow2)
+    rs, v = rows_ref(x, pow2)
+    same(s, rs)
+    same(q, f8(v).view(torch.uint8))
+    # half a step of e4m3, and half of its smallest step (2^-9) for magnitudes near zero
+    within(q.view(F8).double() * spread(s, d), x, x.double().abs() * 2.0 ** -4 + spread(s, d) * 2.0 ** -10)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("pow2", [0, 1])
+def test_rows_f8_odd_blocks(dt, pow2):
+    """Zero blocks, tiny blocks, exact powers of two, blocks with an infinity or a NaN; the blocks
+    beside them and the largest values."""
+    x = randn(gen(3), 9, 300).to(DT[dt])
+    x[1, :128] = 0.0
+    x[2, 128:256] *= 1e-37          # 4e-37 / 448: below the smallest normal number
+    x[3, 5], x[4, 299], x[5, 130] = math.inf, math.nan, -math.inf
+    x[6] = 0.0
+    x[6, ::128] = 3.5               # 448 x 2^-7
+    x[7] = torch.finfo(DT[dt]).max
+    x[8, :128] *= 1e-30
+    q = torch.full((9, 300), 7, dtype=torch.uint8, device="cuda")
+    s = torch.full((9, 3), 7.0, device="cuda")
+    # 300 is no multiple of 8: the first 296 channels
+    x, q = x[:, :296].contiguous(), q[:, :296].contiguous()
+    x[4, 295] = math.nan
+    smoe.smoe_rows_f8(rows_desc(dt), x, q, s, pow2=pow2)
+    bad = torch.zeros(9, 3, dtype=torch.bool, device="cuda")
+    bad[3, 0] = bad[4, 2] = bad[5, 1] = True
+    zero = torch.zeros_like(bad)
+    zero[1, 0] = zero[2, 1] = True
+    assert s[bad].isnan().all() and (s[zero] == 0).all()
+    off = (bad | zero).repeat_interleave(128, 1)[:, :296]
+    assert (q[off] == 0).all()
+    rs, v = rows_ref(torch.where(off, torch.zeros_like(x), x), pow2)
+    same(s[~(bad | zero)], rs[~(bad | zero)])
+    same(q[~off], f8(torch.where(off, torch.zeros_like(v), v)).view(torch.uint8)[~off])
+    assert (s[6] == 2.0 ** -7).all() and (q[6, ::128] == 0x7e).all()
+
+
+# ------------------------------------------------------------------ SwiGLU, kept in 8 bits
+def swiglu_tol(dt):
+    """exp, a division and three products around them in fp32 (under 2^-20 with the fast forms of
+    bf16 layers, 2^-21 with the accurate ones), and the result's rounding."""
+    return HALF[dt] + (2.0 ** -20 if dt == "bf16" else 2.0 ** -21)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 8), (5, 128), (384, 1536), (37, 1000), (3001, 768), (9, 14336)])
+def test_swiglu_f8(T, d, dt):
+    g_ = gen(T * 7 + d)
+    g, u, dh = ((randn(g_, T, d) * s).to(DT[dt]) for s in (2.0, 1.0, 0.1))
+    if d >= 128:
+        g[0, :8] = torch.tensor([-200.0, -90, -20, -1e-6, 0, 1e-6, 60, 300], device="cuda").to(DT[dt])
+    new = lambda: (torch.full((T, d), 7, dtype=torch.uint8, device="cuda"),  # noqa: E731
+                   torch.full((T, blocks(d)), 7.0, device="cuda"))
+    (h8, hs), (g8, gs), (u8, us) = new(), new(), new()
+    h = torch.full_like(g, 7.0)
+    desc = rows_desc(dt)
+    smoe.smoe_swiglu_f8(desc, g, u, h=h, h8=h8, h8_scale=hs, g8=g8, g8_scale=gs, u8=u8, u8_scale=us)
+    for x, q, s in ((g, g8, gs), (u, u8, us)):
+        rs, v = rows_ref(x, 1)
+        same(s, rs)
+        same(q, f8(v).view(torch.uint8))
+    G, U = g.double(), u.double()
+    ref = G * torch.sigmoid(G) * U
+    # sig below 2^-126 is zero in fp32: 1e-37 |g u|
+    within(h, ref, swiglu_tol(dt) * ref.abs() + 1e-37 * (G * U).abs() + 1e-38)
+    back = h8.view(F8).double() * spread(hs, d)
+    within(back, ref, ref.abs() * (2.0 ** -4 + 2.0 ** -19) + spread(hs, d) * 2.0 ** -9)
+    # each output alone, h over g and over u
+    for k in ("h8", "g8", "u8"):
+        q, s = new()
+        smoe.smoe_swiglu_f8(desc, g, u, **{k: q, k + "_scale": s})
+        want = {"h8": (h8, hs), "g8": (g8, gs), "u8": (u8, us)}[k]
+        same(q, want[0])
+        same(s, want[1])
+    for over in (0, 1):
+        a = [g.clone(), u.clone()]
+        smoe.smoe_swiglu_f8(desc, *a, h=a[over])
+        same(a[over], h)
+    # backward, from what was kept
+    G, U, D = g8.view(F8).double() * spread(gs, d), u8.view(F8).double() * spread(us, d), dh.double()
+    sig = torch.sigmoid(G)
+    dg, du, h2 = (torch.full_like(g, 7.0) for _ in range(3))
+    smoe.smoe_swiglu_grad_f8(desc, dh, g8, gs, u8, us, dg, du, h=h2)
+    tol = swiglu_tol(dt)
+    small = 1e-37 * (1 + (G * U * D).abs() + (G * D).abs() + (G * U).abs()) + 1e-38
+    # 1 + g (1 - sig) has a root near g = -1.28: what its terms lose is relative to them
+    terms = (D * U * sig).abs() * (1 + G.abs() * (1 - sig))
+    ref = D * U * sig * (1 + G * (1 - sig))
+    # (1 - sig is off by a step of 1 where sig is near it: 2^-23 |g|)
+    within(dg, ref, HALF[dt] * ref.abs() + 2 * (tol - HALF[dt]) * terms + 2.0 ** -23 * (D * U * sig * G).abs() + small)
+    within(du, D * G * sig, tol * (D * G * sig).abs() + small)
+    within(h2, G * sig * U, tol * (G * sig * U).abs() + small)
+    dg2 = dh.clone()
+    smoe.smoe_swiglu_grad_f8(desc, dg2, g8, gs, u8, us, dg2, torch.empty_like(du))
+    same(dg2, dg)
+
+
+def test_swiglu_gradient_against_differences():
+    """dg and du of sum(h dh), by central differences in 64 bits of the kept values."""
+    g_ = gen(11)
+    desc, dh = rows_desc("f32"), randn(g_, 4, 128)
+    g, u = randn(g_, 4, 128) * 2, randn(g_, 4, 128)
+    q = [torch.empty(4, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.empty(4, 1, device="cuda") for _ in range(2)]
+    smoe.smoe_swiglu_f8(desc, g, u, g8=q[0], g8_scale=s[0], u8=q[1], u8_scale=s[1])
+    dg, du = torch.empty_like(g), torch.empty_like(g)
+    smoe.smoe_swiglu_grad_f8(desc, dh, q[0], s[0], q[1], s[1], dg, du)
+    G, U = (a.view(F8).double() * spread(b, 128) for a, b in zip(q, s))
+    f = lambda g, u: g * torch.sigmoid(g) * u * dh.double()  # noqa: E731
+    e = 1e-5
+    # the differences' own error: e^2 |h'''| / 6, and 2^-52 / e of the values
+    num = (f(G + e, U) - f(G - e, U)) / (2 * e)
+    within(dg, num, 1e-6 * (1 + num.abs()))
+    num = (f(G, U + e) - f(G, U - e)) / (2 * e)
+    within(du, num, 1e-6 * (1 + num.abs()))
+
+
+def test_swiglu_kept_block_that_is_not_finite():
+    """A kept block with a NaN scale gives NaN gradients there, and nowhere else."""
+    g = randn(gen(2), 3, 384)
+    u, dh = torch.ones_like(g), torch.ones_like(g)
+    g[1, 200] = math.inf
+    q = [torch.empty(3, 384, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.empty(3, 3, device="cuda") for _ in range(2)]
+    smoe.smoe_swiglu_f8(rows_desc("f32"), g, u, g8=q[0], g8_scale=s[0], u8=q[1], u8_scale=s[1])
+    dg, du = torch.empty_like(g), torch.empty_like(g)
+    smoe.smoe_swiglu_grad_f8(rows_desc("f32"), dh, q[0], s[0], q[1], s[1], dg, du)
+    bad = torch.zeros(3, 384, dtype=torch.bool, device="cuda")
+    bad[1, 128:256] = True
+    assert torch.equal(dg.isnan(), bad) and torch.equal(du.isnan(), bad)
+
+
+# ------------------------------------------------------------------ products
+def offsets(kind, R, E, seed):
+    """expert_off of R rows: even; skewed with empty experts; all on one expert; the last rows
+    (and the first) on nobody."""
+    rng = torch.Generator().manual_seed(seed)
+    if kind == "one":
+        n = torch.zeros(E, dtype=torch.long)
+        n[E // 2] = R
+    elif kind == "even":
+        n = torch.full((E,), R // E)
+        n[: R - int(n.sum())] += 1
+    else:
+        p = torch.rand(E, generator=rng) ** 3
+        p[torch.rand(E, generator=rng) < 0.3] = 0.0
+        if float(p.sum()) == 0:
+            p[0] = 1.0
+        used = R if kind == "skew" else max(1, R - R // 5)
+        n = torch.bincount(torch.multinomial(p, used, replacement=True, generator=rng), minlength=E)
+    first = R // 10 if kind == "gaps" else 0
+    off = torch.cat([torch.zeros(1, dtype=torch.long), n.cumsum(0)]) + first
+    return off.to(torch.int32).cuda().clamp_(max=R)
+
+
+class Case:
+    def __init__(self, T, K, E, n_in, n_out, dt, kind, seed=0):
+        self.T, self.K, self.E, self.n_in, self.n_out, self.dt = T, K, E, n_in, n_out, dt
+        self.R = T * K
+        self.off = offsets(kind, self.R, E, seed + T)
+        o = self.off.tolist()
+        self.seg = [slice(o[e], o[e + 1]) for e in range(E)]
+        self.inside = torch.zeros(self.R, dtype=torch.bool, device="cuda")
+        self.inside[o[0]:o[E]] = True
+        self.desc = smoe.make_desc(T, n_in, E, K, 1, n_out, 0, 1, 1, dt)
+        self.ws = smoe.workspace_products(self.desc)
+        self.g = gen(seed + T * 31 + n_in + n_out)
+
+    def rows(self, n, scale=1.0):
+        """Rows with NaN outside the segments."""
+        x = (randn(self.g, self.R, n) * scale).to(DT[self.dt])
+        x[~self.inside] = math.nan
+        return x
+
+    def weights(self):
+        return (randn(self.g, self.E, self.n_out, self.n_in) / math.sqrt(self.n_in)).to(DT[self.dt])
+
+    def out(self, n):
+        return torch.full((self.R, n), 7.0, dtype=DT[self.dt], device="cuda")
+
+    def check_rows(self, out, ref, mag, adds):
+        smoe.smoe_get_status(self.ws)
+        assert (out[~self.inside] == 7.0).all()
+        i = self.inside
+        within(out[i], ref[i], HALF[self.dt] * ref[i].abs() + adds * 2.0 ** -23 * mag[i] + 1e-37)
+
+
+SHAPES = [
+    # T, K, E, n_in, n_out, kind
+    (1, 1, 1, 16, 8, "even"), (1, 2, 4, 64, 72, "even"), (3, 2, 8, 272, 136, "skew"),
+    (64, 6, 160, 256, 384, "skew"), (40, 2, 3, 1008, 520, "gaps"), (129, 1, 1, 128, 256, "one"),
+    (64, 1, 1, 144, 264, "one"), (301, 3, 24, 1008, 200, "skew"), (400, 2, 2, 128, 1416, "gaps"),
+    (1000, 1, 3, 512, 512, "skew"), (777, 4, 16, 80, 776, "gaps"), (2048, 2, 8, 384, 640, "even"),
+    (95, 2, 512, 64, 64, "skew"), (17, 1, 1, 5120, 64, "one"), (700, 2, 5, 2064, 24, "skew"),
+]
+
+
+def adds16(n):
+    return n / 16 + 24  # the tensor core's additions, and a few around them
+
+
+def adds1(n):
+    return n + 4
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", SHAPES)
+def test_expert_matmul(T, K, E, n_in, n_out, kind, dt):
+    c = Case(T, K, E, n_in, n_out, dt, kind)
+    x, w, out = c.rows(n_in), c.weights(), c.out(n_out)
+    smoe.smoe_expert_matmul(c.desc, x, c.off, w, out, c.ws)
+    ref, mag = torch.zeros(2, c.R, n_out, dtype=F64, device="cuda")
+    for e, s in enumerate(c.seg):
+        ref[s] = x[s].double() @ w[e].double().T
+        mag[s] = x[s].double().abs() @ w[e].double().abs().T
+    c.check_rows(out, ref, mag, adds16(n_in) if dt == "bf16" else adds1(n_in))
+    again = c.out(n_out)
+    smoe.smoe_expert_matmul(c.desc, x, c.off, w, again, c.ws)
+    same(again, out)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", SHAPES)
+def test_expert_matmul_dx(T, K, E, n_in, n_out, kind, dt):
+    c = Case(T, K, E, n_in, n_out, dt, kind, seed=1)
+    dy, w, dy2, w2 = c.rows(n_out), c.weights(), c.rows(n_out), c.weights()
+    for two in (False, True):
+        dx = c.out(n_in)
+        smoe.smoe_expert_matmul_dx(c.desc, dy, w, c.off, dx, c.ws, **(dict(dy2=dy2, w2=w2) if two else {}))
+        ref, mag = torch.zeros(2, c.R, n_in, dtype=F64, device="cuda")
+        for e, s in enumerate(c.seg):
+            for a, b in ((dy, w), (dy2, w2))[: 1 + two]:
+                ref[s] += a[s].double() @ b[e].double()
+                mag[s] += a[s].double().abs() @ b[e].double().abs()
+        n = n_out * (1 + two)
+        c.check_rows(dx, ref, mag, adds16(n) if dt == "bf16" else adds1(n))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", SHAPES)
+def test_expert_matmul_dw(T, K, E, n_in, n_out, kind, dt):
+    c = Case(T, K, E, n_in, n_out, dt, kind, seed=2)
+    dy, x = c.rows(n_out), c.rows(n_in)
+    ref, mag = torch.zeros(2, E, n_out, n_in, dtype=F64, device="cuda")
+    most = 0
+    for e, s in enumerate(c.seg):
+        ref[e] = dy[s].double().T @ x[s].double()
+        mag[e] = dy[s].double().abs().T @ x[s].double().abs()
+        most = max(most, s.stop - s.start)
+    adds = adds16(most) if dt == "bf16" else adds1(most)
+    dw = torch.full((E, n_out, n_in), 7.0, device="cuda")
+    smoe.smoe_expert_matmul_dw(c.desc, dy, x, c.off, dw, c.ws)
+    smoe.smoe_get_status(c.ws)
+    within(dw, ref, adds * 2.0 ** -23 * mag)
+    # added to an earlier gradient, in a buffer of its own and in place
+    before = randn(c.g, E, n_out, n_in)
+    want = dw + before
+    both = torch.full_like(dw, 7.0)
+    smoe.smoe_expert_matmul_dw(c.desc, dy, x, c.off, both, c.ws, add=before)
+    same(both, want)
+    smoe.smoe_expert_matmul_dw(c.desc, dy, x, c.off, before, c.ws, add=before)
+    same(before, want)
+
+
+@pytest.mark.parametrize("pow2", [0, 1])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", [s for s in SHAPES if s[3] % 16 == 0])
+def test_expert_matmul_dw_f8(T, K, E, n_in, n_out, kind, dt, pow2):
+    """From token rows kept in 8 bits through row_src, and from dispatched ones: what the product of
+    the widened rows gives, to the bit."""
+    c = Case(T, K, E, n_in, n_out, dt, kind, seed=3)
+    dy = c.rows(n_out)
+    x = (randn(c.g, T, n_in) * 2).to(DT[dt])
+    q, s = torch.empty(T, n_in, dtype=F8, device="cuda"), torch.empty(T, blocks(n_in), device="cuda")
+    smoe.smoe_rows_f8(c.desc, x, q, s, pow2=pow2)
+    src = torch.randint(0, T, (c.R,), generator=c.g, device="cuda", dtype=torch.int32)
+    wide = (q.float() * s.repeat_interleave(128, 1)[:, :n_in]).to(DT[dt])
+    if pow2:
+        same(wide.double(), q.double() * spread(s, n_in))
+    rows = wide[src.long()]
+    want, got = (torch.full((E, n_out, n_in), 7.0, device="cuda") for _ in range(2))
+    smoe.smoe_expert_matmul_dw(c.desc, dy, rows, c.off, want, c.ws)
+    src[~c.inside] = -5  # rows of nobody are not looked up
+    smoe.smoe_expert_matmul_dw_f8(c.desc, dy, q, s, c.off, got, c.ws, row_src=src)
+    smoe.smoe_get_status(c.ws)
+    same(got, want)
+    got.fill_(7.0)
+    src = src.long().clamp(min=0)
+    smoe.smoe_expert_matmul_dw_f8(c.desc, dy, q.view(torch.uint8)[src], s[src], c.off, got, c.ws, add=want)
+    same(got, want + want)
+
+
+class F8Case(Case):
+    def __init__(self, *a, pow2=0, seed=4):
+        super().__init__(*a, seed=seed)
+        T, E, n_in, n_out = self.T, self.E, self.n_in, self.n_out
+        self.x = randn(self.g, T, n_in).to(DT[self.dt])
+        self.q = torch.empty(T, n_in, dtype=F8, device="cuda")
+        self.s = torch.empty(T, blocks(n_in), device="cuda")
+        smoe.smoe_rows_f8(self.desc, self.x, self.q, self.s, pow2=pow2)
+        self.wq = f8(randn(self.g, E, n_out, n_in) * 60)
+        self.sw = torch.rand(E, blocks(n_out), blocks(n_in), generator=self.g, device="cuda") * 1e-3 + 1e-4
+        self.src = torch.randint(0, T, (self.R,), generator=self.g, device="cuda", dtype=torch.int32)
+
+    def run(self, src=True, **kw):
+        out = self.out(self.n_out)
+        q, s = (self.q, self.s) if src else (self.q.view(torch.uint8)[self.src.long()].view(F8),
+                                              self.s[self.src.long()])
+        smoe.smoe_expert_matmul_f8(self.desc, q, s, self.off, self.wq, self.sw, out, self.ws,
+                                   row_src=self.src if src else None, **kw)
+        return out
+
+    def reference(self):
+        x = (self.q.double() * spread(self.s, self.n_in))[self.src.long()]
+        ref, mag = torch.zeros(2, self.R, self.n_out, dtype=F64, device="cuda")
+        for e, s in enumerate(self.seg):
+            w = self.wq[e].double() * spread(self.sw[e].repeat_interleave(128, 0)[:self.n_out], self.n_in)
+            ref[s], mag[s] = x[s] @ w.T, x[s].abs() @ w.abs().T
+        return ref, mag
+
+    def check(self, out):
+        # additions of 32 products each, one more a block for its scaled sum
+        self.check_rows(out, *self.reference(), self.n_in / 32 + blocks(self.n_in) + 8)
+
+
+@pytest.mark.parametrize("pow2", [0, 1])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", SHAPES)
+def test_expert_matmul_f8(T, K, E, n_in, n_out, kind, dt, pow2):
+    c = F8Case(T, K, E, n_in, n_out, dt, kind, pow2=pow2)
+    out = c.run()
+    c.check(out)
+    same(c.run(src=False), out)
