@@ -27,18 +27,20 @@ template <bool WIDE> struct F8Cfg;
 // Registers hold the accumulators: 128 a thread in the wide form (8 epilogue warps), 64 in the
 // narrow one (4 warps).
 template <> struct F8Cfg<true> {
-  static constexpr int kThreads = 384, kStages = 4, kChan = 256, kRows = 128, kBufs = 2, kCols = 256;
+  static constexpr int kThreads = 512, kGather = 4, kStages = 4, kChan = 256, kRows = 128, kBufs = 2, kCols = 256;
   static constexpr int kStage = 48 * 1024, kEpiWarps = 8, kEpiSmem = 8 * 2048;
+  static constexpr int kScale = 2 * 2 * 128 * 16;  // scales: two slots of four blocks, both halves
 };
 template <> struct F8Cfg<false> {
-  static constexpr int kThreads = 256, kStages = 8, kChan = 128, kRows = 64, kBufs = 8, kCols = 64;
-  static constexpr int kStage = 24 * 1024, kEpiWarps = 4, kEpiSmem = 4 * 256;
+  static constexpr int kThreads = 256, kGather = 2, kStages = 8, kChan = 128, kRows = 64, kBufs = 8, kCols = 64;
+  static constexpr int kStage = 24 * 1024, kEpiWarps = 4, kEpiSmem = 4 * 256, kScale = 0;
 };
 
 template <bool WIDE>
 constexpr size_t f8_smem() {
   using C = F8Cfg<WIDE>;
-  return 1024 + (size_t)C::kStages * C::kStage + C::kEpiSmem + 8 * (2 * C::kStages + 2 * C::kBufs + 1) + 16 +
+  return 1024 + (size_t)C::kStages * C::kStage + C::kEpiSmem + C::kScale +
+         8 * (2 * C::kStages + 2 * C::kBufs + 5) + 16 +
          4 * 2 * (kMaxGroups + 2);
 }
 
@@ -112,19 +114,22 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
                const F8Args p) {
   using C = F8Cfg<WIDE>;
   constexpr int kWBytes = C::kChan * 128, kXBytes = C::kRows * 128;
-  constexpr int kGatherWarps = 2, kGatherRows = C::kRows / kGatherWarps;
+  constexpr int kGatherWarps = C::kGather, kGatherRows = C::kRows / kGatherWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sW = base;                                  // [kStages][kChan x 128 bytes]
   uint8_t* sX = sW + C::kStages * kWBytes;             // [kStages][kRows x 128 bytes]
   uint8_t* sE = sX + C::kStages * kXBytes;             // epilogue warps' own space
-  uint64_t* full = reinterpret_cast<uint64_t*>(sE + C::kEpiSmem);
+  float4* sS = reinterpret_cast<float4*>(sE + C::kEpiSmem);  // wide: [slot][half][row]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + C::kEpiSmem + C::kScale);
   uint64_t* empty = full + C::kStages;
   uint64_t* dfull = empty + C::kStages;
   uint64_t* dempty = dfull + C::kBufs;
   uint64_t* drain = dempty + C::kBufs;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* sfull = drain + 1;
+  uint64_t* sempty = sfull + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sempty + 2);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
   int32_t* s_ts = reinterpret_cast<int32_t*>(s_abort + 3);
   int32_t* s_off = s_ts + kMaxGroups + 2;
@@ -140,6 +145,10 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
       tc::mbar_init(&dempty[b], C::kEpiWarps);
     }
     tc::mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sfull[i], 2);
+      tc::mbar_init(&sempty[i], C::kEpiWarps);
+    }
     *s_abort = 0;
     tc::mbar_init_fence();
     tc::tma_prefetch_map(&tmW);
@@ -159,7 +168,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
   const int total = s_ts[p.E] * ntile;
   const int nk = (p.KD + 127) / 128;
   volatile int* abort = s_abort;
-
+  // Wide: 512 threads of 128 registers at launch, 2 x 72 + 2 x 184 = 4 x 128 from here on.
+  if (warp < (WIDE ? 8 : 4)) {
+  if (WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // ---------------------------------------------------------------- weights
     const bool lead = tc::elect_one();
@@ -197,11 +208,66 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
         if (!tc::mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1u, &never)) break;
     }
     __syncwarp();
-  } else if (warp == 2 || warp == 3) {
+  } else if (WIDE && (warp == 2 || warp == 3)) {
+    // ---------------------------------------------------------------- scales
+    // The product of both scales, for four blocks at a time and both halves of the channels. (Loaded
+    // by the epilogue warps, whose load instructions then queue behind the gathering warps'
+    // copies, 131072 rows of 2048 to 768 channels took 269 us; now 240.)
+    uint32_t slot = 0, ph = 1;
+    bool ok = true;
+    int g = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      const int nblk = (p.N + 127) / 128, r0 = (warp - 2) * 64 + lane;
+      const float* ws = p.ws + ((size_t)tl.g * nblk + tl.n0 / 128) * nk;
+      const int second = tl.n0 + 128 < p.N ? nk : 0;
+      int src[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = r0 + 32 * u;
+        src[u] = r >= tl.rows ? -1 : p.row_src ? __ldcg(p.row_src + tl.row0 + r) : tl.row0 + r;
+      }
+      auto four = [&](const float* f, int k0, bool in) {
+        if ((nk & 3) == 0)
+          return in ? __ldcg(reinterpret_cast<const float4*>(f + k0)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 v;
+        v.x = in ? __ldcg(f + k0) : 0.0f;
+        v.y = in && k0 + 1 < nk ? __ldcg(f + k0 + 1) : 0.0f;
+        v.z = in && k0 + 2 < nk ? __ldcg(f + k0 + 2) : 0.0f;
+        v.w = in && k0 + 3 < nk ? __ldcg(f + k0 + 3) : 0.0f;
+        return v;
+      };
+      for (int k0 = 0; k0 < nk; k0 += 4) {
+        float4 x[2], w[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const bool in = (unsigned)src[u] < (unsigned)p.n_src;
+          x[u] = four(p.xs + (in ? (size_t)src[u] * nk : 0), k0, in);
+          w[u] = four(ws + u * second, k0, true);
+        }
+        ok = tc::mbar_wait_warp(&sempty[slot], ph, abort);
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            sS[(slot * 2 + h) * 128 + r0 + 32 * u] =
+                make_float4(x[u].x * w[h].x, x[u].y * w[h].y, x[u].z * w[h].z, x[u].w * w[h].w);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sfull[slot]);
+        if (++slot == 2) { slot = 0; ph ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+    }
+    __syncwarp();
+  } else if (WIDE ? warp >= 4 : warp >= 2) {
     // ---------------------------------------------------------------- rows
     // Four rows of 128 bytes an instruction, into the 128-byte-swizzled stage. Rows past the
     // tile's are zeros (narrow: up to the MMA's columns).
-    const int c = lane & 7, sub = (warp - 2) * kGatherRows + (lane >> 3);
+    const int c = lane & 7, sub = (warp - (WIDE ? 4 : 2)) * kGatherRows + (lane >> 3);
     constexpr int kIter = kGatherRows / 4;
     uint32_t s = 0, ph = 1;
     bool ok = true;
@@ -209,17 +275,20 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
       const int used = WIDE ? C::kRows : (tl.rows + 15) & ~15;
+      // (all loads before the first check: one latency a tile, not one a row)
       int id[kIter];
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
         const int r = sub + 4 * i;
-        id[i] = -1;
-        if (r < tl.rows) {
-          const int row = tl.row0 + r, src = p.row_src ? __ldcg(p.row_src + row) : row;
-          if ((unsigned)src < (unsigned)p.n_src) id[i] = src;
-          else if (tl.n0 == 0 && c == 0) record_error(p.st, kStatusData, kBadPerm, row);
-        }
+        id[i] = r >= tl.rows ? -1 : p.row_src ? __ldcg(p.row_src + tl.row0 + r) : tl.row0 + r;
       }
+#pragma unroll
+      for (int i = 0; i < kIter; ++i)
+        if ((unsigned)id[i] >= (unsigned)p.n_src) {
+          if (sub + 4 * i < tl.rows && tl.n0 == 0 && c == 0)
+            record_error(p.st, kStatusData, kBadPerm, tl.row0 + sub + 4 * i);
+          id[i] = -1;
+        }
       for (int kb = 0; kb < nk; ++kb) {
         ok = tc::mbar_wait_warp(&empty[s], ph, abort);
         if (!ok) break;
@@ -245,6 +314,8 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
+    // (The halves of a tile's channels as MMAs of N = 128 into buffers of their own, so that one
+    // half is read while the other's run: 131072 rows of 2048 to 768 channels 306 us, against 274.)
     const bool lead = tc::elect_one();
     uint32_t s = 0, ph = 0, b = 0, bph = 1;
     bool ok = true, in = false, free = false;
@@ -255,26 +326,28 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
           WIDE ? tc::instr_desc_f8(128, tl.n0 + 128 < p.N ? 256 : 128) : tc::instr_desc_f8(128, (tl.rows + 15) & ~15);
       for (int kb = 0; kb < nk; ++kb) {
         if (!in) ok = tc::mbar_wait_warp(&full[s], ph, abort);
-        if (!free && ok) ok = tc::mbar_wait_warp(&dempty[b], bph, abort);
         if (!ok) break;
-        tc::fence_after_sync();
         // the gathered rows were written through the generic proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         const uint64_t wd = tc::sw128_kmajor_desc(tc::smem_u32(sW + s * kWBytes));
         const uint64_t xd = tc::sw128_kmajor_desc(tc::smem_u32(sX + s * kXBytes));
         const uint32_t acc = tmem + b * C::kCols;
         uint64_t *e_bar = &empty[s], *d_bar = &dfull[b];
-        if (++s == C::kStages) { s = 0; ph ^= 1u; }
-        if (++b == C::kBufs) { b = 0; bph ^= 1u; }
-        // the next stage's barriers are asked for while this stage's MMAs are issued
-        const bool in_next = tc::mbar_test(&full[s], ph), free_next = tc::mbar_test(&dempty[b], bph);
+        // (last before the MMAs: the hand-over of a buffer is what this loop waits for)
+        if (!free) ok = tc::mbar_wait_warp(&dempty[b], bph, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
         if (lead) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc::mma_f8(acc, (WIDE ? xd : wd) + 2 * k, (WIDE ? wd : xd) + 2 * k, idesc, k > 0);
-          tc::commit(e_bar);
           tc::commit(d_bar);
+          tc::commit(e_bar);
         }
+        __syncwarp();
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+        if (++b == C::kBufs) { b = 0; bph ^= 1u; }
+        const bool in_next = tc::mbar_test(&full[s], ph), free_next = tc::mbar_test(&dempty[b], bph);
         in = __all_sync(0xffffffffu, in_next);
         free = __all_sync(0xffffffffu, free_next);
       }
@@ -290,57 +363,59 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
       tc::mbar_wait(drain, 0, &never);
     }
     __syncwarp();
+  }
   } else if (WIDE) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---------------------------------------------------------------- epilogue, wide
-    // warps 4-7 the tile's first 128 channels, 8-11 the other 128; a thread holds one row
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* buf = sE + (warp - 4) * 2048;
-    uint32_t b = 0, bph = 0;
+    // warps 8-11 the tile's first 128 channels, 12-15 the other 128; a thread holds one row.
+    // (A tile's last channels may lie past the matrix: they are not stored. A half that has none
+    // reads what its TMEM holds, and stores nothing.)
+    // (In pairs, by fma.rn.f32x2, 131072 rows of 2048 to 768 channels took 297 us, against 269.)
+    const int q = warp & 3, half = (warp - 8) >> 2, r = q * 32 + lane;
+    uint8_t* buf = sE + (warp - 8) * 2048;
+    uint32_t b = 0, bph = 0, slot = 0, sph = 0;
     bool ok = true;
     int g = 0;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
-      const int n0 = tl.n0 + 128 * half, r = q * 32 + lane;
-      const bool has = n0 < p.N;  // (its last channels may lie past the matrix: they are not stored)
-      int src = -1;
-      if (r < tl.rows) {
-        src = p.row_src ? __ldcg(p.row_src + tl.row0 + r) : tl.row0 + r;
-        if ((unsigned)src >= (unsigned)p.n_src) src = -1;
-      }
-      const float* xs = p.xs + (size_t)max(src, 0) * nk;
-      const float* ws = p.ws + ((size_t)tl.g * ((p.N + 127) / 128) + (has ? n0 / 128 : 0)) * nk;
+      F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
+      tl.n0 += 128 * half;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      float sc = src >= 0 ? __ldcg(xs) * __ldcg(ws) : 0.0f;
+      float sc[4];
+#pragma unroll 1
       for (int kb = 0; kb < nk; ++kb) {
-        const float now = sc;
-        if (kb + 1 < nk) sc = src >= 0 ? __ldcg(xs + kb + 1) * __ldcg(ws + kb + 1) : 0.0f;
+        if ((kb & 3) == 0) {
+          ok = tc::mbar_wait_warp(&sfull[slot], sph, abort);
+          if (!ok) break;
+          const float4 f = sS[(slot * 2 + half) * 128 + r];
+          sc[0] = f.x; sc[1] = f.y; sc[2] = f.z; sc[3] = f.w;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sempty[slot]);
+          if (++slot == 2) { slot = 0; sph ^= 1u; }
+        }
+        const float now = sc[0];
+        sc[0] = sc[1]; sc[1] = sc[2]; sc[2] = sc[3];
         ok = tc::mbar_wait_warp(&dfull[b], bph, abort);
         if (!ok) break;
         tc::fence_after_sync();
-        if (has) {
-          const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + b * C::kCols + half * 128;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + b * C::kCols + half * 128;
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t v[32];
-            tc::tmem_ld32(taddr + c, v);
-            tc::tmem_ld_wait();
-            if (c == 96) {
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(&dempty[b]);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), now, acc[c + i]);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc::tmem_ld32(taddr + 32 * c, v);
+          tc::tmem_ld_wait(v);
+          if (c == 3) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&dempty[b]);
           }
-        } else if (lane == 0) {
-          tc::mbar_arrive(&dempty[b]);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(v[j]), now, acc[32 * c + j]);
         }
         if (++b == C::kBufs) { b = 0; bph ^= 1u; }
       }
       if (!ok) break;
-      if (!has) continue;
       // 32 rows x 64 bytes at a time through the warp's own 2 KB (16-byte chunks swizzled by
       // pairs of rows: no bank conflicts either way), stored as segments of 64 bytes
       constexpr int kVec = 16 / (int)sizeof(TO), kWin = 4 * kVec;
@@ -349,11 +424,15 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
       for (int c = 0; c < 128; c += kWin) {
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
+          float f[kVec];
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) f[i] = acc[c + j * kVec + i];
           *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-              pack16(acc + c + j * kVec, (const TO*)nullptr);
+              pack16(f, (const TO*)nullptr);
+        }
         __syncwarp();
-        const int ch = lane & 3, col = n0 + c + ch * kVec;
+        const int ch = lane & 3, col = tl.n0 + c + ch * kVec;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int rr = i * 8 + (lane >> 2);
@@ -392,16 +471,25 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
       float acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-      float w = __ldcg(ws), s0 = has[0] ? __ldcg(xs[0]) * w : 0.0f, s1 = has[1] ? __ldcg(xs[1]) * w : 0.0f;
+      // scales of the next two blocks
+      float w[2], s0[2], s1[2];
+      auto load = [&](int kb, int i) {
+        const bool in = kb < nk;
+        w[i] = in ? __ldcg(ws + kb) : 0.0f;
+        s0[i] = in && has[0] ? __ldcg(xs[0] + kb) : 0.0f;
+        s1[i] = in && has[1] ? __ldcg(xs[1] + kb) : 0.0f;
+      };
+      load(0, 0);
+      load(1, 1);
       for (int kb = 0; kb < nk; ++kb) {
         __syncwarp();
-        s_sc[lane] = s0;
-        s_sc[lane + 32] = s1;
-        if (kb + 1 < nk) {
-          w = __ldcg(ws + kb + 1);
-          s0 = has[0] ? __ldcg(xs[0] + kb + 1) * w : 0.0f;
-          s1 = has[1] ? __ldcg(xs[1] + kb + 1) * w : 0.0f;
-        }
+        s_sc[lane] = s0[0] * w[0];
+        s_sc[lane + 32] = s1[0] * w[0];
+        __syncwarp();
+        w[0] = w[1];
+        s0[0] = s0[1];
+        s1[0] = s1[1];
+        load(kb + 2, 1);
         ok = tc::mbar_wait_warp(&dfull[b], bph, abort);
         if (!ok) break;
         tc::fence_after_sync();
