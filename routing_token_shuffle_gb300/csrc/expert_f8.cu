@@ -27,8 +27,8 @@ template <bool WIDE> struct F8Cfg;
 // Registers hold the accumulators: 128 a thread in the wide form (8 epilogue warps), 64 in the
 // narrow one (4 warps).
 template <> struct F8Cfg<true> {
-  static constexpr int kThreads = 512, kGather = 4, kStages = 4, kChan = 256, kRows = 128, kBufs = 2, kCols = 256;
-  static constexpr int kStage = 48 * 1024, kEpiWarps = 8, kEpiSmem = 8 * 2048;
+  static constexpr int kThreads = 512, kGather = 4, kStages = 3, kChan = 256, kRows = 128, kBufs = 2, kCols = 256;
+  static constexpr int kStage = 48 * 1024, kEpiWarps = 8, kEpiSmem = 8 * 8192;
   static constexpr int kScale = 2 * 2 * 128 * 16;  // scales: two slots of four blocks, both halves
 };
 template <> struct F8Cfg<false> {
@@ -111,6 +111,7 @@ __device__ __forceinline__ F8Tile f8_decode(const F8Args& p, const int32_t* ts, 
 template <bool WIDE, typename TO>
 __global__ void __launch_bounds__(F8Cfg<WIDE>::kThreads, 1)
 f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pairs, 128-row box
+               const __grid_constant__ CUtensorMap tmO,  // wide: the output, boxes of 32 rows x 128 bytes
                const F8Args p) {
   using C = F8Cfg<WIDE>;
   constexpr int kWBytes = C::kChan * 128, kXBytes = C::kRows * 128;
@@ -152,6 +153,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
     *s_abort = 0;
     tc::mbar_init_fence();
     tc::tma_prefetch_map(&tmW);
+    if (WIDE) tc::tma_prefetch_map(&tmO);
   }
   pdl_wait_and_trigger();
   __syncwarp();
@@ -372,7 +374,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
     // reads what its TMEM holds, and stores nothing.)
     // (In pairs, by fma.rn.f32x2, 131072 rows of 2048 to 768 channels took 297 us, against 269.)
     const int q = warp & 3, half = (warp - 8) >> 2, r = q * 32 + lane;
-    uint8_t* buf = sE + (warp - 8) * 2048;
+    uint8_t* buf = sE + (warp - 8) * 8192;
     uint32_t b = 0, bph = 0, slot = 0, sph = 0;
     bool ok = true;
     int g = 0;
@@ -416,32 +418,42 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
         if (++b == C::kBufs) { b = 0; bph ^= 1u; }
       }
       if (!ok) break;
-      // 32 rows x 64 bytes at a time through the warp's own 2 KB (16-byte chunks swizzled by
-      // pairs of rows: no bank conflicts either way), stored as segments of 64 bytes
-      constexpr int kVec = 16 / (int)sizeof(TO), kWin = 4 * kVec;
-      TO* out = static_cast<TO*>(p.out) + (size_t)tl.row0 * p.N;
+      // 32 rows x 128 bytes, two such windows at a time, through the warp's own 8 KB (16-byte
+      // chunks swizzled by row as TMA reads them: no bank conflicts), stored by TMA, or where
+      // the tile's rows end inside by the warp. (Read back and stored by the warp throughout,
+      // in windows of 64 bytes: 246 us.)
+      constexpr int kVec = 16 / (int)sizeof(TO), kWin = 8 * kVec;
+      const int row = tl.row0 + q * 32, rows = min(32, tl.rows - q * 32);
 #pragma unroll
-      for (int c = 0; c < 128; c += kWin) {
+      for (int c = 0; c < 128; c += 2 * kWin) {
+        if (lane == 0) tc::bulk_wait_read();
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f[kVec];
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) f[i] = acc[c + j * kVec + i];
-          *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-              pack16(f, (const TO*)nullptr);
-        }
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(buf + w * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                pack16(acc + c + w * kWin + j * kVec, (const TO*)nullptr);
+        tc::fence_async_shared();
         __syncwarp();
-        const int ch = lane & 3, col = tl.n0 + c + ch * kVec;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2);
-          const uint4 v = *reinterpret_cast<const uint4*>(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
-          if (q * 32 + rr < tl.rows && col < p.N)
-            *reinterpret_cast<uint4*>(out + (size_t)(q * 32 + rr) * p.N + col) = v;
+        for (int w = 0; w < 2; ++w) {
+          const int col = tl.n0 + c + w * kWin;
+          if (col >= p.N) break;
+          if (rows == 32) {
+            if (lane == 0) tc::tma_store_2d(&tmO, buf + w * 4096, col, row);
+          } else {
+            const int ch = lane & 7;
+            for (int rr = lane >> 3; rr < rows; rr += 4)
+              if (col + ch * kVec < p.N)
+                *reinterpret_cast<uint4*>(static_cast<TO*>(p.out) + (size_t)(row + rr) * p.N + col + ch * kVec) =
+                    *reinterpret_cast<const uint4*>(buf + w * 4096 + rr * 128 + ((ch ^ (rr & 7)) << 4));
+          }
         }
+        if (lane == 0) tc::bulk_commit();
       }
     }
+    if (lane == 0) tc::bulk_wait();  // before the shared memory goes away
     if (!ok && lane == 0) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
@@ -540,14 +552,17 @@ constexpr int kWideRows = 48;
 
 template <bool WIDE, typename TO>
 cudaError_t run_f8(const F8Args& p, const void* wq, long long tile_bound, cudaStream_t s) {
-  alignas(64) CUtensorMap tw;
-  if (!encode_tmap_2d(&tw, wq, false, (uint64_t)p.E * p.N, p.KD / 2, 128, 64)) return cudaErrorInvalidValue;
+  alignas(64) CUtensorMap tw, to;
+  constexpr bool kF32 = sizeof(TO) == 4;
+  if (!encode_tmap_2d(&tw, wq, false, (uint64_t)p.E * p.N, p.KD / 2, 128, 64) ||
+      !encode_tmap_2d(&to, p.out, kF32, p.TK, p.N, 32, kF32 ? 32 : 64))
+    return cudaErrorInvalidValue;
   auto kern = f8_gemm_kernel<WIDE, TO>;
   const int smem = (int)f8_smem<WIDE>();
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<long long>(device_sms(), std::max<long long>(tile_bound, 1));
-  SMOE_LAUNCH(kern, grid, F8Cfg<WIDE>::kThreads, smem, s, tw, p);
+  SMOE_LAUNCH(kern, grid, F8Cfg<WIDE>::kThreads, smem, s, tw, to, p);
   return cudaGetLastError();
 }
 
