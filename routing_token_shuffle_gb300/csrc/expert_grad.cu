@@ -7,9 +7,12 @@
 // nothing is transposed. A segment ends anywhere: an MMA takes 16 rows, those of the last one
 // that belong to the next expert (or to nobody) are set to zero in shared memory, in both
 // operands, before it runs, so that neither their values nor their infinities reach the sum.
-// One persistent CTA per SM walks 128 x 256 tiles of the gradients:
-//   warp 0  TMA;  warp 1  the last rows' zeros, tcgen05.mma into one of two TMEM accumulators;
-//   warps 4-11  add and store, while the next tile's MMAs run.
+// A persistent pair of CTAs (a cluster on the two SMs of a TPC) walks 256 x 256 tiles of the
+// gradients: each CTA stages 128 channels of dy and 128 of x for each 64 rows, holds 128 x 256 sums
+// and stores them. (128 x 256 tiles of single CTAs stage half as much again, and the L2's
+// bandwidth bounded them at large row counts.)
+//   warp 0  TMA;  warp 1  the last rows' zeros, and on the leader tcgen05.mma into one of two
+//   TMEM accumulators;  warps 4-11  add and store, while the next tile's MMAs run.
 // An expert's R rows give 2 R flops per element of 4 bytes (8 with add): below about 550 rows an
 // expert the stores bound it, not the tensor cores.
 #include <algorithm>
@@ -20,10 +23,10 @@
 namespace smoe {
 namespace {
 
-constexpr int kDwThreads = 384, kDwStages = 4, kDwWarps = 8;
-constexpr int kDwA = 128 * 128, kDwB = 256 * 128;  // bytes of a stage: 64 rows of 128 and 256 channels
-constexpr size_t kDwSmem = 1024 + kDwStages * (kDwA + kDwB) + kDwWarps * 2048 +
-                           8 * (2 * kDwStages + 2 * 2 + 1) + 16 + 4 * (kMaxGroups + 2);
+constexpr int kDwThreads = 384, kDwStages = 6, kDwWarps = 8;
+constexpr int kDwHalf = 128 * 128;  // bytes of an operand's stage in a CTA: 64 rows of 128 channels
+constexpr size_t kDwSmem = 1024 + kDwStages * 2 * kDwHalf + kDwWarps * 2048 +
+                           8 * (3 * kDwStages + 2 * 2 + 1) + 16 + 4 * (kMaxGroups + 2);
 
 struct DwArgs {
   const int32_t* expert_off;
@@ -42,12 +45,24 @@ __device__ __forceinline__ DwTile dw_decode(const DwArgs& p, const int32_t* off,
   DwTile r;
   const int per = p.mt * p.nt;
   r.e = t / per;
-  const int in = t - r.e * per, n = in / p.mt;
-  r.m0 = (in - n * p.mt) * 128;
-  r.n0 = n * 256;
+  const int in = t - r.e * per, m = in / p.nt;
+  r.m0 = m * 256;
+  r.n0 = (in - m * p.nt) * 256;
   r.row0 = off[r.e];
   r.rows = off[r.e + 1] - r.row0;
   return r;
+}
+
+// The rows [left, the next multiple of 16) of a stage become zeros, by a warp.
+__device__ __forceinline__ void dw_clear(uint8_t* a, uint8_t* b, int left, int lane) {
+  for (int i = left * 8 + lane; i < ((left + 15) & ~15) * 8; i += 32)  // 16 bytes each
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      *reinterpret_cast<uint4*>(a + j * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(b + j * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
 }
 
 __global__ void __launch_bounds__(kDwThreads, 1)
@@ -57,11 +72,12 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = base;
-  uint8_t* sB = sA + kDwStages * kDwA;
-  uint8_t* sE = sB + kDwStages * kDwB;
+  uint8_t* sB = sA + kDwStages * kDwHalf;
+  uint8_t* sE = sB + kDwStages * kDwHalf;
   uint64_t* full = reinterpret_cast<uint64_t*>(sE + kDwWarps * 2048);
   uint64_t* empty = full + kDwStages;
-  uint64_t* dfull = empty + kDwStages;
+  uint64_t* last = empty + kDwStages;  // the peer's copies of a segment's last stage
+  uint64_t* dfull = last + kDwStages;
   uint64_t* dempty = dfull + 2;
   uint64_t* drain = dempty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -70,14 +86,17 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   int32_t* s_off = s_bad + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDwStages; ++s) {
-      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&full[s], 2);  // on the leader: each CTA's word, and the copies' bytes
       tc::mbar_init(&empty[s], 1);
+      tc::mbar_init(&last[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&dfull[a], 1);
-      tc::mbar_init(&dempty[a], kDwWarps);
+      tc::mbar_init(&dempty[a], 2 * kDwWarps);
     }
     tc::mbar_init(drain, 1);
     *s_abort = 0;
@@ -87,6 +106,7 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   }
   pdl_wait_and_trigger();
   __syncwarp();
+  tc::cluster_arrive();
   if (warp == 3) {  // a bad expert_off schedules nothing
     bool bad = false;
     for (int g = lane; g <= p.E; g += 32) {
@@ -100,9 +120,12 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       if (bad) record_error(p.st, kStatusData, kBadPairRow, -1);
     }
   }
+  __syncwarp();
+  // the peer runs, and both CTAs' barriers are initialised before any remote signal
+  tc::cluster_wait();
   if (warp == 2) {
-    tc::tmem_alloc(s_tmem, 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc_pair(s_tmem, 512);
+    tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -110,26 +133,46 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   const uint32_t tmem = *s_tmem;
   const int total = *s_bad ? 0 : p.E * p.mt * p.nt;
   volatile int* abort = s_abort;
+  // A tile's columns: 256, or 128 where the matrix has no more; half of them staged by each CTA.
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
+    // The leader's barrier of a stage counts both CTAs' bytes. A segment's last stage, where it
+    // holds rows that are cleared first, is different on the peer: its copies complete on a barrier
+    // of its own, and its warp 1 gives the leader its word once the rows are cleared.
     const bool lead = tc::elect_one();
-    uint32_t s = 0, ph = 1, it = 0;
+    uint32_t s = 0, ph = 1, it = 0, lph = 0;  // lph: bits of `last`'s phases
+    uint32_t own = 0;                         // stages whose copies are counted by `last`
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
-      const int na = tl.m0 + 64 < p.M ? 2 : 1, nb = min(4, (p.N - tl.n0 + 63) / 64);
+      const int nb = tl.n0 + 128 < p.N ? 2 : 1, m0 = tl.m0 + (int)rank * 128, n0 = tl.n0 + (int)rank * 64 * nb;
       for (int r = 0; r < tl.rows; r += 64) {
         ok = tc::mbar_wait_warp(&empty[s], ph, abort);
         if (!ok) break;
+        const bool cut = tl.rows - r < 64 && ((tl.rows - r) & 15) != 0;
         if (lead) {
-          tc::mbar_expect_tx(&full[s], (na + nb) * 8192);
-          for (int j = 0; j < na; ++j)
-            tc::tma_load_2d(sA + s * kDwA + j * 8192, &tmA, &full[s], tl.m0 + 64 * j, tl.row0 + r);
+          const uint32_t bytes = (2 + nb) * 8192, leader = tc::cluster_addr(&full[s], 0);
+          uint32_t on = leader;
+          if (rank == 0) {
+            tc::mbar_expect_tx(&full[s], cut ? bytes : 2 * bytes);
+          } else if (cut) {
+            tc::mbar_expect_tx(&last[s], bytes);
+            on = tc::cluster_addr(&last[s], 1);
+          } else {
+            tc::mbar_arrive_remote(leader);
+          }
+          for (int j = 0; j < 2; ++j)
+            tc::tma_load_2d_pair(sA + s * kDwHalf + j * 8192, &tmA, on, m0 + 64 * j, tl.row0 + r);
           for (int j = 0; j < nb; ++j)
-            tc::tma_load_2d(sB + s * kDwB + j * 8192, &tmB, &full[s], tl.n0 + 64 * j, tl.row0 + r);
+            tc::tma_load_2d_pair(sB + s * kDwHalf + j * 8192, &tmB, on, n0 + 64 * j, tl.row0 + r);
         }
         __syncwarp();
+        own &= ~(1u << s);
+        if (cut && rank == 1) {
+          own |= 1u << s;
+          lph ^= 1u << s;  // the phase that these copies complete is the one before
+        }
         ++it;
         if (++s == kDwStages) { s = 0; ph ^= 1u; }
       }
@@ -139,43 +182,48 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
         *abort = 1;
         record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
       }
-      // the copies in flight land before shared memory goes away, whichever role gave up
+      // The copies in flight land before shared memory goes away, whichever role gave up: the
+      // leader waits for both CTAs' (a barrier that the peer did not get to never completes: then
+      // the limit is waited out once), the peer sees only its last stages' complete.
       volatile int never = 0;
-      for (uint32_t j = it > kDwStages ? it - kDwStages : 0; j < it; ++j)
-        tc::mbar_wait(&full[j % kDwStages], (j / kDwStages) & 1u, &never);
+      if (rank == 0) {
+        for (uint32_t j = it > kDwStages ? it - kDwStages : 0; j < it; ++j)
+          if (!tc::mbar_wait(&full[j % kDwStages], (j / kDwStages) & 1u, &never)) break;
+      } else {
+        for (int j = 0; j < kDwStages; ++j)
+          if (own >> j & 1u) tc::mbar_wait(&last[j], (lph >> j & 1u) ^ 1u, &never);
+        if (*abort) tc::wait_out();
+      }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- MMA issuer (of the pair)
     const bool lead = tc::elect_one();
     uint32_t s = 0, ph = 0, d = 0, dph = 1;
     bool ok = true, in = false;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
       if (tl.rows == 0) continue;
-      const uint32_t idesc = tc::instr_desc(false, 128, 64 * min(4, (p.N - tl.n0 + 63) / 64)) |
+      const uint32_t idesc = tc::instr_desc(false, 256, tl.n0 + 128 < p.N ? 256 : 128) |
                              tc::kIdescTransA | tc::kIdescTransB;
       ok = tc::mbar_wait_warp(&dempty[d], dph, abort);
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t acc = tmem + d * 256;
       for (int r = 0; r < tl.rows; r += 64) {
-        if (!in) ok = tc::mbar_wait_warp(&full[s], ph, abort);
-        if (!ok) break;
         const int left = min(64, tl.rows - r);
-        if (left & 15) {  // the rows past the segment, up to the 16th, become zeros
-          const int n = 16 - (left & 15);
-          for (int i = lane; i < 6 * 8 * n; i += 32) {
-            const int box = i / (8 * n), in = i - box * 8 * n;
-            uint8_t* b = box < 2 ? sA + s * kDwA + box * 8192 : sB + s * kDwB + (box - 2) * 8192;
-            *reinterpret_cast<uint4*>(b + left * 128 + in * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
+        if (left & 15) {
+          // the peer's zeros are acquired with its word
+          ok = tc::mbar_wait_warp_shared(&full[s], ph, abort);
+          if (!ok) break;
+          dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, left, lane);
+        } else if (!in) {
+          ok = tc::mbar_wait_warp(&full[s], ph, abort);
+          if (!ok) break;
         }
         tc::fence_after_sync();
-        const uint64_t ad = tc::sw128_mnmajor_desc(tc::smem_u32(sA + s * kDwA));
-        const uint64_t bd = tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kDwB));
+        const uint64_t ad = tc::sw128_mnmajor_desc(tc::smem_u32(sA + s * kDwHalf));
+        const uint64_t bd = tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kDwHalf));
         uint64_t* e_bar = &empty[s];
         if (++s == kDwStages) { s = 0; ph ^= 1u; }
         const bool in_next = tc::mbar_test(&full[s], ph);
@@ -183,13 +231,13 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
           const int steps = (left + 15) >> 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (k < steps) tc::mma_bf16(acc, ad + 128 * k, bd + 128 * k, idesc, r > 0 || k > 0);
-          tc::commit(e_bar);
+            if (k < steps) tc::mma_bf16_pair(acc, ad + 128 * k, bd + 128 * k, idesc, r > 0 || k > 0);
+          tc::commit_pair(e_bar, 0x3);
         }
         in = __all_sync(0xffffffffu, in_next);
       }
       if (!ok) break;
-      if (lead) tc::commit(&dfull[d]);
+      if (lead) tc::commit_pair(&dfull[d], 0x3);
       __syncwarp();
       if (++d == 2) { d = 0; dph ^= 1u; }
     }
@@ -200,8 +248,28 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       }
       // wait for every MMA this thread issued before TMEM is released
       volatile int never = 0;
-      tc::commit(drain);
+      tc::commit_pair(drain, 0x1);
       tc::mbar_wait(drain, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- the peer's last rows
+    uint32_t it = 0, lph = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += stride) {
+      const DwTile tl = dw_decode(p, s_off, t);
+      it += (tl.rows + 63) >> 6;
+      if ((tl.rows & 15) == 0) continue;
+      const uint32_t s = (it - 1) % kDwStages;
+      ok = tc::mbar_wait_warp(&last[s], lph >> s & 1u, abort);
+      if (!ok) break;
+      lph ^= 1u << s;
+      dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, tl.rows & 63, lane);
+      if (lane == 0) tc::mbar_arrive_cluster_shared(tc::cluster_addr(&full[s], 0));
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -214,9 +282,9 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
     const int ch = lane & 3, sub = lane >> 2;
     uint32_t d = 0, dph = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
-      const int m0 = tl.m0 + q * 32, n0 = tl.n0 + half * 128;
+      const int m0 = tl.m0 + (int)rank * 128 + q * 32, n0 = tl.n0 + half * 128;
       const size_t at = ((size_t)tl.e * p.M + m0) * p.N + n0;
       const int mrows = min(32, p.M - m0), ncols = min(128, p.N - n0);  // may be below 1
       const int nwin = mrows > 0 && ncols > 0 ? (ncols + 15) >> 4 : 0;
@@ -273,7 +341,7 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       if (tl.rows > 0) {
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&dempty[d]);
+        if (lane == 0) tc::mbar_arrive_remote(tc::cluster_addr(&dempty[d], 0));
         if (++d == 2) { d = 0; dph ^= 1u; }
       }
     }
@@ -285,8 +353,9 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();  // no signal or copy of the other CTA is on its way here
   tc::fence_after_sync();
-  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+  if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
 }
 
 // ------------------------------------------------------------------ kept rows
@@ -575,10 +644,23 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDwSmem);
   if (e != cudaSuccess) return e;
-  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 128), ceil_div(n_in, 256)};
-  const int grid = (int)std::min<long long>(device_sms(), (long long)d.E * p.mt * p.nt);
-  SMOE_LAUNCH(dw_kernel, grid, kDwThreads, kDwSmem, s, A, B, p);
-  return cudaGetLastError();
+  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 256), ceil_div(n_in, 256)};
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2 * (int)std::min<long long>(device_sms() / 2, (long long)d.E * p.mt * p.nt));
+  cfg.blockDim = dim3(kDwThreads);
+  cfg.dynamicSmemBytes = kDwSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  SMOE_COUNT_LAUNCH(1);
+  return cudaLaunchKernelEx(&cfg, dw_kernel, A, B, p);
 }
 
 cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,

@@ -1066,11 +1066,12 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, bool fp32, uint64_t rows
   return encode_tmap(map, base, fp32, 2, dims, strides, box);
 }
 
-bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t rows, uint64_t cols) {
-  const cuuint64_t dims[3] = {cols, rows, outer};
-  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
-  return encode_tmap(map, base, false, 3, dims, strides, box);
+bool encode_tmap_3d(CUtensorMap* map, const void* base, bool fp32, uint64_t outer, uint64_t rows,
+                    uint64_t cols, uint32_t box_rows, uint32_t box_cols) {
+  const cuuint64_t esz = fp32 ? 4 : 2, dims[3] = {cols, rows, outer};
+  const cuuint64_t strides[2] = {cols * esz, rows * cols * esz};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  return encode_tmap(map, base, fp32, 3, dims, strides, box);
 }
 
 cudaError_t launch_expert_ffn(const smoe_desc& d, const void* x_disp, const void* x,
@@ -1106,7 +1107,8 @@ cudaError_t launch_expert_rows_bf16(const smoe_desc& d, int n_out, int n_in, con
   if (!encode_tmap_2d(&A, a, false, TK, KD, 128, 64) || !encode_tmap_2d(&A2, a2, false, TK, KD, 128, 64))
     return cudaErrorInvalidValue;
   if (transposed) {
-    if (!encode_tmap_3d(&B, w, d.E, n_out, n_in) || !encode_tmap_3d(&B2, w2, d.E, n_out, n_in))
+    if (!encode_tmap_3d(&B, w, false, d.E, n_out, n_in, 64, 64) ||
+        !encode_tmap_3d(&B2, w2, false, d.E, n_out, n_in, 64, 64))
       return cudaErrorInvalidValue;
   } else if (!encode_tmap_2d(&B, w, false, (uint64_t)d.E * N, KD, pairs ? 128 : 256, 64)) {
     return cudaErrorInvalidValue;

@@ -144,9 +144,18 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                "r"(c0), "r"(c1), "r"(smem_u32(smem_src))
                : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int c0, int c1,
+                                             int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(smem_src))
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's stores have read their shared memory, or are complete.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// (all but the last group's)
+__device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -500,8 +509,9 @@ __host__ __device__ constexpr uint32_t instr_desc_f8(int M, int N) {
 // box and 128-byte swizzle. Returns false (and sets the last error) on failure.
 bool encode_tmap_2d(CUtensorMap* map, const void* base, bool fp32, uint64_t rows, uint64_t cols,
                     uint32_t box_rows, uint32_t box_cols);
-// The same of a 3-D bf16 tensor [outer, rows, cols] with a (64 x 64) box of one outer index: rows
-// and columns past a matrix' own read as zeros, not as the next matrix.
-bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t rows, uint64_t cols);
+// The same of a 3-D tensor [outer, rows, cols], a box of one outer index: rows and columns past a
+// matrix' own read as zeros, not as the next matrix, and are not stored.
+bool encode_tmap_3d(CUtensorMap* map, const void* base, bool fp32, uint64_t outer, uint64_t rows,
+                    uint64_t cols, uint32_t box_rows, uint32_t box_cols);
 
 }  // namespace smoe
