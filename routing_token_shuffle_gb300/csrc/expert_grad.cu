@@ -23,9 +23,10 @@
 namespace smoe {
 namespace {
 
-constexpr int kDwThreads = 384, kDwStages = 6, kDwWarps = 8;
+constexpr int kDwStages = 5, kDwWarps = 8, kDwThreads = 128 + 32 * kDwWarps;
+constexpr int kDwCols = 1024 / kDwWarps;  // columns of an epilogue warp
 constexpr int kDwHalf = 128 * 128;  // bytes of an operand's stage in a CTA: 64 rows of 128 channels
-constexpr size_t kDwSmem = 1024 + kDwStages * 2 * kDwHalf + kDwWarps * 2048 +
+constexpr size_t kDwSmem = 1024 + kDwStages * 2 * kDwHalf + kDwWarps * 4096 +
                            8 * (3 * kDwStages + 2 * 2 + 1) + 16 + 4 * (kMaxGroups + 2);
 
 struct DwArgs {
@@ -74,7 +75,7 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   uint8_t* sA = base;
   uint8_t* sB = sA + kDwStages * kDwHalf;
   uint8_t* sE = sB + kDwStages * kDwHalf;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sE + kDwWarps * 2048);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + kDwWarps * 4096);
   uint64_t* empty = full + kDwStages;
   uint64_t* last = empty + kDwStages;  // the peer's copies of a segment's last stage
   uint64_t* dfull = last + kDwStages;
@@ -274,69 +275,67 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    // warps 4-7 the tile's first 128 columns, 8-11 the other 128, 32 rows each; 32 rows x 64
-    // bytes at a time through the warp's own 2 KB, added to and stored as segments of 64 bytes.
-    // What is added is loaded two such windows ahead.
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* buf = sE + (warp - 4) * 2048;
-    const int ch = lane & 3, sub = lane >> 2;
+    // Each warp 32 rows of kDwCols columns, in windows of 32 columns through 4 KB of its own
+    // (16-byte chunks swizzled by row: no bank conflicts), added to and stored as whole lines. What
+    // is added is loaded a window ahead.
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    constexpr int kWins = kDwCols / 32;
+    uint8_t* buf = sE + (warp - 4) * 4096;
+    const int ch = lane & 7, sub = lane >> 3;
     uint32_t d = 0, dph = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
-      const int m0 = tl.m0 + (int)rank * 128 + q * 32, n0 = tl.n0 + half * 128;
-      const size_t at = ((size_t)tl.e * p.M + m0) * p.N + n0;
-      const int mrows = min(32, p.M - m0), ncols = min(128, p.N - n0);  // may be below 1
-      const int nwin = mrows > 0 && ncols > 0 ? (ncols + 15) >> 4 : 0;
-      float4 add[2][4];
-      auto load = [&](int w, float4 (&a)[4]) {
+      const int m0 = tl.m0 + (int)rank * 128 + q * 32, n0 = tl.n0 + part * kDwCols;
+      const int mrows = min(32, p.M - m0), ncols = min(kDwCols, p.N - n0);  // may be below 1
+      const size_t at = ((size_t)tl.e * p.M + m0 + sub) * p.N + n0 + ch * 4;
+      const int nwin = mrows > 0 && ncols > 0 ? (ncols + 31) >> 5 : 0;
+      float4 add[8];
+      auto load = [&](int w) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + sub, col = w * 16 + ch * 4;
-          a[i] = rr < mrows && col < ncols
-                     ? __ldcs(reinterpret_cast<const float4*>(p.add + at + (size_t)rr * p.N + col))
-                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
+        for (int i = 0; i < 8; ++i)
+          add[i] = i * 4 + sub < mrows && w * 32 + ch * 4 < ncols
+                       ? __ldcs(reinterpret_cast<const float4*>(p.add + at + (size_t)(i * 4) * p.N + w * 32))
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       };
-      if (p.add) {
-        load(0, add[0]);
-        load(1, add[1]);
-      }
+      if (p.add) load(0);
       if (tl.rows > 0) {
         ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
         if (!ok) break;
         tc::fence_after_sync();
       }
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + d * 256 + half * 128;
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + d * 256 + part * kDwCols;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < kWins; ++w) {
         if (w >= nwin) break;
         __syncwarp();  // TMEM loads are a whole warp's
-        float v[16];
+        uint32_t v[32];
         if (tl.rows > 0) {
-          tc::tmem_ld16(taddr + 16 * w, v);
+          tc::tmem_ld32(taddr + 32 * w, v);
+          tc::tmem_ld_wait(v);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         __syncwarp();
+        float4 o[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + sub, col = w * 16 + ch * 4;
-          float4 o = *reinterpret_cast<const float4*>(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + sub;
+          o[i] = *reinterpret_cast<const float4*>(buf + rr * 128 + ((ch ^ (rr & 7)) << 4));
           if (p.add) {
-            const float4 a = add[w & 1][i];
-            o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
+            o[i].x += add[i].x; o[i].y += add[i].y; o[i].z += add[i].z; o[i].w += add[i].w;
           }
-          if (rr < mrows && col < ncols)
-            __stcs(reinterpret_cast<float4*>(p.dw + at + (size_t)rr * p.N + col), o);
         }
-        if (p.add && w + 2 < 8) load(w + 2, add[w & 1]);
+        if (p.add && w + 1 < kWins) load(w + 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 4 + sub < mrows && w * 32 + ch * 4 < ncols)
+            __stcs(reinterpret_cast<float4*>(p.dw + at + (size_t)(i * 4) * p.N + w * 32), o[i]);
       }
       if (tl.rows > 0) {
         tc::fence_before_sync();
@@ -359,49 +358,52 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
 }
 
 // ------------------------------------------------------------------ kept rows
-// dst[r] = q[map[r]] times its scales, in the layer's type; a map entry out of range gives a row
-// of zeros. 16 values a thread.
+// dst[r] = q[map[r]] times its scales, in the layer's type, for the rows of the segments; a map
+// entry out of range gives a row of zeros. A warp a row, 8 values a lane at a time (stores of 512
+// bytes in a row for bf16), eight loads ahead of their use.
+// (The product can read its rows through map itself, by asynchronous copies, and none is written:
+// its stores, which fill the load and store units' queues, then hold the copies up: 160 experts of
+// 1536 x 5120, 49152 rows of 8192 tokens 1293 us, against 1040 with this copy.)
 template <typename TE>
 __global__ void __launch_bounds__(256)
-widen_rows_kernel(const uint4* q, const float* scale, const int32_t* map, const int32_t* expert_off,
+widen_rows_kernel(const uint2* q, const float* scale, const int32_t* map, const int32_t* expert_off,
                   int E, int rows, int n_src, int cols, TE* dst, DeviceStatus* st) {
   pdl_wait_and_trigger();
-  const int vecs = cols >> 4, nblk = (cols + 127) >> 7, lane = threadIdx.x & 31;
+  const int vecs = cols >> 3, nblk = (cols + 127) >> 7, lane = threadIdx.x & 31;
   const int begin = max(expert_off[0], 0), end = min(expert_off[E], rows);
   for (int r = begin + blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
     const int src = map ? map[r] : r;
     const bool in = (unsigned)src < (unsigned)n_src;
     if (!in && lane == 0) record_error(st, kStatusData, kBadPerm, r);
-    for (int v0 = lane; v0 < vecs; v0 += 128) {
-      uint4 w[4];
-      float s[4];
+    const uint2* from = q + (in ? (size_t)src * vecs : 0);
+    const float* sc = scale + (in ? (size_t)src * nblk : 0);
+    for (int v0 = lane; v0 < vecs; v0 += 32 * 8) {
+      uint2 w[8];
+      float s[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int v = v0 + 32 * u;
-        w[u] = make_uint4(0u, 0u, 0u, 0u);
-        s[u] = 0.0f;
-        if (in && v < vecs) {
-          w[u] = q[(size_t)src * vecs + v];
-          s[u] = scale[(size_t)src * nblk + (v >> 3)];
-        }
+        const bool has = in && v < vecs;
+        w[u] = has ? __ldcg(from + v) : make_uint2(0u, 0u);
+        s[u] = has ? __ldcg(sc + (v >> 4)) : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int v = v0 + 32 * u;
         if (v >= vecs) break;
-        const uint32_t b[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        float f[16];
+        float f[8];
+        const uint32_t b[2] = {w[u].x, w[u].y};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
               (__nv_fp8x2_storage_t)(b[i >> 1] >> (16 * (i & 1)) & 0xffffu), __NV_E4M3)));
           f[2 * i] = h.x * s[u];
           f[2 * i + 1] = h.y * s[u];
         }
-        uint4* out = reinterpret_cast<uint4*>(dst + (size_t)r * cols + v * 16);
+        uint4* out = reinterpret_cast<uint4*>(dst + (size_t)r * cols + v * 8);
         constexpr int kVec = 16 / (int)sizeof(TE);
 #pragma unroll
-        for (int i = 0; i < 16 / kVec; ++i) out[i] = pack16(f + i * kVec, (const TE*)nullptr);
+        for (int i = 0; i < 8 / kVec; ++i) out[i] = pack16(f + i * kVec, (const TE*)nullptr);
       }
     }
   }
@@ -675,7 +677,7 @@ cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, cons
   const int grid = std::min(ceil_div(TK, 8), 152 * 8);
   auto run = [&](auto* out) -> cudaError_t {
     using TE = std::remove_pointer_t<decltype(out)>;
-    SMOE_LAUNCH((widen_rows_kernel<TE>), grid, 256, 0, s, static_cast<const uint4*>(xq), scale, row_src,
+    SMOE_LAUNCH((widen_rows_kernel<TE>), grid, 256, 0, s, static_cast<const uint2*>(xq), scale, row_src,
                 expert_off, d.E, TK, row_src ? d.T : TK, cols, out, st);
     return cudaGetLastError();
   };
