@@ -409,190 +409,6 @@ widen_rows_kernel(const uint2* q, const float* scale, const int32_t* map, const 
   }
 }
 
-// ------------------------------------------------------------------ fp32
-// fp32 layers multiply in fp32 on the CUDA cores (the tensor cores' tf32 keeps 11 bits):
-//   kind 0  y[r, n] = sum_k x[r, k] w[e, n, k]           rows x n_out, over n_in
-//   kind 1  dx[r, k] = sum_n dy[r, n] w[e, n, k] (twice) rows x n_in, over n_out
-//   kind 2  dw[e, n, k] = sum_r dy[r, n] x[r, k] (+ add)  n_out x n_in, over the rows
-// Tiles of BM x 128, 256 threads with BM / 16 x 8 sums each (16 x 128: 2 x 4), 16 of the contraction at
-// a time through shared memory, the next 16 in registers meanwhile.
-struct F32Args {
-  const float *a, *b, *a2, *b2, *add;
-  float* out;
-  const int32_t* expert_off;
-  DeviceStatus* st;
-  int E, TK, n_out, n_in;
-};
-
-template <int KIND, int BM>
-__global__ void __launch_bounds__(256)
-grouped_f32_kernel(const F32Args p) {
-  constexpr int BN = 128, BK = 16, TM = BM == 16 ? 2 : BM / 16, TN = BM == 16 ? 4 : 8;
-  constexpr int kTx = BN / TN;                  // threads along N
-  __shared__ alignas(16) float As[BK][BM + 4];
-  __shared__ alignas(16) float Bs[BK][BN + 4];
-  __shared__ int32_t s_ts[kMaxGroups + 2], s_off[kMaxGroups + 2];
-  pdl_wait_and_trigger();
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 32) {
-    bool bad = false;
-    for (int g = lane; g <= p.E; g += 32) {
-      const int lo = p.expert_off[g], hi = g < p.E ? p.expert_off[g + 1] : lo;
-      bad |= lo < 0 || hi < lo || hi > p.TK;
-      s_off[g] = lo;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad && lane == 0) record_error(p.st, kStatusData, kBadPairRow, -1);
-    __syncwarp();
-    int carry = 0;
-    for (int g0 = 0; g0 < p.E; g0 += 32) {
-      const int g = g0 + lane;
-      int n = 0;
-      if (!bad && g < p.E) n = KIND == 2 ? (p.n_out + BM - 1) / BM : (s_off[g + 1] - s_off[g] + BM - 1) / BM;
-      int incl = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-      }
-      if (g < p.E) s_ts[g] = carry + incl - n;
-      carry += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) s_ts[p.E] = carry;
-  }
-  __syncthreads();
-  const int N = KIND == 0 ? p.n_out : p.n_in, ntile = (N + BN - 1) / BN;
-  const int total = s_ts[p.E] * ntile;
-  const int tx = tid % kTx, ty = tid / kTx;
-  int g = 0;
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    while (s_ts[g + 1] * ntile <= t) ++g;
-    const int mt = s_ts[g + 1] - s_ts[g], local = t - s_ts[g] * ntile;
-    const int n_tile = local / mt, n0 = n_tile * BN, m0 = (local - n_tile * mt) * BM;
-    const int row0 = s_off[g], rows = s_off[g + 1] - row0;
-    const int M = KIND == 2 ? p.n_out : rows;
-    const int K1 = KIND == 0 ? p.n_in : KIND == 1 ? p.n_out : rows;
-    const int nk1 = (K1 + BK - 1) / BK, nk = KIND == 1 && p.a2 ? 2 * nk1 : nk1;
-    float acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
-
-    constexpr int kA = (BM * BK / 4 + 255) / 256, kB = BN * BK / 4 / 256;
-    float4 ra[kA], rb[kB];
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto fetch = [&](int kb) {
-      const bool second = kb >= nk1;
-      const float* a = second ? p.a2 : p.a;
-      const float* b = second ? p.b2 : p.b;
-      const int k0 = (second ? kb - nk1 : kb) * BK;
-#pragma unroll
-      for (int i = 0; i < kA; ++i) {
-        const int v = tid + i * 256;
-        ra[i] = zero;
-        if (v >= BM * BK / 4) continue;
-        if (KIND == 2) {  // [row][n_out]
-          const int k = v / (BM / 4), m = (v - k * (BM / 4)) * 4;
-          if (k0 + k < K1 && m0 + m < M)
-            ra[i] = *reinterpret_cast<const float4*>(a + (size_t)(row0 + k0 + k) * p.n_out + m0 + m);
-        } else {
-          const int m = v >> 2, k = (v & 3) * 4;
-          if (m0 + m < M && k0 + k < K1)
-            ra[i] = *reinterpret_cast<const float4*>(a + (size_t)(row0 + m0 + m) * K1 + k0 + k);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kB; ++i) {
-        const int v = tid + i * 256;
-        rb[i] = zero;
-        if (KIND == 0) {  // [n_out][n_in]
-          const int n = v >> 2, k = (v & 3) * 4;
-          if (n0 + n < N && k0 + k < K1)
-            rb[i] = *reinterpret_cast<const float4*>(b + ((size_t)g * p.n_out + n0 + n) * p.n_in + k0 + k);
-        } else {
-          const int k = v >> 5, n = (v & 31) * 4;
-          const size_t row = KIND == 1 ? (size_t)g * p.n_out + k0 + k : (size_t)row0 + k0 + k;
-          if (k0 + k < K1 && n0 + n < N)
-            rb[i] = *reinterpret_cast<const float4*>(b + row * p.n_in + n0 + n);
-        }
-      }
-    };
-    if (nk > 0) fetch(0);
-    for (int kb = 0; kb < nk; ++kb) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kA; ++i) {
-        const int v = tid + i * 256;
-        if (v >= BM * BK / 4) continue;
-        const float f[4] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w};
-        if (KIND == 2) {
-          const int k = v / (BM / 4), m = (v - k * (BM / 4)) * 4;
-          *reinterpret_cast<float4*>(&As[k][m]) = ra[i];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) As[(v & 3) * 4 + j][v >> 2] = f[j];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kB; ++i) {
-        const int v = tid + i * 256;
-        const float f[4] = {rb[i].x, rb[i].y, rb[i].z, rb[i].w};
-        if (KIND == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) Bs[(v & 3) * 4 + j][v >> 2] = f[j];
-        } else {
-          *reinterpret_cast<float4*>(&Bs[v >> 5][(v & 31) * 4]) = rb[i];
-        }
-      }
-      __syncthreads();
-      if (kb + 1 < nk) fetch(kb + 1);
-#pragma unroll
-      for (int k = 0; k < BK; ++k) {
-        float a[TM], b[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) a[i] = As[k][ty * TM + i];
-#pragma unroll
-        for (int j = 0; j < TN; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&Bs[k][tx * 4 + j * kTx]);
-          b[j] = f.x; b[j + 1] = f.y; b[j + 2] = f.z; b[j + 3] = f.w;
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int m = m0 + ty * TM + i;
-      if (m >= M) continue;
-      const size_t row = (KIND == 2 ? (size_t)g * p.n_out : (size_t)row0) + m;
-#pragma unroll
-      for (int j = 0; j < TN; j += 4) {
-        const int n = n0 + tx * 4 + j * kTx;
-        if (n >= N) continue;
-        float4 o = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
-        if (KIND == 2 && p.add) {
-          const float4 f = *reinterpret_cast<const float4*>(p.add + row * N + n);
-          o.x += f.x; o.y += f.y; o.z += f.z; o.w += f.w;
-        }
-        *reinterpret_cast<float4*>(p.out + row * N + n) = o;
-      }
-    }
-  }
-}
-
-template <int KIND, int BM>
-cudaError_t run_f32(const F32Args& p, long long tiles, cudaStream_t s) {
-  const int grid = (int)std::min<long long>(std::max<long long>(tiles, 1), (long long)device_sms() * 4);
-  SMOE_LAUNCH((grouped_f32_kernel<KIND, BM>), grid, 256, 0, s, p);
-  return cudaGetLastError();
-}
-
-// Rows an expert from which the 64-row tiles take over from the 16-row ones.
-constexpr int kF32Rows = 24;
-
 }  // namespace
 
 int device_sms() {
@@ -620,15 +436,9 @@ cudaError_t launch_expert_rows(const smoe_desc& d, int n_out, int n_in, const vo
                                const int32_t* expert_off, void* out, void* ws, cudaStream_t s) {
   if (d.dtype != SMOE_F32)
     return launch_expert_rows_bf16(d, n_out, n_in, a, w, a2, w2, transposed, expert_off, out, ws, s);
-  const int TK = d.T * d.K;
-  const F32Args p{static_cast<const float*>(a), static_cast<const float*>(w),
-                  static_cast<const float*>(a2), static_cast<const float*>(w2), nullptr,
-                  static_cast<float*>(out), expert_off, static_cast<DeviceStatus*>(ws), d.E, TK, n_out, n_in};
-  const bool few = (long long)TK < (long long)kF32Rows * d.E;
-  const long long tiles = ((long long)ceil_div(TK, few ? 16 : 64) + std::min(TK, d.E)) *
-                          ceil_div(transposed ? n_in : n_out, 128);
-  if (transposed) return few ? run_f32<1, 16>(p, tiles, s) : run_f32<1, 64>(p, tiles, s);
-  return few ? run_f32<0, 16>(p, tiles, s) : run_f32<0, 64>(p, tiles, s);
+  return launch_expert_rows_f32(d, n_out, n_in, static_cast<const float*>(a), static_cast<const float*>(w),
+                                static_cast<const float*>(a2), static_cast<const float*>(w2), transposed,
+                                expert_off, static_cast<float*>(out), static_cast<DeviceStatus*>(ws), s);
 }
 
 cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void* dy, const void* x,
@@ -636,11 +446,9 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
                              cudaStream_t s) {
   const int TK = d.T * d.K;
   DeviceStatus* st = static_cast<DeviceStatus*>(ws);
-  if (d.dtype == SMOE_F32) {
-    const F32Args p{static_cast<const float*>(dy), static_cast<const float*>(x), nullptr, nullptr, add,
-                    dw, expert_off, st, d.E, TK, n_out, n_in};
-    return run_f32<2, 64>(p, (long long)d.E * ceil_div(n_out, 64) * ceil_div(n_in, 128), s);
-  }
+  if (d.dtype == SMOE_F32)
+    return launch_expert_dw_f32(d, n_out, n_in, static_cast<const float*>(dy), static_cast<const float*>(x),
+                                expert_off, add, dw, st, s);
   alignas(64) CUtensorMap A, B;
   if (!encode_tmap_2d(&A, dy, false, TK, n_out, 64, 64) || !encode_tmap_2d(&B, x, false, TK, n_in, 64, 64))
     return cudaErrorInvalidValue;

@@ -326,6 +326,13 @@ cudaError_t launch_expert_rows_bf16(const smoe_desc& d, int n_out, int n_in, con
 cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void* dy, const void* x,
                              const int32_t* expert_off, const float* add, float* dw, void* ws,
                              cudaStream_t s);
+// fp32 layers (expert_f32.cu)
+cudaError_t launch_expert_rows_f32(const smoe_desc& d, int n_out, int n_in, const float* a,
+                                   const float* w, const float* a2, const float* w2, bool transposed,
+                                   const int32_t* expert_off, float* out, DeviceStatus* st, cudaStream_t s);
+cudaError_t launch_expert_dw_f32(const smoe_desc& d, int n_out, int n_in, const float* dy,
+                                 const float* x, const int32_t* expert_off, const float* add, float* dw,
+                                 DeviceStatus* st, cudaStream_t s);
 // the workspace's rows = kept rows in the layer's type
 cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,
                               const int32_t* row_src, const int32_t* expert_off, void* ws,
