@@ -16,6 +16,7 @@
 // An expert's R rows give 2 R flops per element of 4 bytes (8 with add): below about 550 rows an
 // expert the stores bound it, not the tensor cores.
 #include <algorithm>
+#include <climits>
 #include <cuda_fp8.h>
 
 #include "tc_common.cuh"
@@ -66,6 +67,10 @@ __device__ __forceinline__ void dw_clear(uint8_t* a, uint8_t* b, int left, int l
   __syncwarp();
 }
 
+// PL = 3: fp32 operands as three bf16 planes each, [3][TK][channels], whose sum they are: the six
+// products of planes that reach 2^-24 of a term are added up, which is a product in fp32. A
+// plane of both operands takes a stage; the MMAs of 64 rows wait for three stages.
+template <int PL>
 __global__ void __launch_bounds__(kDwThreads, 1)
 dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
           const DwArgs p) {
@@ -148,7 +153,8 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
     for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
       const int nb = tl.n0 + 128 < p.N ? 2 : 1, m0 = tl.m0 + (int)rank * 128, n0 = tl.n0 + (int)rank * 64 * nb;
-      for (int r = 0; r < tl.rows; r += 64) {
+      for (int i = 0; i < PL * ((tl.rows + 63) >> 6); ++i) {
+        const int r = i / PL * 64, row = i % PL * p.TK + tl.row0 + r;
         ok = tc::mbar_wait_warp(&empty[s], ph, abort);
         if (!ok) break;
         const bool cut = tl.rows - r < 64 && ((tl.rows - r) & 15) != 0;
@@ -164,9 +170,9 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
             tc::mbar_arrive_remote(leader);
           }
           for (int j = 0; j < 2; ++j)
-            tc::tma_load_2d_pair(sA + s * kDwHalf + j * 8192, &tmA, on, m0 + 64 * j, tl.row0 + r);
+            tc::tma_load_2d_pair(sA + s * kDwHalf + j * 8192, &tmA, on, m0 + 64 * j, row);
           for (int j = 0; j < nb; ++j)
-            tc::tma_load_2d_pair(sB + s * kDwHalf + j * 8192, &tmB, on, n0 + 64 * j, tl.row0 + r);
+            tc::tma_load_2d_pair(sB + s * kDwHalf + j * 8192, &tmB, on, n0 + 64 * j, row);
         }
         __syncwarp();
         own &= ~(1u << s);
@@ -212,28 +218,42 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       tc::fence_after_sync();
       const uint32_t acc = tmem + d * 256;
       for (int r = 0; r < tl.rows; r += 64) {
-        const int left = min(64, tl.rows - r);
-        if (left & 15) {
-          // the peer's zeros are acquired with its word
-          ok = tc::mbar_wait_warp_shared(&full[s], ph, abort);
-          if (!ok) break;
-          dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, left, lane);
-        } else if (!in) {
-          ok = tc::mbar_wait_warp(&full[s], ph, abort);
-          if (!ok) break;
+        const int left = min(64, tl.rows - r), steps = (left + 15) >> 4;
+        uint64_t ad[PL], bd[PL];
+        uint64_t* e_bar[PL];
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          if (left & 15) {
+            // the peer's zeros are acquired with its word
+            ok = tc::mbar_wait_warp_shared(&full[s], ph, abort);
+            if (!ok) break;
+            dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, left, lane);
+          } else if (i > 0 || !in) {
+            ok = tc::mbar_wait_warp(&full[s], ph, abort);
+            if (!ok) break;
+          }
+          ad[i] = tc::sw128_mnmajor_desc(tc::smem_u32(sA + s * kDwHalf));
+          bd[i] = tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kDwHalf));
+          e_bar[i] = &empty[s];
+          if (++s == kDwStages) { s = 0; ph ^= 1u; }
         }
+        if (!ok) break;
         tc::fence_after_sync();
-        const uint64_t ad = tc::sw128_mnmajor_desc(tc::smem_u32(sA + s * kDwHalf));
-        const uint64_t bd = tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kDwHalf));
-        uint64_t* e_bar = &empty[s];
-        if (++s == kDwStages) { s = 0; ph ^= 1u; }
         const bool in_next = tc::mbar_test(&full[s], ph);
         if (lead) {
-          const int steps = (left + 15) >> 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps) tc::mma_bf16_pair(acc, ad + 128 * k, bd + 128 * k, idesc, r > 0 || k > 0);
-          tc::commit_pair(e_bar, 0x3);
+          for (int k = 0; k < 4; ++k) {
+            if (k >= steps) break;
+            // the smallest products first: (2, 0), (1, 1), (0, 2), (1, 0), (0, 1), (0, 0)
+#pragma unroll
+            for (int sum = PL - 1; sum >= 0; --sum)
+#pragma unroll
+              for (int i = sum; i >= 0; --i)
+                tc::mma_bf16_pair(acc, ad[i] + 128 * k, bd[sum - i] + 128 * k, idesc,
+                                  r > 0 || k > 0 || i != PL - 1);
+          }
+#pragma unroll
+          for (int i = 0; i < PL; ++i) tc::commit_pair(e_bar[i], 0x3);
         }
         in = __all_sync(0xffffffffu, in_next);
       }
@@ -259,14 +279,16 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
     bool ok = true;
     for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
-      it += (tl.rows + 63) >> 6;
+      it += PL * ((tl.rows + 63) >> 6);
       if ((tl.rows & 15) == 0) continue;
-      const uint32_t s = (it - 1) % kDwStages;
-      ok = tc::mbar_wait_warp(&last[s], lph >> s & 1u, abort);
-      if (!ok) break;
-      lph ^= 1u << s;
-      dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, tl.rows & 63, lane);
-      if (lane == 0) tc::mbar_arrive_cluster_shared(tc::cluster_addr(&full[s], 0));
+      for (int i = PL; i > 0 && ok; --i) {
+        const uint32_t s = (it - i) % kDwStages;
+        ok = tc::mbar_wait_warp(&last[s], lph >> s & 1u, abort);
+        if (!ok) break;
+        lph ^= 1u << s;
+        dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, tl.rows & 63, lane);
+        if (lane == 0) tc::mbar_arrive_cluster_shared(tc::cluster_addr(&full[s], 0));
+      }
     }
     if (!ok && lane == 0) {
       *abort = 1;
@@ -428,6 +450,9 @@ void product_ws_layout(const smoe_desc& d, ProductLayout* L) {
   L->status = take(256);
   L->tiles = take(4 * (kMaxGroups + 2));
   L->rows = take((size_t)d.T * d.K * std::max(d.d, d.F) * elem_size(d));
+  const size_t planes = d.dtype == SMOE_F32 ? (size_t)d.T * d.K * std::max(d.d, d.F) * 6 : 0;
+  L->planes_a = take(planes);
+  L->planes_b = take(planes);
   L->total = off;
 }
 
@@ -441,20 +466,17 @@ cudaError_t launch_expert_rows(const smoe_desc& d, int n_out, int n_in, const vo
                                 expert_off, static_cast<float*>(out), static_cast<DeviceStatus*>(ws), s);
 }
 
-cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void* dy, const void* x,
-                             const int32_t* expert_off, const float* add, float* dw, void* ws,
-                             cudaStream_t s) {
-  const int TK = d.T * d.K;
-  DeviceStatus* st = static_cast<DeviceStatus*>(ws);
-  if (d.dtype == SMOE_F32)
-    return launch_expert_dw_f32(d, n_out, n_in, static_cast<const float*>(dy), static_cast<const float*>(x),
-                                expert_off, add, dw, st, s);
+namespace {
+
+template <int PL>
+cudaError_t run_dw(const void* dy, const void* x, const DwArgs& p, cudaStream_t s) {
   alignas(64) CUtensorMap A, B;
-  if (!encode_tmap_2d(&A, dy, false, TK, n_out, 64, 64) || !encode_tmap_2d(&B, x, false, TK, n_in, 64, 64))
+  if (!encode_tmap_2d(&A, dy, false, (uint64_t)PL * p.TK, p.M, 64, 64) ||
+      !encode_tmap_2d(&B, x, false, (uint64_t)PL * p.TK, p.N, 64, 64))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDwSmem);
+  auto kern = dw_kernel<PL>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDwSmem);
   if (e != cudaSuccess) return e;
-  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 256), ceil_div(n_in, 256)};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -463,14 +485,70 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * (int)std::min<long long>(device_sms() / 2, (long long)d.E * p.mt * p.nt));
+  cfg.gridDim = dim3(2 * (int)std::min<long long>(device_sms() / 2, (long long)p.E * p.mt * p.nt));
   cfg.blockDim = dim3(kDwThreads);
   cfg.dynamicSmemBytes = kDwSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   SMOE_COUNT_LAUNCH(1);
-  return cudaLaunchKernelEx(&cfg, dw_kernel, A, B, p);
+  return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+}
+
+// x = p0 + p1 + p2, each a bf16 value: the rest is exact at every step, and 24 bits are three times
+// eight. (A value that would round up to infinity is cut off instead; an infinity or a NaN
+// stays in p0, with zeros behind it.) Both operands' rows of the segments, 8 values a thread.
+__global__ void __launch_bounds__(256)
+split_rows_kernel(const float* a, const float* b, int na, int nb, uint4* pa, uint4* pb,
+                  const int32_t* expert_off, int E, int TK) {
+  pdl_wait_and_trigger();
+  const int begin = max(expert_off[0], 0), end = min(expert_off[E], TK);
+  const int va = na >> 3, vb = nb >> 3;
+  for (int r = begin + blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8)
+    for (int v = threadIdx.x & 31; v < va + vb; v += 32) {
+      const bool first = v < va;
+      const int n = first ? va : vb, c = first ? v : v - va;
+      const float4* from = reinterpret_cast<const float4*>(first ? a : b) + ((size_t)r * n + c) * 2;
+      const float4 x0 = __ldcg(from), x1 = __ldcg(from + 1);
+      float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      uint4* to = (first ? pa : pb) + (size_t)r * n + c;
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
+          if (__hisinf(h)) h = __float2bfloat16_rz(x[i]);
+          y[i] = __bfloat162float(h);
+          x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] - y[i] : 0.0f;
+        }
+        to[(size_t)pl * TK * n] = pack16(y, (const __nv_bfloat16*)nullptr);
+      }
+    }
+}
+
+// From this many multiply-adds on an fp32 weight gradient runs on the tensor cores.
+constexpr double kPlaneMacs = 2e8;
+
+}  // namespace
+
+cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void* dy, const void* x,
+                             const int32_t* expert_off, const float* add, float* dw, void* ws,
+                             cudaStream_t s) {
+  const int TK = d.T * d.K, wide = std::max(d.d, d.F);
+  DeviceStatus* st = static_cast<DeviceStatus*>(ws);
+  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 256), ceil_div(n_in, 256)};
+  if (d.dtype != SMOE_F32) return run_dw<1>(dy, x, p, s);
+  const float *fy = static_cast<const float*>(dy), *fx = static_cast<const float*>(x);
+  // (the planes' place is the descriptor's)
+  if (n_out > wide || n_in > wide || (double)TK * n_out * n_in < kPlaneMacs || 3LL * TK > INT_MAX / 2)
+    return launch_expert_dw_f32(d, n_out, n_in, fy, fx, expert_off, add, dw, st, s);
+  ProductLayout L;
+  product_ws_layout(d, &L);
+  uint4 *pa = ws_ptr<uint4>(ws, L.planes_a), *pb = ws_ptr<uint4>(ws, L.planes_b);
+  SMOE_LAUNCH(split_rows_kernel, std::min(ceil_div(TK, 8), 152 * 8), 256, 0, s, fy, fx, n_out, n_in, pa, pb,
+              expert_off, d.E, TK);
+  return run_dw<3>(pa, pb, p, s);
 }
 
 cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,

@@ -308,7 +308,8 @@ cudaError_t launch_swiglu_grad_f8(const smoe_desc& d, int rows, int cols, const 
 // Expert products in 8-bit floating point (expert_f8.cu), and in the layer's type with their
 // gradients (ffn.cu, expert_grad.cu). One workspace for all of them.
 struct ProductLayout {
-  size_t status, tiles, rows, total;  // rows: widened rows of a weight gradient
+  // rows: widened rows of a weight gradient; planes: its fp32 operands as bf16 planes
+  size_t status, tiles, rows, planes_a, planes_b, total;
 };
 void product_ws_layout(const smoe_desc& d, ProductLayout* out);
 int device_sms();  // of the current device
