@@ -574,8 +574,11 @@ SMOE_API int smoe_expert_matmul_dx(const smoe_desc* desc, int n_out, int n_in, c
  *   dw[e, n, k] = add[e, n, k] + sum_{r of e} dy[r, n] x[r, k].
  *   dy [T K, n_out] dtype; x [T K, n_in] dtype; add nullable [E, n_out, n_in] fp32: the gradient
  *   of earlier batches (may be the same buffer as dw); dw [E, n_out, n_in] fp32, every expert
- *   written: one without rows gets add, or zeros. Rows outside the segments are not read into
- *   any sum. With T = 0 nothing is written. A bad expert_off (SMOE_ERR_DATA) writes nothing. */
+ *   written: one without rows (with T = 0: all) gets add, or zeros. Rows outside the segments
+ *   are not read into any sum. A bad expert_off (SMOE_ERR_DATA) writes nothing.
+ * Sums over many rows are added up in chunks, so that they do not drift. fp32 layers multiply in
+ * fp32, large ones on the tensor cores as bf16 planes of the operands: there an infinity in an
+ * operand may give NaN where the exact sum is infinite.                                  */
 SMOE_API int smoe_expert_matmul_dw(const smoe_desc* desc, int n_out, int n_in, const void* dy,
                                    const void* x, const int32_t* expert_off, const float* add,
                                    float* dw, void* ws, size_t ws_bytes, void* stream);

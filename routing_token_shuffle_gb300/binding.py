@@ -392,16 +392,20 @@ def _matrix(desc, w, name):
     return n_out, n_in
 
 
-def _same(name, a, like):
-    if a is not None and a.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(a.shape)}, not {tuple(like.shape)}")
+def _same(like, **tensors):
+    """Refuses buffers that hold another number of elements than `like` (the shape itself costs
+    more to compare, and a short call's time is the host's)."""
+    n = like.numel()
+    for name, t in tensors.items():
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
 
 
 def smoe_rows_f8(desc, x, q, scale, pow2=0, stream=None):
     """x [rows, cols] in desc's dtype to q (e4m3) and scale [rows, ceil(cols / 128)]."""
     rows, cols = x.shape
-    _same("q", q, x)
-    _check(lib().smoe_rows_f8(ctypes.byref(desc), rows, cols, _ptr(x), int(pow2), _ptr(q), _ptr(scale),
+    _same(x, q=q)
+    _check(lib().smoe_rows_f8(ctypes.byref(desc), rows, cols, _ptr(x), pow2, _ptr(q), _ptr(scale),
                               _stream(stream)), "smoe_rows_f8")
 
 
@@ -426,7 +430,7 @@ def smoe_expert_matmul(desc, x, expert_off, w, out, ws, stream=None):
 def smoe_expert_matmul_dx(desc, dy, w, expert_off, dx, ws, dy2=None, w2=None, stream=None):
     """dx = dy w (+ dy2 w2) by expert; w, w2 [E, n_out, n_in]; ws from workspace_products."""
     n_out, n_in = _matrix(desc, w, "w")
-    _same("w2", w2, w)
+    _same(w, w2=w2)
     _check(lib().smoe_expert_matmul_dx(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(w), _ptr(dy2),
                                        _ptr(w2), _ptr(expert_off), _ptr(dx), _ptr(ws), ws.numel(),
                                        _stream(stream)), "smoe_expert_matmul_dx")
@@ -435,7 +439,7 @@ def smoe_expert_matmul_dx(desc, dy, w, expert_off, dx, ws, dy2=None, w2=None, st
 def smoe_expert_matmul_dw(desc, dy, x, expert_off, dw, ws, add=None, stream=None):
     """dw = (add +) dy^T x by expert, fp32 [E, n_out, n_in]; ws from workspace_products."""
     n_out, n_in = _matrix(desc, dw, "dw")
-    _same("add", add, dw)
+    _same(dw, add=add)
     _check(lib().smoe_expert_matmul_dw(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(x),
                                        _ptr(expert_off), _ptr(add), _ptr(dw), _ptr(ws), ws.numel(),
                                        _stream(stream)), "smoe_expert_matmul_dw")
@@ -445,7 +449,7 @@ def smoe_expert_matmul_dw_f8(desc, dy, xq, x_scale, expert_off, dw, ws, row_src=
                              stream=None):
     """smoe_expert_matmul_dw from rows kept in 8 bits (token rows when row_src is given)."""
     n_out, n_in = _matrix(desc, dw, "dw")
-    _same("add", add, dw)
+    _same(dw, add=add)
     _check(lib().smoe_expert_matmul_dw_f8(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(xq),
                                           _ptr(x_scale), _ptr(row_src), _ptr(expert_off), _ptr(add),
                                           _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
@@ -456,9 +460,11 @@ def smoe_swiglu_f8(desc, g, u, h=None, h8=None, h8_scale=None, g8=None, g8_scale
                    u8_scale=None, pow2=1, stream=None):
     """h = silu(g) u, and h, g, u in 8 bits, each where its buffers are given."""
     rows, cols = g.shape
-    for name, t in (("u", u), ("h", h), ("h8", h8), ("g8", g8), ("u8", u8)):
-        _same(name, t, g)
-    _check(lib().smoe_swiglu_f8(ctypes.byref(desc), rows, cols, _ptr(g), _ptr(u), int(pow2), _ptr(h),
+    n = rows * cols
+    if (u.numel() != n or (h is not None and h.numel() != n) or (h8 is not None and h8.numel() != n)
+            or (g8 is not None and g8.numel() != n) or (u8 is not None and u8.numel() != n)):
+        _same(g, u=u, h=h, h8=h8, g8=g8, u8=u8)
+    _check(lib().smoe_swiglu_f8(ctypes.byref(desc), rows, cols, _ptr(g), _ptr(u), pow2, _ptr(h),
                                 _ptr(h8), _ptr(h8_scale), _ptr(g8), _ptr(g8_scale), _ptr(u8),
                                 _ptr(u8_scale), _stream(stream)), "smoe_swiglu_f8")
 
@@ -466,8 +472,10 @@ def smoe_swiglu_f8(desc, g, u, h=None, h8=None, h8_scale=None, g8=None, g8_scale
 def smoe_swiglu_grad_f8(desc, dh, g8, g8_scale, u8, u8_scale, dg, du, h=None, stream=None):
     """dg, du (and h again) from dh and what smoe_swiglu_f8 kept."""
     rows, cols = dh.shape
-    for name, t in (("g8", g8), ("u8", u8), ("dg", dg), ("du", du), ("h", h)):
-        _same(name, t, dh)
+    n = rows * cols
+    if (g8.numel() != n or u8.numel() != n or dg.numel() != n or du.numel() != n
+            or (h is not None and h.numel() != n)):
+        _same(dh, g8=g8, u8=u8, dg=dg, du=du, h=h)
     _check(lib().smoe_swiglu_grad_f8(ctypes.byref(desc), rows, cols, _ptr(dh), _ptr(g8),
                                      _ptr(g8_scale), _ptr(u8), _ptr(u8_scale), _ptr(dg), _ptr(du),
                                      _ptr(h), _stream(stream)), "smoe_swiglu_grad_f8")

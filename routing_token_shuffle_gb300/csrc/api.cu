@@ -874,10 +874,10 @@ SMOE_API int smoe_rows_f8(const smoe_desc* desc, int rows, int cols, const void*
                           uint8_t* q, float* scale, void* stream) {
   SMOE_CHECK(check_rows_f8(desc, rows, cols));
   SMOE_REQUIRE(pow2 == 0 || pow2 == 1, SMOE_ERR_ARG, "pow2 must be 0 or 1");
+  if (rows == 0) return SMOE_OK;  // (an empty tensor has no address)
   SMOE_PTR(x);
   SMOE_PTR(q);
   SMOE_PTR(scale);
-  if (rows == 0) return SMOE_OK;
   SMOE_CHECK(check_device());
   cudaError_t e = launch_rows_f8(*desc, rows, cols, x, pow2, q, scale, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "8-bit rows launch");
@@ -889,6 +889,7 @@ SMOE_API int smoe_swiglu_f8(const smoe_desc* desc, int rows, int cols, const voi
                             float* g8_scale, uint8_t* u8, float* u8_scale, void* stream) {
   SMOE_CHECK(check_rows_f8(desc, rows, cols));
   SMOE_REQUIRE(pow2 == 0 || pow2 == 1, SMOE_ERR_ARG, "pow2 must be 0 or 1");
+  if (rows == 0) return SMOE_OK;
   SMOE_PTR(g);
   SMOE_PTR(u);
   SMOE_OPT_PTR(h);
@@ -896,7 +897,6 @@ SMOE_API int smoe_swiglu_f8(const smoe_desc* desc, int rows, int cols, const voi
   SMOE_F8_PAIR(g8, g8_scale);
   SMOE_F8_PAIR(u8, u8_scale);
   SMOE_REQUIRE(h || h8 || g8 || u8, SMOE_ERR_ARG, "no output is given");
-  if (rows == 0) return SMOE_OK;
   SMOE_CHECK(check_device());
   cudaError_t e = launch_swiglu_f8(*desc, rows, cols, g, u, pow2, h, F8Rows{h8, h8_scale},
                                    F8Rows{g8, g8_scale}, F8Rows{u8, u8_scale},
@@ -909,6 +909,7 @@ SMOE_API int smoe_swiglu_grad_f8(const smoe_desc* desc, int rows, int cols, cons
                                  const uint8_t* g8, const float* g8_scale, const uint8_t* u8,
                                  const float* u8_scale, void* dg, void* du, void* h, void* stream) {
   SMOE_CHECK(check_rows_f8(desc, rows, cols));
+  if (rows == 0) return SMOE_OK;
   SMOE_PTR(dh);
   SMOE_PTR(g8);
   SMOE_PTR(g8_scale);
@@ -917,7 +918,6 @@ SMOE_API int smoe_swiglu_grad_f8(const smoe_desc* desc, int rows, int cols, cons
   SMOE_PTR(dg);
   SMOE_PTR(du);
   SMOE_OPT_PTR(h);
-  if (rows == 0) return SMOE_OK;
   SMOE_CHECK(check_device());
   cudaError_t e = launch_swiglu_grad_f8(*desc, rows, cols, dh, g8, g8_scale, u8, u8_scale, dg, du, h,
                                         static_cast<cudaStream_t>(stream));
@@ -961,6 +961,7 @@ SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, c
                                    const float* w_scale, void* out, void* ws, size_t ws_bytes,
                                    void* stream) {
   SMOE_CHECK(check_product(desc, n_out, n_in, 16, ws, ws_bytes));
+  if (desc->T == 0) return SMOE_OK;
   SMOE_PTR(xq);
   SMOE_PTR(x_scale);
   SMOE_OPT_PTR(row_src);
@@ -969,7 +970,6 @@ SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, c
   SMOE_PTR(w_scale);
   SMOE_PTR(out);
   SMOE_CHECK(check_device());
-  if (desc->T == 0) return SMOE_OK;
   cudaError_t e = launch_expert_matmul_f8(*desc, n_out, n_in, xq, x_scale, row_src, expert_off, wq,
                                           w_scale, out, ws, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "8-bit floating-point product launch");
@@ -980,12 +980,12 @@ SMOE_API int smoe_expert_matmul(const smoe_desc* desc, int n_out, int n_in, cons
                                 const int32_t* expert_off, const void* w, void* out, void* ws,
                                 size_t ws_bytes, void* stream) {
   SMOE_CHECK(check_product(desc, n_out, n_in, 8, ws, ws_bytes));
+  if (desc->T == 0) return SMOE_OK;
   SMOE_PTR(x);
   SMOE_PTR(expert_off);
   SMOE_PTR(w);
   SMOE_PTR(out);
   SMOE_CHECK(check_device());
-  if (desc->T == 0) return SMOE_OK;
   cudaError_t e = launch_expert_rows(*desc, n_out, n_in, x, w, nullptr, nullptr, false, expert_off, out,
                                      ws, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
@@ -997,6 +997,7 @@ SMOE_API int smoe_expert_matmul_dx(const smoe_desc* desc, int n_out, int n_in, c
                                    const int32_t* expert_off, void* dx, void* ws, size_t ws_bytes,
                                    void* stream) {
   SMOE_CHECK(check_product(desc, n_out, n_in, 8, ws, ws_bytes));
+  if (desc->T == 0) return SMOE_OK;
   SMOE_PTR(dy);
   SMOE_PTR(w);
   SMOE_OPT_PTR(dy2);
@@ -1005,10 +1006,19 @@ SMOE_API int smoe_expert_matmul_dx(const smoe_desc* desc, int n_out, int n_in, c
   SMOE_PTR(expert_off);
   SMOE_PTR(dx);
   SMOE_CHECK(check_device());
-  if (desc->T == 0) return SMOE_OK;
   cudaError_t e = launch_expert_rows(*desc, n_out, n_in, dy, w, dy2, w2, true, expert_off, dx, ws,
                                      static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "row gradient launch");
+  return SMOE_OK;
+}
+
+// The gradient of a batch without tokens: what came before, or zeros.
+static int dw_of_no_rows(const smoe_desc* desc, int n_out, int n_in, const float* add, float* dw,
+                         void* stream) {
+  const size_t bytes = (size_t)desc->E * n_out * n_in * sizeof(float);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (add == dw) return SMOE_OK;
+  SMOE_CUDA(add ? cudaMemcpyAsync(dw, add, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(dw, 0, bytes, s));
   return SMOE_OK;
 }
 
@@ -1016,13 +1026,13 @@ SMOE_API int smoe_expert_matmul_dw(const smoe_desc* desc, int n_out, int n_in, c
                                    const void* x, const int32_t* expert_off, const float* add,
                                    float* dw, void* ws, size_t ws_bytes, void* stream) {
   SMOE_CHECK(check_product(desc, n_out, n_in, 8, ws, ws_bytes));
-  SMOE_PTR(expert_off);
   SMOE_OPT_PTR(add);
   SMOE_PTR(dw);
+  if (desc->T == 0) return dw_of_no_rows(desc, n_out, n_in, add, dw, stream);
+  SMOE_PTR(expert_off);
   SMOE_PTR(dy);
   SMOE_PTR(x);
   SMOE_CHECK(check_device());
-  if (desc->T == 0) return SMOE_OK;
   cudaError_t e = launch_expert_dw(*desc, n_out, n_in, dy, x, expert_off, add, dw, ws,
                                    static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
@@ -1037,15 +1047,15 @@ SMOE_API int smoe_expert_matmul_dw_f8(const smoe_desc* desc, int n_out, int n_in
   SMOE_CHECK(check_product(desc, n_out, n_in, 16, ws, ws_bytes));
   SMOE_REQUIRE(n_in <= std::max(desc->d, desc->F), SMOE_ERR_SHAPE, "n_in=%d must be at most max(d, F)=%d",
                n_in, std::max(desc->d, desc->F));
+  SMOE_OPT_PTR(add);
+  SMOE_PTR(dw);
+  if (desc->T == 0) return dw_of_no_rows(desc, n_out, n_in, add, dw, stream);
   SMOE_PTR(dy);
   SMOE_PTR(xq);
   SMOE_PTR(x_scale);
   SMOE_OPT_PTR(row_src);
   SMOE_PTR(expert_off);
-  SMOE_OPT_PTR(add);
-  SMOE_PTR(dw);
   SMOE_CHECK(check_device());
-  if (desc->T == 0) return SMOE_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const void* rows = nullptr;
   cudaError_t e = launch_widen_rows(*desc, n_in, xq, x_scale, row_src, expert_off, ws, &rows, s);

@@ -26,6 +26,13 @@ namespace {
 
 constexpr int kDwStages = 5, kDwWarps = 8, kDwThreads = 128 + 32 * kDwWarps;
 constexpr int kDwCols = 1024 / kDwWarps;  // columns of an epilogue warp
+// The tensor core cuts its sums off at 24 bits instead of rounding them, addition by addition, so
+// long sums drift (1024 rows: 1.2e-6 of the result). So the rows after the first chunk of an
+// expert go into the other TMEM accumulator, chunk by chunk, which the epilogue adds, rounded, to
+// the first one. For fp32 operands, whose six products add up six times as often, after fewer rows.
+// (131072 rows of 128 experts, accumulated: chunks of 512 rows 483 us, 768: 452, 1024: 434, one: 402.
+// With the sums in registers, 128 of them a thread, 530.)
+template <int PL> constexpr int kDwChunk = PL == 1 ? 1024 : 128;
 constexpr int kDwHalf = 128 * 128;  // bytes of an operand's stage in a CTA: 64 rows of 128 channels
 constexpr size_t kDwSmem = 1024 + kDwStages * 2 * kDwHalf + kDwWarps * 4096 +
                            8 * (3 * kDwStages + 2 * 2 + 1) + 16 + 4 * (kMaxGroups + 2);
@@ -141,6 +148,9 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   volatile int* abort = s_abort;
   // A tile's columns: 256, or 128 where the matrix has no more; half of them staged by each CTA.
 
+  // 384 threads of 168 registers at launch, 104 + 2 x 200 = 3 x 168 from here on
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
     // The leader's barrier of a stage counts both CTAs' bytes. A segment's last stage, where it
@@ -206,19 +216,22 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- MMA issuer (of the pair)
     const bool lead = tc::elect_one();
-    uint32_t s = 0, ph = 0, d = 0, dph = 1;
+    uint32_t s = 0, ph = 0, d = 0, eph = 0x3;  // eph: a phase bit for each accumulator
     bool ok = true, in = false;
     for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
       if (tl.rows == 0) continue;
       const uint32_t idesc = tc::instr_desc(false, 256, tl.n0 + 128 < p.N ? 256 : 128) |
                              tc::kIdescTransA | tc::kIdescTransB;
-      ok = tc::mbar_wait_warp(&dempty[d], dph, abort);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t acc = tmem + d * 256;
       for (int r = 0; r < tl.rows; r += 64) {
         const int left = min(64, tl.rows - r), steps = (left + 15) >> 4;
+        const uint32_t at = r < kDwChunk<PL> ? d : d ^ 1u, acc = tmem + at * 256;
+        const bool start = r % kDwChunk<PL> == 0, end = (r + 64) % kDwChunk<PL> == 0 || r + 64 >= tl.rows;
+        if (start) {
+          ok = tc::mbar_wait_warp(&dempty[at], eph >> at & 1u, abort);
+          if (!ok) break;
+          eph ^= 1u << at;
+        }
         uint64_t ad[PL], bd[PL];
         uint64_t* e_bar[PL];
 #pragma unroll
@@ -241,26 +254,23 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
         tc::fence_after_sync();
         const bool in_next = tc::mbar_test(&full[s], ph);
         if (lead) {
+          // the smallest products first: (2, 0), (1, 1), (0, 2), (1, 0), (0, 1), (0, 0)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= steps) break;
-            // the smallest products first: (2, 0), (1, 1), (0, 2), (1, 0), (0, 1), (0, 0)
+          for (int sum = PL - 1; sum >= 0; --sum)
 #pragma unroll
-            for (int sum = PL - 1; sum >= 0; --sum)
+            for (int i = sum; i >= 0; --i)
 #pragma unroll
-              for (int i = sum; i >= 0; --i)
-                tc::mma_bf16_pair(acc, ad[i] + 128 * k, bd[sum - i] + 128 * k, idesc,
-                                  r > 0 || k > 0 || i != PL - 1);
-          }
+              for (int k = 0; k < 4; ++k)
+                if (k < steps)
+                  tc::mma_bf16_pair(acc, ad[i] + 128 * k, bd[sum - i] + 128 * k, idesc,
+                                    !start || k > 0 || i != PL - 1);
 #pragma unroll
           for (int i = 0; i < PL; ++i) tc::commit_pair(e_bar[i], 0x3);
+          if (end) tc::commit_pair(&dfull[at], 0x3);
         }
         in = __all_sync(0xffffffffu, in_next);
       }
-      if (!ok) break;
-      if (lead) tc::commit_pair(&dfull[d], 0x3);
-      __syncwarp();
-      if (++d == 2) { d = 0; dph ^= 1u; }
+      d ^= 1u;
     }
     if (lead) {
       if (!ok) {
@@ -295,7 +305,9 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---------------------------------------------------------------- epilogue
     // Each warp 32 rows of kDwCols columns, in windows of 32 columns through 4 KB of its own
     // (16-byte chunks swizzled by row: no bank conflicts), added to and stored as whole lines. What
@@ -304,8 +316,18 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
     constexpr int kWins = kDwCols / 32;
     uint8_t* buf = sE + (warp - 4) * 4096;
     const int ch = lane & 7, sub = lane >> 3;
-    uint32_t d = 0, dph = 0;
+    uint32_t d = 0, fph = 0;  // fph: a phase bit for each accumulator
     bool ok = true;
+    auto wait = [&](uint32_t at) {
+      ok = tc::mbar_wait_warp(&dfull[at], fph >> at & 1u, abort);
+      fph ^= 1u << at;
+      tc::fence_after_sync();
+    };
+    auto read_out = [&](uint32_t at) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_remote(tc::cluster_addr(&dempty[at], 0));
+    };
     for (int t = first; t < total && ok; t += stride) {
       const DwTile tl = dw_decode(p, s_off, t);
       const int m0 = tl.m0 + (int)rank * 128 + q * 32, n0 = tl.n0 + part * kDwCols;
@@ -321,19 +343,34 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       };
       if (p.add) load(0);
-      if (tl.rows > 0) {
-        ok = tc::mbar_wait_warp(&dfull[d], dph, abort);
+      const uint32_t sums = tmem + ((uint32_t)(q * 32) << 16) + d * 256 + part * kDwCols;
+      const uint32_t more = tmem + ((uint32_t)(q * 32) << 16) + (d ^ 1u) * 256 + part * kDwCols;
+      if (tl.rows > 0) wait(d);
+      for (int r = kDwChunk<PL>; r < tl.rows && ok; r += kDwChunk<PL>) {  // chunks behind the first
+        wait(d ^ 1u);
         if (!ok) break;
-        tc::fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < kDwCols; c += 32) {
+          uint32_t v[32], u[32];
+          tc::tmem_ld32(sums + c, u);
+          tc::tmem_ld32(more + c, v);
+          tc::tmem_ld_wait(u);
+          tc::tmem_ld_wait(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) + __uint_as_float(v[i]));
+          tc::tmem_st32(sums + c, u);
+        }
+        tc::tmem_st_wait();
+        read_out(d ^ 1u);
       }
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + d * 256 + part * kDwCols;
+      if (!ok) break;
 #pragma unroll
       for (int w = 0; w < kWins; ++w) {
         if (w >= nwin) break;
         __syncwarp();  // TMEM loads are a whole warp's
         uint32_t v[32];
         if (tl.rows > 0) {
-          tc::tmem_ld32(taddr + 32 * w, v);
+          tc::tmem_ld32(sums + 32 * w, v);
           tc::tmem_ld_wait(v);
         } else {
 #pragma unroll
@@ -360,10 +397,8 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
             __stcs(reinterpret_cast<float4*>(p.dw + at + (size_t)(i * 4) * p.N + w * 32), o[i]);
       }
       if (tl.rows > 0) {
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(tc::cluster_addr(&dempty[d], 0));
-        if (++d == 2) { d = 0; dph ^= 1u; }
+        read_out(d);
+        d ^= 1u;
       }
     }
     if (!ok && lane == 0) {

@@ -417,9 +417,371 @@ class F8Case(Case):
 
 @pytest.mark.parametrize("pow2", [0, 1])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", SHAPES)
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", [s for s in SHAPES if s[3] % 16 == 0])
 def test_expert_matmul_f8(T, K, E, n_in, n_out, kind, dt, pow2):
     c = F8Case(T, K, E, n_in, n_out, dt, kind, pow2=pow2)
     out = c.run()
     c.check(out)
     same(c.run(src=False), out)
+
+
+# ------------------------------------------------------------------ what the tiles must keep apart
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,n_in,n_out", [(200, 136, 72), (700, 520, 264), (40, 1000, 104)])
+def test_an_expert_that_is_not_finite_stays_alone(T, n_in, n_out, dt):
+    """Infinities and NaN in one expert's rows or weights reach no other expert's results."""
+    c = Case(T, 1, 5, n_in, n_out, dt, "skew", seed=9)
+    c.off = torch.tensor([0, T // 4 + 3, T // 2 + 1, T // 2 + 8, T - 5, T], dtype=torch.int32, device="cuda")
+    o = c.off.tolist()
+    c.inside[:] = True
+    x, dy, w = c.rows(n_in), c.rows(n_out), c.weights()
+    clean = c.out(n_out), c.out(n_in), torch.empty(5, n_out, n_in, device="cuda")
+    dirty = c.out(n_out), c.out(n_in), torch.empty(5, n_out, n_in, device="cuda")
+    for bad in range(5):
+        s = slice(o[bad], o[bad + 1])
+        for out, spoil in ((clean, False), (dirty, True)):
+            x_, dy_, w_ = x.clone(), dy.clone(), w.clone()
+            if spoil:
+                for t in (x_[s], dy_[s], w_[bad]):
+                    t[...] = math.nan
+                    t.view(-1)[::3] = math.inf
+            smoe.smoe_expert_matmul(c.desc, x_, c.off, w_, out[0], c.ws)
+            smoe.smoe_expert_matmul_dx(c.desc, dy_, w_, c.off, out[1], c.ws)
+            smoe.smoe_expert_matmul_dw(c.desc, dy_, x_, c.off, out[2], c.ws)
+        keep = torch.ones(T, dtype=torch.bool, device="cuda")
+        keep[s] = False
+        same(dirty[0][keep], clean[0][keep])
+        same(dirty[1][keep], clean[1][keep])
+        others = [e for e in range(5) if e != bad]
+        same(dirty[2][others], clean[2][others])
+        assert not dirty[0][s].isfinite().any() and not dirty[2][bad].isfinite().any()
+
+
+@pytest.mark.parametrize("T", [60, 900])
+def test_f8_expert_that_is_not_finite_stays_alone(T):
+    c = F8Case(T, 1, 5, 272, 200, "f32", "skew", seed=9)
+    clean, o = c.run(), c.off.tolist()
+    bad = max(range(5), key=lambda e: o[e + 1] - o[e])
+    c.wq.view(torch.uint8)[bad] = 0x7f      # NaN
+    c.sw[bad] = math.inf
+    dirty = c.run()
+    keep = torch.ones(c.R, dtype=torch.bool, device="cuda")
+    keep[o[bad]:o[bad + 1]] = False
+    same(dirty[keep], clean[keep])
+    # a token whose scale is NaN: its rows alone
+    c = F8Case(T, 1, 5, 272, 200, "f32", "skew", seed=9)
+    c.s[3, 1] = math.nan
+    dirty = c.run()
+    hit = c.src == 3
+    same(dirty[~hit], clean[~hit])
+    assert dirty[hit & c.inside].isnan().all()
+
+
+# ------------------------------------------------------------------ bad data, empty batches
+def test_bad_offsets_write_nothing():
+    for dt in ("bf16", "f32"):
+        for bad in ([0, 40, 30, 60], [0, 20, 40, 61], [-1, 20, 40, 60]):
+            c = Case(60, 1, 3, 64, 128, dt, "even")
+            x, dy, w = c.rows(64), c.rows(128), c.weights()
+            off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+            out, dx, dw = c.out(128), c.out(64), torch.full((3, 128, 64), 7.0, device="cuda")
+            for call in (lambda: smoe.smoe_expert_matmul(c.desc, x, off, w, out, c.ws),
+                         lambda: smoe.smoe_expert_matmul_dx(c.desc, dy, w, off, dx, c.ws),
+                         lambda: smoe.smoe_expert_matmul_dw(c.desc, dy, x, off, dw, c.ws)):
+                call()
+                with pytest.raises(smoe.SmoeError, match="SMOE_ERR_DATA"):
+                    smoe.smoe_get_status(c.ws)
+            assert (out == 7).all() and (dx == 7).all() and (dw == 7).all()
+    f = F8Case(60, 1, 3, 64, 128, "bf16", "even")
+    f.off = torch.tensor([0, 40, 30, 60], dtype=torch.int32, device="cuda")
+    assert (f.run() == 7).all()
+    with pytest.raises(smoe.SmoeError, match="SMOE_ERR_DATA"):
+        smoe.smoe_get_status(f.ws)
+
+
+@pytest.mark.parametrize("T", [30, 600])
+def test_bad_row_src(T):
+    """An entry out of range gives a zero row and an error in the status; the others stay."""
+    f = F8Case(T, 2, 4, 256, 264, "bf16", "even")
+    good = f.run()
+    smoe.smoe_get_status(f.ws)
+    keep = f.src.clone()
+    f.src[[5, 11, 2 * T - 1]] = torch.tensor([-1, T, 1 << 30], dtype=torch.int32, device="cuda")
+    hit = f.src != keep
+    bad = f.run()
+    with pytest.raises(smoe.SmoeError, match="SMOE_ERR_DATA"):
+        smoe.smoe_get_status(f.ws)
+    same(bad[~hit], good[~hit])
+    assert (bad[hit] == 0).all()
+    for dt in ("bf16", "f32"):
+        c = Case(T, 2, 4, 256, 264, dt, "even")
+        dy, dw, want = c.rows(264), torch.empty(4, 264, 256, device="cuda"), torch.empty(4, 264, 256, device="cuda")
+        smoe.smoe_expert_matmul_dw_f8(c.desc, dy, f.q, f.s, c.off, dw, c.ws, row_src=f.src)
+        with pytest.raises(smoe.SmoeError, match="SMOE_ERR_DATA"):
+            smoe.smoe_get_status(c.ws)
+        dy[hit] = 0.0
+        smoe.smoe_expert_matmul_dw_f8(c.desc, dy, f.q, f.s, c.off, want, c.ws, row_src=keep)
+        same(dw, want)
+
+
+def test_empty_batches():
+    for dt in ("bf16", "f32"):
+        d0 = smoe.make_desc(0, 64, 3, 1, 1, 128, 0, 1, 1, dt)
+        ws, e = smoe.workspace_products(d0), torch.empty(0, 64, dtype=DT[dt], device="cuda")
+        y, w = torch.empty(0, 128, dtype=DT[dt], device="cuda"), torch.ones(3, 128, 64, dtype=DT[dt], device="cuda")
+        off = torch.zeros(4, dtype=torch.int32, device="cuda")
+        smoe.smoe_expert_matmul(d0, e, off, w, y, ws)
+        smoe.smoe_expert_matmul_dx(d0, y, w, off, e, ws)
+        dw, add = torch.full((3, 128, 64), 7.0, device="cuda"), torch.rand(3, 128, 64, device="cuda")
+        smoe.smoe_expert_matmul_dw(d0, y, e, off, dw, ws)
+        assert (dw == 0).all()
+        smoe.smoe_expert_matmul_dw(d0, y, e, off, dw, ws, add=add)
+        same(dw, add)
+        q, s = torch.empty(0, 64, dtype=F8, device="cuda"), torch.empty(0, 1, device="cuda")
+        smoe.smoe_rows_f8(d0, e, q, s)
+        smoe.smoe_expert_matmul_dw_f8(d0, y, q, s, off, dw, ws, row_src=off)
+        assert (dw == 0).all()
+        smoe.smoe_swiglu_f8(d0, e, e, h=e, g8=q, g8_scale=s)
+        smoe.smoe_swiglu_grad_f8(d0, e, q, s, q, s, e, e)
+        # tokens, and none of their rows on any expert
+        c = Case(9, 1, 3, 64, 128, dt, "even")
+        x, dy = c.rows(64), c.rows(128)
+        x[:] = math.nan
+        dy[:] = math.nan
+        out = c.out(128)
+        smoe.smoe_expert_matmul(c.desc, x, off, w, out, c.ws)
+        assert (out == 7).all()
+        smoe.smoe_expert_matmul_dw(c.desc, dy, x, off, dw, c.ws, add=add)
+        same(dw, add)
+        smoe.smoe_get_status(c.ws)
+
+
+# ------------------------------------------------------------------ streams, graphs, long offsets
+class Step:
+    """A training step of the experts' FFN from a batch of tokens, as a program runs it: dispatch, up
+    products, SwiGLU kept in 8 bits, down product, combine; and back, with every gradient."""
+
+    def __init__(self, T, d, E, K, F, dt, seed=0):
+        g = gen(seed + T + d + F)
+        t = DT[dt]
+        self.T, self.d, self.E, self.K, self.F, self.dt = T, d, E, K, F, dt
+        R = T * K
+        self.desc = smoe.make_desc(T, d, E, K, 1, F, 0, 1, 1, dt)
+        self.ws, self.wp = smoe.workspace(self.desc), smoe.workspace_products(self.desc)
+        self.x = randn(g, T, d).to(t)
+        self.idx = torch.stack([torch.randperm(E, generator=g, device="cuda")[:K] for _ in range(T)]).int()
+        self.w = torch.softmax(randn(g, T, K), -1)
+        self.w1, self.w3 = ((randn(g, E, F, d) / math.sqrt(d)).to(t) for _ in range(2))
+        self.w2 = (randn(g, E, d, F) / math.sqrt(F)).to(t)
+        self.dout = (randn(g, T, d) * 0.1).to(t)
+        i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        n = lambda *s, dtype=t: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
+        self.off, self.pair, self.tok = i(E + 1), i(T, K), i(R)
+        self.xd, self.y, self.dyd = n(R, d), n(R, d), n(R, d)
+        self.g, self.u, self.h, self.dh, self.dg, self.du, self.h2 = (n(R, F) for _ in range(7))
+        self.x8, self.xs = n(T, d, dtype=F8), n(T, blocks(d), dtype=torch.float32)
+        self.g8, self.u8 = n(R, F, dtype=F8), n(R, F, dtype=F8)
+        self.gs, self.us = (n(R, blocks(F), dtype=torch.float32) for _ in range(2))
+        self.out, self.dxd = n(T, d), n(R, d)
+        self.dw1, self.dw3 = (n(E, F, d, dtype=torch.float32) for _ in range(2))
+        self.dw2 = n(E, d, F, dtype=torch.float32)
+
+    def forward(self):
+        smoe.smoe_dispatch(self.desc, self.idx, self.off, self.pair, self.tok, self.ws, x_src=self.x, x_disp=self.xd)
+        smoe.smoe_rows_f8(self.desc, self.x, self.x8, self.xs, pow2=1)
+        smoe.smoe_expert_matmul(self.desc, self.xd, self.off, self.w1, self.g, self.wp)
+        smoe.smoe_expert_matmul(self.desc, self.xd, self.off, self.w3, self.u, self.wp)
+        smoe.smoe_swiglu_f8(self.desc, self.g, self.u, h=self.h, g8=self.g8, g8_scale=self.gs, u8=self.u8,
+                            u8_scale=self.us)
+        smoe.smoe_expert_matmul(self.desc, self.h, self.off, self.w2, self.y, self.wp)
+        smoe.smoe_combine(self.desc, self.y, self.pair, self.w, self.out, self.ws)
+
+    def backward(self):
+        """dy of each row is its token's gradient times its weight."""
+        wr = torch.empty(self.T * self.K, device="cuda")
+        wr[self.pair.view(-1).long()] = self.w.view(-1)
+        self.dyd.copy_((self.dout.float()[self.tok.long()] * wr[:, None]))
+        smoe.smoe_expert_matmul_dx(self.desc, self.dyd, self.w2, self.off, self.dh, self.wp)
+        smoe.smoe_swiglu_grad_f8(self.desc, self.dh, self.g8, self.gs, self.u8, self.us, self.dg, self.du, h=self.h2)
+        smoe.smoe_expert_matmul_dw(self.desc, self.dyd, self.h2, self.off, self.dw2, self.wp)
+        smoe.smoe_expert_matmul_dw_f8(self.desc, self.dg, self.x8, self.xs, self.off, self.dw1, self.wp, row_src=self.tok)
+        smoe.smoe_expert_matmul_dw_f8(self.desc, self.du, self.x8, self.xs, self.off, self.dw3, self.wp, row_src=self.tok)
+        smoe.smoe_expert_matmul_dx(self.desc, self.dg, self.w1, self.off, self.dxd, self.wp, dy2=self.du, w2=self.w3)
+
+    def outputs(self):
+        return [self.out, self.dw1, self.dw3, self.dw2, self.dxd]
+
+    def check(self):
+        """Against autograd in 64 bits: the 8-bit values are off by up to 2^-4, so a sum of n terms that
+        carry independent such errors is off by about 2^-4 / sqrt(3) of its terms' root sum of
+        squares; five of those (the largest of 10^5 values lies at 4.4)."""
+        T, K, E = self.T, self.K, self.E
+        x, w1, w3, w2 = (t.double().requires_grad_() for t in (self.x, self.w1, self.w3, self.w2))
+        out = torch.zeros(T, self.d, dtype=F64, device="cuda")
+        for e in range(E):
+            t, k = torch.nonzero(self.idx == e, as_tuple=True)
+            if len(t):
+                g, u = x[t] @ w1[e].T, x[t] @ w3[e].T
+                out = out.index_add(0, t, ((g * torch.sigmoid(g) * u) @ w2[e].T) * self.w[t, k].double()[:, None])
+        out.backward(self.dout.double())
+        rel = lambda a, b: float((a.double() - b).norm() / b.norm())  # noqa: E731
+        step = 2.0 ** -8 if self.dt == "bf16" else 2.0 ** -20
+        assert rel(self.out, out.detach()) <= 4 * step
+        # each term of a gradient carries the relative errors of at most three 8-bit values (x, g and
+        # u; dg carries g twice): their norm is within 4 x 2^-4 / sqrt(3) of the gradient's own
+        tol = 4 * 2.0 ** -4 / math.sqrt(3) + 8 * step
+        assert rel(self.dw1, w1.grad) <= tol and rel(self.dw3, w3.grad) <= tol
+        assert rel(self.dw2, w2.grad) <= tol
+        dx = torch.zeros_like(x).index_add(0, self.tok.long(), self.dxd.double())
+        assert rel(dx, x.grad) <= tol
+        smoe.smoe_get_status(self.wp)
+        smoe.smoe_get_status(self.ws)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,K,F", [(64, 128, 8, 2, 256), (300, 272, 24, 3, 144), (1024, 512, 4, 2, 384)])
+def test_training_step(T, d, E, K, F, dt):
+    c = Step(T, d, E, K, F, dt)
+    c.forward()
+    c.backward()
+    c.check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_captured_step_and_two_streams(dt):
+    """Both passes replayed from a graph on new inputs, and two steps on two streams at once, each
+    with its own workspaces, give the eager step's bits."""
+    a, b = Step(300, 256, 12, 2, 272, dt), Step(280, 256, 12, 2, 272, dt, seed=5)
+    want = []
+    for c in (a, b):
+        c.forward()
+        c.backward()
+        want.append([o.clone() for o in c.outputs()])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for c, s in zip((a, b), streams):
+            for o in c.outputs():
+                o.fill_(3.0)
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                c.forward()
+                c.backward()
+        torch.cuda.synchronize()
+        for c, w in zip((a, b), want):
+            for o, v in zip(c.outputs(), w):
+                same(o, v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.forward()
+        a.backward()
+    for o in a.outputs():
+        o.fill_(3.0)
+    graph.replay()
+    for o, v in zip(a.outputs(), want[0]):
+        same(o, v)
+    a.x.copy_(a.x.flip(0))
+    a.idx.copy_(a.idx.flip(0))
+    graph.replay()
+    got = [o.clone() for o in a.outputs()]
+    a.forward()
+    a.backward()
+    for o, v in zip(a.outputs(), got):
+        same(o, v)
+    smoe.smoe_get_status(a.wp)
+
+
+def test_f8_ffn_from_its_parts():
+    """Tokens in 8 bits, gate and up products, SwiGLU to 8 bits, down product: the forward pass on
+    8-bit weights, against 64 bits of the same quantised values."""
+    T, d, E, K, F = 200, 384, 6, 2, 272
+    up, down = F8Case(T, K, E, d, F, "bf16", "even"), F8Case(T, K, E, F, d, "bf16", "even")
+    g, u = up.run(), None
+    wq, sw = f8(randn(up.g, E, F, d) * 60), up.sw * 0.7
+    u = up.out(F)
+    smoe.smoe_expert_matmul_f8(up.desc, up.q, up.s, up.off, wq, sw, u, up.ws, row_src=up.src)
+    h8 = torch.empty(T * K, F, dtype=F8, device="cuda")
+    hs = torch.empty(T * K, blocks(F), device="cuda")
+    smoe.smoe_swiglu_f8(up.desc, g, u, h8=h8, h8_scale=hs, pow2=0)
+    y = down.out(d)
+    smoe.smoe_expert_matmul_f8(down.desc, h8, hs, down.off, down.wq, down.sw, y, down.ws)
+    h = h8.double() * spread(hs, F)
+    ref, mag = torch.zeros(2, T * K, d, dtype=F64, device="cuda")
+    for e, s in enumerate(down.seg):
+        w = down.wq[e].double() * spread(down.sw[e].repeat_interleave(128, 0)[:d], F)
+        ref[s], mag[s] = h[s] @ w.T, h[s].abs() @ w.abs().T
+    down.check_rows(y, ref, mag, F / 32 + blocks(F) + 8)
+    G, U = g.double(), u.double()
+    hr = G * torch.sigmoid(G) * U
+    within(h, hr, hr.abs() * (2.0 ** -4 + 2.0 ** -19) + spread(hs, F) * 2.0 ** -9)
+
+
+def test_offsets_past_32_bits():
+    """Rows and weights whose elements pass 2^31, and bytes 2^32."""
+    d, T = 8192, 270000  # 2.2e9 elements of a matrix of rows
+    desc = smoe.make_desc(T, d, 2, 1, 1, 16, 0, 1, 1, "bf16")
+    g = gen(3)
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    q, s = torch.empty(T, d, dtype=F8, device="cuda"), torch.empty(T, blocks(d), device="cuda")
+    smoe.smoe_rows_f8(desc, x, q, s, pow2=1)
+    rows = torch.tensor([0, 1, 131071, 262143, 262144, T - 2, T - 1], device="cuda")
+    rs, v = rows_ref(x[rows], 1)
+    same(s[rows], rs)
+    same(q[rows].view(torch.uint8), f8(v).view(torch.uint8))
+    off = torch.tensor([0, 150001, T], dtype=torch.int32, device="cuda")
+    w = (randn(g, 2, 16, d) / math.sqrt(d)).bfloat16()
+    ws, y = smoe.workspace_products(desc), torch.empty(T, 16, dtype=torch.bfloat16, device="cuda")
+    e = (rows >= 150001).long()
+    smoe.smoe_expert_matmul(desc, x, off, w, y, ws)
+    ref = torch.einsum("rd,rnd->rn", x[rows].double(), w[e].double())
+    mag = torch.einsum("rd,rnd->rn", x[rows].double().abs(), w[e].double().abs())
+    within(y[rows], ref, HALF["bf16"] * ref.abs() + adds16(d) * 2.0 ** -23 * mag)
+    wq, sw = f8(randn(g, 2, 16, d) * 60), torch.rand(2, 1, blocks(d), generator=g, device="cuda") * 1e-3
+    smoe.smoe_expert_matmul_f8(desc, q, s, off, wq, sw, y, ws)
+    ww = wq.double() * spread(sw.expand(2, 16, -1), d)
+    xx = q[rows].double() * spread(s[rows], d)
+    ref = torch.einsum("rd,rnd->rn", xx, ww[e])
+    mag = torch.einsum("rd,rnd->rn", xx.abs(), ww[e].abs())
+    within(y[rows], ref, HALF["bf16"] * ref.abs() + (d / 32 + blocks(d) + 8) * 2.0 ** -23 * mag)
+    dx = torch.empty_like(x)
+    smoe.smoe_expert_matmul_dx(desc, y, w, off, dx, ws)
+    ref = torch.einsum("rn,rnd->rd", y[rows].double(), w[e].double())
+    mag = torch.einsum("rn,rnd->rd", y[rows].double().abs(), w[e].double().abs())
+    within(dx[rows], ref, HALF["bf16"] * ref.abs() + adds16(16) * 2.0 ** -23 * mag)
+    dw = torch.empty(2, 16, d, device="cuda")
+    smoe.smoe_expert_matmul_dw(desc, y, x, off, dw, ws)
+    got = dw.clone()
+    for i, sl in enumerate((slice(0, 150001), slice(150001, T))):
+        ref, mag = torch.zeros(2, 16, d, dtype=F64, device="cuda")
+        for a in range(sl.start, sl.stop, 20000):
+            b = min(a + 20000, sl.stop)
+            ref += y[a:b].double().T @ x[a:b].double()
+            mag += y[a:b].double().abs().T @ x[a:b].double().abs()
+        # within a chunk of 1024 rows 64 additions of the tensor core, and the chunks' own
+        n = 1024 / 16 + 150000 / 1024 + 24
+        within(got[i], ref, n * 2.0 ** -23 * mag)
+    smoe.smoe_expert_matmul_dw_f8(desc, y, q, s, off, dw, ws)
+    h = torch.empty_like(x)
+    smoe.smoe_swiglu_f8(desc, x, dx, h=h, g8=q, g8_scale=s, pow2=1)
+    G, U = x[rows].double(), dx[rows].double()
+    ref = G * torch.sigmoid(G) * U
+    within(h[rows], ref, swiglu_tol("bf16") * ref.abs() + 1e-38)
+    smoe.smoe_get_status(ws)
+
+
+@pytest.mark.parametrize("rows", [5000, 40000])
+def test_long_sums_do_not_drift(rows):
+    """One expert with many rows: the error stays that of its chunks (1024 rows, 64 additions
+    cut off at 24 bits: 64 x 2^-24 of the running sum on average) and of their rounded sum."""
+    c = Case(rows, 1, 2, 128, 136, "bf16", "one")
+    dy, x = c.rows(136), c.rows(128)
+    dw = torch.empty(2, 136, 128, device="cuda")
+    smoe.smoe_expert_matmul_dw(c.desc, dy, x, c.off, dw, c.ws)
+    ref = dy.double().T @ x.double()
+    assert float((dw[1].double() - ref).norm() / ref.norm()) <= 64 * 2.0 ** -24
+    assert (dw[0] == 0).all()
+    f = Case(rows, 1, 2, 128, 136, "f32", "one")
+    dy, x = f.rows(136), f.rows(128)
+    smoe.smoe_expert_matmul_dw(f.desc, dy, x, f.off, dw, f.ws)
+    ref = dy.double().T @ x.double()
+    assert float((dw[1].double() - ref).norm() / ref.norm()) <= 64 * 2.0 ** -24
