@@ -62,7 +62,8 @@ __device__ __forceinline__ DwTile dw_decode(const DwArgs& p, const int32_t* off,
   return r;
 }
 
-// The rows [left, the next multiple of 16) of a stage become zeros, by a warp.
+// The rows [left, the next multiple of 16) of a stage become zeros, by a warp, which orders them
+// before the async proxy afterwards.
 __device__ __forceinline__ void dw_clear(uint8_t* a, uint8_t* b, int left, int lane) {
   for (int i = left * 8 + lane; i < ((left + 15) & ~15) * 8; i += 32)  // 16 bytes each
 #pragma unroll
@@ -70,8 +71,6 @@ __device__ __forceinline__ void dw_clear(uint8_t* a, uint8_t* b, int left, int l
       *reinterpret_cast<uint4*>(a + j * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(b + j * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
 }
 
 // PL = 3: fp32 operands as three bf16 planes each, [3][TK][channels], whose sum they are: the six
@@ -241,6 +240,10 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
             ok = tc::mbar_wait_warp_shared(&full[s], ph, abort);
             if (!ok) break;
             dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, left, lane);
+            if (i == PL - 1) {
+              tc::fence_async_shared();
+              __syncwarp();
+            }
           } else if (i > 0 || !in) {
             ok = tc::mbar_wait_warp(&full[s], ph, abort);
             if (!ok) break;
@@ -291,14 +294,19 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       const DwTile tl = dw_decode(p, s_off, t);
       it += PL * ((tl.rows + 63) >> 6);
       if ((tl.rows & 15) == 0) continue;
-      for (int i = PL; i > 0 && ok; --i) {
+      for (int i = PL; i > 0; --i) {
         const uint32_t s = (it - i) % kDwStages;
         ok = tc::mbar_wait_warp(&last[s], lph >> s & 1u, abort);
         if (!ok) break;
         lph ^= 1u << s;
         dw_clear(sA + s * kDwHalf, sB + s * kDwHalf, tl.rows & 63, lane);
-        if (lane == 0) tc::mbar_arrive_cluster_shared(tc::cluster_addr(&full[s], 0));
       }
+      if (!ok) break;
+      tc::fence_async_shared();
+      __syncwarp();
+      if (lane == 0)
+        for (int i = PL; i > 0; --i)
+          tc::mbar_arrive_cluster_shared(tc::cluster_addr(&full[(it - i) % kDwStages], 0));
     }
     if (!ok && lane == 0) {
       *abort = 1;
@@ -537,29 +545,28 @@ __global__ void __launch_bounds__(256)
 split_rows_kernel(const float* a, const float* b, int na, int nb, uint4* pa, uint4* pb,
                   const int32_t* expert_off, int E, int TK) {
   pdl_wait_and_trigger();
-  const int begin = max(expert_off[0], 0), end = min(expert_off[E], TK);
   const int va = na >> 3, vb = nb >> 3;
-  for (int r = begin + blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8)
-    for (int v = threadIdx.x & 31; v < va + vb; v += 32) {
-      const bool first = v < va;
-      const int n = first ? va : vb, c = first ? v : v - va;
-      const float4* from = reinterpret_cast<const float4*>(first ? a : b) + ((size_t)r * n + c) * 2;
-      const float4 x0 = __ldcg(from), x1 = __ldcg(from + 1);
-      float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-      uint4* to = (first ? pa : pb) + (size_t)r * n + c;
+  const long long it = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int r = (int)(it / (va + vb)), v = (int)(it - (long long)r * (va + vb));
+  if (r < max(expert_off[0], 0) || r >= min(expert_off[E], TK)) return;
+  const bool first = v < va;
+  const int n = first ? va : vb, c = first ? v : v - va;
+  const float4* from = reinterpret_cast<const float4*>(first ? a : b) + ((size_t)r * n + c) * 2;
+  const float4 x0 = __ldcg(from), x1 = __ldcg(from + 1);
+  float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  uint4* to = (first ? pa : pb) + (size_t)r * n + c;
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        float y[8];
+  for (int pl = 0; pl < 3; ++pl) {
+    float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
-          if (__hisinf(h)) h = __float2bfloat16_rz(x[i]);
-          y[i] = __bfloat162float(h);
-          x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] - y[i] : 0.0f;
-        }
-        to[(size_t)pl * TK * n] = pack16(y, (const __nv_bfloat16*)nullptr);
-      }
+    for (int i = 0; i < 8; ++i) {
+      __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
+      if (__hisinf(h)) h = __float2bfloat16_rz(x[i]);
+      y[i] = __bfloat162float(h);
+      x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] - y[i] : 0.0f;
     }
+    to[(size_t)pl * TK * n] = pack16(y, (const __nv_bfloat16*)nullptr);
+  }
 }
 
 // From this many multiply-adds on an fp32 weight gradient runs on the tensor cores.
@@ -576,12 +583,13 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
   if (d.dtype != SMOE_F32) return run_dw<1>(dy, x, p, s);
   const float *fy = static_cast<const float*>(dy), *fx = static_cast<const float*>(x);
   // (the planes' place is the descriptor's)
-  if (n_out > wide || n_in > wide || (double)TK * n_out * n_in < kPlaneMacs || 3LL * TK > INT_MAX / 2)
+  if (n_out > wide || n_in > wide || (double)TK * n_out * n_in < kPlaneMacs || 3LL * TK > INT_MAX / 2 ||
+      (long long)TK * (n_out / 8 + n_in / 8) > INT_MAX)
     return launch_expert_dw_f32(d, n_out, n_in, fy, fx, expert_off, add, dw, st, s);
   ProductLayout L;
   product_ws_layout(d, &L);
   uint4 *pa = ws_ptr<uint4>(ws, L.planes_a), *pb = ws_ptr<uint4>(ws, L.planes_b);
-  SMOE_LAUNCH(split_rows_kernel, std::min(ceil_div(TK, 8), 152 * 8), 256, 0, s, fy, fx, n_out, n_in, pa, pb,
+  SMOE_LAUNCH(split_rows_kernel, ceil_div((long long)TK * (n_out / 8 + n_in / 8), 256), 256, 0, s, fy, fx, n_out, n_in, pa, pb,
               expert_off, d.E, TK);
   return run_dw<3>(pa, pb, p, s);
 }
