@@ -547,8 +547,14 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
   if (warp == 2) tc::tmem_dealloc(tmem, 512);
 }
 
-// From this many rows an expert on average the wide tiles.
-constexpr int kWideRows = 48;
+// From this many rows an expert on average the wide tiles, where they are enough to go round: a
+// weight passes once for 128 rows, not 64, and the epilogue's work is shared by eight warps.
+// Measured (us, wide and narrow; rows an expert): 160 experts of 5120 to 1536 channels, 2: 177 and
+// 171, 8: 208 and 206, 16: 211 and 213, 32: 216 and 238, 64: 217 and 344; 8 of 4096 to 14336, 2: 74
+// and 71, 8: 79 and 82, 16: 80 and 97, 64: 83 and 153; 128 of 2048 to 768, 4: 44 and 40, 8: 45 and
+// 47, 32: 48 and 56. One expert of 5120 to 5120 (20 wide tiles for 152 SMs), 16: 27 and 15, 64: 26
+// and 23.
+constexpr int kWideRows = 12, kWideRowsAnyhow = 96;
 
 template <bool WIDE, typename TO>
 cudaError_t run_f8(const F8Args& p, const void* wq, long long tile_bound, cudaStream_t s) {
@@ -575,7 +581,8 @@ cudaError_t launch_expert_matmul_f8(const smoe_desc& d, int n_out, int n_in, con
   const int TK = d.T * d.K;
   const F8Args p{static_cast<const uint8_t*>(xq), xs, row_src, expert_off, w_scale, out,
                  static_cast<DeviceStatus*>(ws), d.E, TK, row_src ? d.T : TK, n_out, n_in};
-  const bool wide = (long long)TK >= (long long)kWideRows * d.E;
+  const long long few = (long long)std::max(d.E, ceil_div(TK, 128)) * ceil_div(n_out, 256);
+  const bool wide = (long long)TK >= (long long)(2 * few >= device_sms() ? kWideRows : kWideRowsAnyhow) * d.E;
   // no more tiles than this, whatever the rows' spread over the experts
   const long long bound = ((long long)ceil_div(TK, wide ? 128 : 64) + std::min(TK, d.E)) *
                           ceil_div(n_out, wide ? 256 : 128);

@@ -569,8 +569,12 @@ split_rows_kernel(const float* a, const float* b, int na, int nb, uint4* pa, uin
   }
 }
 
-// From this many multiply-adds on an fp32 weight gradient runs on the tensor cores.
-constexpr double kPlaneMacs = 2e8;
+// From this many rows an expert and multiply-adds on an fp32 weight gradient runs on the tensor
+// cores. Measured (us, planes and CUDA cores; rows an expert): 24 experts of 1416 x 1000, 8: 43 and
+// 38, 16: 44 and 51, 128: 89 and 255; 8 of 512 x 512, 32: 14 and 10, 64: 15 and 18, 128: 20 and 32; 4
+// of 256 x 256, 128: 17 and 15.
+constexpr int kPlaneRows = 16;
+constexpr double kPlaneMacs = 1e8;
 
 }  // namespace
 
@@ -583,7 +587,8 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
   if (d.dtype != SMOE_F32) return run_dw<1>(dy, x, p, s);
   const float *fy = static_cast<const float*>(dy), *fx = static_cast<const float*>(x);
   // (the planes' place is the descriptor's)
-  if (n_out > wide || n_in > wide || (double)TK * n_out * n_in < kPlaneMacs || 3LL * TK > INT_MAX / 2 ||
+  if (n_out > wide || n_in > wide || (double)TK * n_out * n_in < kPlaneMacs ||
+      (long long)TK < (long long)kPlaneRows * d.E || 3LL * TK > INT_MAX / 2 ||
       (long long)TK * (n_out / 8 + n_in / 8) > INT_MAX)
     return launch_expert_dw_f32(d, n_out, n_in, fy, fx, expert_off, add, dw, st, s);
   ProductLayout L;
