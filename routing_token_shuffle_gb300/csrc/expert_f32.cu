@@ -22,6 +22,8 @@ struct F32Args {
   const int32_t* expert_off;
   DeviceStatus* st;
   int E, TK, n_out, n_in;
+  int slices;        // of the contraction (tiles): each slice's sums in a matrix of their own
+  long long size;    // floats of such a matrix
 };
 
 // Row tiles of each expert (fixed > 0: that many for each; s_ts, prefix) and their first rows
@@ -223,11 +225,14 @@ struct TileSmem {
 
 struct F32Tile {
   int g, m0, n0, row0, M, K1, nk1, nk;
+  int k0, slice;     // the slice's first stage, and its number
 };
 
 template <int KIND>
 __device__ __forceinline__ F32Tile f32_decode(const F32Args& p, const int32_t* ts, const int32_t* off,
                                               int ntile, int t, int& g) {
+  const int slice = t % p.slices;
+  t /= p.slices;
   while (ts[g + 1] * ntile <= t) ++g;
   const int mt = ts[g + 1] - ts[g], local = t - ts[g] * ntile;
   const int n_tile = local / mt;
@@ -240,7 +245,10 @@ __device__ __forceinline__ F32Tile f32_decode(const F32Args& p, const int32_t* t
   r.M = KIND == 2 ? p.n_out : rows;
   r.K1 = KIND == 0 ? p.n_in : KIND == 1 ? p.n_out : rows;
   r.nk1 = (r.K1 + kBK - 1) / kBK;
-  r.nk = KIND == 1 && p.a2 ? 2 * r.nk1 : r.nk1;
+  const int nk = KIND == 1 && p.a2 ? 2 * r.nk1 : r.nk1, step = (nk + p.slices - 1) / p.slices;
+  r.slice = slice;
+  r.k0 = min(nk, slice * step);
+  r.nk = min(nk - r.k0, step);
   return r;
 }
 
@@ -258,7 +266,7 @@ tiled_f32_kernel(const F32Args p) {
   if (tid < 32) f32_table(p, kBM, KIND == 2 ? (p.n_out + kBM - 1) / kBM : 0, s_ts, s_off, tid);
   __syncthreads();
   const int N = KIND == 0 ? p.n_out : p.n_in, ntile = (N + kBN - 1) / kBN;
-  const int total = s_ts[p.E] * ntile;
+  const int total = s_ts[p.E] * ntile * p.slices;
   const int tx = tid & 15, ty = tid >> 4;  // columns tx * 4 + {0, 64}; rows ty * 4 + {0 .. 3}
 
   // the copies' own walk over (tile, 16 of the contraction), ahead of the sums'
@@ -277,10 +285,10 @@ tiled_f32_kernel(const F32Args p) {
       fresh = true;
     }
     if (lt < total) {
-      const bool second = lk >= ld.nk1;
+      const bool second = ld.k0 + lk >= ld.nk1;
       const float* a = second ? p.a2 : p.a;
       const float* b = second ? p.b2 : p.b;
-      const int k0 = (second ? lk - ld.nk1 : lk) * kBK;
+      const int k0 = (ld.k0 + lk - (second ? ld.nk1 : 0)) * kBK;
       {
         const float* from = a;
         bool in;
@@ -343,7 +351,7 @@ tiled_f32_kernel(const F32Args p) {
       if (++slot == kRing) slot = 0;
 #pragma unroll
       for (int k = 0; k < kBK; k += 4) {
-        if (KIND == 2 && kb * kBK + k >= tl.K1) break;  // short contractions end inside a stage
+        if (KIND == 2 && (tl.k0 + kb) * kBK + k >= tl.K1) break;  // short contractions end inside a stage
         float a[4][4], b[4][8];  // [k][row], [k][column]
         if (KIND == 2) {
 #pragma unroll
@@ -386,7 +394,7 @@ tiled_f32_kernel(const F32Args p) {
     for (int i = 0; i < 4; ++i) {
       const int m = tl.m0 + ty * 4 + i;
       if (m >= tl.M) continue;
-      float* out = p.out + ((KIND == 2 ? (size_t)tl.g * p.n_out : (size_t)tl.row0) + m) * N;
+      float* out = p.out + tl.slice * p.size + ((KIND == 2 ? (size_t)tl.g * p.n_out : (size_t)tl.row0) + m) * N;
       if (KIND == 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -412,14 +420,28 @@ tiled_f32_kernel(const F32Args p) {
 }
 
 template <int KIND>
-cudaError_t run_tiled(const F32Args& p, long long tiles, cudaStream_t s) {
+cudaError_t run_tiled(F32Args p, long long tiles, long long stages, void* ws, const ProductLayout& L,
+                      cudaStream_t s) {
+  // (500 rows of one expert, 5120 to 256 channels: one slice 377 us)
+  const int row_len = KIND == 0 ? p.n_out : p.n_in;
+  const long long rows = KIND == 2 ? (long long)p.E * p.n_out : p.TK;
+  p.size = rows * row_len;
+  p.slices = slices_of(tiles, device_sms() * 3LL, stages / 4, p.size);
+  float* const out = p.out;
+  const float* const add = p.add;
+  if (p.slices > 1) {
+    p.out = ws_ptr<float>(ws, L.parts);
+    p.add = nullptr;
+  }
+
   auto kern = tiled_f32_kernel<KIND>;
   const int smem = (int)TileSmem<KIND>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<long long>(std::max<long long>(tiles, 1), (long long)device_sms() * 3);
+  const int grid = (int)std::min<long long>(std::max<long long>(tiles * p.slices, 1), (long long)device_sms() * 3);
   SMOE_LAUNCH(kern, grid, 256, smem, s, p);
-  return cudaGetLastError();
+  if (p.slices == 1) return cudaGetLastError();
+  return launch_sum_slices(p.out, p.slices, rows, row_len, KIND != 2, p.expert_off, p.E, p.TK, add, out, s);
 }
 
 // Rows an expert on average from which the tiles take over. Measured (us, tiles and streaming): 24
@@ -432,12 +454,15 @@ constexpr int kTileRows = 56;
 
 cudaError_t launch_expert_rows_f32(const smoe_desc& d, int n_out, int n_in, const float* a,
                                    const float* w, const float* a2, const float* w2, bool transposed,
-                                   const int32_t* expert_off, float* out, DeviceStatus* st, cudaStream_t s) {
+                                   const int32_t* expert_off, float* out, void* ws, cudaStream_t s) {
+  ProductLayout L;
+  product_ws_layout(d, &L);
   const int TK = d.T * d.K;
-  const F32Args p{a, w, a2, w2, nullptr, out, expert_off, st, d.E, TK, n_out, n_in};
+  const F32Args p{a, w, a2, w2, nullptr, out, expert_off, ws_ptr<DeviceStatus>(ws, L.status), d.E, TK, n_out, n_in, 1, 0};
   if ((long long)TK >= (long long)kTileRows * d.E) {
     const long long tiles = ((long long)ceil_div(TK, kBM) + std::min(TK, d.E)) * ceil_div(transposed ? n_in : n_out, kBN);
-    return transposed ? run_tiled<1>(p, tiles, s) : run_tiled<0>(p, tiles, s);
+    return transposed ? run_tiled<1>(p, tiles, ceil_div(n_out, kBK) * (a2 ? 2 : 1), ws, L, s)
+                      : run_tiled<0>(p, tiles, ceil_div(n_in, kBK), ws, L, s);
   }
   const long long passes = (long long)ceil_div(TK, kFewRows) + std::min(TK, d.E), most = (long long)device_sms() * 4;
   if (transposed) {
@@ -450,9 +475,12 @@ cudaError_t launch_expert_rows_f32(const smoe_desc& d, int n_out, int n_in, cons
 
 cudaError_t launch_expert_dw_f32(const smoe_desc& d, int n_out, int n_in, const float* dy,
                                  const float* x, const int32_t* expert_off, const float* add, float* dw,
-                                 DeviceStatus* st, cudaStream_t s) {
-  const F32Args p{dy, x, nullptr, nullptr, add, dw, expert_off, st, d.E, d.T * d.K, n_out, n_in};
-  return run_tiled<2>(p, (long long)d.E * ceil_div(n_out, kBM) * ceil_div(n_in, kBN), s);
+                                 void* ws, cudaStream_t s) {
+  ProductLayout L;
+  product_ws_layout(d, &L);
+  const int TK = d.T * d.K;
+  const F32Args p{dy, x, nullptr, nullptr, add, dw, expert_off, ws_ptr<DeviceStatus>(ws, L.status), d.E, TK, n_out, n_in, 1, 0};
+  return run_tiled<2>(p, (long long)d.E * ceil_div(n_out, kBM) * ceil_div(n_in, kBN), TK / d.E / kBK, ws, L, s);
 }
 
 }  // namespace smoe

@@ -44,14 +44,17 @@ struct DwArgs {
   DeviceStatus* st;
   int E, TK, M, N;    // M = n_out, N = n_in
   int mt, nt;         // tiles of each
+  int slices;         // of an expert's rows: each slice's sums in a matrix of their own
 };
 
 struct DwTile {
-  int e, m0, n0, row0, rows;
+  int e, m0, n0, row0, rows, slice;
 };
 
 __device__ __forceinline__ DwTile dw_decode(const DwArgs& p, const int32_t* off, int t) {
   DwTile r;
+  r.slice = t % p.slices;
+  t /= p.slices;
   const int per = p.mt * p.nt;
   r.e = t / per;
   const int in = t - r.e * per, m = in / p.nt;
@@ -59,6 +62,11 @@ __device__ __forceinline__ DwTile dw_decode(const DwArgs& p, const int32_t* off,
   r.n0 = (in - m * p.nt) * 256;
   r.row0 = off[r.e];
   r.rows = off[r.e + 1] - r.row0;
+  if (p.slices > 1) {
+    const int step = ((r.rows + p.slices - 1) / p.slices + 63) & ~63, from = min(r.rows, r.slice * step);
+    r.row0 += from;
+    r.rows = min(r.rows - from, step);
+  }
   return r;
 }
 
@@ -143,7 +151,7 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
-  const int total = *s_bad ? 0 : p.E * p.mt * p.nt;
+  const int total = *s_bad ? 0 : p.E * p.mt * p.nt * p.slices;
   volatile int* abort = s_abort;
   // A tile's columns: 256, or 128 where the matrix has no more; half of them staged by each CTA.
 
@@ -340,7 +348,7 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
       const DwTile tl = dw_decode(p, s_off, t);
       const int m0 = tl.m0 + (int)rank * 128 + q * 32, n0 = tl.n0 + part * kDwCols;
       const int mrows = min(32, p.M - m0), ncols = min(kDwCols, p.N - n0);  // may be below 1
-      const size_t at = ((size_t)tl.e * p.M + m0 + sub) * p.N + n0 + ch * 4;
+      const size_t at = (((size_t)tl.slice * p.E + tl.e) * p.M + m0 + sub) * p.N + n0 + ch * 4;
       const int nwin = mrows > 0 && ncols > 0 ? (ncols + 31) >> 5 : 0;
       float4 add[8];
       auto load = [&](int w) {
@@ -422,6 +430,32 @@ dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
 }
 
+// ------------------------------------------------------------------ slices
+// A contraction whose output tiles do not fill the GPU is cut into slices, whose sums are added here
+// in their order: the result does not depend on timing.
+__global__ void __launch_bounds__(256)
+sum_slices_kernel(const float4* parts, int slices, long long rows, int row_vecs, bool segments,
+                  const int32_t* expert_off, int E, int TK, const float4* add, float4* out) {
+  pdl_wait_and_trigger();
+  bool bad = false;
+  for (int g = threadIdx.x; g <= E; g += 256) {
+    const int lo = expert_off[g], hi = g < E ? expert_off[g + 1] : lo;
+    bad |= lo < 0 || hi < lo || hi > TK;
+  }
+  if (__syncthreads_or(bad)) return;  // the products recorded it
+  const long long first = segments ? expert_off[0] : 0, last = segments ? expert_off[E] : rows;
+  for (long long i = first * row_vecs + (long long)blockIdx.x * 256 + threadIdx.x; i < last * row_vecs;
+       i += (long long)gridDim.x * 256) {
+    float4 s = add ? add[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 t = __ldcs(parts + i);
+    for (int k = 1; k < slices; ++k) {
+      const float4 v = __ldcs(parts + k * rows * row_vecs + i);
+      t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+    }
+    out[i] = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
+  }
+}
+
 // ------------------------------------------------------------------ kept rows
 // dst[r] = q[map[r]] times its scales, in the layer's type, for the rows of the segments; a map
 // entry out of range gives a row of zeros. A warp a row, 8 values a lane at a time (stores of 512
@@ -476,6 +510,15 @@ widen_rows_kernel(const uint2* q, const float* scale, const int32_t* map, const 
 
 }  // namespace
 
+cudaError_t launch_sum_slices(const float* parts, int slices, long long rows, int row_len, bool segments,
+                              const int32_t* expert_off, int E, int TK, const float* add, float* out,
+                              cudaStream_t s) {
+  const int grid = std::min(ceil_div(rows * (row_len / 4), 256), 152 * 8);
+  SMOE_LAUNCH(sum_slices_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(parts), slices, rows, row_len / 4,
+              segments, expert_off, E, TK, reinterpret_cast<const float4*>(add), reinterpret_cast<float4*>(out));
+  return cudaGetLastError();
+}
+
 int device_sms() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -496,6 +539,7 @@ void product_ws_layout(const smoe_desc& d, ProductLayout* L) {
   const size_t planes = d.dtype == SMOE_F32 ? (size_t)d.T * d.K * std::max(d.d, d.F) * 6 : 0;
   L->planes_a = take(planes);
   L->planes_b = take(planes);
+  L->parts = take(kPartBytes);
   L->total = off;
 }
 
@@ -506,13 +550,21 @@ cudaError_t launch_expert_rows(const smoe_desc& d, int n_out, int n_in, const vo
     return launch_expert_rows_bf16(d, n_out, n_in, a, w, a2, w2, transposed, expert_off, out, ws, s);
   return launch_expert_rows_f32(d, n_out, n_in, static_cast<const float*>(a), static_cast<const float*>(w),
                                 static_cast<const float*>(a2), static_cast<const float*>(w2), transposed,
-                                expert_off, static_cast<float*>(out), static_cast<DeviceStatus*>(ws), s);
+                                expert_off, static_cast<float*>(out), ws, s);
 }
 
 namespace {
 
 template <int PL>
-cudaError_t run_dw(const void* dy, const void* x, const DwArgs& p, cudaStream_t s) {
+cudaError_t run_dw(const void* dy, const void* x, DwArgs p, float* parts, cudaStream_t s) {
+  const long long size = (long long)p.E * p.M * p.N;
+  p.slices = slices_of((long long)p.E * p.mt * p.nt, device_sms() / 2, p.TK / p.E / (PL == 1 ? 512 : 128), size);
+  float* const dw = p.dw;
+  const float* const add = p.add;
+  if (p.slices > 1) {
+    p.dw = parts;
+    p.add = nullptr;
+  }
   alignas(64) CUtensorMap A, B;
   if (!encode_tmap_2d(&A, dy, false, (uint64_t)PL * p.TK, p.M, 64, 64) ||
       !encode_tmap_2d(&B, x, false, (uint64_t)PL * p.TK, p.N, 64, 64))
@@ -528,14 +580,16 @@ cudaError_t run_dw(const void* dy, const void* x, const DwArgs& p, cudaStream_t 
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * (int)std::min<long long>(device_sms() / 2, (long long)p.E * p.mt * p.nt));
+  cfg.gridDim = dim3(2 * (int)std::min<long long>(device_sms() / 2, (long long)p.E * p.mt * p.nt * p.slices));
   cfg.blockDim = dim3(kDwThreads);
   cfg.dynamicSmemBytes = kDwSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   SMOE_COUNT_LAUNCH(1);
-  return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+  const cudaError_t launched = cudaLaunchKernelEx(&cfg, kern, A, B, p);
+  if (launched != cudaSuccess || p.slices == 1) return launched;
+  return launch_sum_slices(parts, p.slices, (long long)p.E * p.M, p.N, false, p.expert_off, p.E, p.TK, add, dw, s);
 }
 
 // x = p0 + p1 + p2, each a bf16 value: the rest is exact at every step, and 24 bits are three times
@@ -583,20 +637,21 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
                              cudaStream_t s) {
   const int TK = d.T * d.K, wide = std::max(d.d, d.F);
   DeviceStatus* st = static_cast<DeviceStatus*>(ws);
-  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 256), ceil_div(n_in, 256)};
-  if (d.dtype != SMOE_F32) return run_dw<1>(dy, x, p, s);
+  const DwArgs p{expert_off, add, dw, st, d.E, TK, n_out, n_in, ceil_div(n_out, 256), ceil_div(n_in, 256), 1};
+  ProductLayout L;
+  product_ws_layout(d, &L);
+  float* parts = ws_ptr<float>(ws, L.parts);
+  if (d.dtype != SMOE_F32) return run_dw<1>(dy, x, p, parts, s);
   const float *fy = static_cast<const float*>(dy), *fx = static_cast<const float*>(x);
   // (the planes' place is the descriptor's)
   if (n_out > wide || n_in > wide || (double)TK * n_out * n_in < kPlaneMacs ||
       (long long)TK < (long long)kPlaneRows * d.E || 3LL * TK > INT_MAX / 2 ||
       (long long)TK * (n_out / 8 + n_in / 8) > INT_MAX)
-    return launch_expert_dw_f32(d, n_out, n_in, fy, fx, expert_off, add, dw, st, s);
-  ProductLayout L;
-  product_ws_layout(d, &L);
+    return launch_expert_dw_f32(d, n_out, n_in, fy, fx, expert_off, add, dw, ws, s);
   uint4 *pa = ws_ptr<uint4>(ws, L.planes_a), *pb = ws_ptr<uint4>(ws, L.planes_b);
   SMOE_LAUNCH(split_rows_kernel, ceil_div((long long)TK * (n_out / 8 + n_in / 8), 256), 256, 0, s, fy, fx, n_out, n_in, pa, pb,
               expert_off, d.E, TK);
-  return run_dw<3>(pa, pb, p, s);
+  return run_dw<3>(pa, pb, p, parts, s);
 }
 
 cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "smoe.h"
 
 namespace smoe {
@@ -308,9 +310,22 @@ cudaError_t launch_swiglu_grad_f8(const smoe_desc& d, int rows, int cols, const 
 // Expert products in 8-bit floating point (expert_f8.cu), and in the layer's type with their
 // gradients (ffn.cu, expert_grad.cu). One workspace for all of them.
 struct ProductLayout {
-  // rows: widened rows of a weight gradient; planes: its fp32 operands as bf16 planes
-  size_t status, tiles, rows, planes_a, planes_b, total;
+  // rows: widened rows of a weight gradient; planes: its fp32 operands as bf16 planes; parts:
+  // sums of a long contraction's slices
+  size_t status, tiles, rows, planes_a, planes_b, parts, total;
 };
+constexpr size_t kPartBytes = 40u << 20;
+// Slices of a contraction whose output tiles do not fill the GPU: `most` at most, their sums
+// (`size` floats each) in the workspace.
+inline int slices_of(long long tiles, long long fill, long long most, long long size) {
+  return (int)std::max(1LL, std::min(std::min(fill / std::max(tiles, 1LL), most),
+                                     std::min(16LL, (long long)(kPartBytes / 4) / std::max(size, 1LL))));
+}
+// out = add + the slices' sums, in their order; rows of row_len floats, those of the segments
+// alone where `segments`. A bad expert_off writes nothing.
+cudaError_t launch_sum_slices(const float* parts, int slices, long long rows, int row_len, bool segments,
+                              const int32_t* expert_off, int E, int TK, const float* add, float* out,
+                              cudaStream_t s);
 void product_ws_layout(const smoe_desc& d, ProductLayout* out);
 int device_sms();  // of the current device
 cudaError_t launch_expert_matmul_f8(const smoe_desc& d, int n_out, int n_in, const void* xq,
@@ -330,10 +345,10 @@ cudaError_t launch_expert_dw(const smoe_desc& d, int n_out, int n_in, const void
 // fp32 layers (expert_f32.cu)
 cudaError_t launch_expert_rows_f32(const smoe_desc& d, int n_out, int n_in, const float* a,
                                    const float* w, const float* a2, const float* w2, bool transposed,
-                                   const int32_t* expert_off, float* out, DeviceStatus* st, cudaStream_t s);
+                                   const int32_t* expert_off, float* out, void* ws, cudaStream_t s);
 cudaError_t launch_expert_dw_f32(const smoe_desc& d, int n_out, int n_in, const float* dy,
                                  const float* x, const int32_t* expert_off, const float* add, float* dw,
-                                 DeviceStatus* st, cudaStream_t s);
+                                 void* ws, cudaStream_t s);
 // the workspace's rows = kept rows in the layer's type
 cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,
                               const int32_t* row_src, const int32_t* expert_off, void* ws,

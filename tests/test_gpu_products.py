@@ -283,7 +283,8 @@ SHAPES = [
     (64, 6, 160, 256, 384, "skew"), (40, 2, 3, 1008, 520, "gaps"), (129, 1, 1, 128, 256, "one"),
     (64, 1, 1, 144, 264, "one"), (301, 3, 24, 1008, 200, "skew"), (400, 2, 2, 128, 1416, "gaps"),
     (1000, 1, 3, 512, 512, "skew"), (777, 4, 16, 80, 776, "gaps"), (2048, 2, 8, 384, 640, "even"),
-    (95, 2, 512, 64, 64, "skew"), (950, 2, 7, 520, 264, "gaps"), (17, 1, 1, 5120, 64, "one"), (700, 2, 5, 2064, 24, "skew"),
+    (95, 2, 512, 64, 64, "skew"), (950, 2, 7, 520, 264, "gaps"),
+    (1500, 1, 1, 640, 72, "gaps"), (3000, 1, 2, 128, 136, "skew"), (2600, 1, 1, 1040, 264, "one"), (17, 1, 1, 5120, 64, "one"), (700, 2, 5, 2064, 24, "skew"),
 ]
 
 
