@@ -509,7 +509,9 @@ SMOE_API int smoe_expert_ffn_i8(const smoe_desc* desc, const int8_t* xq, const f
                                 const smoe_i8_weights* weights, void* y_disp, void* y_shared,
                                 void* ws, size_t ws_bytes, void* stream);
 
-/* Rows in 8-bit floating point (e4m3) with a scale per row and block of 128 channels (the last
+/* (Buffers of the entry points below overlap only where an argument says that it may be another.)
+ *
+ * Rows in 8-bit floating point (e4m3) with a scale per row and block of 128 channels (the last
  * block may be shorter):
  *   scale = max |x| / 448 over the block, in fp32; pow2 = 1: the power of two that is not below
  *   it;  q = x / scale rounded to e4m3 (to nearest, ties to even).

@@ -31,5 +31,7 @@ __all__ = list(_BINDING_NAMES)
 def __getattr__(name):
     if name in _BINDING_NAMES:
         binding = importlib.import_module(".binding", __name__)
-        return getattr(binding, name)
+        # found directly from now on: looking it up here takes 1.3 us of a 6 us call
+        value = globals()[name] = getattr(binding, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -16,6 +16,14 @@
 //   narrow 128 channels x at most 64 rows: for batches that do not fill an expert's tile the
 //          weights' stream is the work; the channels are the MMA's M, its N the rows rounded up
 //          to 16, and the row scales are read from shared memory
+//
+// Measured: 384 rows over 160 experts of 5120 to 1536 channels (narrow) 181 us, 6.3 TB/s of
+// weights; 131072 rows over 128 experts of 2048 to 768 (wide) 226 us, 1.83 PFLOP/s; 2002 rows over
+// 8 experts of 4096 to 14336, fp32 out, 152 us. What bounds the wide form: without its stores the
+// prefill product took 205 us, without the epilogue's FMAs and TMEM loads besides 170, without the
+// gathering and the weights' loads besides 125: the work of each of the three overlaps the MMAs (96 us
+// at the nominal rate) and still takes from them, and a block's way from the MMAs to the epilogue and
+// back (two TMEM buffers of 256 columns are all there is) takes longer than its four MMAs.
 #include <algorithm>
 
 #include "tc_common.cuh"
@@ -214,7 +222,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
     // ---------------------------------------------------------------- scales
     // The product of both scales, for four blocks at a time and both halves of the channels. (Loaded
     // by the epilogue warps, whose load instructions then queue behind the gathering warps'
-    // copies, 131072 rows of 2048 to 768 channels took 269 us; now 240.)
+    // copies, 131072 rows of 2048 to 768 channels took 269 us; now 246.)
     uint32_t slot = 0, ph = 1;
     bool ok = true;
     int g = 0;
@@ -561,8 +569,9 @@ cudaError_t run_f8(const F8Args& p, const void* wq, long long tile_bound, cudaSt
   alignas(64) CUtensorMap tw, to;
   constexpr bool kF32 = sizeof(TO) == 4;
   if (!encode_tmap_2d(&tw, wq, false, (uint64_t)p.E * p.N, p.KD / 2, 128, 64) ||
-      !encode_tmap_2d(&to, p.out, kF32, p.TK, p.N, 32, kF32 ? 32 : 64))
+      (WIDE && !encode_tmap_2d(&to, p.out, kF32, p.TK, p.N, 32, kF32 ? 32 : 64)))
     return cudaErrorInvalidValue;
+  if (!WIDE) to = tw;  // (not used)
   auto kern = f8_gemm_kernel<WIDE, TO>;
   const int smem = (int)f8_smem<WIDE>();
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -15,6 +15,11 @@
 //   TMEM accumulators;  warps 4-11  add and store, while the next tile's MMAs run.
 // An expert's R rows give 2 R flops per element of 4 bytes (8 with add): below about 550 rows an
 // expert the stores bound it, not the tensor cores.
+// Measured: 160 experts of 1536 x 5120, 49152 rows, 940 us (5.0 GB of gradients: 5.4 TB/s; a fill of
+// that buffer takes 655); 128 of 768 x 2048, 131072 rows, added to earlier gradients, 434 us. Without
+// its stores the first took 676 us: loads, MMAs and the epilogue's passage through shared memory
+// overlap, and each still slows the others. The sums leaving through TMA instead of the warps'
+// stores: 1046 us.
 #include <algorithm>
 #include <climits>
 #include <cuda_fp8.h>
