@@ -553,7 +553,9 @@ SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, c
 
 /* Grouped product: for every expert e and each of its dispatched rows r,
  *   out[r, n] = sum_k x[r, k] w[e, n, k],
- * fp32 accumulation. fp32 layers multiply in fp32 (not tf32).
+ * fp32 accumulation. fp32 layers multiply in fp32 (not tf32): large products on the tensor cores as
+ * bf16 planes of the operands, with a relative error of about 2^-24 a term; there an infinity in an
+ * operand may give NaN where the exact sum is infinite (of this product and its gradients).
  *   x [T K, n_in] dtype in dispatched order; expert_off [E+1] int32; w [E, n_out, n_in] dtype;
  *   out [T K, n_out] dtype, rows outside the segments are not written
  * n_in and n_out are multiples of 8 (of this product and its two gradients). Descriptors of
@@ -578,9 +580,7 @@ SMOE_API int smoe_expert_matmul_dx(const smoe_desc* desc, int n_out, int n_in, c
  *   of earlier batches (may be the same buffer as dw); dw [E, n_out, n_in] fp32, every expert
  *   written: one without rows (with T = 0: all) gets add, or zeros. Rows outside the segments
  *   are not read into any sum. A bad expert_off (SMOE_ERR_DATA) writes nothing.
- * Sums over many rows are added up in chunks, so that they do not drift. fp32 layers multiply in
- * fp32, large ones on the tensor cores as bf16 planes of the operands: there an infinity in an
- * operand may give NaN where the exact sum is infinite.                                  */
+ * Sums over many rows are added up in chunks, so that they do not drift.                 */
 SMOE_API int smoe_expert_matmul_dw(const smoe_desc* desc, int n_out, int n_in, const void* dy,
                                    const void* x, const int32_t* expert_off, const float* add,
                                    float* dw, void* ws, size_t ws_bytes, void* stream);

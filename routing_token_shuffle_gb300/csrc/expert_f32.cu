@@ -1,5 +1,5 @@
 // The experts' products and their gradients in fp32 layers, on the CUDA cores (the tensor cores'
-// tf32 keeps 11 bits of an operand):
+// tf32 keeps 11 bits of an operand; large ones go to expert_planes.cu and expert_grad.cu):
 //   kind 0  y[r, n] = sum_k x[r, k] w[e, n, k]            rows x n_out, over n_in
 //   kind 1  dx[r, k] = sum_n dy[r, n] w[e, n, k] (twice)  rows x n_in, over n_out
 //   kind 2  dw[e, n, k] = sum_r dy[r, n] x[r, k] (+ add)  n_out x n_in, over the rows
@@ -10,7 +10,7 @@
 // memory filled by asynchronous copies that run ahead across tiles, so that the short contractions of
 // a weight gradient (an expert's rows) do not wait for memory tile by tile; FMAs bound it.
 // Measured: 39 rows of 24 experts of 1000 to 1416 channels 23 us (4.8 TB/s of the weights that are
-// touched); 8192 rows of 8 experts of 1024 to 2048 870 us, 39 TFLOP/s.
+// touched); tiles at 39 TFLOP/s (8192 rows of 8 experts of 1024 to 2048 870 us, where planes take 232).
 #include <algorithm>
 
 #include "tc_common.cuh"
@@ -451,6 +451,13 @@ cudaError_t run_tiled(F32Args p, long long tiles, long long stages, void* ws, co
 // gradients 24: 175 and 99, 48: 244 and 173; 8 experts of 2048 to 1024, 48: 153 and 88, and 122
 // and 75.
 constexpr int kTileRows = 56;
+// ... and from which, with so many multiply-adds, products of bf16 planes on the tensor cores
+// (expert_planes.cu) do, the planes' making included. Measured (us, planes and CUDA cores): 24 experts
+// of 1000 to 1416, 32 rows: 164 and 139, 64: 167 and 197, 256: 224 and 580, 1024: 517 and 2024; 8 of
+// 2048 to 1024, 64: 87 and 134, 1024: 232 and 994; 4 of 512 to 512, 128: 24 and 21, 256: 26 and 30,
+// 1024: 33 and 99; one of 5120 to 256, 64: 27 and 32, 1024: 43 and 84; row gradients alike.
+constexpr int kPlaneRows = kPlaneRowsMin;
+constexpr double kPlaneMacs = 1.5e8;
 
 }  // namespace
 
@@ -461,6 +468,10 @@ cudaError_t launch_expert_rows_f32(const smoe_desc& d, int n_out, int n_in, cons
   product_ws_layout(d, &L);
   const int TK = d.T * d.K;
   const F32Args p{a, w, a2, w2, nullptr, out, expert_off, ws_ptr<DeviceStatus>(ws, L.status), d.E, TK, n_out, n_in, 1, 0};
+  if (has_weight_planes(d) && n_out <= std::max(d.d, d.F) && n_in <= std::max(d.d, d.F) &&
+      (long long)n_out * n_in <= (long long)d.d * d.F && 3LL * TK < 1LL << 30 &&
+      (long long)TK >= (long long)kPlaneRows * d.E && (double)TK * n_out * n_in * (a2 ? 2 : 1) >= kPlaneMacs)
+    return launch_expert_rows_planes(d, n_out, n_in, a, w, a2, w2, transposed, expert_off, out, ws, s);
   if ((long long)TK >= (long long)kTileRows * d.E) {
     const long long tiles = ((long long)ceil_div(TK, kBM) + std::min(TK, d.E)) * ceil_div(transposed ? n_in : n_out, kBN);
     return transposed ? run_tiled<1>(p, tiles, ceil_div(n_out, kBK) * (a2 ? 2 : 1), ws, L, s)

@@ -544,6 +544,9 @@ void product_ws_layout(const smoe_desc& d, ProductLayout* L) {
   const size_t planes = d.dtype == SMOE_F32 ? (size_t)d.T * d.K * std::max(d.d, d.F) * 6 : 0;
   L->planes_a = take(planes);
   L->planes_b = take(planes);
+  const size_t weights = has_weight_planes(d) ? (size_t)d.E * d.d * d.F * 6 : 0;
+  L->planes_w = take(weights);
+  L->planes_w2 = take(weights);
   L->parts = take(kPartBytes);
   L->total = off;
 }
@@ -597,9 +600,7 @@ cudaError_t run_dw(const void* dy, const void* x, DwArgs p, float* parts, cudaSt
   return launch_sum_slices(parts, p.slices, (long long)p.E * p.M, p.N, false, p.expert_off, p.E, p.TK, add, dw, s);
 }
 
-// x = p0 + p1 + p2, each a bf16 value: the rest is exact at every step, and 24 bits are three times
-// eight. (A value that would round up to infinity is cut off instead; an infinity or a NaN
-// stays in p0, with zeros behind it.) Both operands' rows of the segments, 8 values a thread.
+// The planes of both operands' rows of the segments, 8 values a thread.
 __global__ void __launch_bounds__(256)
 split_rows_kernel(const float* a, const float* b, int na, int nb, uint4* pa, uint4* pb,
                   const int32_t* expert_off, int E, int TK) {
@@ -617,13 +618,7 @@ split_rows_kernel(const float* a, const float* b, int na, int nb, uint4* pa, uin
 #pragma unroll
   for (int pl = 0; pl < 3; ++pl) {
     float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
-      if (__hisinf(h)) h = __float2bfloat16_rz(x[i]);
-      y[i] = __bfloat162float(h);
-      x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] - y[i] : 0.0f;
-    }
+    split_planes(x, y);
     to[(size_t)pl * TK * n] = pack16(y, (const __nv_bfloat16*)nullptr);
   }
 }

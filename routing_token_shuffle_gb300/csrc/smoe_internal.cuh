@@ -78,6 +78,19 @@ __device__ __forceinline__ uint4 pack16(const float* in, const __nv_bfloat16*) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The next bf16 plane y of each x, and what is left of it: x = p0 + p1 + p2, as the rest is exact at
+// every step and 24 bits are three times eight. A value that would round up to infinity is cut off
+// instead; an infinity or a NaN stays in p0, with zeros behind it.
+__device__ __forceinline__ void split_planes(float (&x)[8], float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
+    if (__hisinf(h)) h = __float2bfloat16_rz(x[i]);
+    y[i] = __bfloat162float(h);
+    x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] - y[i] : 0.0f;
+  }
+}
+
 // ---------------------------------------------------------------- workspace
 // Every entry point carves the same layout out of the caller's workspace, so one
 // buffer of smoe_workspace_size bytes serves all of them.
@@ -312,8 +325,15 @@ cudaError_t launch_swiglu_grad_f8(const smoe_desc& d, int rows, int cols, const 
 struct ProductLayout {
   // rows: widened rows of a weight gradient; planes: its fp32 operands as bf16 planes; parts:
   // sums of a long contraction's slices
-  size_t status, tiles, rows, planes_a, planes_b, parts, total;
+  size_t status, tiles, rows, planes_a, planes_b, planes_w, planes_w2, parts, total;
 };
+// Whether the workspace has room for the weights' planes: fp32 layers whose experts have rows for it,
+// and whose matrices are not past 2^28 values (1.6 GB of planes).
+constexpr int kPlaneRowsMin = 64;
+inline bool has_weight_planes(const smoe_desc& d) {
+  return d.dtype == SMOE_F32 && (long long)d.T * d.K >= (long long)kPlaneRowsMin * d.E &&
+         (long long)d.E * d.d * d.F <= 1LL << 28;
+}
 constexpr size_t kPartBytes = 40u << 20;
 // Slices of a contraction whose output tiles do not fill the GPU: `most` at most, their sums
 // (`size` floats each) in the workspace.
@@ -349,6 +369,9 @@ cudaError_t launch_expert_rows_f32(const smoe_desc& d, int n_out, int n_in, cons
 cudaError_t launch_expert_dw_f32(const smoe_desc& d, int n_out, int n_in, const float* dy,
                                  const float* x, const int32_t* expert_off, const float* add, float* dw,
                                  void* ws, cudaStream_t s);
+cudaError_t launch_expert_rows_planes(const smoe_desc& d, int n_out, int n_in, const float* a,
+                                      const float* w, const float* a2, const float* w2, bool transposed,
+                                      const int32_t* expert_off, float* out, void* ws, cudaStream_t s);
 // the workspace's rows = kept rows in the layer's type
 cudaError_t launch_widen_rows(const smoe_desc& d, int cols, const void* xq, const float* scale,
                               const int32_t* row_src, const int32_t* expert_off, void* ws,

@@ -428,7 +428,7 @@ def test_expert_matmul_f8(T, K, E, n_in, n_out, kind, dt, pow2):
 
 # ------------------------------------------------------------------ what the tiles must keep apart
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("T,n_in,n_out", [(200, 136, 72), (700, 520, 264), (40, 1000, 104)])
+@pytest.mark.parametrize("T,n_in,n_out", [(200, 136, 72), (700, 520, 264), (40, 1000, 104), (4200, 520, 264)])
 def test_an_expert_that_is_not_finite_stays_alone(T, n_in, n_out, dt):
     """Infinities and NaN in one expert's rows or weights reach no other expert's results."""
     c = Case(T, 1, 5, n_in, n_out, dt, "skew", seed=9)
