@@ -130,9 +130,11 @@ few_rows_kernel(const F32Args p) {
 // shared memory; the warps' sums meet there too.
 constexpr int kFewN = 512;  // matrix rows between two fills of shared memory
 
-// (three blocks an SM: 240 rows of 24 experts of 1416 x 1000, both pairs, 110 us, against 147; 39
-// rows, one pair, 41, against 39)
-__global__ void __launch_bounds__(256, 3)
+// Two blocks an SM, eight loads of a lane ahead. (Without the loads ahead and three blocks an SM: 128
+// rows of 8 experts of 256 x 128, both pairs, 13.7 us, against 10.3; 39 of 24 of 1416 x 1000 41,
+// against 30; 260 of 76 of 1392 x 304, both pairs, 101, against 68; but 216 of 152 of 936 x 432 42,
+// against 49.)
+__global__ void __launch_bounds__(256, 2)
 few_rows_t_kernel(const F32Args p) {
   __shared__ int32_t s_ts[kMaxGroups + 2], s_off[kMaxGroups + 2];
   __shared__ alignas(16) float s_dy[kFewN][kFewRows];
@@ -158,36 +160,58 @@ few_rows_t_kernel(const F32Args p) {
       const float* w = (pair ? p.b2 : p.b) + (size_t)g * p.n_out * p.n_in + (in ? col : 0);
       for (int n0 = 0; n0 < p.n_out; n0 += kFewN) {
         const int nn = min(kFewN, p.n_out - n0);
-        __syncthreads();
-        for (int i = tid; i < kFewN * kFewRows; i += 256) {
-          const int r = i / kFewN, n = i % kFewN;
-          s_dy[n][r] = n < nn && r < rows ? dy[(size_t)r * p.n_out + n0 + n] : 0.0f;
-        }
-        __syncthreads();
-        for (int n = warp; n < nn; n += 64) {
-          float4 wv[8];
+        // the next eight matrix rows are on their way while these are multiplied, the first ones
+        // while dy is laid out
+        float4 wv[2][8];
+        auto fetch = [&](int n, float4 (&v)[8]) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            wv[j] = in && n + 8 * j < nn ? __ldcs(reinterpret_cast<const float4*>(w + (size_t)(n0 + n + 8 * j) * p.n_in))
-                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[j] = in && n + 8 * j < nn ? __ldcs(reinterpret_cast<const float4*>(w + (size_t)(n0 + n + 8 * j) * p.n_in))
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        };
+        auto multiply = [&](int n, const float4 (&v)[8]) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            // (past the matrix' rows the factor is that of another row, times zeros of w; past the
-            // fill it stays inside s_dy)
-            const int at = min(n + 8 * j, kFewN - 1);
+            if (n + 8 * j >= nn) break;
+            const float* at = &s_dy[n + 8 * j][0];
             float f[kFewRows];
-            *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&s_dy[at][0]);
-            if (rows > 4) *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&s_dy[at][4]);
+            *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(at);
+            if (rows > 4) *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(at + 4);
 #pragma unroll
             for (int r = 0; r < kFewRows; ++r) {
               if (r >= 4 && rows <= 4) break;
-              if (n + 8 * j >= nn) break;
-              acc[r].x = fmaf(f[r], wv[j].x, acc[r].x);
-              acc[r].y = fmaf(f[r], wv[j].y, acc[r].y);
-              acc[r].z = fmaf(f[r], wv[j].z, acc[r].z);
-              acc[r].w = fmaf(f[r], wv[j].w, acc[r].w);
+              acc[r].x = fmaf(f[r], v[j].x, acc[r].x);
+              acc[r].y = fmaf(f[r], v[j].y, acc[r].y);
+              acc[r].z = fmaf(f[r], v[j].z, acc[r].z);
+              acc[r].w = fmaf(f[r], v[j].w, acc[r].w);
             }
           }
+        };
+        fetch(warp, wv[0]);
+        __syncthreads();
+        {  // (all loads ahead of the stores)
+          float f[kFewN / 256][kFewRows];
+#pragma unroll
+          for (int i = 0; i < kFewN / 256; ++i)
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+              const int n = tid + 256 * i;
+              f[i][r] = n < nn && r < rows ? dy[(size_t)r * p.n_out + n0 + n] : 0.0f;
+            }
+#pragma unroll
+          for (int i = 0; i < kFewN / 256; ++i) {
+            float4* to = reinterpret_cast<float4*>(&s_dy[tid + 256 * i][0]);
+            to[0] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+            to[1] = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
+          }
+        }
+        __syncthreads();
+        for (int n = warp; n < nn; n += 128) {
+          fetch(n + 64, wv[1]);
+          multiply(n, wv[0]);
+          if (n + 64 >= nn) break;
+          fetch(n + 128, wv[0]);
+          multiply(n + 64, wv[1]);
         }
       }
     }

@@ -279,7 +279,7 @@ class Case:
 
 SHAPES = [
     # T, K, E, n_in, n_out, kind
-    (1, 1, 1, 16, 8, "even"), (1, 2, 4, 64, 72, "even"), (3, 2, 8, 272, 136, "skew"),
+    (1, 1, 1, 16, 8, "even"), (5, 2, 3, 8, 8, "skew"), (600, 1, 2, 16, 8, "skew"), (1, 2, 4, 64, 72, "even"), (3, 2, 8, 272, 136, "skew"),
     (64, 6, 160, 256, 384, "skew"), (40, 2, 3, 1008, 520, "gaps"), (129, 1, 1, 128, 256, "one"),
     (64, 1, 1, 144, 264, "one"), (301, 3, 24, 1008, 200, "skew"), (400, 2, 2, 128, 1416, "gaps"),
     (1000, 1, 3, 512, 512, "skew"), (777, 4, 16, 80, 776, "gaps"), (2048, 2, 8, 384, 640, "even"),
@@ -786,3 +786,47 @@ def test_long_sums_do_not_drift(rows):
     smoe.smoe_expert_matmul_dw(f.desc, dy, x, f.off, dw, f.ws)
     ref = dy.double().T @ x.double()
     assert float((dw[1].double() - ref).norm() / ref.norm()) <= 64 * 2.0 ** -24
+
+
+def test_weight_gradient_wider_than_the_descriptor():
+    """n_out above the descriptor's d and F: no room is kept for its planes, and none is needed."""
+    T, E, n_in, n_out = 512, 2, 512, 1024
+    c = Case(T, 1, E, n_in, n_out, "f32", "even")
+    desc = smoe.make_desc(T, n_in, E, 1, 1, 64, 0, 1, 1, "f32")
+    ws = smoe.workspace_products(desc)
+    dy, x, w = c.rows(n_out), c.rows(n_in), c.weights()
+    dw, out, dx = torch.empty(E, n_out, n_in, device="cuda"), c.out(n_out), c.out(n_in)
+    smoe.smoe_expert_matmul_dw(desc, dy, x, c.off, dw, ws)
+    smoe.smoe_expert_matmul(desc, x, c.off, w, out, ws)
+    smoe.smoe_expert_matmul_dx(desc, dy, w, c.off, dx, ws)
+    smoe.smoe_get_status(ws)
+    for e, s in enumerate(c.seg):
+        d = lambda a, b: (a.double() @ b.double(), a.double().abs() @ b.double().abs())  # noqa: E731
+        for got, (ref, mag), n in ((dw[e], d(dy[s].T, x[s]), T), (out[s], d(x[s], w[e].T), n_in),
+                                   (dx[s], d(dy[s], w[e]), n_out)):
+            within(got, ref, adds1(n) * 2.0 ** -23 * mag)
+
+
+def test_two_graphs_in_turn():
+    """Two captured steps, each with its own workspaces, replayed in turn on one stream."""
+    a, b = Step(200, 128, 6, 2, 144, "bf16"), Step(90, 128, 6, 2, 144, "f32", seed=3)
+    want, graphs = [], []
+    for c in (a, b):
+        c.forward()
+        c.backward()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in c.outputs()])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.forward()
+            c.backward()
+        graphs.append(g)
+    for _ in range(3):
+        for c in (a, b):
+            for o in c.outputs():
+                o.fill_(3.0)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        for c, w in zip((a, b), want):
+            for o, v in zip(c.outputs(), w):
+                same(o, v)
