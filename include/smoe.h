@@ -555,7 +555,8 @@ SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, c
  *   out[r, n] = sum_k x[r, k] w[e, n, k],
  * fp32 accumulation. fp32 layers multiply in fp32 (not tf32): large products on the tensor cores as
  * bf16 planes of the operands, with a relative error of about 2^-24 a term; there an infinity in an
- * operand may give NaN where the exact sum is infinite (of this product and its gradients).
+ * operand may give NaN where the exact sum is infinite, and operands below 1e-33 lose bits (of
+ * this product and its gradients).
  *   x [T K, n_in] dtype in dispatched order; expert_off [E+1] int32; w [E, n_out, n_in] dtype;
  *   out [T K, n_out] dtype, rows outside the segments are not written
  * n_in and n_out are multiples of 8 (of this product and its two gradients). Descriptors of

@@ -830,3 +830,23 @@ def test_two_graphs_in_turn():
         for c, w in zip((a, b), want):
             for o, v in zip(c.outputs(), w):
                 same(o, v)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e30])
+def test_fp32_products_over_the_range(scale):
+    """Rows far from one: the planes of an fp32 operand keep its 24 bits (to 1e-33)."""
+    c = Case(2048, 1, 4, 384, 264, "f32", "even", seed=6)
+    x, dy, w = c.rows(384) * scale, c.rows(264) * scale, c.weights()
+    x[::7] = x[::7].bfloat16().float()  # rows whose lower planes are zero
+    out, dx, dw = c.out(264), c.out(384), torch.empty(4, 264, 384, device="cuda")
+    smoe.smoe_expert_matmul(c.desc, x, c.off, w, out, c.ws)
+    smoe.smoe_expert_matmul_dx(c.desc, dy, w, c.off, dx, c.ws)
+    smoe.smoe_expert_matmul_dw(c.desc, dy / scale, x, c.off, dw, c.ws)
+    smoe.smoe_get_status(c.ws)
+    for e, s in enumerate(c.seg):
+        d = lambda a, b: (a.double() @ b.double(), a.double().abs() @ b.double().abs())  # noqa: E731
+        for got, (ref, mag) in ((out[s], d(x[s], w[e].T)), (dx[s], d(dy[s], w[e])), (dw[e], d((dy / scale)[s].T, x[s]))):
+            # six products of planes, each with a dropped rest of 2^-24 of its term, and chunks of
+            # 128 with 48 additions cut off at 24 bits
+            within(got, ref, 64 * 2.0 ** -23 * mag)
+            assert float((got.double() - ref).norm() / ref.norm()) <= 2e-6
