@@ -527,8 +527,11 @@ SMOE_API int smoe_rows_f8(const smoe_desc* desc, int rows, int cols, const void*
                           uint8_t* q, float* scale, void* stream);
 
 /* Bytes of the workspace of smoe_expert_matmul_f8, smoe_expert_matmul, _dx, _dw and _dw_f8 for
- * this shape (of the same manner as every workspace). One size for all: it holds the widened
- * rows of _dw_f8 also where a program does not call that. 0 if the descriptor is invalid. */
+ * this shape (of the same manner as every workspace). One size for all: 40 MB for the sums of
+ * sliced contractions, the widened rows of _dw_f8 (T K max(d, F) values of the layer's type), and in
+ * fp32 layers bf16 planes: 12 bytes for each of so many values, and, from 64 rows an expert on
+ * average, for each of the experts' E d F values where those are at most 2^28. 0 if the
+ * descriptor is invalid. */
 SMOE_API size_t smoe_product_workspace_size(const smoe_desc* desc);
 
 /* Grouped product in 8-bit floating point with block scales: for every expert e and each of
