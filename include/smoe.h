@@ -556,7 +556,8 @@ SMOE_API int smoe_expert_matmul_f8(const smoe_desc* desc, int n_out, int n_in, c
 
 /* Grouped product: for every expert e and each of its dispatched rows r,
  *   out[r, n] = sum_k x[r, k] w[e, n, k],
- * fp32 accumulation. fp32 layers multiply in fp32 (not tf32): large products on the tensor cores as
+ * fp32 accumulation; long sums are added up in chunks of at most 1024 channels, so that they do not
+ * drift (of this product and its gradients). fp32 layers multiply in fp32 (not tf32): large products on the tensor cores as
  * bf16 planes of the operands, with a relative error of about 2^-24 a term; there an infinity in an
  * operand may give NaN where the exact sum is infinite, and operands below 1e-33 lose bits (of
  * this product and its gradients).

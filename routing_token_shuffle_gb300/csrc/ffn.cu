@@ -195,11 +195,118 @@ __device__ __forceinline__ void decode_tile(const int32_t* ts, const int32_t* eo
   }
 }
 
+// ------------------------------------------------------------------ single products
+// The tensor core cuts its sums off instead of rounding them: 28672 positive terms in one
+// accumulator came out low by 1.5e-4 (1.4 steps of 2^-23 of the running sum for each 16 of them), and
+// terms below the running sum's last place were lost one and all. So the single products (LONG) begin
+// anew after each 1024 of the contraction, as the weight gradients do after so many rows, and their
+// epilogue adds the chunks' sums up, rounded: eight warps, half of a tile's columns each, hold them in
+// registers, so that an accumulator goes back to the MMAs as soon as it is read and the next chunk or
+// tile runs on in the other one. Measured (us, one sum / chunks, on one GPU in turn): pairs, both row
+// gradients of 8192 rows of 8 experts of 4096 x 14336 1324 / 1285, added up in TMEM by four warps 1458; 8192
+// rows of 8 experts, 14336 to 4096 channels, 593 / 593; 49152 of 160, 1536 to 5120 642 / 648, 5120 to 1536
+// 681 / 672; 131072 of 128, 2048 to 768 272 / 277; one SM, 512 of 8, 14336 to 4096 156 / 156; 30000 of
+// 160, 5120 to 1536 522 / 526; 64 of one, 5120 to 5120 32 / 32.
+constexpr int kChunkBlocks = 16;  // 64-wide k-blocks
+constexpr int kLongWarps = 8, kLongThreads = 128 + 32 * kLongWarps;
+
+template <bool UP>
+__device__ __forceinline__ void decode_pair_tile(const int32_t* ts, const int32_t* eo, const GemmArgs& p, int t,
+                                                 uint32_t rank, Tile& r);
+
+// buf: 2 KB of the warp's own. PAIR: of the two-SM kernel.
+template <bool PAIR>
+__device__ __forceinline__ void long_epilogue(const GemmArgs& p, const int32_t* s_ts, const int32_t* s_eo,
+                                              uint32_t rank, uint32_t tmem, int nkb, uint8_t* buf,
+                                              uint64_t* tfull, uint64_t* tempty, int* s_abort) {
+  using TE = __nv_bfloat16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = (warp - 4) >> 2;
+  const int total = s_ts[p.G] * p.NT;
+  volatile int* abort = s_abort;
+  uint32_t n = 0;  // sums read
+  for (int t = blockIdx.x >> PAIR; t < total; t += gridDim.x >> PAIR) {
+    Tile tl;
+    if (PAIR) {
+      decode_pair_tile<false>(s_ts, s_eo, p, t, rank, tl);
+    } else {
+      decode_tile<false>(s_ts, s_eo, p, t, tl);
+      tl.swap = false;
+      tl.N = 256;
+    }
+    // this warp's columns of the accumulator: up to 128 from c0 on, a multiple of 32
+    const int first = ((tl.N >> 5) + 1) / 2 * 32, c0 = part ? first : 0, ncols = part ? tl.N - first : first;
+    float sum[128];
+#pragma unroll
+    for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; kb += kChunkBlocks, ++n) {
+      const uint32_t a = n & 1u;
+      if (!tc::mbar_wait_warp(&tfull[a], (n >> 1) & 1u, abort)) {
+        if (lane == 0) {
+          *abort = 1;
+          record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
+        }
+        return;
+      }
+      tc::fence_after_sync();
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + a * kAccCols + c0;
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {  // (by 32 the form of one SM spills, and is 2 % slower)
+        if (c >= ncols) break;
+        float v[16];
+        tc::tmem_ld16(taddr + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) tc::mbar_arrive_cluster(tc::cluster_addr(&tempty[a], 0));
+        else tc::mbar_arrive(&tempty[a]);
+      }
+    }
+    TE* out = static_cast<TE*>(p.out);
+    if (tl.swap) {
+      // column = token, lane = weight row (see the two-SM variant's notes above)
+      const int half = tl.N >> 1, ntok = tl.rows - (tl.m0 - (int)rank * half) - c0;
+      const int col = tl.n0 + 128 * (int)rank + 32 * q + lane, used = min(ncols, ntok);
+      if (col < p.N) {
+        TE* at = out + (size_t)(tl.out_row - (long long)rank * half + c0) * p.N + col;
+#pragma unroll
+        for (int i = 0; i < 128; ++i, at += p.N)
+          if (i < used) *at = Elem<TE>::from_f32(sum[i]);
+      }
+      __syncwarp();
+      continue;
+    }
+    // windows of 32 columns (64 bytes) through the warp's 2 KB, 16-byte chunks swizzled by pairs of
+    // rows: no bank conflicts, whole sectors
+    const int valid = clamp_rows(tl.rows - tl.m0 - q * 32), ch = lane & 3;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      const int col = tl.n0 + c0 + c + ch * 8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+            pack16(sum + c + j * 8, (const TE*)nullptr);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2);
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+        if (rr < valid && col < p.N)
+          *reinterpret_cast<uint4*>(out + (size_t)(tl.out_row + q * 32 + rr) * p.N + col) = v;
+      }
+      __syncwarp();
+    }
+  }
+}
+
 // TW: Y[r, n] = sum_k A[r, k] W[g, k, n] (a row gradient): the weights' rows are the contraction,
 // B is staged as boxes of 64 columns x 64 rows and read MN-major. With p.two the contraction goes on
 // over a second A (tmA_sh) and W (tmB3).
-template <bool UP, bool F32, bool TW = false>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool UP, bool F32, bool TW = false, bool LONG = TW>
+__global__ void __launch_bounds__(LONG ? kLongThreads : kThreads, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     const __grid_constant__ CUtensorMap tmA_sh,
                     const __grid_constant__ CUtensorMap tmB1,
@@ -236,7 +343,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&tfull[a], 1);
-      tc::mbar_init(&tempty[a], 128);
+      tc::mbar_init(&tempty[a], LONG ? kLongWarps : 128);
     }
     tc::mbar_init(drain, 1);
     *s_abort = 0;
@@ -246,8 +353,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     tc::tma_prefetch_map(&tmB1);
     tc::tma_prefetch_map(&tmB3);
   }
-  for (int i = threadIdx.x; i <= p.G; i += kThreads) s_ts[i] = p.tile_start[i];
-  for (int i = threadIdx.x; i <= p.E; i += kThreads) s_eo[i] = p.expert_off[i];
+  for (int i = threadIdx.x; i <= p.G; i += blockDim.x) s_ts[i] = p.tile_start[i];
+  for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_eo[i] = p.expert_off[i];
   if (warp == 2) {
     tc::tmem_alloc(s_tmem, 2 * kAccCols);
     tc::tmem_relinquish();
@@ -260,6 +367,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   const int nkb1 = (p.KD + BK - 1) / BK, nkb = TW && p.two ? 2 * nkb1 : nkb1;
   volatile int* abort = s_abort;
 
+  // LONG: 384 threads of 168 registers at launch, 104 + 2 x 200 = 3 x 168 from here on
+  if (LONG && warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    long_epilogue<false>(p, s_ts, s_eo, 0, tmem, nkb, sOut + (warp - 4) * 2048, tfull, tempty, s_abort);
+  } else {
+  if (LONG) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
     uint32_t it = 0;
@@ -301,35 +414,39 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       tc::mbar_wait(&full[j % kStages], (j / kStages) & 1u, &never);
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
-    uint32_t it = 0, tcount = 0;
+    // (One loop over the k-blocks that tests each for a chunk's start: 64 rows, 4096 to 2560
+    // channels 26 us, against 24.)
+    uint32_t it = 0, n = 0;  // stages, sums (of a tile, or of a chunk)
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++tcount) {
-      const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
-      if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
-      tc::fence_after_sync();
-      const uint32_t d_tmem = tmem + a * kAccCols;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-        if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x)
+      for (int k0 = 0; k0 < nkb && ok; k0 += LONG ? kChunkBlocks : nkb, ++n) {
+        const int k1 = LONG ? min(k0 + kChunkBlocks, nkb) : nkb;
+        const uint32_t a = n & 1u, aph = (n >> 1) & 1u;
+        if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
         tc::fence_after_sync();
-        const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kStageA));
-        const uint64_t bdesc = TW ? tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kStageB))
-                                  : tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kStageB));
+        const uint32_t d_tmem = tmem + a * kAccCols;
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+          if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * kStageA));
+          const uint64_t bdesc = TW ? tc::sw128_mnmajor_desc(tc::smem_u32(sB + s * kStageB))
+                                    : tc::sw128_kmajor_desc(tc::smem_u32(sB + s * kStageB));
 #pragma unroll
-        for (int k = 0; k < kMmaPerStage; ++k) {
-          const uint32_t acc = (kb > 0 || k > 0) ? 1u : 0u;
-          if (TW)
-            tc::mma_bf16(d_tmem, adesc + 2 * k, bdesc + 128 * k, kIdesc, acc);
-          else if (F32)
-            tc::mma_tf32(d_tmem, adesc + 2 * k, bdesc + 2 * k, kIdesc, acc);
-          else
-            tc::mma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, kIdesc, acc);
+          for (int k = 0; k < kMmaPerStage; ++k) {
+            const uint32_t acc = (kb > k0 || k > 0) ? 1u : 0u;
+            if (TW)
+              tc::mma_bf16(d_tmem, adesc + 2 * k, bdesc + 128 * k, kIdesc, acc);
+            else if (F32)
+              tc::mma_tf32(d_tmem, adesc + 2 * k, bdesc + 2 * k, kIdesc, acc);
+            else
+              tc::mma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, kIdesc, acc);
+          }
+          tc::commit(&empty[s]);
         }
-        tc::commit(&empty[s]);
+        if (!ok) break;
+        tc::commit(&tfull[a]);
       }
-      if (!ok) break;
-      tc::commit(&tfull[a]);
-    }
     if (!ok) {
       *abort = 1;
       record_error(p.st, kStatusTimeout, kTimeoutGemm, blockIdx.x);
@@ -338,7 +455,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     volatile int never = 0;
     tc::commit(drain);
     tc::mbar_wait(drain, 0, &never);
-  } else if (warp >= 4) {
+  } else if (!LONG && warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
     uint32_t tcount = 0;
@@ -394,6 +511,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         }
       }
     }
+  }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -544,7 +662,7 @@ __device__ __forceinline__ void decode_pair_tile(const int32_t* ts, const int32_
 }
 
 // TW: as in the single-SM kernel; the second A in tmA_sh and tmA_sh64, the second W in tmB3.
-template <bool UP, bool TW = false>
+template <bool UP, bool TW = false, bool LONG = TW>
 __global__ void __launch_bounds__(kPairThreads, 1)
 grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row box
                          const __grid_constant__ CUtensorMap tmA_sh,  // 128-row box
@@ -583,7 +701,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&tfull[a], 1);
-      tc::mbar_init(&tempty[a], 256);
+      tc::mbar_init(&tempty[a], LONG ? 2 * kLongWarps : 256);
     }
     tc::mbar_init(drain, 1);
     *s_abort = 0;
@@ -614,6 +732,11 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
   const int nkb1 = (p.KD + 63) / 64, nkb = TW && p.two ? 2 * nkb1 : nkb1;
   volatile int* abort = s_abort;
 
+  if (LONG && warp >= 4) {  // (registers as in the single-SM kernel)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    long_epilogue<true>(p, s_ts, s_eo, rank, tmem, nkb, sOut + (warp - 4) * 2048, tfull, tempty, s_abort);
+  } else {
+  if (LONG) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
     uint32_t it = 0;
@@ -672,39 +795,42 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---------------------------------------------------------------- MMA issuer (leader)
-    uint32_t it = 0, tcount = 0;
+    uint32_t it = 0, n = 0;  // stages, sums (of a tile, or of a chunk)
     bool ok = true;
-    for (int t = pair; t < total && ok; t += npairs, ++tcount) {
+    for (int t = pair; t < total && ok; t += npairs) {
       Tile tl;
       decode_pair_tile<UP>(s_ts, s_eo, p, t, rank, tl);
       // swapped tile: the weight rows (B stage) are the MMA's A, the tokens its B
       const uint32_t idesc =
           tl.swap ? tc::instr_desc(false, 256, tl.N) | (TW ? tc::kIdescTransA : 0u) : kIdesc;
-      const uint32_t a = tcount & 1u, aph = (tcount >> 1) & 1u;
-      if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
-      tc::fence_after_sync();
-      const uint32_t d_tmem = tmem + a * kAccCols;
-      for (int kb2 = 0; kb2 < nkb; kb2 += 2, ++it) {
-        const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1u;
-        const int nj = min(2, nkb - kb2);
-        if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
+      for (int k0 = 0; k0 < nkb && ok; k0 += LONG ? kChunkBlocks : nkb, ++n) {
+        const int k1 = LONG ? min(k0 + kChunkBlocks, nkb) : nkb;
+        const uint32_t a = n & 1u, aph = (n >> 1) & 1u;
+        if (!tc::mbar_wait(&tempty[a], aph ^ 1u, abort)) { ok = false; break; }
         tc::fence_after_sync();
-        for (int j = 0; j < nj; ++j) {
-          const uint64_t tok_desc = tc::sw128_kmajor_desc(tc::smem_u32(sA + (s * 2 + j) * kPairStage));
-          const uint32_t w_addr = tc::smem_u32(sB + (s * 2 + j) * kPairStage);
-          const uint64_t w_desc = TW ? tc::sw128_mnmajor_desc(w_addr) : tc::sw128_kmajor_desc(w_addr);
-          const uint64_t adesc = tl.swap ? w_desc : tok_desc;
-          const uint64_t bdesc = tl.swap ? tok_desc : w_desc;
-          const uint32_t a_step = TW && tl.swap ? 128 : 2, b_step = TW && !tl.swap ? 128 : 2;
+        const uint32_t d_tmem = tmem + a * kAccCols;
+        for (int kb2 = k0; kb2 < k1; kb2 += 2, ++it) {
+          const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1u;
+          const int nj = min(2, k1 - kb2);
+          if (!tc::mbar_wait(&full[s], ph, abort)) { ok = false; break; }
+          tc::fence_after_sync();
+          for (int j = 0; j < nj; ++j) {
+            const uint64_t tok_desc = tc::sw128_kmajor_desc(tc::smem_u32(sA + (s * 2 + j) * kPairStage));
+            const uint32_t w_addr = tc::smem_u32(sB + (s * 2 + j) * kPairStage);
+            const uint64_t w_desc = TW ? tc::sw128_mnmajor_desc(w_addr) : tc::sw128_kmajor_desc(w_addr);
+            const uint64_t adesc = tl.swap ? w_desc : tok_desc;
+            const uint64_t bdesc = tl.swap ? tok_desc : w_desc;
+            const uint32_t a_step = TW && tl.swap ? 128 : 2, b_step = TW && !tl.swap ? 128 : 2;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_pair(d_tmem, adesc + a_step * k, bdesc + b_step * k, idesc,
-                              (kb2 + j > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16_pair(d_tmem, adesc + a_step * k, bdesc + b_step * k, idesc,
+                                (kb2 + j > k0 || k > 0) ? 1u : 0u);
+          }
+          tc::commit_pair(&empty[s], 0x3);
         }
-        tc::commit_pair(&empty[s], 0x3);
+        if (!ok) break;
+        tc::commit_pair(&tfull[a], 0x3);
       }
-      if (!ok) break;
-      tc::commit_pair(&tfull[a], 0x3);
     }
     if (!ok) {
       *abort = 1;
@@ -716,7 +842,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
   } else if (UP && p.g_src && (warp == 2 || warp == 3 || warp >= 8)) {
     // ---------------------------------------------------------------- row gather
     gather_worker(p, lane);
-  } else if (warp >= 4 && warp < 8) {
+  } else if (!LONG && warp >= 4 && warp < 8) {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;
     uint32_t tcount = 0;
@@ -848,6 +974,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,     // 128-row
       }
     }
   }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();
@@ -863,25 +990,25 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
-template <bool UP, bool F32, bool TW = false>
+template <bool UP, bool F32, bool TW = false, bool LONG = TW>
 cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& Ash, const CUtensorMap& B1,
                         const CUtensorMap& B3, const GemmArgs& args, long long tile_bound,
                         cudaStream_t s) {
-  auto kern = grouped_gemm_kernel<UP, F32, TW>;
+  auto kern = grouped_gemm_kernel<UP, F32, TW, LONG>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<long long>(sm_count(), std::max<long long>(tile_bound, 1));
-  SMOE_LAUNCH(kern, grid, kThreads, kSmemBytes, s, A, Ash, B1, B3, args);
+  SMOE_LAUNCH(kern, grid, LONG ? kLongThreads : kThreads, kSmemBytes, s, A, Ash, B1, B3, args);
   return cudaGetLastError();
 }
 
-template <bool UP, bool TW = false>
+template <bool UP, bool TW = false, bool LONG = TW>
 cudaError_t launch_gemm_pair(const CUtensorMap& A, const CUtensorMap& Ash, const CUtensorMap& A64,
                              const CUtensorMap& Ash64, const CUtensorMap& B1,
                              const CUtensorMap& B3, const GemmArgs& args, long long tile_bound,
                              cudaStream_t s) {
-  auto kern = grouped_gemm_pair_kernel<UP, TW>;
+  auto kern = grouped_gemm_pair_kernel<UP, TW, LONG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kPairSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1083,11 +1210,11 @@ cudaError_t launch_expert_ffn(const smoe_desc& d, const void* x_disp, const void
   return run_ffn<false>(d, x_disp, x, expert_off, w1, w3, w2, y_disp, y_sh, ws, s, gather);
 }
 
-// Both products of rows, on the kernels of the FFN's down product. (A pair's a_row maps need no
+// Both products of rows, on the kernels of the FFN's down product with an epilogue of their own. (A pair's a_row maps need no
 // shared experts' rows: the second operands of a row gradient take their place.) Measured: 49152
-// rows of 160 experts, 1536 to 5120 channels, 620 to 670 us (2.5 GB of weights and 0.77 TFLOP:
+// rows of 160 experts, 1536 to 5120 channels, 620 to 690 us (2.5 GB of weights and 0.77 TFLOP:
 // 5.1 TB/s and 1.25 PFLOP/s at once); both row gradients of 8192 rows of 8 experts of 4096 x 14336
-// 1285 to 1390 us, 1.4 to 1.5 PFLOP/s at the clock that the power cap allows; 384 rows of 160
+// 1260 to 1390 us, 1.4 to 1.5 PFLOP/s at the clock that the power cap allows; 384 rows of 160
 // experts, 5120 to 1536, 330 us (the weights of 145 of them: 6.9 TB/s), their gradient 311.
 cudaError_t launch_expert_rows_bf16(const smoe_desc& d, int n_out, int n_in, const void* a,
                                     const void* w, const void* a2, const void* w2, bool transposed,
@@ -1120,11 +1247,11 @@ cudaError_t launch_expert_rows_bf16(const smoe_desc& d, int n_out, int n_in, con
   const long long bound = ((long long)ceil_div(TK, bm) + d.E) * p.NT;
   if (!pairs)
     return transposed ? launch_gemm<false, false, true>(A, A2, B, B2, p, bound, s)
-                      : launch_gemm<false, false>(A, A, B, B, p, bound, s);
+                      : launch_gemm<false, false, false, true>(A, A, B, B, p, bound, s);
   if (!encode_tmap_2d(&A64, a, false, TK, KD, 64, 64) || !encode_tmap_2d(&A264, a2, false, TK, KD, 64, 64))
     return cudaErrorInvalidValue;
   return transposed ? launch_gemm_pair<false, true>(A, A2, A64, A264, B, B2, p, bound, s)
-                    : launch_gemm_pair<false>(A, A, A64, A64, B, B, p, bound, s);
+                    : launch_gemm_pair<false, false, true>(A, A, A64, A64, B, B, p, bound, s);
 }
 
 }  // namespace smoe

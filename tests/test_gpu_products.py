@@ -850,3 +850,90 @@ def test_fp32_products_over_the_range(scale):
             # 128 with 48 additions cut off at 24 bits
             within(got, ref, 64 * 2.0 ** -23 * mag)
             assert float((got.double() - ref).norm() / ref.norm()) <= 2e-6
+
+
+# ------------------------------------------------------------------ long contractions in bf16
+def dropped_terms(n, rows, cols):
+    """Rows and weights whose exact products lie a little above the middle of two bf16 numbers:
+    1 + 2^-8 - 2^-14 at the front and n - 16 terms of 2^-28 behind it, 2^-13.2 in all. Every one
+    of those is below half a step of a running sum near 1, whether it is rounded or cut off, sixteen
+    at once too. (rows, cols: powers of two that the rows and columns are scaled by.)"""
+    x, w = torch.full((n,), 2.0 ** -14, device="cuda"), torch.full((n,), 2.0 ** -14, device="cuda")
+    x[:16], w[:16] = 0.0, 0.0
+    x[:3], w[:3] = torch.tensor([1.0, 2.0 ** -8, -2.0 ** -14], device="cuda"), 1.0
+    return (rows[:, None] * x).bfloat16(), (cols[:, None] * w).bfloat16()
+
+
+@pytest.mark.parametrize("T", [100, 300, 512])
+def test_long_sums_keep_small_terms(T):
+    """Products and row gradients over 28672 channels (100 rows: tiles of one SM; 300: a tile of 256
+    and a remainder with its operands swapped; 512: whole tiles): a sum in one accumulator loses what
+    lies behind its first terms, sums over chunks do not."""
+    n, m = 28672, 264
+    rows = 2.0 ** (torch.arange(T, device="cuda") % 5 - 2)
+    cols = 2.0 ** (torch.arange(m, device="cuda") % 3)
+    x, w = dropped_terms(n, rows, cols)
+    want = (rows[:, None] * cols * (1 + 2.0 ** -7)).bfloat16()
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    desc = smoe.make_desc(T, n, 1, 1, 1, m, 0, 1, 1, "bf16")
+    ws, out = smoe.workspace_products(desc), torch.full((T, m), 7.0, dtype=torch.bfloat16, device="cuda")
+    smoe.smoe_expert_matmul(desc, x, off, w[None].contiguous(), out, ws)
+    same(out, want)
+    wt = w.T.contiguous()  # [n_out, n_in] of a gradient over n_out = n channels
+    out.fill_(7.0)
+    smoe.smoe_expert_matmul_dx(desc, x, wt[None], off, out, ws)
+    same(out, want)
+    out.fill_(7.0)
+    h = n // 2
+    smoe.smoe_expert_matmul_dx(desc, x[:, :h].contiguous(), wt[None, :h].contiguous(), off, out, ws,
+                               dy2=x[:, h:].contiguous(), w2=wt[None, h:].contiguous())
+    same(out, want)
+    smoe.smoe_get_status(ws)
+
+
+@pytest.mark.parametrize("T", [100, 300, 512])
+def test_long_sums_are_not_biased(T):
+    """Positive terms: 64 additions to a chunk of 1024, each cut off by about 2^-23 of a running sum
+    that is half of the chunk's on average: about 2^-18 of the result, and as much again for cuts above
+    one step and for the noise of the values that this moves across the middle of two bf16 numbers
+    (2^-8 sqrt(2^-10 / N), N > 25000: below 2^-20). One accumulator over 28672 channels loses 2^-13."""
+    n, m = 28672, 256
+    g = gen(T)
+    x = (torch.rand(T, n, generator=g, device="cuda") * (1 + torch.rand(T, 1, generator=g, device="cuda"))).bfloat16()
+    w = (torch.rand(m, n, generator=g, device="cuda") * (1 + torch.rand(m, 1, generator=g, device="cuda"))).bfloat16()
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    desc = smoe.make_desc(T, n, 1, 1, 1, m, 0, 1, 1, "bf16")
+    ws, out = smoe.workspace_products(desc), torch.empty(T, m, dtype=torch.bfloat16, device="cuda")
+    ref = x.double() @ w.double().T
+    near = ref.float().bfloat16().double()  # (the first rounding moves a value by 2^-24 at most)
+    for call in (lambda: smoe.smoe_expert_matmul(desc, x, off, w[None], out, ws),
+                 lambda: smoe.smoe_expert_matmul_dx(desc, x, w.T.contiguous()[None], off, out, ws)):
+        call()
+        assert float(((out.double() - near) / ref).mean().abs()) <= 2.0 ** -17
+        within(out, ref, HALF["bf16"] * ref * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", [
+    (100, 1, 1, 4168, 136, "one"), (700, 2, 3, 2056, 1032, "skew"), (512, 1, 1, 1024, 2048, "one"),
+    (64, 2, 6, 1032, 2056, "gaps"), (1024, 1, 2, 5128, 520, "even"), (450, 1, 1, 136, 9000, "one"),
+])
+def test_long_products(T, K, E, n_in, n_out, kind):
+    """bf16 products and row gradients whose contractions end in, at and behind a chunk, both
+    pairs' too: 64 additions a chunk, one more for each."""
+    c = Case(T, K, E, n_in, n_out, "bf16", kind, seed=8)
+    x, dy, w, dy2, w2 = c.rows(n_in), c.rows(n_out), c.weights(), c.rows(n_out), c.weights()
+    for call, n, pairs, width in (
+            (lambda o: smoe.smoe_expert_matmul(c.desc, x, c.off, w, o, c.ws), n_in, [(x, w.transpose(1, 2))], n_out),
+            (lambda o: smoe.smoe_expert_matmul_dx(c.desc, dy, w, c.off, o, c.ws), n_out, [(dy, w)], n_in),
+            (lambda o: smoe.smoe_expert_matmul_dx(c.desc, dy, w, c.off, o, c.ws, dy2=dy2, w2=w2), 2 * n_out,
+             [(dy, w), (dy2, w2)], n_in)):
+        out, again = c.out(width), c.out(width)
+        call(out)
+        ref, mag = torch.zeros(2, c.R, width, dtype=F64, device="cuda")
+        for e, s in enumerate(c.seg):
+            for a, b in pairs:
+                ref[s] += a[s].double() @ b[e].double()
+                mag[s] += a[s].double().abs() @ b[e].double().abs()
+        c.check_rows(out, ref, mag, 64 + n / 1024 + 8)
+        call(again)
+        same(again, out)
