@@ -384,6 +384,28 @@ def smoe_expert_ffn_i8(desc, xq, x_scale, expert_off, weights: I8Weights, y_disp
            "smoe_expert_ffn_i8")
 
 
+_KINDS = {}  # torch's types by what an argument holds
+
+
+def _room(kind, n, *tensors):
+    """Refuses buffers of another type, or with fewer than n elements: what a call reads or writes past a
+    buffer's end is somebody else's. tensors: names and tensors in turn (None, or an address, is not
+    looked at). The wrappers compare bytes first and come here where they are not just as many, since a
+    short call's time is the host's: one comparison of bytes takes 0.07 us, this 0.4."""
+    if not _KINDS:
+        import torch
+        _KINDS.update({"fp32": (torch.float32,), "int32": (torch.int32,), SMOE_F32: (torch.float32,),
+                       SMOE_BF16: (torch.bfloat16,), "8-bit": (torch.float8_e4m3fn, torch.uint8, torch.int8)})
+    types = _KINDS.get(kind)
+    for name, t in zip(tensors[::2], tensors[1::2]):
+        # (types is None: no type of the library's, which refuses the descriptor)
+        if t is None or isinstance(t, int) or types is None:
+            continue
+        if t.dtype not in types or t.numel() < n:
+            raise ValueError(f"{name} has shape {tuple(t.shape)} and type {t.dtype}; the call takes {n} elements "
+                             f"of type {types[0]}")
+
+
 def _matrix(desc, w, name):
     """(n_out, n_in) of expert weights [E, n_out, n_in]."""
     E, n_out, n_in = w.shape
@@ -393,18 +415,37 @@ def _matrix(desc, w, name):
 
 
 def _same(like, **tensors):
-    """Refuses buffers that hold another number of elements than `like` (the shape itself costs
-    more to compare, and a short call's time is the host's)."""
+    """Refuses buffers that hold another number of elements than `like`."""
     n = like.numel()
     for name, t in tensors.items():
         if t is not None and t.numel() != n:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
 
 
+def _like(like, name, t):
+    """Refuses a matrix of another size than `like`, or with rows of another length: a transposed
+    one has as many elements."""
+    if t is not None and (t.numel() != like.numel() or (t.dim() > 1 and t.shape[-1] != like.shape[-1])):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
+
+
+def _esize(desc):
+    return 4 if desc.dtype == SMOE_F32 else 2
+
+
 def smoe_rows_f8(desc, x, q, scale, pow2=0, stream=None):
     """x [rows, cols] in desc's dtype to q (e4m3) and scale [rows, ceil(cols / 128)]."""
     rows, cols = x.shape
-    _same(x, q=q)
+    n, ns = rows * cols, rows * (-(-cols // 128))
+    try:
+        odd = (x.nbytes != n * _esize(desc) or q.nbytes != n or scale.nbytes != 4 * ns)
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
+        _same(x, q=q)
+        _room(desc.dtype, n, "x", x)
+        _room("8-bit", n, "q", q)
+        _room("fp32", ns, "scale", scale)
     _check(lib().smoe_rows_f8(ctypes.byref(desc), rows, cols, _ptr(x), pow2, _ptr(q), _ptr(scale),
                               _stream(stream)), "smoe_rows_f8")
 
@@ -413,24 +454,65 @@ def smoe_expert_matmul_f8(desc, xq, x_scale, expert_off, wq, w_scale, out, ws, r
                           stream=None):
     """wq [E, n_out, n_in]; n_out and n_in are taken from its shape; ws from workspace_products."""
     n_out, n_in = _matrix(desc, wq, "wq")
+    R, kb, E = desc.T * desc.K, -(-n_in // 128), desc.E
+    rows, nw, no = R if row_src is None else desc.T, E * (-(-n_out // 128)) * kb, R * n_out
+    try:
+        odd = (xq.nbytes != rows * n_in or x_scale.nbytes != 4 * rows * kb or expert_off.nbytes != 4 * (E + 1)
+               or wq.nbytes != E * n_out * n_in or w_scale.nbytes != 4 * nw or out.nbytes != no * _esize(desc)
+               or (row_src is not None and row_src.nbytes != 4 * R))
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
+        _ptr(wq)
+        _room("8-bit", rows * n_in, "xq", xq)
+        _room("8-bit", 0, "wq", wq)
+        _room("fp32", rows * kb, "x_scale", x_scale)
+        _room("fp32", nw, "w_scale", w_scale)
+        _room("int32", R, "row_src", row_src)
+        _room("int32", E + 1, "expert_off", expert_off)
+        _room(desc.dtype, no, "out", out)
     _check(lib().smoe_expert_matmul_f8(ctypes.byref(desc), n_out, n_in, _ptr(xq), _ptr(x_scale),
-                                       _ptr(row_src), _ptr(expert_off), _ptr(wq), _ptr(w_scale),
-                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
-           "smoe_expert_matmul_f8")
+                                       _ptr(row_src), _ptr(expert_off), _ptr(wq), _ptr(w_scale), _ptr(out),
+                                       _ptr(ws), ws.numel(), _stream(stream)), "smoe_expert_matmul_f8")
 
 
 def smoe_expert_matmul(desc, x, expert_off, w, out, ws, stream=None):
     """out = x w^T by expert; w [E, n_out, n_in]; ws from workspace_products."""
     n_out, n_in = _matrix(desc, w, "w")
-    _check(lib().smoe_expert_matmul(ctypes.byref(desc), n_out, n_in, _ptr(x), _ptr(expert_off),
-                                    _ptr(w), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
-           "smoe_expert_matmul")
+    R, E, b = desc.T * desc.K, desc.E, _esize(desc)
+    try:
+        odd = (x.nbytes != R * n_in * b or expert_off.nbytes != 4 * (E + 1) or w.nbytes != E * n_out * n_in * b
+               or out.nbytes != R * n_out * b)
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
+        _ptr(w)
+        _room(desc.dtype, 0, "w", w)
+        _room(desc.dtype, R * n_in, "x", x)
+        _room(desc.dtype, R * n_out, "out", out)
+        _room("int32", E + 1, "expert_off", expert_off)
+    _check(lib().smoe_expert_matmul(ctypes.byref(desc), n_out, n_in, _ptr(x), _ptr(expert_off), _ptr(w),
+                                    _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "smoe_expert_matmul")
 
 
 def smoe_expert_matmul_dx(desc, dy, w, expert_off, dx, ws, dy2=None, w2=None, stream=None):
     """dx = dy w (+ dy2 w2) by expert; w, w2 [E, n_out, n_in]; ws from workspace_products."""
     n_out, n_in = _matrix(desc, w, "w")
-    _same(w, w2=w2)
+    _like(w, "w2", w2)
+    R, E, b = desc.T * desc.K, desc.E, _esize(desc)
+    nw, ny = E * n_out * n_in * b, R * n_out * b
+    try:
+        odd = (dy.nbytes != ny or w.nbytes != nw or expert_off.nbytes != 4 * (E + 1)
+               or dx.nbytes != R * n_in * b or (dy2 is not None and dy2.nbytes != ny)
+               or (w2 is not None and w2.nbytes != nw))
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
+        _ptr(w)
+        _room(desc.dtype, 0, "w", w, "w2", w2)
+        _room(desc.dtype, R * n_out, "dy", dy, "dy2", dy2)
+        _room(desc.dtype, R * n_in, "dx", dx)
+        _room("int32", E + 1, "expert_off", expert_off)
     _check(lib().smoe_expert_matmul_dx(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(w), _ptr(dy2),
                                        _ptr(w2), _ptr(expert_off), _ptr(dx), _ptr(ws), ws.numel(),
                                        _stream(stream)), "smoe_expert_matmul_dx")
@@ -439,31 +521,69 @@ def smoe_expert_matmul_dx(desc, dy, w, expert_off, dx, ws, dy2=None, w2=None, st
 def smoe_expert_matmul_dw(desc, dy, x, expert_off, dw, ws, add=None, stream=None):
     """dw = (add +) dy^T x by expert, fp32 [E, n_out, n_in]; ws from workspace_products."""
     n_out, n_in = _matrix(desc, dw, "dw")
-    _same(dw, add=add)
-    _check(lib().smoe_expert_matmul_dw(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(x),
-                                       _ptr(expert_off), _ptr(add), _ptr(dw), _ptr(ws), ws.numel(),
-                                       _stream(stream)), "smoe_expert_matmul_dw")
+    _like(dw, "add", add)
+    R, E, b = desc.T * desc.K, desc.E, _esize(desc)
+    nw = 4 * E * n_out * n_in
+    try:
+        odd = (dy.nbytes != R * n_out * b or x.nbytes != R * n_in * b or expert_off.nbytes != 4 * (E + 1)
+               or dw.nbytes != nw or (add is not None and add.nbytes != nw))
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
+        _ptr(dw)
+        _room("fp32", 0, "dw", dw, "add", add)
+        _room(desc.dtype, R * n_out, "dy", dy)
+        _room(desc.dtype, R * n_in, "x", x)
+        _room("int32", E + 1, "expert_off", expert_off)
+    _check(lib().smoe_expert_matmul_dw(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(x), _ptr(expert_off),
+                                       _ptr(add), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
+           "smoe_expert_matmul_dw")
 
 
 def smoe_expert_matmul_dw_f8(desc, dy, xq, x_scale, expert_off, dw, ws, row_src=None, add=None,
                              stream=None):
     """smoe_expert_matmul_dw from rows kept in 8 bits (token rows when row_src is given)."""
     n_out, n_in = _matrix(desc, dw, "dw")
-    _same(dw, add=add)
-    _check(lib().smoe_expert_matmul_dw_f8(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(xq),
-                                          _ptr(x_scale), _ptr(row_src), _ptr(expert_off), _ptr(add),
-                                          _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
-           "smoe_expert_matmul_dw_f8")
+    _like(dw, "add", add)
+    R, kb, E = desc.T * desc.K, -(-n_in // 128), desc.E
+    rows, nw = R if row_src is None else desc.T, 4 * E * n_out * n_in
+    try:
+        odd = (dy.nbytes != R * n_out * _esize(desc) or xq.nbytes != rows * n_in
+               or x_scale.nbytes != 4 * rows * kb or expert_off.nbytes != 4 * (E + 1) or dw.nbytes != nw
+               or (add is not None and add.nbytes != nw) or (row_src is not None and row_src.nbytes != 4 * R))
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
+        _ptr(dw)
+        _room("fp32", 0, "dw", dw, "add", add)
+        _room(desc.dtype, R * n_out, "dy", dy)
+        _room("8-bit", rows * n_in, "xq", xq)
+        _room("fp32", rows * kb, "x_scale", x_scale)
+        _room("int32", R, "row_src", row_src)
+        _room("int32", E + 1, "expert_off", expert_off)
+    _check(lib().smoe_expert_matmul_dw_f8(ctypes.byref(desc), n_out, n_in, _ptr(dy), _ptr(xq), _ptr(x_scale),
+                                          _ptr(row_src), _ptr(expert_off), _ptr(add), _ptr(dw), _ptr(ws),
+                                          ws.numel(), _stream(stream)), "smoe_expert_matmul_dw_f8")
 
 
 def smoe_swiglu_f8(desc, g, u, h=None, h8=None, h8_scale=None, g8=None, g8_scale=None, u8=None,
                    u8_scale=None, pow2=1, stream=None):
     """h = silu(g) u, and h, g, u in 8 bits, each where its buffers are given."""
     rows, cols = g.shape
-    n = rows * cols
-    if (u.numel() != n or (h is not None and h.numel() != n) or (h8 is not None and h8.numel() != n)
-            or (g8 is not None and g8.numel() != n) or (u8 is not None and u8.numel() != n)):
+    n, ns = rows * cols, rows * (-(-cols // 128))
+    nb, sb = n * _esize(desc), 4 * ns
+    try:
+        odd = (g.nbytes != nb or u.nbytes != nb or (h is not None and h.nbytes != nb)
+               or (h8 is not None and h8.nbytes != n) or (h8_scale is not None and h8_scale.nbytes != sb)
+               or (g8 is not None and g8.nbytes != n) or (g8_scale is not None and g8_scale.nbytes != sb)
+               or (u8 is not None and u8.nbytes != n) or (u8_scale is not None and u8_scale.nbytes != sb))
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
         _same(g, u=u, h=h, h8=h8, g8=g8, u8=u8)
+        _room(desc.dtype, n, "g", g, "u", u, "h", h)
+        _room("8-bit", n, "h8", h8, "g8", g8, "u8", u8)
+        _room("fp32", ns, "h8_scale", h8_scale, "g8_scale", g8_scale, "u8_scale", u8_scale)
     _check(lib().smoe_swiglu_f8(ctypes.byref(desc), rows, cols, _ptr(g), _ptr(u), pow2, _ptr(h),
                                 _ptr(h8), _ptr(h8_scale), _ptr(g8), _ptr(g8_scale), _ptr(u8),
                                 _ptr(u8_scale), _stream(stream)), "smoe_swiglu_f8")
@@ -472,10 +592,19 @@ def smoe_swiglu_f8(desc, g, u, h=None, h8=None, h8_scale=None, g8=None, g8_scale
 def smoe_swiglu_grad_f8(desc, dh, g8, g8_scale, u8, u8_scale, dg, du, h=None, stream=None):
     """dg, du (and h again) from dh and what smoe_swiglu_f8 kept."""
     rows, cols = dh.shape
-    n = rows * cols
-    if (g8.numel() != n or u8.numel() != n or dg.numel() != n or du.numel() != n
-            or (h is not None and h.numel() != n)):
+    n, ns = rows * cols, rows * (-(-cols // 128))
+    nb, sb = n * _esize(desc), 4 * ns
+    try:
+        odd = (dh.nbytes != nb or g8.nbytes != n or g8_scale.nbytes != sb or u8.nbytes != n
+               or u8_scale.nbytes != sb or dg.nbytes != nb or du.nbytes != nb
+               or (h is not None and h.nbytes != nb))
+    except AttributeError:  # an address among them
+        odd = True
+    if odd:
         _same(dh, g8=g8, u8=u8, dg=dg, du=du, h=h)
+        _room(desc.dtype, n, "dh", dh, "dg", dg, "du", du, "h", h)
+        _room("8-bit", n, "g8", g8, "u8", u8)
+        _room("fp32", ns, "g8_scale", g8_scale, "u8_scale", u8_scale)
     _check(lib().smoe_swiglu_grad_f8(ctypes.byref(desc), rows, cols, _ptr(dh), _ptr(g8),
                                      _ptr(g8_scale), _ptr(u8), _ptr(u8_scale), _ptr(dg), _ptr(du),
                                      _ptr(h), _stream(stream)), "smoe_swiglu_grad_f8")

@@ -148,3 +148,50 @@ def test_binding_refuses_other_shapes(lib):
         B.smoe_expert_matmul_dw(desc(), z, z, z, torch.zeros(8, 16, 16), z, add=w, stream=0)
     with pytest.raises(ValueError, match="u8 has shape"):
         B.smoe_swiglu_f8(desc(), torch.zeros(2, 16), torch.zeros(2, 16), u8=z, u8_scale=z, stream=0)
+
+
+def test_binding_refuses_buffers_that_are_too_small(lib):
+    """Each buffer's type and room, before any call: a call of [T K] = 32 rows on 8 experts of 256 x 128."""
+    import torch
+    bf, f4, f8, i4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+    z = lambda t, *s: torch.zeros(*s, dtype=t)  # noqa: E731
+    d, R = desc(), 32
+    ws = z(torch.uint8, 16)
+    w, w8, off, src = z(bf, 8, 256, 128), z(f8, 8, 256, 128), z(i4, 9), z(i4, R)
+    x, y, dw = z(bf, R, 128), z(bf, R, 256), z(f4, 8, 256, 128)
+    x8, xs, wsc = z(f8, 16, 128), z(f4, 16, 1), z(f4, 8, 2, 1)
+    g, g8, gs = z(bf, R, 136), z(f8, R, 136), z(f4, R, 2)
+    calls = {
+        B.smoe_rows_f8: dict(x=g, q=g8, scale=gs),
+        B.smoe_expert_matmul_f8: dict(xq=x8, x_scale=xs, expert_off=off, wq=w8, w_scale=wsc, out=y, row_src=src),
+        B.smoe_expert_matmul: dict(x=x, expert_off=off, w=w, out=y),
+        B.smoe_expert_matmul_dx: dict(dy=y, w=w, expert_off=off, dx=x, dy2=y, w2=w),
+        B.smoe_expert_matmul_dw: dict(dy=y, x=x, expert_off=off, dw=dw, add=dw),
+        B.smoe_expert_matmul_dw_f8: dict(dy=y, xq=x8, x_scale=xs, expert_off=off, dw=dw, row_src=src, add=dw),
+        B.smoe_swiglu_f8: dict(g=g, u=g, h=g, h8=g8, h8_scale=gs, g8=g8, g8_scale=gs, u8=g8, u8_scale=gs),
+        B.smoe_swiglu_grad_f8: dict(dh=g, g8=g8, g8_scale=gs, u8=g8, u8_scale=gs, dg=g, du=g, h=g),
+    }
+    for f, kw in calls.items():
+        more = {} if "swiglu" in f.__name__ or "rows" in f.__name__ else dict(ws=ws)
+        # whole buffers pass the binding: the C side refuses the workspace, or goes on to the device
+        if more:
+            with pytest.raises(B.SmoeError, match="workspace"):
+                f(d, **kw, **more, stream=0)
+        for name, t in kw.items():
+            short = t.reshape(-1)[:-1] if t.dim() == 1 else t[:-1]
+            other = t.to({bf: f4, f4: bf, f8: bf, i4: torch.int64}[t.dtype])
+            for bad in (short, other):
+                with pytest.raises(ValueError, match="has shape|holds 7 experts"):
+                    f(d, **{**kw, name: bad}, **more, stream=0)
+    # longer buffers are taken, as of a larger batch; matrices that are another's transpose are not
+    with pytest.raises(B.SmoeError):
+        B.smoe_expert_matmul(d, z(bf, 40, 128), z(i4, 12), w, z(bf, 40, 256), ws, stream=0)
+    with pytest.raises(ValueError, match="w2 has shape"):
+        B.smoe_expert_matmul_dx(d, y, w, off, x, ws, dy2=y, w2=z(bf, 8, 128, 256), stream=0)
+    with pytest.raises(ValueError, match="add has shape"):
+        B.smoe_expert_matmul_dw(d, y, x, off, dw, ws, add=z(f4, 8, 128, 256), stream=0)
+    # rows in dispatched order, not token rows
+    with pytest.raises(ValueError, match="xq has shape"):
+        B.smoe_expert_matmul_f8(d, x8, z(f4, R, 1), off, w8, wsc, y, ws, stream=0)
+    with pytest.raises(ValueError, match="x_scale has shape"):
+        B.smoe_expert_matmul_dw_f8(d, y, z(f8, R, 128), xs, off, dw, ws, stream=0)
