@@ -389,6 +389,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       F8Tile tl = f8_decode<WIDE>(p, s_ts, s_off, ntile, t, g);
       tl.n0 += 128 * half;
+      // a row without a token is zero whatever the weights are (0 NaN is not); looked at below
+      int src = 0;
+      if (p.row_src && r < tl.rows) src = __ldcg(p.row_src + tl.row0 + r);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
@@ -426,6 +429,10 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
         if (++b == C::kBufs) { b = 0; bph ^= 1u; }
       }
       if (!ok) break;
+      if ((unsigned)src >= (unsigned)p.n_src) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      }
       // 32 rows x 128 bytes, two such windows at a time, through the warp's own 8 KB (16-byte
       // chunks swizzled by row as TMA reads them: no bank conflicts), stored by TMA, or where
       // the tile's rows end inside by the warp. (Read back and stored by the warp throughout,
@@ -536,11 +543,13 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW,  // weights as 16-bit pa
         if (++b == C::kBufs) { b = 0; bph ^= 1u; }
       }
       if (!ok) break;
+      // a row without a token is zero whatever the weights are (0 NaN is not)
+      const uint32_t some[2] = {__ballot_sync(0xffffffffu, has[0]), __ballot_sync(0xffffffffu, has[1])};
       if (chan < p.N) {
         TO* out = static_cast<TO*>(p.out) + (size_t)tl.row0 * p.N + chan;
 #pragma unroll
         for (int i = 0; i < 64; ++i, out += p.N)
-          if (i < tl.rows) *out = Elem<TO>::from_f32(acc[i]);
+          if (i < tl.rows) *out = Elem<TO>::from_f32(some[i >> 5] >> (i & 31) & 1u ? acc[i] : 0.0f);
       }
     }
     if (!ok && lane == 0) {

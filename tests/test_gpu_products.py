@@ -937,3 +937,21 @@ def test_long_products(T, K, E, n_in, n_out, kind):
         c.check_rows(out, ref, mag, 64 + n / 1024 + 8)
         call(again)
         same(again, out)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [30, 600])
+def test_bad_row_src_beside_weights_that_are_not_finite(T, dt):
+    """An entry out of range gives a row of zeros whatever its expert's weights and scales are."""
+    f = F8Case(T, 2, 4, 256, 264, dt, "even")
+    o, keep = f.off.tolist(), f.src.clone()
+    f.wq.view(torch.uint8)[0] = 0x7f       # NaN
+    f.sw[1], f.sw[2] = math.inf, math.nan
+    rows = [s for e in range(4) for s in (o[e], (o[e] + o[e + 1]) // 2, o[e + 1] - 1)]
+    f.src[rows] = torch.tensor([-1, T, 1 << 30] * 4, dtype=torch.int32, device="cuda")
+    out = f.run()
+    with pytest.raises(smoe.SmoeError, match="SMOE_ERR_DATA"):
+        smoe.smoe_get_status(f.ws)
+    hit = f.src != keep
+    assert int(hit.sum()) == 12 and (out[hit] == 0).all()
+    assert not out[:o[3]][~hit[:o[3]]].isfinite().any() and out[o[3]:].isfinite().all()
