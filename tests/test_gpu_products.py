@@ -955,3 +955,40 @@ def test_bad_row_src_beside_weights_that_are_not_finite(T, dt):
     hit = f.src != keep
     assert int(hit.sum()) == 12 and (out[hit] == 0).all()
     assert not out[:o[3]][~hit[:o[3]]].isfinite().any() and out[o[3]:].isfinite().all()
+
+
+# ------------------------------------------------------------------ products in fp32, not in fewer bits
+# T, K, E, n_in, n_out, kind: few rows an expert (streamed weights), 64-row tiles, whole and
+# in slices, planes on the tensor cores, whole and in slices
+FP32_SHAPES = [
+    (40, 2, 24, 1000, 1416, "skew"), (9, 1, 2, 1416, 200, "even"), (4096, 1, 1, 64, 512, "one"), (256, 2, 4, 264, 256, "skew"),
+    (300, 1, 1, 1416, 136, "gaps"), (2048, 2, 4, 1000, 2056, "skew"), (512, 1, 4, 1032, 1000, "even"), (700, 1, 1, 1416, 264, "one"),
+]
+
+
+@pytest.mark.parametrize("T,K,E,n_in,n_out,kind", FP32_SHAPES)
+def test_fp32_products_keep_24_bits(T, K, E, n_in, n_out, kind):
+    """Relative error in the Frobenius norm. On the CUDA cores each of n additions is off by at most
+    2^-24 of a running sum whose square grows evenly: 2^-24 sqrt(n / 2) of the result, below 2e-6 up to
+    2200 additions in a row (a sum over 2 x 2056 is split over eight warps or slices). On the tensor cores
+    chunks of 128: 48 additions, each cut off by half of 2^-23 on average of a running sum that is 2/3 of the
+    chunk's, 1.9e-6. Operands of 11 bits (tf32) give 3e-4, without the three smallest plane products
+    5e-6."""
+    c = Case(T, K, E, n_in, n_out, "f32", kind, seed=12)
+    x, dy, w, dy2, w2 = c.rows(n_in), c.rows(n_out), c.weights(), c.rows(n_out), c.weights()
+    out, dx, dx2, dw = c.out(n_out), c.out(n_in), c.out(n_in), torch.empty(E, n_out, n_in, device="cuda")
+    smoe.smoe_expert_matmul(c.desc, x, c.off, w, out, c.ws)
+    smoe.smoe_expert_matmul_dx(c.desc, dy, w, c.off, dx, c.ws)
+    smoe.smoe_expert_matmul_dx(c.desc, dy, w, c.off, dx2, c.ws, dy2=dy2, w2=w2)
+    smoe.smoe_expert_matmul_dw(c.desc, dy, x, c.off, dw, c.ws)
+    smoe.smoe_get_status(c.ws)
+    refs = [torch.zeros_like(t, dtype=F64) for t in (out, dx, dx2, dw)]
+    for e, s in enumerate(c.seg):
+        refs[0][s] = x[s].double() @ w[e].double().T
+        refs[1][s] = dy[s].double() @ w[e].double()
+        refs[2][s] = refs[1][s] + dy2[s].double() @ w2[e].double()
+        refs[3][e] = dy[s].double().T @ x[s].double()
+    for got, ref in zip((out, dx, dx2), refs):
+        assert (got[~c.inside] == 7).all()
+        assert float((got.double() - ref)[c.inside].norm() / ref.norm()) <= 2e-6
+    assert float((dw.double() - refs[3]).norm() / refs[3].norm()) <= 2e-6
