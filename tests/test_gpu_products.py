@@ -992,3 +992,19 @@ def test_fp32_products_keep_24_bits(T, K, E, n_in, n_out, kind):
         assert (got[~c.inside] == 7).all()
         assert float((got.double() - ref)[c.inside].norm() / ref.norm()) <= 2e-6
     assert float((dw.double() - refs[3]).norm() / refs[3].norm()) <= 2e-6
+
+
+@pytest.mark.parametrize("T", [60, 900])
+def test_f8_token_whose_scale_is_nan(T):
+    """The rows of a token with a NaN scale are NaN, and no others (rows of that token among them)."""
+    c = F8Case(T, 1, 5, 272, 200, "f32", "skew", seed=9)
+    o = c.off.tolist()
+    c.src[c.src == 3] = 4
+    c.src[[o[0], o[5] - 1, (o[0] + o[5]) // 2]] = 3
+    clean = c.run()
+    c.s[3, 1] = math.nan
+    dirty = c.run()
+    hit = (c.src == 3) & c.inside
+    assert int(hit.sum()) == 3
+    same(dirty[~hit], clean[~hit])
+    assert dirty[hit].isnan().all()
