@@ -1008,3 +1008,28 @@ def test_f8_token_whose_scale_is_nan(T):
     assert int(hit.sum()) == 3
     same(dirty[~hit], clean[~hit])
     assert dirty[hit].isnan().all()
+
+
+def test_swiglu_far_from_zero():
+    """bf16 layers take sig from a fast exponential that is off by (2 + 1.2 |g|) steps of 2^-23, and a
+    division and sums off by two more: (4 + 1.2 |g|) 2^-23 of the result, beside its rounding. Below
+    g = -87 sig is under 2^-126 and may be zero."""
+    g = torch.linspace(-100, 100, 4096, device="cuda").bfloat16().view(32, 128)
+    u, dh = torch.full_like(g, 0.75), torch.full_like(g, 1.5)
+    q, s = [torch.empty(32, 128, dtype=F8, device="cuda") for _ in range(2)], [torch.empty(32, 1, device="cuda") for _ in range(2)]
+    h, h2, dg, du = (torch.full_like(g, 7.0) for _ in range(4))
+    smoe.smoe_swiglu_f8(rows_desc("bf16"), g, u, h=h, g8=q[0], g8_scale=s[0], u8=q[1], u8_scale=s[1])
+    smoe.smoe_swiglu_grad_f8(rows_desc("bf16"), dh, q[0], s[0], q[1], s[1], dg, du, h=h2)
+    err = lambda g: (4 + 1.2 * g.abs()) * 2.0 ** -23  # noqa: E731
+    G, U, D = g.double(), u.double(), dh.double()
+    ref = G * torch.sigmoid(G) * U
+    within(h, ref, (HALF["bf16"] + err(G) + 2.0 ** -22) * ref.abs() + 2.0 ** -126 * (G * U).abs() + 1e-38)
+    G, U = (a.double() * spread(b, 128) for a, b in zip(q, s))
+    sig = torch.sigmoid(G)
+    tiny = 2.0 ** -126 * (1 + (G * U * D).abs() + (G * D).abs()) * (1 + G.abs())
+    within(h2, G * sig * U, (HALF["bf16"] + err(G) + 2.0 ** -22) * (G * sig * U).abs() + tiny)
+    within(du, D * G * sig, (HALF["bf16"] + err(G) + 2.0 ** -22) * (D * G * sig).abs() + tiny)
+    # 1 + g (1 - sig): its terms' errors are relative to them, and 1 - sig is off by a step of 1
+    terms = (D * U * sig).abs() * (1 + G.abs() * (1 - sig))
+    ref = D * U * sig * (1 + G * (1 - sig))
+    within(dg, ref, HALF["bf16"] * ref.abs() + 2 * (err(G) + 2.0 ** -22) * terms + 2.0 ** -23 * (D * U * sig * G).abs() + tiny)
