@@ -18,7 +18,7 @@
 //          to 16, and the row scales are read from shared memory
 //
 // Measured: 384 rows over 160 experts of 5120 to 1536 channels (narrow) 181 us, 6.3 TB/s of
-// weights; 131072 rows over 128 experts of 2048 to 768 (wide) 226 us, 1.83 PFLOP/s; 2002 rows over
+// weights; 131072 rows over 128 experts of 2048 to 768 (wide) 229 us, 1.80 PFLOP/s; 2002 rows over
 // 8 experts of 4096 to 14336, fp32 out, 152 us. What bounds the wide form: without its stores the
 // prefill product took 205 us, without the epilogue's FMAs and TMEM loads besides 170, without the
 // gathering and the weights' loads besides 125: the work of each of the three overlaps the MMAs (96 us

@@ -38,8 +38,11 @@ constexpr int kDwCols = 1024 / kDwWarps;  // columns of an epilogue warp
 // long sums drift (1024 rows: 1.2e-6 of the result). So the rows after the first chunk of an
 // expert go into the other TMEM accumulator, chunk by chunk, which the epilogue adds, rounded, to
 // the first one. For fp32 operands, whose six products add up six times as often, after fewer rows.
-// (131072 rows of 128 experts, accumulated: chunks of 512 rows 483 us, 768: 452, 1024: 434, one: 402.
-// With the sums in registers, 128 of them a thread, 530.)
+// A choice of time against accuracy (131072 rows of 128 experts, accumulated, us and relative error in the
+// norm, a plain fp32 sum 2.7e-7: chunks of 256 rows 554 and 2.2e-7, 512: 479 and 4.3e-7, 768: 447 and
+// 6.7e-7, 1024: 432 and 8.5e-7, one: 402; 8192 rows of one expert, plain 9.5e-7: 27.9 and 2.4e-7, 25.7 and
+// 4.7e-7, 25.1 and 6.7e-7, 24.5 and 9.9e-7; terms of one sign lose up to 5e-6 with 1024): what enters
+// the sums has 2^-9 of its own. (With the sums in registers, 128 of them a thread, 530 us.)
 template <int PL> constexpr int kDwChunk = PL == 1 ? 1024 : 128;
 constexpr int kDwHalf = 128 * 128;  // bytes of an operand's stage in a CTA: 64 rows of 128 channels
 constexpr size_t kDwSmem = kDwSlack + kDwStages * 2 * kDwHalf + kDwWarps * 4096 +

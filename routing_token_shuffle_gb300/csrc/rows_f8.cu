@@ -111,9 +111,11 @@ __device__ __forceinline__ float sigmoid(float x) {
   return 1.0f / (1.0f + expf(-x));
 }
 
-// This thread's place: item `it` of `items` is 128 channels of a row. One item a thread: many
-// small blocks kept more loads in flight than two or four items of a thread with their loads first
-// (131072 rows of 768, forward and backward: one 291 us, two 325, four 435).
+// This thread's place: item `it` of `items` is 128 channels of a row. One item a thread: in the
+// SwiGLU kernels, which load two or three vectors an item, many small blocks kept more loads in flight
+// than two or four items of a thread with their loads first (131072 rows of 768, forward and backward: one
+// 291 us, two 325, four 435). (rows_f8_kernel, one load an item, has the same form and was not measured
+// with more.)
 struct Place {
   bool in, lead;   // inside the row; the block's first lane
   size_t at, block;  // element and scale index
