@@ -1033,3 +1033,47 @@ def test_swiglu_far_from_zero():
     terms = (D * U * sig).abs() * (1 + G.abs() * (1 - sig))
     ref = D * U * sig * (1 + G * (1 - sig))
     within(dg, ref, HALF["bf16"] * ref.abs() + 2 * (err(G) + 2.0 ** -22) * terms + 2.0 ** -23 * (D * U * sig * G).abs() + tiny)
+
+
+@pytest.mark.parametrize("T", [90, 700])
+def test_long_products_captured_and_on_two_streams(T):
+    """Contractions of several chunks on two streams at once, each with its own workspace, and replayed
+    from a graph on new rows, give the eager calls' bits."""
+    cases = [Case(T, 2, 2, 2568, 4104, "bf16", kind, seed=s) for kind, s in (("skew", 20), ("gaps", 21))]
+    for c in cases:
+        c.x, c.dy, c.w, c.dy2, c.w2 = c.rows(2568), c.rows(4104), c.weights(), c.rows(4104), c.weights()
+        c.y, c.dx = c.out(4104), c.out(2568)
+
+    def run(c):
+        smoe.smoe_expert_matmul(c.desc, c.x, c.off, c.w, c.y, c.ws)
+        smoe.smoe_expert_matmul_dx(c.desc, c.dy, c.w, c.off, c.dx, c.ws, dy2=c.dy2, w2=c.w2)
+
+    want = []
+    for c in cases:
+        run(c)
+        want.append((c.y.clone(), c.dx.clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for c, s in zip(cases, streams):
+            c.y.fill_(7.0)
+            c.dx.fill_(7.0)
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                run(c)
+        torch.cuda.synchronize()
+        for c, (y, dx) in zip(cases, want):
+            same(c.y, y)
+            same(c.dx, dx)
+    c = cases[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(c)
+    for t in (c.x, c.dy, c.dy2):
+        t.neg_()
+    c.y.fill_(7.0)
+    c.dx.fill_(7.0)
+    graph.replay()
+    for got, was in ((c.y, want[0][0]), (c.dx, want[0][1])):
+        same(got[c.inside], -was[c.inside])
+        assert (got[~c.inside] == 7.0).all()
+    smoe.smoe_get_status(c.ws)
